@@ -399,7 +399,7 @@ def run(s):
         return _written(s)
     if c["op"] == "read":
         return s["cache"].read(s["cu"], s["starts"], s["table"], s["T"], k_out=s["k_out"], v_out=s["v_out"])
-    return s["cache"].attend(s["q"], s["cu"], s["lens"], s["table"], c["d"] ** -0.5, window=c["window"],
+    return s["cache"].attend(s["q"], s["cu"], s["starts"], s["table"], c["d"] ** -0.5, window=c["window"],
                              sinks=c["sinks"], o=s["o"], lse=s["lse"])
 
 
