@@ -57,6 +57,10 @@ typedef enum {
 #define FLAMIA_DEV_RANGE       0x8  /* a scale exponent left the E8M0 range a mode
                                        supports (per-token operand scales with
                                        |V| near 2^96 or beyond); outputs invalid */
+#define FLAMIA_DEV_BAD_PAGE    0x10 /* a page-table entry that a call needs lies outside
+                                       [0, num_pages), or a sequence's positions
+                                       outside its table; that page is neither read
+                                       nor written                               */
 
 /* Quantiser output formats. */
 #define FLAMIA_FORMAT_MXFP8       0 /* E4M3 codes + per-token E8M0 scales          */
@@ -138,6 +142,12 @@ typedef enum {
                                        measured about 1.5x slower on the
                                        packed 4 x 4096 and variable-length
                                        workloads)                              */
+
+/* Rotary flags. */
+#define FLAMIA_FLAG_ROPE_INTERLEAVED 0x2000 /* pair i of a row is elements (2i, 2i + 1);
+                                       default: (i, i + rot_dim / 2)              */
+#define FLAMIA_FLAG_ROPE_INVERSE 0x4000 /* the transposed rotation: gradients of the
+                                       rotated rows -> gradients of the rows      */
 
 /*
  * One quantised operand, all device pointers owned by the caller.
@@ -412,6 +422,129 @@ flamia_status flamia_attn_bwd_gqa(const flamia_qtensor* q, const flamia_qtensor*
                                   int flags, void* wl, void* dq_bf16, void* dk_bf16,
                                   void* dv_bf16, void* ws, size_t ws_bytes, int* dev_status,
                                   void* stream);
+
+/*
+ * Rotary positions of Q and K (and, inverted, of dQ and dK).  The paper has no
+ * counterpart: it is what a model applies to Q and K before the quantiser, and
+ * to dQ and dK after the backward.
+ *
+ * Token t of document b stands at position p = starts[b] + t - cu_seqlens[b]
+ * (starts NULL: 0).  Pair i < rot_dim / 2 of every head's row is turned by the
+ * angle 2 pi frac(p * turns[i] / 2^64) and multiplied by mscale:
+ *   (x, y) -> mscale (x cos - y sin, x sin + y cos);
+ * FLAMIA_FLAG_ROPE_INVERSE turns the other way (the transpose, mscale kept).
+ * Elements rot_dim .. d - 1 of a row are copied.  turns[i] is the step of one
+ * position in 2^-64 turns, round(2^64 w_i / (2 pi)) for an angle of p w_i: the
+ * product with p wraps at whole turns, so far positions lose nothing.
+ *
+ *  q_in, q_out  BF16 rows [T][H][d]: head h of token t at t * stride + h * d
+ *               (strides in elements, multiples of 8, >= H * d; rows 16-byte
+ *               aligned, so a slice of a packed QKV tensor will do).  q_out
+ *               may be q_in with the same stride (in place); otherwise the
+ *               two must not overlap.  k_in, k_out the same with H_kv heads
+ *               (H_kv 0: no K; otherwise it need not divide H).
+ *  turns        device uint64[rot_dim / 2].  rot_dim: a multiple of 16, 16 .. d.
+ *  starts       device int32[ndocs] or NULL.
+ *  cu_seqlens   as elsewhere, but it may end before T (a padded batch): rows
+ *               behind the last document are neither read nor written.
+ *  flags        FLAMIA_FLAG_ROPE_INTERLEAVED | FLAMIA_FLAG_ROPE_INVERSE.
+ * T == 0 enqueues nothing.  ndocs <= 2^20.
+ */
+flamia_status flamia_rope(const void* q_in, void* q_out, int64_t q_in_stride,
+                          int64_t q_out_stride, const void* k_in, void* k_out,
+                          int64_t k_in_stride, int64_t k_out_stride, int T, int H, int H_kv,
+                          int d, const uint64_t* turns, int rot_dim, float mscale, int flags,
+                          const int32_t* cu_seqlens, int ndocs, const int32_t* starts,
+                          int* dev_status, void* stream);
+
+/*
+ * Paged key-value cache: the K and V of running sequences in the quantiser's
+ * format, for the calls below.  All device pointers, owned by the caller.
+ *  k_codes, v_codes    u8 [num_pages][H_kv][page_size][d]  E4M3 codes.
+ *  k_scales, v_scales  u8 [num_pages][H_kv][page_size]     E8M0 byte per token.
+ * codes 128-byte aligned, scales 32-byte aligned.  page_size: 32, 64 or a
+ * multiple of 128 up to 2^20; num_pages * H_kv < 2^31; 1 <= H_kv <= 4096.
+ * Position p of sequence b is row p % page_size of page
+ * page_table[b * table_stride + p / page_size] (device int32, entries of pages
+ * that no call needs are not read; table_stride entries per sequence).  Two
+ * sequences may share pages that are only read.
+ */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t H_kv;
+  int32_t d;
+} flamia_kvcache;
+
+/*
+ * Quantises new tokens into the cache.  Token t of document b goes to position
+ * starts[b] + t - cu_seqlens[b] of sequence b (starts NULL: 0).
+ * format FLAMIA_FORMAT_MXFP8: one exponent per 32-token block (positions 32 i ..
+ * 32 i + 31) and head, the rule of flamia_quantize_tokenblock over the new
+ * tokens of the block; where the block already holds tokens (starts[b] inside
+ * it) the exponent is the larger of that and the held one, and if it grew the
+ * held codes c become RNE_E4M3(c 2^(e_old - e)).  So a prompt written at
+ * starts 0 gets the codes and scale bytes that flamia_quantize_tokenblock
+ * gives it, bit for bit, and a call repeated on the same tokens changes nothing.
+ * FLAMIA_FORMAT_TOKEN_SCALES OR-ed in: one exponent per token and head.
+ * Infinities and NaN become NaN codes and do not enter the block maximum.
+ * Positions behind the last new token keep what they held.
+ *
+ *  k_bf16, v_bf16  BF16 rows [T][H_kv][d], token strides in elements (multiples
+ *                  of 8), rows 16-byte aligned.
+ * cu_seqlens may end before T; documents may be empty (idle sequences).  No
+ * two documents of a call may write the same page.  T == 0 enqueues nothing.
+ */
+flamia_status flamia_cache_write(const flamia_kvcache* cache, const void* k_bf16,
+                                 int64_t k_stride, const void* v_bf16, int64_t v_stride, int T,
+                                 const int32_t* cu_seqlens, int ndocs, const int32_t* starts,
+                                 const int32_t* page_table, int table_stride, int format,
+                                 int* dev_status, void* stream);
+
+/*
+ * Reads cached tokens back: positions starts[b] .. of sequence b into packed
+ * tokens [cu_seqlens[b], cu_seqlens[b + 1]) as BF16 (code * 2^e, rounded to
+ * nearest even where BF16 cannot hold it: only below its normal range).
+ * Arguments as for flamia_cache_write, k_bf16 / v_bf16 the outputs (strides
+ * >= H_kv * d); rows without a cached token or a valid page keep what they held.
+ */
+flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16, int64_t k_stride,
+                                void* v_bf16, int64_t v_stride, int T, const int32_t* cu_seqlens,
+                                int ndocs, const int32_t* starts, const int32_t* page_table,
+                                int table_stride, int* dev_status, void* stream);
+
+/*
+ * Attention of new tokens over the cache (single tokens, drafted tokens or
+ * the next chunk of a prompt, mixed freely in one call), after they were
+ * written to it with the same cu_seqlens, starts and page_table.  Query i of
+ * sequence b stands at position p = starts[b] + i (starts NULL: 0).  It sees
+ * key j iff 0 <= j <= p and, with window > 0, j > p - window or j < sinks.
+ *   o = softmax(softmax_scale q K^T) V over the seen keys, K and V the cached
+ *   values code * 2^e; lse = log sum exp of the scaled scores (natural log).
+ * A query that sees no key (p < 0) gets o = 0 and lse = -inf.  A NaN key or
+ * value that a query sees makes its output NaN; one that it does not see, and
+ * whatever lies behind a sequence's last token, changes nothing.
+ * Query head h reads K / V head h / (H / H_kv).
+ *
+ *  q_bf16     BF16 rows [T][H][d], token stride in elements (multiple of 8).
+ *  o_bf16     [T, H, d] BF16.   lse  float [H, T], or NULL.
+ *  window     0: every earlier key.   sinks  >= 0; needs window > 0 if > 0.
+ *  ws         flamia_attn_cache_workspace_bytes bytes, 256-byte aligned; calls
+ *             that may overlap need one each.  Nothing is kept in it.
+ * cu_seqlens may end before T: rows behind the last sequence are not written
+ * (lse columns neither).  T == 0 enqueues nothing.
+ */
+size_t flamia_attn_cache_workspace_bytes(int T, int ndocs, int H, int H_kv, int d);
+flamia_status flamia_attn_cache(const flamia_kvcache* cache, const void* q_bf16, int64_t q_stride,
+                                int T, int H, const int32_t* cu_seqlens, int ndocs,
+                                const int32_t* starts, const int32_t* page_table,
+                                int table_stride, float softmax_scale, int window, int sinks,
+                                void* o_bf16, float* lse, void* ws, size_t ws_bytes,
+                                int* dev_status, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* flamia_status_str(flamia_status s);

@@ -1,0 +1,308 @@
+// Paged key-value cache in the quantiser's format: write (quantise BF16 K and
+// V rows into it) and read back.
+//
+// One warp owns one 32-token block of one head of K or V: the block's rows
+// (32 x d BF16, 8 or 4 KB) stay in its registers between the maximum and the
+// codes, so each element is read once, and no shared memory or block-wide
+// barrier is needed.  Blocks are found without a prefix sum over the
+// sequences: sequence b owns the block numbers from cu[b] / 32 + 2 b on, which
+// leaves room for its ragged first and last block whatever its start.
+// HBM-bound: 2 bytes on the BF16 side, 1 code byte and d^-1 scale bytes on the
+// other.
+#include <cuda_bf16.h>
+
+#include "paged.cuh"
+
+namespace flamia {
+namespace {
+
+constexpr int kCacheThreads = 128;
+
+struct CacheArgs {
+  uint8_t* codes[2];   // K, V
+  uint8_t* scales[2];
+  __nv_bfloat16* rows[2];
+  long long stride[2];
+  const int32_t* cu;
+  const int32_t* starts;
+  const int32_t* table;
+  int* status;
+  int T, H_kv, ndocs, table_stride, num_pages, page_size;
+  long long units;  // warps of the launch: blocks x heads x {K, V}
+};
+
+// The block of one warp: positions [p0, p0 + 32) of a sequence, of which the
+// call's tokens are [lo, hi) (as offsets into the block).
+struct Block {
+  int lo, hi;
+  int h, kv;          // head, 0 = K / 1 = V
+  long long row;      // first row of the block in the codes / scales arrays
+  long long token;    // packed row of offset 0 (may lie before the document)
+};
+
+__device__ __forceinline__ bool find_block(const CacheArgs& g, long long unit, int lane,
+                                           Block& blk) {
+  const int per = 2 * g.H_kv;
+  const int vb = static_cast<int>(unit / per);
+  const int hk = static_cast<int>(unit - static_cast<long long>(vb) * per);
+  blk.kv = hk >= g.H_kv;
+  blk.h = hk - blk.kv * g.H_kv;
+  const int b = warp_last_not_above(
+      g.ndocs, vb, lane, [&](int i) { return (__ldg(g.cu + i) >> 5) + 2 * i; });
+  const DocRange r = doc_range(g.cu, b, g.T);
+  const int start = g.starts != nullptr ? __ldg(g.starts + b) : 0;
+  if (r.e <= r.s) return false;
+  if (start < 0) {
+    if (lane == 0) report(g.status, FLAMIA_DEV_BAD_PAGE);
+    return false;
+  }
+  const int j = vb - ((r.s >> 5) + 2 * b);  // block of the sequence's new tokens
+  const int lead = start & 31, n = r.e - r.s;
+  if (j < 0 || 32ll * j >= static_cast<long long>(lead) + n) return false;
+  const long long p0 = static_cast<long long>(start - lead) + 32ll * j;
+  blk.lo = j == 0 ? lead : 0;
+  blk.hi = static_cast<int>(min(32ll, static_cast<long long>(start) + n - p0));
+  const long long slot = p0 / g.page_size;
+  int page = -1;
+  if (slot < g.table_stride)
+    page = __ldg(g.table + static_cast<long long>(b) * g.table_stride + slot);
+  if (page < 0 || page >= g.num_pages) {
+    if (lane == 0) report(g.status, FLAMIA_DEV_BAD_PAGE);
+    return false;
+  }
+  blk.row = (static_cast<long long>(page) * g.H_kv + blk.h) * g.page_size + (p0 - slot * g.page_size);
+  blk.token = r.s + p0 - start;
+  return true;
+}
+
+// A BF16 pair with infinities turned into NaN.
+__device__ __forceinline__ float2 finite_or_nan(uint32_t w) {
+  float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
+  if ((w & 0x7F80u) == 0x7F80u) a = __uint_as_float(0x7FC00000u);
+  if ((w & 0x7F800000u) == 0x7F800000u) b = __uint_as_float(0x7FC00000u);
+  return make_float2(a, b);
+}
+
+// Magnitudes of a BF16 pair as two 16-bit integers (their order is the
+// values'), non-finite ones as 0.
+__device__ __forceinline__ uint32_t finite_mag(uint32_t w) {
+  uint32_t m = w & 0x7FFF7FFFu;
+  if ((m & 0x7F80u) == 0x7F80u) m &= 0xFFFF0000u;
+  if ((m & 0x7F800000u) == 0x7F800000u) m &= 0x0000FFFFu;
+  return m;
+}
+
+template <int DIM, bool TOK>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheArgs g) {
+  constexpr int LPR = DIM / 8;   // lanes per row: 8 elements each
+  constexpr int RPI = 32 / LPR;  // rows per warp-wide access
+  constexpr int NLD = 32 / RPI;  // accesses per block
+  const int lane = threadIdx.x & 31;
+  const long long unit =
+      static_cast<long long>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  check_offsets(g.cu, g.ndocs, g.T,
+                static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x,
+                static_cast<long long>(gridDim.x) * kCacheThreads, g.status);
+  Block blk;
+  if (unit >= g.units || !find_block(g, unit, lane, blk)) return;
+  const int sub = lane / LPR, chunk = lane % LPR;
+  const __nv_bfloat16* rows = blk.kv ? g.rows[1] : g.rows[0];
+  const long long stride = blk.kv ? g.stride[1] : g.stride[0];
+  uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + blk.row * DIM;
+  uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + blk.row;
+
+  uint4 x[NLD];
+#pragma unroll
+  for (int i = 0; i < NLD; ++i) {
+    const int r = i * RPI + sub;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (r >= blk.lo && r < blk.hi)
+      x[i] = __ldg(reinterpret_cast<const uint4*>(rows + (blk.token + r) * stride + blk.h * DIM +
+                                                  chunk * 8));
+  }
+  // what the block holds before the call keeps its exponent, or a larger one
+  int held = -127;
+  if (!TOK && blk.lo > 0) held = static_cast<int>(scales[0]) - 127;
+
+  // maxima as 16-bit integers
+  uint32_t m[NLD];
+  uint32_t all = 0;
+#pragma unroll
+  for (int i = 0; i < NLD; ++i) {
+    const uint32_t a = __vmaxu2(finite_mag(x[i].x), finite_mag(x[i].y));
+    const uint32_t b = __vmaxu2(finite_mag(x[i].z), finite_mag(x[i].w));
+    const uint32_t c = __vmaxu2(a, b);
+    m[i] = max(c & 0xFFFFu, c >> 16);
+    all = max(all, m[i]);
+  }
+  int e = 0;
+  if (!TOK) {
+    all = __reduce_max_sync(0xffffffffu, all);
+    e = max(held, roundup_exponent(__uint_as_float(all << 16)));
+    if (blk.lo > 0 && e > held) {
+      // the held codes are rounded again under the larger exponent
+      const float f = held - e < -126 ? 0.f : exp2i(held - e);
+#pragma unroll 4
+      for (int i = 0; i < NLD; ++i) {
+        const int r = i * RPI + sub;
+        if (r < blk.lo) {
+          uint2* at = reinterpret_cast<uint2*>(codes + r * DIM) + chunk;
+          uint2 c = *at;
+          const float2 v0 = e4m3x2_to_float2(c.x & 0xFFFFu), v1 = e4m3x2_to_float2(c.x >> 16);
+          const float2 v2 = e4m3x2_to_float2(c.y & 0xFFFFu), v3 = e4m3x2_to_float2(c.y >> 16);
+          c.x = cvt_e4m3x4(v0.x * f, v0.y * f, v1.x * f, v1.y * f);
+          c.y = cvt_e4m3x4(v2.x * f, v2.y * f, v3.x * f, v3.y * f);
+          *at = c;
+        }
+      }
+      if (lane < blk.lo) scales[lane] = static_cast<uint8_t>(e + 127);
+    }
+    if (lane >= blk.lo && lane < blk.hi) scales[lane] = static_cast<uint8_t>(e + 127);
+  }
+#pragma unroll
+  for (int i = 0; i < NLD; ++i) {
+    const int r = i * RPI + sub;
+    if (TOK) {
+      uint32_t mm = m[i];
+#pragma unroll
+      for (int off = LPR / 2; off > 0; off >>= 1)
+        mm = max(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+      e = roundup_exponent(__uint_as_float(mm << 16));
+    }
+    const float inv = exp2i(-e);  // e in [-127, 120]: 2^-e is a normal float
+    if (r >= blk.lo && r < blk.hi) {
+      const float2 v0 = finite_or_nan(x[i].x), v1 = finite_or_nan(x[i].y);
+      const float2 v2 = finite_or_nan(x[i].z), v3 = finite_or_nan(x[i].w);
+      uint2 c;
+      c.x = cvt_e4m3x4(v0.x * inv, v0.y * inv, v1.x * inv, v1.y * inv);
+      c.y = cvt_e4m3x4(v2.x * inv, v2.y * inv, v3.x * inv, v3.y * inv);
+      reinterpret_cast<uint2*>(codes + r * DIM)[chunk] = c;
+      if (TOK && chunk == 0) scales[r] = static_cast<uint8_t>(e + 127);
+    }
+  }
+}
+
+template <int DIM>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheArgs g) {
+  constexpr int LPR = DIM / 8;
+  constexpr int RPI = 32 / LPR;
+  constexpr int NLD = 32 / RPI;
+  const int lane = threadIdx.x & 31;
+  const long long unit =
+      static_cast<long long>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  check_offsets(g.cu, g.ndocs, g.T,
+                static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x,
+                static_cast<long long>(gridDim.x) * kCacheThreads, g.status);
+  Block blk;
+  if (unit >= g.units || !find_block(g, unit, lane, blk)) return;
+  const int sub = lane / LPR, chunk = lane % LPR;
+  __nv_bfloat16* rows = blk.kv ? g.rows[1] : g.rows[0];
+  const long long stride = blk.kv ? g.stride[1] : g.stride[0];
+  const uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + blk.row * DIM;
+  const uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + blk.row;
+  uint2 x[NLD];
+#pragma unroll
+  for (int i = 0; i < NLD; ++i) {
+    const int r = i * RPI + sub;
+    x[i] = make_uint2(0, 0);
+    if (r >= blk.lo && r < blk.hi) x[i] = __ldg(reinterpret_cast<const uint2*>(codes + r * DIM) + chunk);
+  }
+  const int sc = __ldg(scales + lane);
+#pragma unroll
+  for (int i = 0; i < NLD; ++i) {
+    const int r = i * RPI + sub;
+    const int byte = __shfl_sync(0xffffffffu, sc, r);
+    const float f = byte > 0 ? __uint_as_float(static_cast<uint32_t>(byte) << 23) : 0x1p-127f;
+    if (r >= blk.lo && r < blk.hi) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = e4m3x2_to_float2(((j < 2 ? x[i].x : x[i].y) >> (16 * (j & 1))) & 0xFFFFu);
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v.x * f, v.y * f);
+        w[j] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(rows + (blk.token + r) * stride + blk.h * DIM + chunk * 8) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+flamia_status fill_args(CacheArgs& g, const flamia_kvcache* cache, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, int T, const int32_t* cu, int ndocs,
+                        const int32_t* starts, const int32_t* table, int table_stride,
+                        int* status) {
+  const flamia_status st = check_cache(cache);
+  if (st != FLAMIA_OK) return st;
+  if (!valid_batch(T, ndocs) || table_stride <= 0) return FLAMIA_ERR_INVALID_ARG;
+  if (T == 0) return FLAMIA_OK;
+  if (!valid_rows(k, k_stride) || !valid_rows(v, v_stride) || cu == nullptr || table == nullptr)
+    return FLAMIA_ERR_INVALID_ARG;
+  g.codes[0] = cache->k_codes;
+  g.codes[1] = cache->v_codes;
+  g.scales[0] = cache->k_scales;
+  g.scales[1] = cache->v_scales;
+  g.rows[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(k));
+  g.rows[1] = static_cast<__nv_bfloat16*>(const_cast<void*>(v));
+  g.stride[0] = k_stride;
+  g.stride[1] = v_stride;
+  g.cu = cu;
+  g.starts = starts;
+  g.table = table;
+  g.status = status;
+  g.T = T;
+  g.H_kv = cache->H_kv;
+  g.ndocs = ndocs;
+  g.table_stride = table_stride;
+  g.num_pages = cache->num_pages;
+  g.page_size = cache->page_size;
+  // block numbers run to cu[ndocs] / 32 + 2 ndocs
+  g.units = (static_cast<long long>(T) / 32 + 2ll * ndocs) * 2 * g.H_kv;
+  return FLAMIA_OK;
+}
+
+flamia_status launch(void (*kern)(const CacheArgs), const CacheArgs& g, cudaStream_t s) {
+  const long long blocks = (g.units * 32 + kCacheThreads - 1) / kCacheThreads;
+  if (blocks >= (1ll << 31)) return FLAMIA_ERR_INVALID_ARG;
+  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, s>>>(g);
+  count_launches(1);
+  return cudaGetLastError() == cudaSuccess ? FLAMIA_OK : FLAMIA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace flamia
+
+using namespace flamia;
+
+extern "C" flamia_status flamia_cache_write(const flamia_kvcache* cache, const void* k_bf16,
+                                            int64_t k_stride, const void* v_bf16,
+                                            int64_t v_stride, int T, const int32_t* cu_seqlens,
+                                            int ndocs, const int32_t* starts,
+                                            const int32_t* page_table, int table_stride,
+                                            int format, int* dev_status, void* stream) {
+  if (format != FLAMIA_FORMAT_MXFP8 && format != FLAMIA_FORMAT_TOKEN_SCALES)
+    return FLAMIA_ERR_UNSUPPORTED;
+  CacheArgs g{};
+  const flamia_status st = fill_args(g, cache, k_bf16, k_stride, v_bf16, v_stride, T, cu_seqlens,
+                                     ndocs, starts, page_table, table_stride, dev_status);
+  if (st != FLAMIA_OK || T == 0) return st;
+  const bool tok = format == FLAMIA_FORMAT_TOKEN_SCALES;
+  return launch(cache->d == 128
+                    ? (tok ? cache_write_kernel<128, true> : cache_write_kernel<128, false>)
+                    : (tok ? cache_write_kernel<64, true> : cache_write_kernel<64, false>),
+                g, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16,
+                                           int64_t k_stride, void* v_bf16, int64_t v_stride,
+                                           int T, const int32_t* cu_seqlens, int ndocs,
+                                           const int32_t* starts, const int32_t* page_table,
+                                           int table_stride, int* dev_status, void* stream) {
+  CacheArgs g{};
+  const flamia_status st = fill_args(g, cache, k_bf16, k_stride, v_bf16, v_stride, T, cu_seqlens,
+                                     ndocs, starts, page_table, table_stride, dev_status);
+  if (st != FLAMIA_OK || T == 0) return st;
+  const int64_t row = static_cast<int64_t>(cache->H_kv) * cache->d;
+  if (T > 1 && (k_stride < row || v_stride < row)) return FLAMIA_ERR_INVALID_ARG;
+  return launch(cache->d == 128 ? cache_read_kernel<128> : cache_read_kernel<64>, g,
+                static_cast<cudaStream_t>(stream));
+}

@@ -8,6 +8,7 @@ returns an error status, a RuntimeError is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -33,10 +34,13 @@ FLAG_TOKEN_SCALES = 0x200
 FLAG_DS_ZERO_COUNT = 0x400
 FLAG_BWD_CTA_PAIR = 0x800
 FLAG_BWD_ONE_CTA = 0x1000
+FLAG_ROPE_INTERLEAVED = 0x2000
+FLAG_ROPE_INVERSE = 0x4000
 DEV_BAD_SEQLENS = 0x1
 DEV_CAPACITY = 0x2
 DEV_TIMEOUT = 0x4
 DEV_RANGE = 0x8
+DEV_BAD_PAGE = 0x10
 
 _LIB = None
 
@@ -46,8 +50,17 @@ class QTensorStruct(ctypes.Structure):
                 ("nvfp4_codes", ctypes.c_void_p), ("nvfp4_scales", ctypes.c_void_p)]
 
 
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+_i64 = ctypes.c_int64
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _QP = ctypes.POINTER(QTensorStruct)
+_CP = ctypes.POINTER(KVCacheStruct)
 SIGNATURES = {
     "flamia_quantize_tokenblock": (_i, [_vp, _i, _i, _i, _vp, _i, _i, _vp, _vp, _QP, _vp, _vp]),
     "flamia_quantize_qkv": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _i, _i, _QP, _QP, _QP, _vp,
@@ -65,6 +78,14 @@ SIGNATURES = {
     "flamia_attn_bwd_gqa": (_i, [_QP, _QP, _QP, _QP, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i,
                                  _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "flamia_build_worklist_static": (_i, [_vp, _i, _i, _vp, _sz, _vp, _vp]),
+    "flamia_rope": (_i, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i, _i, _i, _i, _vp, _i, _f,
+                         _i, _vp, _i, _vp, _vp, _vp]),
+    "flamia_cache_write": (_i, [_CP, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _i, _vp,
+                                _vp]),
+    "flamia_cache_read": (_i, [_CP, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _vp, _vp]),
+    "flamia_attn_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "flamia_attn_cache": (_i, [_CP, _vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i, _f, _i, _i, _vp,
+                               _vp, _vp, _sz, _vp, _vp]),
     "flamia_status_str": (ctypes.c_char_p, [_i]),
     "flamia_debug_mma_tile": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "flamia_debug_bounded_waits": (_i, [_vp, _vp, _vp]),
@@ -219,6 +240,254 @@ def flamia_attn_bwd_gqa(q: QTensor, k: QTensor, v: QTensor, dout: QTensor, D, ls
                                       _stream()), "flamia_attn_bwd_gqa")
 
 
+def _rows(x, name, heads=None, d=None, out=False):
+    """(pointer, token stride in elements) of BF16 rows [T, heads, d]: any
+    token stride, the heads of a token side by side."""
+    if x.dtype is not torch.bfloat16 or x.dim() != 3:
+        raise RuntimeError(f"{name}: flamia needs BF16 rows [T, heads, d]")
+    T, h, n = x.shape
+    if (heads is not None and h != heads) or (d is not None and n != d):
+        raise RuntimeError(f"{name}: shape {tuple(x.shape)}, expected [T, {heads}, {d}]")
+    stride, sh, sd = x.stride()
+    if sd != 1 or (h > 1 and sh != n):
+        raise RuntimeError(f"{name}: the heads of a token must be contiguous")
+    if T <= 1:
+        stride = h * n
+    elif out and stride < h * n:
+        raise RuntimeError(f"{name}: an output's rows must not overlap")
+    return _on_device(x, name), stride
+
+
+def _on_device(t, name):
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise RuntimeError(f"{name}: flamia needs tensors on the current CUDA device")
+    return t.data_ptr()
+
+
+def _ints(t, name, numel=None):
+    """Pointer of a contiguous int32 tensor (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise RuntimeError(f"{name}: flamia needs contiguous int32 tensors")
+    if numel is not None and t.numel() != numel:
+        raise RuntimeError(f"{name}: {t.numel()} entries, expected {numel}")
+    return _on_device(t, name)
+
+
+def _page_table(t, nseq):
+    if t.dim() != 2 or t.shape[0] != nseq:
+        raise RuntimeError(f"page_table: shape {tuple(t.shape)}, expected [{nseq}, pages]")
+    return _ints(t, "page_table")
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0,
+                     method: str = "linear", original_len: int = 8192, low: float = 1.0,
+                     high: float = 4.0):
+    """Angles per position w_i (float64, [rot_dim / 2]) for Rotary, scaled for
+    contexts ``factor`` times longer than a model was trained on:
+
+    ``linear``  w_i / factor (positions squeezed);
+    ``base``    the base grows to base * factor^(r / (r - 2)), so the slowest
+                pair turns ``factor`` times slower and the fastest keeps its pace;
+    ``bands``   pairs that turn more than ``high`` times over ``original_len``
+                positions keep w_i, those that turn less than ``low`` times take
+                w_i / factor, a linear blend between."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if method not in ("linear", "base", "bands"):
+        raise ValueError(f"unknown scaling method {method!r}")
+    if method == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    w = base ** (-i / rot_dim)
+    if method == "linear":
+        w = w / factor
+    elif method == "bands":
+        turns = original_len * w / (2 * math.pi)
+        keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        w = keep * w + (1 - keep) * (w / factor)
+    return w
+
+
+class Rotary:
+    """Rotary positions with the angles p * frequencies[i] (see
+    rope_frequencies); holds the device table of turns per position."""
+
+    def __init__(self, frequencies, interleaved: bool = False, mscale: float = 1.0,
+                 device="cuda"):
+        w = [float(f) for f in frequencies]
+        self.rot_dim, self.interleaved, self.mscale = 2 * len(w), bool(interleaved), float(mscale)
+        if not all(math.isfinite(f) for f in w):
+            raise ValueError("frequencies must be finite")
+        steps = [int(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for f in w]
+        self.turns = torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps],
+                                  dtype=torch.int64, device=device)
+        self.flags = FLAG_ROPE_INTERLEAVED if interleaved else 0
+
+    def __call__(self, q, k, cu_seqlens, starts=None, q_out=None, k_out=None,
+                 inverse: bool = False, dev_status=None):
+        """Rotated q and k (k may be None); inverse: gradients of the rotated
+        rows -> gradients of the rows.  q_out / k_out may be q / k."""
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+        if k is not None and k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        flamia_rope(q, q_out, k, k_out, self, cu_seqlens, starts, inverse, dev_status)
+        return q_out, k_out
+
+
+def flamia_rope(q_in, q_out, k_in, k_out, rotary: Rotary, cu_seqlens, starts=None,
+                inverse: bool = False, dev_status=None):
+    T, H, d = q_in.shape
+    qi, qis = _rows(q_in, "q_in")
+    qo, qos = _rows(q_out, "q_out", H, d, out=True)
+    H_kv, ki, kis, ko, kos = 0, None, 0, None, 0
+    if q_out.shape[0] != T:
+        raise RuntimeError("q_out: another number of rows than q_in")
+    if k_in is not None:
+        H_kv = k_in.shape[1]
+        ki, kis = _rows(k_in, "k_in", H_kv, d)
+        ko, kos = _rows(k_out, "k_out", H_kv, d, out=True)
+        if k_in.shape[0] != T or k_out.shape[0] != T:
+            raise RuntimeError("k: another number of rows than q")
+    n = cu_seqlens.numel() - 1
+    _check(load().flamia_rope(
+        qi, qo, qis, qos, ki, ko, kis, kos, T, H, H_kv, d, _on_device(rotary.turns, "turns"),
+        rotary.rot_dim, rotary.mscale, rotary.flags | (FLAG_ROPE_INVERSE if inverse else 0),
+        _ints(cu_seqlens, "cu_seqlens"), n, _ints(starts, "starts", n),
+        _ints(dev_status, "dev_status"), _stream()), "flamia_rope")
+
+
+class KVCache:
+    """Paged key-value cache in E4M3 codes with one E8M0 exponent per 32-token
+    block and head (token_scales: per token and head).  Position p of sequence
+    b is row p % page_size of page page_table[b, p // page_size]; the caller
+    hands out the pages."""
+
+    def __init__(self, num_pages: int, page_size: int, H_kv: int, d: int,
+                 token_scales: bool = False, device="cuda"):
+        shape = (num_pages, H_kv, page_size)
+        codes = [torch.zeros(*shape, d, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+        self._set(codes[0], scales[0], codes[1], scales[1], token_scales)
+
+    @classmethod
+    def from_buffers(cls, k_codes, k_scales, v_codes, v_scales, token_scales: bool = False):
+        """A cache over the caller's uint8 buffers: codes [pages, H_kv,
+        page_size, d], scales [pages, H_kv, page_size]."""
+        self = cls.__new__(cls)
+        self._set(k_codes, k_scales, v_codes, v_scales, token_scales)
+        return self
+
+    def _set(self, k_codes, k_scales, v_codes, v_scales, token_scales):
+        if k_codes.dim() != 4:
+            raise RuntimeError("k_codes: expected [pages, H_kv, page_size, d]")
+        for t, name, shape in ((k_codes, "k_codes", k_codes.shape),
+                               (v_codes, "v_codes", k_codes.shape),
+                               (k_scales, "k_scales", k_codes.shape[:3]),
+                               (v_scales, "v_scales", k_codes.shape[:3])):
+            if t.dtype is not torch.uint8 or not t.is_contiguous() or t.shape != shape:
+                raise RuntimeError(f"{name}: expected contiguous uint8 {tuple(shape)}")
+            if not t.is_cuda or t.device != k_codes.device:
+                raise RuntimeError(f"{name}: flamia needs CUDA tensors on one device")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = (k_codes, k_scales, v_codes,
+                                                                    v_scales)
+        self.num_pages, self.H_kv, self.page_size, self.d = k_codes.shape
+        self.token_scales = bool(token_scales)
+        self._struct = KVCacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                                     v_scales.data_ptr(), self.num_pages, self.page_size,
+                                     self.H_kv, self.d)
+        self._ref = ctypes.byref(self._struct)
+        self._ws = None
+
+    def write(self, k, v, cu_seqlens, starts, page_table, dev_status=None):
+        """Quantises rows k, v [T, H_kv, d] into positions starts[b] .. of each
+        sequence (starts None: 0)."""
+        flamia_cache_write(self, k, v, cu_seqlens, starts, page_table, dev_status)
+
+    def read(self, cu_seqlens, starts, page_table, T: int, k_out=None, v_out=None,
+             dev_status=None):
+        """BF16 rows of positions starts[b] .. of each sequence, packed [T, H_kv, d]."""
+        if k_out is None:
+            k_out = torch.empty(T, self.H_kv, self.d, dtype=torch.bfloat16,
+                                device=self.k_codes.device)
+        if v_out is None:
+            v_out = torch.empty_like(k_out)
+        flamia_cache_read(self, k_out, v_out, cu_seqlens, starts, page_table, dev_status)
+        return k_out, v_out
+
+    def attend(self, q, cu_seqlens, starts, page_table, softmax_scale: float, window: int = 0,
+               sinks: int = 0, o=None, lse=None, ws=None, dev_status=None):
+        """(o, lse) of queries q [T, H, d] at positions starts[b] .. over the
+        cache.  ws None: a workspace that the cache keeps, for calls that do
+        not overlap."""
+        T, H = q.shape[0], q.shape[1]
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+        if ws is None:
+            need = flamia_attn_cache_workspace_bytes(T, cu_seqlens.numel() - 1, H, self.H_kv,
+                                                     self.d)
+            if self._ws is None or self._ws.numel() < need:
+                self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
+            ws = self._ws
+        flamia_attn_cache(self, q, cu_seqlens, starts, page_table, softmax_scale, window, sinks, o,
+                          lse, ws, dev_status)
+        return o, lse
+
+
+def flamia_cache_write(cache: KVCache, k, v, cu_seqlens, starts, page_table, dev_status=None):
+    kp, ks = _rows(k, "k", cache.H_kv, cache.d)
+    vp, vs = _rows(v, "v", cache.H_kv, cache.d)
+    n = cu_seqlens.numel() - 1
+    if v.shape[0] != k.shape[0]:
+        raise RuntimeError("v: another number of rows than k")
+    _on_device(cache.k_codes, "cache")
+    _check(load().flamia_cache_write(
+        cache._ref, kp, ks, vp, vs, k.shape[0], _ints(cu_seqlens, "cu_seqlens"), n,
+        _ints(starts, "starts", n), _page_table(page_table, n), page_table.shape[1],
+        FORMAT_TOKEN_SCALES if cache.token_scales else FORMAT_MXFP8,
+        _ints(dev_status, "dev_status"), _stream()), "flamia_cache_write")
+
+
+def flamia_cache_read(cache: KVCache, k_out, v_out, cu_seqlens, starts, page_table,
+                      dev_status=None):
+    kp, ks = _rows(k_out, "k_out", cache.H_kv, cache.d, out=True)
+    vp, vs = _rows(v_out, "v_out", cache.H_kv, cache.d, out=True)
+    n = cu_seqlens.numel() - 1
+    if v_out.shape[0] != k_out.shape[0]:
+        raise RuntimeError("v_out: another number of rows than k_out")
+    _on_device(cache.k_codes, "cache")
+    _check(load().flamia_cache_read(
+        cache._ref, kp, ks, vp, vs, k_out.shape[0], _ints(cu_seqlens, "cu_seqlens"), n,
+        _ints(starts, "starts", n), _page_table(page_table, n), page_table.shape[1],
+        _ints(dev_status, "dev_status"), _stream()), "flamia_cache_read")
+
+
+def flamia_attn_cache_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: int) -> int:
+    return int(load().flamia_attn_cache_workspace_bytes(T, ndocs, H, H_kv, d))
+
+
+def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax_scale, window,
+                      sinks, o, lse, ws, dev_status=None):
+    T, H, d = q.shape
+    qp, qs = _rows(q, "q", None, cache.d)
+    n = cu_seqlens.numel() - 1
+    if o.dtype is not torch.bfloat16 or o.shape != q.shape or not o.is_contiguous():
+        raise RuntimeError("o: expected contiguous BF16 of q's shape")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (H, T)
+                            or not lse.is_contiguous()):
+        raise RuntimeError("lse: expected contiguous float32 [H, T]")
+    _on_device(cache.k_codes, "cache")
+    _check(load().flamia_attn_cache(
+        cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens"), n, _ints(starts, "starts", n),
+        _page_table(page_table, n), page_table.shape[1], softmax_scale, window, sinks,
+        _on_device(o, "o"), None if lse is None else _on_device(lse, "lse"),
+        _on_device(ws, "ws"), ws.numel() * ws.element_size(), _ints(dev_status, "dev_status"),
+        _stream()), "flamia_attn_cache")
+
+
 def flamia_debug_tmem_ldred(x, vals, mx):
     _check(load().flamia_debug_tmem_ldred(_ptr(x), _ptr(vals), _ptr(mx), _stream()),
            "flamia_debug_tmem_ldred")
@@ -256,7 +525,8 @@ class TrainingCall:
                  hadamard: bool = False, causal: bool = True, H_kv=None,
                  deterministic_dq: bool = False, dq_accum: str = "fp32", schedule: str = "dynamic",
                  ds_rows: bool = False, token_scales: bool = False,
-                 ds_zero_count: bool = False, bwd_ctas: str = "rule", device="cuda"):
+                 ds_zero_count: bool = False, bwd_ctas: str = "rule", rope: Rotary = None,
+                 device="cuda"):
         self.T, self.H, self.d = T, H, d
         self.H_kv = H if H_kv is None else H_kv
         self.scale = softmax_scale
@@ -298,9 +568,18 @@ class TrainingCall:
         # CTAs of the quantiser's one large launch
         self.side = torch.cuda.Stream(device, priority=-1)
         self.wl_ready = torch.cuda.Event()
+        # rotary positions (document-local): rotated Q and K before the
+        # quantiser, dQ and dK turned back in place after the backward
+        self.rope = rope
+        if rope is not None:
+            self.xq = torch.empty((T, H, d), dtype=torch.bfloat16, device=device)
+            self.xk = torch.empty((T, self.H_kv, d), dtype=torch.bfloat16, device=device)
 
     def forward(self, xq, xk, xv):
         main = torch.cuda.current_stream()
+        if self.rope is not None:
+            xq, xk = self.rope(xq, xk, self.cu, q_out=self.xq, k_out=self.xk,
+                               dev_status=self.status)
         # cu_seqlens is ready and the previous call has finished with the list
         self.side.wait_stream(main)
         with torch.cuda.stream(self.side):
@@ -320,6 +599,9 @@ class TrainingCall:
         flamia_attn_bwd_gqa(self.q, self.k, self.v, self.dout, self.D, self.lse, self.cu, self.T,
                             self.H, self.H_kv, self.d, self.scale, self.wl, self.dq, self.dk,
                             self.dv, self.ws, self.bwd_flags, dev_status=self.status)
+        if self.rope is not None:
+            self.rope(self.dq, self.dk, self.cu, q_out=self.dq, k_out=self.dk, inverse=True,
+                      dev_status=self.status)
         return self.dq, self.dk, self.dv
 
     def __call__(self, xq, xk, xv, xdo):
@@ -332,6 +614,44 @@ class TrainingCall:
         off = flamia_bwd_ds_counts_offset(self.T, self.H, self.d)
         c = self.ws[off:off + 16].view(torch.int64).cpu()
         return int(c[0]), int(c[1])
+
+    def check_status(self):
+        st = int(self.status.item())
+        if st != 0:
+            raise RuntimeError(f"flamia device status 0x{st:x}")
+
+
+class DecodeCall:
+    """Buffers and the sequence of C-ABI calls of one serving step over a
+    KVCache (rotary positions -> cache write -> attention) for up to T new
+    tokens of nseq sequences.  The calls read cu_seqlens, starts and page_table
+    on the device, so a captured step can be replayed while the caller updates
+    them in place."""
+
+    def __init__(self, cache: KVCache, T: int, nseq: int, H: int, softmax_scale: float,
+                 rope: Rotary = None, window: int = 0, sinks: int = 0):
+        dev = cache.k_codes.device
+        self.cache, self.T, self.H, self.scale = cache, T, H, float(softmax_scale)
+        self.rope, self.window, self.sinks = rope, int(window), int(sinks)
+        self.o = torch.empty((T, H, cache.d), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty((H, T), dtype=torch.float32, device=dev)
+        self.ws = torch.empty(flamia_attn_cache_workspace_bytes(T, nseq, H, cache.H_kv, cache.d),
+                              dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        if rope is not None:
+            self.q = torch.empty((T, H, cache.d), dtype=torch.bfloat16, device=dev)
+            self.k = torch.empty((T, cache.H_kv, cache.d), dtype=torch.bfloat16, device=dev)
+
+    def __call__(self, q, k, v, cu_seqlens, starts, page_table):
+        """o [T, H, d] of the new tokens at positions starts[b] .. of each
+        sequence; rows behind the last sequence are left as they were."""
+        if self.rope is not None:
+            q, k = self.rope(q, k, cu_seqlens, starts, q_out=self.q, k_out=self.k,
+                             dev_status=self.status)
+        self.cache.write(k, v, cu_seqlens, starts, page_table, dev_status=self.status)
+        self.cache.attend(q, cu_seqlens, starts, page_table, self.scale, self.window, self.sinks,
+                          o=self.o, lse=self.lse, ws=self.ws, dev_status=self.status)
+        return self.o
 
     def check_status(self):
         st = int(self.status.item())
