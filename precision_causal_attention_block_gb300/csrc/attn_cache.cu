@@ -6,30 +6,38 @@
 // and V go from HBM to the tensor core by TMA as the E4M3 codes that the cache
 // holds, V read MN-major, so nothing converts or transposes them; BF16 queries
 // and float32 weights become sums of E4M3 terms instead, side by side in N:
-//   q 2^-e = h + 2^-4 l            (e per row; exact for the elements above
-//                                   2^-14 of the row's largest),
-//   w = 2^-4 (h + 2^-5 m + 2^-10 l)  (relative error 2^-14, floor 2^-24 of the
-//                                   largest weight),
+//   q 2^-e = h + 2^-4 l              (e per row; exact for the elements above
+//                                     2^-14 of the row's largest),
+//   w      = h + 2^-5 m + 2^-10 l    (relative error 2^-14, floor 2^-24 of the
+//                                     largest weight),
 // which costs N = 2 R and 3 R columns of a product that reads M = 128 rows of
 // shared memory in any case.
 //
-// The key factor 2^eK multiplies the score, V's 2^eV goes into the weight: the
-// thread that owns a key adds eV to its score.  The softmax keeps two running
-// references a row, of the scores (for the sum l) and of score + eV (for the
-// weights), so that values of very different exponents, and zero values under
-// a heavy first token, keep their precision.  References move only when a tile
-// exceeds them by more than their slack (kSlackW, kSlackM), which the one
-// barrier of a tile votes on; then O^T is rescaled in tensor memory.
+// The key factor 2^eK multiplies the score x (in log2 units); V's 2^eV goes into
+// the weight, as the thread that owns a key adds eV to its score:
+//   w = 2^(x + eV - ref + kShift),   l = sum w 2^(E0 - eV),
+//   o = O^T 2^E0 / l,   log2 sum 2^x = ref - kShift - E0 + log2 l,
+// with one integer reference a row (a running maximum of x + eV) and one
+// integer E0 (a running maximum of eV) for all rows.  Keys whose values are
+// more than 2^kLow below E0 (zero values under a heavy first token) enter the
+// references with eV raised to E0 - kLow and have their weight lowered
+// afterwards, so that l keeps them and stays inside float32.  References move
+// only when a tile exceeds them by more than kSlack, which the one barrier of
+// a tile votes on; O^T is then rescaled in tensor memory.
 //
-// Work: all (sequence, K / V head, row tile) items' key tiles are laid end to
-// end and cut into equal runs, one for each resident CTA, so that a batch of
-// ragged lengths keeps every SM reading until the end.  A CTA finishes the
-// items that lie whole inside its run; of the (at most two) it shares it
-// leaves (m, l, O) in the workspace, and a second small kernel, launched
-// with programmatic dependent launch, joins them in order of position (no
-// atomics: results do not depend on timing).
+// Work: the key tiles of all (sequence, K / V head, row tile) items are laid end
+// to end, with kItemCost tiles' worth for each item's own steps, and cut into
+// equal runs, one for each resident CTA, so that a batch of ragged lengths keeps
+// every SM reading until the end.  A CTA finishes the items that lie whole
+// inside its run; of the (at most two) it shares it leaves o and log2 sum 2^x
+// in the workspace, and a second small kernel, launched with programmatic
+// dependent launch, joins them in order of position (no atomics: results do not
+// depend on timing).  Where the page table is too narrow for more than
+// kWholeTiles tiles an item, items stay whole and the second kernel is not
+// launched.
 //
-// Warps 0-3: softmax (thread = key = TMEM lane); 4: TMA producer; 5: MMA issuer.
+// Warps 0-3 (R = 32: 0-7, two halves of the rows): softmax (thread = key = TMEM
+// lane); then one TMA producer warp and one MMA issuer warp.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -39,17 +47,18 @@
 namespace flamia {
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for it)
+constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
+constexpr int kItemCost = 2;    // an item's own steps (queries, output) in tiles
+constexpr int kWholeTiles = 4;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kUnset = -1e30f;   // reference of a row that has seen no key
-constexpr float kSlackM = 60.f;    // l <= 2^60 x keys: far inside float32
-constexpr float kSlackW = 4.f;     // weights <= 2^(kShiftW + 4) = 256 < 448
-constexpr float kShiftW = 4.f;
-// parameters of the partial results: [slot][R] {m, l, w, -}, then [slot][R][d]
-constexpr int kSlots = 2 * kMaxCtas;
+constexpr float kShift = 4.f;   // weights are 2^kShift at the reference and at
+constexpr float kSlack = 4.f;   // most 2^(kShift + kSlack) = 256 < 448
+constexpr float kUnset = 1e30f; // -reference of a row that has seen no key yet
+constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
+constexpr int kLow = 60;
 
 struct AttendArgs {
   const uint8_t *k_scales, *v_scales;
@@ -58,11 +67,12 @@ struct AttendArgs {
   float* lse;
   const int32_t *cu, *starts, *table;
   int4* joins;       // [kMaxCtas][2]: items to join
-  float4* stats;     // [kSlots][R]
-  float* partial;    // [kSlots][R][d]
+  float* stats;      // [kSlots][R] log2 sum 2^x
+  float* partial;    // [kSlots][R][d] o
   int* status;
   long long q_stride;
   int T, H, H_kv, G, ndocs, table_stride, num_pages, page_size, window, sinks;
+  int whole;         // items stay whole
   float scale_log2;
 };
 
@@ -78,20 +88,21 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Barrier of the softmax warps that also ORs a predicate over them.
+// Barrier of the N threads of the softmax warps that also ORs a predicate over
+// them.
+template <int N>
 __device__ __forceinline__ bool softmax_vote(bool p) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
       "selp.b32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<int>(p))
+      : "r"(static_cast<int>(p)), "n"(N)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void softmax_sync() { named_barrier_sync(1, 128); }
 
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -99,8 +110,15 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-__device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
 __device__ __forceinline__ float pow2_byte(int byte) {
@@ -109,14 +127,15 @@ __device__ __forceinline__ float pow2_byte(int byte) {
 
 // ------------------------------------------------------------------ work
 
-// Sequence b's share of the work: row tiles x K / V heads x key tiles (an upper
-// bound of the tiles of its row tiles: a segment that runs past its item's last
-// tile is cut there).
+// Sequence b's share of the work: row tiles x K / V heads items of `tiles` key
+// tiles (an upper bound over its row tiles: a segment that runs past its item's
+// last tile is cut there).  An item is `units` long: kItemCost, then a unit
+// for each tile; one unit if items stay whole.
 struct SeqWork {
   int s, n, start;     // packed rows [s, s + n) at positions start ..
-  int row_tiles, tiles;
-  __device__ __forceinline__ long long units(int H_kv) const {
-    return static_cast<long long>(row_tiles) * tiles * H_kv;
+  int row_tiles, tiles, units;
+  __device__ __forceinline__ long long total(int H_kv) const {
+    return static_cast<long long>(row_tiles) * H_kv * units;
   }
 };
 
@@ -136,6 +155,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
                            ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);
   w.tiles = max(tiles, 1);
+  w.units = g.whole ? 1 : w.tiles + kItemCost;
   return w;
 }
 
@@ -156,11 +176,17 @@ __device__ __forceinline__ int tile_of(const Segment& g, int i) {
 
 template <int DIM, int R>
 struct Cfg {
-  static constexpr int kCtas = R == 8 ? 3 : 2;  // resident CTAs per SM
+  static constexpr int kHalves = R == 32 ? 2 : 1;   // softmax warpgroups
+  static constexpr int kRows = R / kHalves;         // rows of a softmax thread
+  static constexpr int kSoftmax = 128 * kHalves;    // softmax threads
+  static constexpr int kThreads = kSoftmax + 64;
+  static constexpr int kCtas = R == 8 ? 3 : 2;      // resident CTAs per SM
   static constexpr int kStages = (R == 16 ? 3 : 2) * (128 / DIM);
   static constexpr int kTileBytes = 128 * DIM;
   static constexpr int kNS = 2 * R;                 // columns of S^T
-  static constexpr int kNO = (3 * R + 15) / 16 * 16;  // columns of O^T
+  static constexpr int kNO = R == 8 ? 32 : 3 * R;   // columns of O^T
+  static constexpr int kPBufs = R == 32 ? 2 : 1;
+  static constexpr int kAtoms = (kNO + 31) / 32;    // P^T: 32 columns x 128 keys each
   static constexpr uint32_t kColO = 2 * kNS;
   static constexpr uint32_t kCols = R == 8 ? 64 : R == 16 ? 128 : 256;
   static_assert(kColO + kNO <= kCols, "tensor memory");
@@ -169,19 +195,20 @@ struct Cfg {
 template <int DIM, int R>
 struct Smem {
   using C = Cfg<DIM, R>;
-  // The last P^T rows of a product with R = 8 (columns 24 .. 31, ignored) read
-  // on into the bytes behind p.
   alignas(1024) uint8_t v[C::kStages][C::kTileBytes];
   alignas(1024) uint8_t k[C::kStages][C::kTileBytes];
-  alignas(1024) uint8_t p[2][3 * R * 128];
+  alignas(1024) uint8_t p[C::kPBufs][C::kAtoms * 4096];
   alignas(1024) uint8_t q[2 * R * DIM];
   alignas(128) uint8_t ks[C::kStages][128];
   alignas(128) uint8_t vs[C::kStages][128];
   alignas(16) float qf[R];      // 2^e of a row x softmax scale x log2 e
-  alignas(16) float ref_m[R], ref_w[R], f_m[R], f_w[R];
+  alignas(16) float nref[R];    // kShift - reference
+  alignas(16) float fac[R], facl[R];  // changes of scale of O^T and l
+  int has[R];                   // the row has a reference
   alignas(16) int pos[R];       // position of a row's token, -1: no such row
   alignas(16) int orow[R];      // its row of o, -1: none
-  float red[4][R][2];
+  float red[4][R];
+  int rede[C::kSoftmax / 32];
   uint64_t full[C::kStages], empty[C::kStages];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_empty;
@@ -190,27 +217,28 @@ struct Smem {
   int loaded[C::kStages];       // pieces of the tile that were loaded
   int plan_b;
   long long plan_off, plan_u0, plan_u1, plan_total;
-  long long scan[kThreads / 32];
+  long long scan[C::kThreads / 32];
   uint32_t tmem_base;
   int stop[2];                  // softmax warps: a wait ran out (by tile parity)
   volatile int abort;
 };
 
 // CTAs that get a run: at least two tiles each, as far as there are any.
-__device__ __forceinline__ long long active_ctas(long long total) {
-  return min(static_cast<long long>(gridDim.x), (total + 1) / 2);
+__device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long total) {
+  const int least = g.whole ? 1 : kItemCost + 2;
+  return min(static_cast<long long>(gridDim.x), (total + least - 1) / least);
 }
 
 // Total units, and this CTA's run of them: [u0, u1), starting at unit `off` of
 // sequence b.  Every thread sums a stretch of sequences; the one whose stretch
 // holds u0 walks it.
-template <int R, class Sm>
+template <int R, int kThreads, class Sm>
 __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (g.ndocs + kThreads - 1) / kThreads;
   const int b0 = min(tid * each, g.ndocs), b1 = min(b0 + each, g.ndocs);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_work<R>(g, b).units(g.H_kv);
+  for (int b = b0; b < b1; ++b) sum += seq_work<R>(g, b).total(g.H_kv);
   long long inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -226,7 +254,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
   }
-  const long long ctas = active_ctas(total);
+  const long long ctas = active_ctas(g, total);
   const long long c = blockIdx.x;
   const long long u0 = c < ctas ? total * c / ctas : total;
   const long long u1 = c < ctas ? total * (c + 1) / ctas : total;
@@ -239,7 +267,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     long long off = u0 - before;
     int b = b0;
     for (; b < b1 - 1; ++b) {
-      const long long u = seq_work<R>(g, b).units(g.H_kv);
+      const long long u = seq_work<R>(g, b).total(g.H_kv);
       if (off < u) break;
       off -= u;
     }
@@ -249,11 +277,83 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   __syncthreads();
 }
 
+// The queries of a segment held by one softmax thread: 16-byte chunks of rows
+// r0 + tid / (d / 8), r0 = 0, kPer, 2 kPer, ...
 template <int DIM, int R>
-__global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
+struct Queries {
+  using C = Cfg<DIM, R>;
+  static constexpr int kLanes = DIM / 8, kPer = C::kSoftmax / kLanes;
+  static constexpr int kIters = (R + kPer - 1) / kPer;
+  uint4 w[kIters];
+
+  __device__ __forceinline__ void load(const AttendArgs& g, const Segment& sg, int tid) {
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int r = it * kPer + tid / kLanes;
+      const int row = sg.row0 + r;
+      w[it] = make_uint4(0, 0, 0, 0);
+      if (r < R && row < static_cast<long long>(sg.n) * g.G) {
+        const int i = row / g.G, hq = sg.hk * g.G + row - i * g.G;
+        w[it] = __ldg(reinterpret_cast<const uint4*>(g.q + (sg.s + i) * g.q_stride +
+                                                     static_cast<long long>(hq) * DIM +
+                                                     tid % kLanes * 8));
+      }
+    }
+  }
+
+  // Two E4M3 terms a row into shared memory (K-major rows of DIM bytes, 16-byte
+  // chunks swizzled as TMA does), and the row factors.
+  __device__ __forceinline__ void split(uint8_t* q, float* qf, float scale_log2, int tid) const {
+    const int ch = tid % kLanes;
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int r = it * kPer + tid / kLanes;
+      float x[8];
+      const uint32_t ww[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(ww[j] << 16);
+        x[2 * j + 1] = __uint_as_float(ww[j] & 0xFFFF0000u);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!(fabsf(x[j]) < INFINITY)) x[j] = __uint_as_float(0x7FC00000u);
+        amax = fmaxf(amax, fabsf(x[j]));  // of the finite ones
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int e = roundup_exponent(amax);
+      const float inv = exp2i(-e);
+      uint32_t hc[4], lc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = x[2 * j] * inv, c = x[2 * j + 1] * inv;
+        hc[j] = cvt_e4m3x2(a, c);
+        const float2 h = e4m3x2_to_float2(hc[j]);
+        lc[j] = cvt_e4m3x2((a - h.x) * 16.f, (c - h.y) * 16.f);
+      }
+      if (r < R) {
+        auto at = [&](int n) {
+          const int c16 = ch >> 1;
+          const int sw = DIM == 128 ? (c16 ^ (n & 7)) : (c16 ^ ((n >> 1) & 3));
+          return reinterpret_cast<uint2*>(q + n * DIM + sw * 16 + (ch & 1) * 8);
+        };
+        *at(r) = make_uint2(hc[0] | (hc[1] << 16), hc[2] | (hc[3] << 16));
+        *at(R + r) = make_uint2(lc[0] | (lc[1] << 16), lc[2] | (lc[3] << 16));
+        if (ch == 0) qf[r] = scale_log2 * (e < -126 ? 0x1p-127f : exp2i(e));
+      }
+    }
+  }
+};
+
+template <int DIM, int R>
+__global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     attend_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttendArgs g) {
   using C = Cfg<DIM, R>;
+  constexpr int kProducer = C::kSoftmax / 32, kIssuer = kProducer + 1;
   extern __shared__ uint8_t smem_raw[];
   Smem<DIM, R>& sm = *reinterpret_cast<Smem<DIM, R>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -267,31 +367,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_full[i]), 128);
+      mbar_init(smem_u32(&sm.p_full[i]), C::kSoftmax);
       mbar_init(smem_u32(&sm.pv_done[i]), 1);
       sm.stop[i] = 0;
     }
-    mbar_init(smem_u32(&sm.q_full), 128);
-    mbar_init(smem_u32(&sm.o_empty), 128);
+    mbar_init(smem_u32(&sm.q_full), C::kSoftmax);
+    mbar_init(smem_u32(&sm.o_empty), C::kSoftmax);
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(smem_u32(&sm.seg_full[i]), 1);
-      mbar_init(smem_u32(&sm.seg_empty[i]), 5);  // four softmax warps, the MMA issuer
+      mbar_init(smem_u32(&sm.seg_empty[i]), kProducer + 1);  // softmax warps, MMA issuer
     }
     sm.abort = 0;
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == kIssuer) {
     tmem_alloc(smem_u32(&sm.tmem_base), C::kCols);
     tmem_relinquish();
   }
-  check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * kThreads + tid,
-                static_cast<long long>(gridDim.x) * kThreads, g.status);
+  check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
+                static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   tc_fence_before();
-  make_plan<R>(g, sm);
+  make_plan<R, C::kThreads>(g, sm);
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  if (warp == 4) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------ producer
     const long long u0 = sm.plan_u0, u1 = sm.plan_u1, total = sm.plan_total;
     const int pieces = g.page_size >= 128 ? 1 : 128 / g.page_size;
@@ -301,30 +401,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
       prefetch_tensormap(&map_v);
     }
     int b = sm.plan_b, tc = 0, nseg = 0;
-    long long off = sm.plan_off, u = u0;
+    long long u = u0;
     bool ok = true, first = true;
     int4 join0 = make_int4(0, 0, 0, 0), join1 = make_int4(0, 0, 0, 0);
+    // place inside sequence b: item (hk, rt), unit o of it
+    SeqWork w{};
+    int hk = 0, rt = 0, o = 0;
+    if (u < u1) {
+      w = seq_work<R>(g, b);
+      const long long item = sm.plan_off / w.units;
+      o = static_cast<int>(sm.plan_off - item * w.units);
+      hk = static_cast<int>(item / w.row_tiles);
+      rt = static_cast<int>(item - static_cast<long long>(hk) * w.row_tiles);
+    }
     while (ok) {
       Segment sg{};
       int hi = 0, wlo = 0;
-      if (u >= u1 || b >= g.ndocs) {
+      if (u >= u1) {
         sg.s = -1;
       } else {
-        const SeqWork w = seq_work<R>(g, b);
-        if (off >= w.units(g.H_kv)) {  // the next sequence
-          off = 0;
-          ++b;
-          continue;
-        }
-        const int i = static_cast<int>(off % w.tiles);
-        const long long item = off / w.tiles;
+        const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
+        const int cost = g.whole ? 0 : kItemCost;
+        const int i0 = max(o - cost, 0);
+        const int i1 = g.whole ? w.tiles : max(o + take - cost, 0);
         sg.s = w.s;
         sg.n = w.n;
         sg.start = w.start;
-        sg.hk = static_cast<int>(item / w.row_tiles);
-        sg.row0 = static_cast<int>(item % w.row_tiles) * R;
-        const long long left = u1 - u;
-        const int take = static_cast<int>(min(left, static_cast<long long>(w.tiles - i)));
+        sg.hk = hk;
+        sg.row0 = rt * R;
         // positions of the row tile's first and last token
         const int pf = w.start + sg.row0 / g.G;
         const int pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
@@ -335,31 +439,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
         sg.wt = wlo >> 7;
         sg.ns = min((g.sinks + 127) >> 7, sg.wt);
         const int list = sg.ns + max(((hi + 127) >> 7) - sg.wt, 0);
-        sg.i0 = min(i, list);
-        sg.i1 = min(i + take, list);
+        sg.i0 = min(i0, list);
+        sg.i1 = min(i1, list);
         sg.slot = -1;
-        if (i > 0)
+        if (i0 > 0)
           sg.slot = 2 * blockIdx.x;
-        else if (take < w.tiles)
+        else if (i1 < w.tiles)
           sg.slot = 2 * blockIdx.x + 1;
-        if (first && i > 0) {
-          // the second CTA of an item's run has it joined: parts are the
-          // CTA before this one (slot 1) and slots 0 from here on
-          const long long ctas = active_ctas(total);
-          const long long c = blockIdx.x, ui = u0 - i;
-          if (c > 0 && total * (c - 1) / ctas <= ui) {
-            const long long last = ((ui + w.tiles) * ctas + total - 1) / total - 1;
-            join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, sg.hk);
+        if (first && i0 > 0) {
+          // the second CTA of an item has it joined: parts are the CTA before
+          // this one (slot 1) and slots 0 from here on
+          const long long ctas = active_ctas(g, total), c = blockIdx.x, ui = u0 - o;
+          if (c > 0 && total * (c - 1) / ctas <= ui + kItemCost) {
+            const long long last = ((ui + w.units) * ctas + total - 1) / total - 1;
+            join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, hk);
             join1 = make_int4(sg.row0, 0, 0, 0);
           }
         }
-        first = false;
-        if (lane == 0 && i == 0 && sg.hk == 0 && sg.row0 == 0) {
+        if (lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
           const int raw = g.starts != nullptr ? __ldg(g.starts + b) : 0;
           if (raw > kMaxPos - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
         }
-        off += take;
+        first = false;
         u += take;
+        if (i1 <= i0) continue;  // the run ends before the item's first tile
       }
       // hand it on
       const int sl = nseg % kSegSlots;
@@ -386,6 +489,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
       bool need;
       int in_page;
       int page = sg.i0 < sg.i1 ? entry(sg.i0, need, in_page) : -1;
+      // the next item meanwhile
+      o = 0;
+      if (u < u1 && ++rt == w.row_tiles) {
+        rt = 0;
+        if (++hk == g.H_kv) {
+          hk = 0;
+          do {
+            w = seq_work<R>(g, ++b);  // there is one: u < u1
+          } while (w.row_tiles == 0 && b + 1 < g.ndocs);
+        }
+      }
       for (int i = sg.i0; i < sg.i1; ++i, ++tc) {
         const int pg = page, ip = in_page;
         const bool nd = need, good = nd && pg >= 0 && pg < g.num_pages;
@@ -415,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
       }
     }
     // what the second kernel has to join for this CTA's first item
-    if (lane == 0) {
+    if (lane == 0 && !g.whole) {
       g.joins[2 * blockIdx.x] = join0;
       g.joins[2 * blockIdx.x + 1] = join1;
     }
@@ -423,19 +537,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
     for (int j = max(0, tc - C::kStages); j < tc; ++j)
       ok &= mbar_wait_w(smem_u32(&sm.full[j % C::kStages]), (j / C::kStages) & 1);
     if (!ok) sm.abort = 1;
-  } else if (warp == 5) {
+  } else if (warp == kIssuer) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t lay = DIM == 128 ? kLayoutSW128 : kLayoutSW64;
     constexpr uint32_t sbo = 8 * DIM;
     const uint32_t id_s = idesc_f8(128, C::kNS, 0, 0);
-    const uint32_t id_o = idesc_f8(128, C::kNO, 1, 0);
+    const uint32_t id_o = idesc_f8(128, C::kNO, 1, 1);
     const uint64_t dk0 = smem_desc(smem_u32(sm.k[0]), 0, sbo, lay);
     const uint64_t dq = smem_desc(smem_u32(sm.q), 0, sbo, lay);
     // head dim 64: M = 128 takes a second 64-row atom; it reads the tile of K
     // that lies behind V's, into lanes 64 .. 127 of O^T, which nobody reads
     const uint64_t dv0 = smem_desc(
         smem_u32(sm.v[0]), DIM == 64 ? smem_u32(sm.k[0]) - smem_u32(sm.v[0]) : 0, sbo, lay);
-    const uint64_t dp0 = smem_desc(smem_u32(sm.p[0]), 0, 1024, kLayoutSW128);
+    // P^T: MN-major, atoms of 32 columns x 8 keys, 4,096 bytes from one set of
+    // 32 columns to the next
+    const uint64_t dp0 = smem_desc(smem_u32(sm.p[0]), 4096, 256, kLayoutSW32);
     constexpr uint32_t kStep = C::kTileBytes / 16;
     int tc = 0, nlive = 0;
     bool ok = true;
@@ -477,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
             issue_s(t + 1);
           }
         }
-        const int x = tc + t, pb = x & 1;
-        ok = mbar_wait_w_ab(smem_u32(&sm.p_full[pb]), (x >> 1) & 1, &sm.abort);
+        const int x = tc + t;
+        ok = mbar_wait_w_ab(smem_u32(&sm.p_full[x & 1]), (x >> 1) & 1, &sm.abort);
         // O^T of the segment before has been read
         if (ok && t == 0 && nlive > 0)
           ok = mbar_wait_w_ab(smem_u32(&sm.o_empty), (nlive - 1) & 1, &sm.abort);
@@ -488,9 +604,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_f8_w(tmem + C::kColO, dv0 + st * kStep + ks * (32 * DIM / 16),
-                   dp0 + pb * (3 * R * 128 / 16) + 2 * ks, id_o, t > 0 || ks > 0);
+                   dp0 + (x % C::kPBufs) * (C::kAtoms * 4096 / 16) + ks * (1024 / 16), id_o,
+                   t > 0 || ks > 0);
         tc_commit_w(smem_u32(&sm.empty[st]));
-        tc_commit_w(smem_u32(&sm.pv_done[pb]));
+        tc_commit_w(smem_u32(&sm.pv_done[x & 1]));
         if (t + 1 < nt && !ahead) {
           ok = wait_full(t + 1);
           if (!ok) break;
@@ -504,246 +621,291 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
     if (!ok) sm.abort = 1;
   } else {
     // ------------------------------------------------------------ softmax
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    constexpr int RW = C::kRows;
+    const int half = warp >> 2, r0 = half * RW;     // this thread's rows r0 ..
+    const int key_in = tid & 127;                   // its key inside a tile
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    auto vote = [&](bool p) { return softmax_vote<C::kSoftmax>(p); };
+    auto sync = [&]() { named_barrier_sync(1, C::kSoftmax); };
     int tc = 0;
     bool ok = true, late = false;  // late: a wait ran out where the warps cannot part
+    // a segment's queries are loaded while the one before ends; its ring slot is
+    // free again when the segment is done
+    Queries<DIM, R> queries;
+    auto await = [&](int n) {
+      const bool got = mbar_wait_w_ab(smem_u32(&sm.seg_full[n % kSegSlots]),
+                                      (n / kSegSlots) & 1, &sm.abort);
+      if (got) {
+        const Segment& x = sm.seg[n % kSegSlots];
+        if (x.s >= 0 && x.i1 > x.i0) queries.load(g, x, tid);
+      }
+      return got;
+    };
+    ok = await(0);
     for (int ns = 0;; ++ns) {
-      const int sl = ns % kSegSlots;
-      ok = mbar_wait_w_ab(smem_u32(&sm.seg_full[sl]), (ns / kSegSlots) & 1, &sm.abort);
-      if (!ok) sm.stop[0] = sm.stop[1] = 1;
-      Segment sg{};
-      if (ok) sg = sm.seg[sl];
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[sl]));
       // (also: everybody is done with the row tables of the segment before)
-      if (softmax_vote(!ok)) {
+      if (vote(!ok || late)) {
         ok = false;
         break;
       }
+      const Segment& sg = sm.seg[ns % kSegSlots];
       if (sg.s < 0) break;
       const int nt = sg.i1 - sg.i0;
       const int rows = static_cast<int>(
           min(static_cast<long long>(R), static_cast<long long>(sg.n) * g.G - sg.row0));
-      // row tables, and the queries as two E4M3 terms
       if (tid < R) {
         const int i = (sg.row0 + tid) / g.G, hq = sg.hk * g.G + (sg.row0 + tid) % g.G;
         const bool live = tid < rows;
         sm.pos[tid] = live ? sg.start + i : -1;
         sm.orow[tid] = live ? (sg.s + i) * g.H + hq : -1;
-        sm.ref_m[tid] = sm.ref_w[tid] = kUnset;
+        sm.nref[tid] = kShift;
+        sm.has[tid] = 0;
       }
       if (nt > 0) {
-        constexpr int LPR = DIM / 8, PER = 128 / LPR;
-#pragma unroll 1
-        for (int r0 = 0; r0 < R; r0 += PER) {
-          const int r = r0 + tid / LPR, ch = tid % LPR;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            const int i = (sg.row0 + r) / g.G, hq = sg.hk * g.G + (sg.row0 + r) % g.G;
-            w = __ldg(reinterpret_cast<const uint4*>(
-                g.q + (sg.s + i) * g.q_stride + static_cast<long long>(hq) * DIM + ch * 8));
-          }
-          float x[8];
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          float amax = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(ww[j] << 16);
-            x[2 * j + 1] = __uint_as_float(ww[j] & 0xFFFF0000u);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (!(fabsf(x[j]) < INFINITY)) x[j] = __uint_as_float(0x7FC00000u);
-            amax = fmaxf(amax, fabsf(x[j]));  // of the finite ones
-          }
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          const int e = roundup_exponent(amax);
-          const float inv = exp2i(-e);
-          uint32_t hc[4], lc[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float a = x[2 * j] * inv, c = x[2 * j + 1] * inv;
-            hc[j] = cvt_e4m3x2(a, c);
-            const float2 h = e4m3x2_to_float2(hc[j]);
-            lc[j] = cvt_e4m3x2((a - h.x) * 16.f, (c - h.y) * 16.f);
-          }
-          if (r < R) {
-            // K-major rows of DIM bytes, 16-byte chunks swizzled as TMA does
-            auto at = [&](int n) {
-              const int c16 = ch >> 1;
-              const int sw = DIM == 128 ? (c16 ^ (n & 7)) : (c16 ^ ((n >> 1) & 3));
-              return reinterpret_cast<uint2*>(sm.q + n * DIM + sw * 16 + (ch & 1) * 8);
-            };
-            *at(r) = make_uint2(hc[0] | (hc[1] << 16), hc[2] | (hc[3] << 16));
-            *at(R + r) = make_uint2(lc[0] | (lc[1] << 16), lc[2] | (lc[3] << 16));
-            if (ch == 0) sm.qf[r] = g.scale_log2 * (e < -126 ? 0x1p-127f : exp2i(e));
-          }
-        }
+        queries.split(sm.q, sm.qf, g.scale_log2, tid);
         fence_proxy_async_smem();
         mbar_arrive(smem_u32(&sm.q_full));
       }
-      softmax_sync();  // row tables
-      float l[R];
+      sync();  // row tables
+      float2 l[RW / 2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = 0.f;
-      // every row sees the keys below pf + 1 (and, windowed, from wlast on)
-      const int pf = sg.start + sg.row0 / g.G;
-      const int pl = sg.start + (sg.row0 + rows - 1) / g.G;
-      const int wlast = g.window > 0 ? pl - g.window + 1 : 0;
+      for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
+      int e0 = -127;
+      const int pf = sg.start + sg.row0 / g.G;               // positions of the first
+      const int pl = sg.start + (sg.row0 + rows - 1) / g.G;  // and the last row
       const int all_pieces = g.page_size >= 128 ? 1 : (1 << (128 / g.page_size)) - 1;
 
       for (int t = 0; t < nt; ++t, ++tc) {
         const int st = tc % C::kStages, buf = tc & 1;
-        const int k0 = tile_of(sg, sg.i0 + t) * 128, key = k0 + tid;
+        const int k0 = tile_of(sg, sg.i0 + t) * 128, key = k0 + key_in;
         ok = mbar_wait_w_ab(smem_u32(&sm.s_full[buf]), (tc >> 1) & 1, &sm.abort);
         // the scale bytes: landed before the scores could be computed
         ok = ok && mbar_wait_w_ab(smem_u32(&sm.full[st]), (tc / C::kStages) & 1, &sm.abort);
-        // the product two tiles back has read this buffer of P^T
-        if (tc >= 2)
-          ok = ok && mbar_wait_w_ab(smem_u32(&sm.pv_done[buf]), ((tc - 2) >> 1) & 1, &sm.abort);
-        if (!ok) sm.stop[tc & 1] = 1;
+        if (!ok) sm.stop[buf] = 1;
         tc_fence_after();
-        float x[R];
-        const int eb = sm.vs[st][tid];
-        const float kf = pow2_byte(sm.ks[st][tid]), ev = static_cast<float>(eb - 127);
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < R; c += 8) {
-            uint32_t h[8], lo[8];
-            tmem_ld8(tmem + lanes + buf * C::kNS + c, h);
-            tmem_ld8(tmem + lanes + buf * C::kNS + R + c, lo);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              x[c + i] = fmaf(__uint_as_float(lo[i]), 0.0625f, __uint_as_float(h[i])) *
-                         (kf * sm.qf[c + i]);
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < R; ++r) x[r] = 0.f;
-        }
+        const int eb = sm.vs[st][key_in];
+        const float kf = pow2_byte(sm.ks[st][key_in]);
         // keys that not every row sees
         const int loaded = sm.loaded[st];
         const bool whole = loaded == all_pieces && k0 + 127 <= pf &&
-                           (g.window == 0 || k0 >= wlast || k0 + 127 < g.sinks);
+                           (g.window == 0 || k0 > pl - g.window || k0 + 127 < g.sinks);
+        bool any = true;        // some row sees the key
+        uint32_t seen = ~0u;    // of this thread's rows
+        bool nan = false;
         if (!whole) {
-          const int piece = g.page_size >= 128 ? 0 : tid / g.page_size;
-          const bool here = (loaded >> piece) & 1;
-          bool any = false, every = true;
-          uint32_t seen[(R + 31) / 32] = {};
+          const bool here = (loaded >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
+          const bool first = g.window == 0 || key < g.sinks;
+          any = here && key <= pl && (first || key > pf - g.window);
+          const bool every = here && key <= pf && (first || key > pl - g.window) && rows == R;
+          if (!every) {
+            seen = 0;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int p = sm.pos[r];
-            const bool s = here && key <= p &&
-                           (g.window == 0 || key > p - g.window || key < g.sinks);
-            if (s) seen[r / 32] |= 1u << (r % 32);
-            else x[r] = -INFINITY;
-            any |= s;
-            every &= s || r >= rows;
+            for (int r = 0; r < RW; ++r) {
+              const int p = sm.pos[r0 + r];
+              if (here && key <= p && (first || key > p - g.window)) seen |= 1u << r;
+            }
           }
           // A value that some rows see and others do not must not reach the
           // others: 0 x NaN is NaN.  Unseen rows of V are cleared; a NaN in a
           // half-seen one moves into the weights of those that see it.
-          if (!every) {
-            uint4* vr = reinterpret_cast<uint4*>(sm.v[st] + tid * DIM);
-            bool nan = false;
-            if (any) {
-              for (int i = 0; i < DIM / 16; ++i) {
-                const uint4 a = vr[i];
-                const uint32_t aa[4] = {a.x, a.y, a.z, a.w};
+          if (any && !every) {
+            const uint4* vr = reinterpret_cast<const uint4*>(sm.v[st] + key_in * DIM);
+#pragma unroll 4
+            for (int i = 0; i < DIM / 16; ++i) {
+              const uint4 a = vr[i];
+              const uint32_t aa[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  nan |= ((((aa[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
-              }
-            }
-            if (!any || nan)
-              for (int i = 0; i < DIM / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
-            if (nan) {
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-                if ((seen[r / 32] >> (r % 32)) & 1) x[r] = __uint_as_float(0x7FC00000u);
+              for (int j = 0; j < 4; ++j)
+                nan |= ((((aa[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
             }
           }
+          if (C::kHalves > 1) sync();  // both halves have looked
+          if ((!any || nan) && half == 0) {
+            uint4* vr = reinterpret_cast<uint4*>(sm.v[st] + key_in * DIM);
+#pragma unroll 4
+            for (int i = 0; i < DIM / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+          }
         }
-        // do the references hold?
-        bool over = false;
+        // V's exponent; what nobody sees has the neutral one
+        const int ev = any ? eb - 127 : -127;
+        int evc = max(ev, e0 - kLow);
+        float2 y[RW / 2];
+        auto scores = [&]() {
+          const float2 kf2 = make_float2(kf, kf);
+          const float evf = static_cast<float>(evc);
+          const float2 ev2 = make_float2(evf, evf), lo2 = make_float2(0.0625f, 0.0625f);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          over |= x[r] > sm.ref_m[r] + kSlackM || x[r] + ev > sm.ref_w[r] + kSlackW;
-        const bool move = softmax_vote(over);
-        if (sm.stop[tc & 1]) {  // the same for all: written before the barrier
+          for (int c = 0; c < RW; c += 8) {
+            uint32_t h[8], lo[8];
+            tmem_ld8(tmem + lanes + buf * C::kNS + r0 + c, h);
+            tmem_ld8(tmem + lanes + buf * C::kNS + R + r0 + c, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int r = 0; r < 8; r += 4) {
+              const float4 qf = *reinterpret_cast<const float4*>(sm.qf + r0 + c + r);
+              const float4 nr = *reinterpret_cast<const float4*>(sm.nref + r0 + c + r);
+              const float2 a = __ffma2_rn(as_f2(lo[r], lo[r + 1]), lo2, as_f2(h[r], h[r + 1]));
+              const float2 b =
+                  __ffma2_rn(as_f2(lo[r + 2], lo[r + 3]), lo2, as_f2(h[r + 2], h[r + 3]));
+              y[(c + r) / 2] = __ffma2_rn(a, __fmul2_rn(kf2, make_float2(qf.x, qf.y)),
+                                          __fadd2_rn(ev2, make_float2(nr.x, nr.y)));
+              y[(c + r) / 2 + 1] = __ffma2_rn(b, __fmul2_rn(kf2, make_float2(qf.z, qf.w)),
+                                              __fadd2_rn(ev2, make_float2(nr.z, nr.w)));
+            }
+          }
+          if (!whole) {
+            const float nv = __uint_as_float(0x7FC00000u);
+#pragma unroll
+            for (int r = 0; r < RW; r += 2) {
+              y[r / 2].x = !((seen >> r) & 1) ? -INFINITY : nan ? nv : y[r / 2].x;
+              y[r / 2].y = !((seen >> (r + 1)) & 1) ? -INFINITY : nan ? nv : y[r / 2].y;
+            }
+          }
+        };
+        // do the references hold?
+        bool over = t == 0;
+        if (t > 0) {
+          scores();
+          float mx = -INFINITY;
+#pragma unroll
+          for (int r = 0; r < RW / 2; ++r) mx = fmax3(mx, y[r].x, y[r].y);
+          over = mx > kShift + kSlack || ev > e0 + kHigh;
+        }
+        const bool move = vote(over);
+        if (sm.stop[buf]) {  // the same for all: written before the barrier
           ok = false;
           break;
         }
         if (move) {
+          // E0, then the rows' references
+          const int em = __reduce_max_sync(0xffffffffu, ev + 127);
+          if (lane == 0) sm.rede[warp] = em;
+          // rows without a reference are measured from 0
+          if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = kShift;
+          sync();
+          int top = -127, rise = 0;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float a = warp_max(x[r]), c = warp_max(x[r] + ev);
-            if (lane == 0) {
-              sm.red[warp][r][0] = a;
-              sm.red[warp][r][1] = c;
-            }
+          for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
+          if (t == 0) {
+            e0 = top;
+          } else if (top > e0 + kHigh) {
+            rise = top - e0;
+            e0 = top;
           }
-          softmax_sync();
+          evc = max(ev, e0 - kLow);
+          scores();
+#pragma unroll
+          for (int r = 0; r < RW; ++r) {
+            const float a = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
+            if (lane == 0) sm.red[warp & 3][r0 + r] = a;
+          }
+          sync();
           if (tid < R) {
-            float a = -INFINITY, c = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              a = fmaxf(a, sm.red[w][tid][0]);
-              c = fmaxf(c, sm.red[w][tid][1]);
+            const float a = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
+                                  fmaxf(sm.red[2][tid], sm.red[3][tid]));
+            // A row keeps its reference while it holds; one that has seen
+            // nothing (or nothing but NaN) has none.  If E0 rose by more than
+            // 40, the references follow, so that l (whose terms are at most
+            // 2^(kShift + kSlack + kLow + rise)) stays inside float32.
+            const float n0 = sm.nref[tid];
+            float n1 = n0, f = 1.f, fl = 1.f;
+            if (tid >= rows) {
+              n1 = -kUnset;
+            } else if (!sm.has[tid]) {
+              const bool now = a > -INFINITY;
+              n1 = now ? n0 - ceilf(a - kShift) : kUnset;
+              sm.has[tid] = now;
+            } else {
+              const float up = fmaxf(a > kShift + kSlack ? ceilf(a - kShift) : 0.f,
+                                     static_cast<float>(rise - 40));
+              const float by = fmaxf(up, 0.f);
+              n1 = n0 - by;
+              f = ex2_approx(-by);
+              fl = ex2_approx(static_cast<float>(rise) - by);
             }
-            const float m0 = sm.ref_m[tid], w0 = sm.ref_w[tid];
-            const float m1 = a > m0 + kSlackM ? ceilf(a) : m0;
-            const float w1 = c > w0 + kSlackW ? ceilf(c) : w0;
-            sm.ref_m[tid] = m1;
-            sm.ref_w[tid] = w1;
-            sm.f_m[tid] = ex2_approx(m0 - m1);
-            sm.f_w[tid] = ex2_approx(w0 - w1);
+            sm.nref[tid] = n1;
+            sm.fac[tid] = f;
+            sm.facl[tid] = fl;
           }
-          softmax_sync();
+          sync();
 #pragma unroll
-          for (int r = 0; r < R; ++r) l[r] *= sm.f_m[r];
+          for (int r = 0; r < RW; r += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sm.facl + r0 + r);
+            l[r / 2] = __fmul2_rn(l[r / 2], make_float2(f.x, f.y));
+            l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
+          }
           if (t > 0) {  // O^T, once the product before has added to it
             if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort)) {
               late = true;
-              sm.stop[(tc + 1) & 1] = 1;
+              sm.stop[buf ^ 1] = 1;
             }
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 3 * R; c += 8) {
-              uint32_t a[8];
-              tmem_ld8(tmem + lanes + C::kColO + c, a);
-              tmem_ld_wait();
+            for (int term = 0; term < 3; ++term) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                a[i] = __float_as_uint(__uint_as_float(a[i]) * sm.f_w[(c + i) % R]);
-              tmem_st8(tmem + lanes + C::kColO + c, a);
+              for (int c = 0; c < RW; c += 8) {
+                uint32_t a[8];
+                const uint32_t at = tmem + lanes + C::kColO + term * R + r0 + c;
+                tmem_ld8(at, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  a[i] = __float_as_uint(__uint_as_float(a[i]) * sm.fac[r0 + c + i]);
+                tmem_st8(at, a);
+              }
             }
             tmem_st_wait();
           }
+          scores();
         }
-        // weights: P^T as rows of 128 bytes (one a query row and term), keys
-        // along them, 16-byte chunks swizzled
-        const uint32_t pbase = smem_u32(sm.p[buf]) + (tid & 15);
+        // weights and their E4M3 terms, 4 rows a word
+        const float gl = ex2_approx(static_cast<float>(e0 - evc));
+        const float2 g2 = make_float2(gl, gl);
+        const float z = ev < evc ? ex2_approx(static_cast<float>(max(ev - evc, -126))) : 1.f;
+        uint32_t tw[3][RW / 4];
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          l[r] += ex2_approx(x[r] - sm.ref_m[r]);
-          l[r + 1] += ex2_approx(x[r + 1] - sm.ref_m[r + 1]);
-          float a = ex2_approx(x[r] + (ev - sm.ref_w[r] + kShiftW));
-          float b = ex2_approx(x[r + 1] + (ev - sm.ref_w[r + 1] + kShiftW));
+        for (int r = 0; r < RW; r += 4) {
+          float2 a = make_float2(ex2_approx(y[r / 2].x), ex2_approx(y[r / 2].y));
+          float2 b = make_float2(ex2_approx(y[r / 2 + 1].x), ex2_approx(y[r / 2 + 1].y));
+          l[r / 2] = __ffma2_rn(a, g2, l[r / 2]);
+          l[r / 2 + 1] = __ffma2_rn(b, g2, l[r / 2 + 1]);
+          if (ev < evc) {
+            a.x *= z;
+            a.y *= z;
+            b.x *= z;
+            b.y *= z;
+          }
+          const float2 n32 = make_float2(-32.f, -32.f), p32 = make_float2(32.f, 32.f);
 #pragma unroll
           for (int term = 0; term < 3; ++term) {
-            const uint32_t c = cvt_e4m3x2(a, b);
-            const int n0 = term * R + r, n1 = n0 + 1;
-            sts8(pbase + n0 * 128 + (((tid >> 4) ^ (n0 & 7)) << 4), c);
-            sts8(pbase + n1 * 128 + (((tid >> 4) ^ (n1 & 7)) << 4), c >> 8);
-            if (term < 2) {
-              const float2 h = e4m3x2_to_float2(c);
-              a = (a - h.x) * 32.f;
-              b = (b - h.y) * 32.f;
+            const uint32_t ca = cvt_e4m3x2(a.x, a.y), cb = cvt_e4m3x2(b.x, b.y);
+            tw[term][r / 4] = ca | (cb << 16);
+            if (term < 2) {  // 32 (w - h), exact
+              a = __ffma2_rn(e4m3x2_to_float2(ca), n32, __fmul2_rn(a, p32));
+              b = __ffma2_rn(e4m3x2_to_float2(cb), n32, __fmul2_rn(b, p32));
             }
+          }
+        }
+        // the product that last read this buffer of P^T
+        if (tc >= C::kPBufs) {
+          const int x = tc - C::kPBufs;
+          if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[x & 1]), (x >> 1) & 1, &sm.abort)) {
+            late = true;
+            sm.stop[buf ^ 1] = 1;
+          }
+        }
+        // P^T: key rows of 32 columns (32 bytes), 16-byte chunks swizzled
+        const uint32_t pb = smem_u32(sm.p[tc % C::kPBufs]) + key_in * 32;
+        const uint32_t sw = ((key_in >> 2) & 1) * 16;
+        if constexpr (R == 8) {
+          sts128(pb + sw, tw[0][0], tw[0][1], tw[1][0], tw[1][1]);
+          sts128(pb + (sw ^ 16), tw[2][0], tw[2][1], 0, 0);
+        } else {
+#pragma unroll
+          for (int term = 0; term < 3; ++term) {
+            const int n = term * R + r0;  // first column: a multiple of 16
+            sts128(pb + (n / 32) * 4096 + (sw ^ (n & 16)), tw[term][0], tw[term][1], tw[term][2],
+                   tw[term][3]);
           }
         }
         fence_proxy_async_smem();
@@ -752,66 +914,66 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
       }
       if (!ok) break;
 
+      // the next segment's queries come while this one's last product runs
+      ok = await(ns + 1);
       // ---------------------------------------------------------- epilogue
       if (nt > 0) {
         const int x = tc - 1;
-        ok = mbar_wait_w_ab(smem_u32(&sm.pv_done[x & 1]), (x >> 1) & 1, &sm.abort);
+        if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[x & 1]), (x >> 1) & 1, &sm.abort)) late = true;
         tc_fence_after();
       }
+      const int slot = sg.slot;
       // l over the keys (threads)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float s = l[r];
+      for (int r = 0; r < RW; ++r) {
+        float s = r & 1 ? l[r / 2].y : l[r / 2].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) sm.red[warp][r][0] = s;
+        if (lane == 0) sm.red[warp & 3][r0 + r] = s;
       }
-      if (softmax_vote(!ok || late)) {
-        ok = false;
-        break;
-      }
+      sync();
       if (tid < rows) {
-        const float s = (sm.red[0][tid][0] + sm.red[1][tid][0]) +
-                        (sm.red[2][tid][0] + sm.red[3][tid][0]);
-        const float m = sm.ref_m[tid], w = sm.ref_w[tid];
-        if (sg.slot >= 0) {
-          g.stats[static_cast<size_t>(sg.slot) * R + tid] = make_float4(m, s, w, 0.f);
-        } else {
-          // o = O^T 2^(w - shift - m) / l; nothing seen: l = 0
-          sm.f_m[tid] = s == 0.f ? 0.f : 1.f / s;
-          sm.f_w[tid] = s == 0.f ? 0.f : exp2f(w - kShiftW - m);
-          const int orow = sm.orow[tid];
-          if (g.lse != nullptr)
-            g.lse[static_cast<size_t>(orow % g.H) * g.T + orow / g.H] = (m + log2f(s)) * kLn2;
-        }
+        const float s = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+        sm.fac[tid] = s == 0.f ? 0.f : 1.f / s;  // nothing seen: l = 0
+        const float lg = s == 0.f ? -INFINITY
+                                  : log2f(s) - sm.nref[tid] - static_cast<float>(e0);
+        const int orow = sm.orow[tid];
+        if (slot >= 0)
+          g.stats[static_cast<size_t>(slot) * R + tid] = lg;
+        else if (g.lse != nullptr)
+          g.lse[static_cast<size_t>(orow % g.H) * g.T + orow / g.H] = lg * kLn2;
       }
-      softmax_sync();
-      const bool active = DIM == 128 || tid < DIM;
+      sync();
+      const float ve = e0 < -126 ? 0x1p-127f : exp2i(e0);
+      const bool active = DIM == 128 || key_in < DIM;
 #pragma unroll
-      for (int c = 0; c < R; c += 8) {
+      for (int c = 0; c < RW; c += 8) {
         uint32_t h[8], m[8], lo[8];
         if (nt > 0) {
-          tmem_ld8(tmem + lanes + C::kColO + c, h);
-          tmem_ld8(tmem + lanes + C::kColO + R + c, m);
-          tmem_ld8(tmem + lanes + C::kColO + 2 * R + c, lo);
+          const uint32_t at = tmem + lanes + C::kColO + r0 + c;
+          tmem_ld8(at, h);
+          tmem_ld8(at + R, m);
+          tmem_ld8(at + 2 * R, lo);
           tmem_ld_wait();
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int r = c + i;
+          const int r = r0 + c + i;
           if (r < rows && active) {
-            const float v =
-                nt > 0 ? fmaf(fmaf(__uint_as_float(lo[i]), 0x1p-5f, __uint_as_float(m[i])), 0x1p-5f,
-                              __uint_as_float(h[i]))
-                       : 0.f;
-            if (sg.slot >= 0)
-              g.partial[(static_cast<size_t>(sg.slot) * R + r) * DIM + tid] = v;
+            const float f = sm.fac[r];
+            float v = 0.f;
+            if (nt > 0 && f != 0.f)
+              v = fmaf(fmaf(__uint_as_float(lo[i]), 0x1p-5f, __uint_as_float(m[i])), 0x1p-5f,
+                       __uint_as_float(h[i])) * f * ve;
+            if (slot >= 0)
+              g.partial[(static_cast<size_t>(slot) * R + r) * DIM + key_in] = v;
             else
-              g.o[static_cast<size_t>(sm.orow[r]) * DIM + tid] =
-                  __float2bfloat16(sm.f_m[r] == 0.f ? 0.f : v * sm.f_m[r] * sm.f_w[r]);
+              g.o[static_cast<size_t>(sm.orow[r]) * DIM + key_in] = __float2bfloat16(v);
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[ns % kSegSlots]));
       if (nt > 0) {
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.o_empty));
@@ -822,52 +984,51 @@ __global__ void __launch_bounds__(kThreads, Cfg<DIM, R>::kCtas)
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && sm.abort) report(g.status, FLAMIA_DEV_TIMEOUT);
-  if (warp == 5) {
+  if (warp == kIssuer) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
 }
 
-// Joins the parts of an item that several CTAs shared: part 0 in slot 1 of the
-// CTA before, the others in slots 0 from this CTA on.
+// Joins the parts of an item that several CTAs shared (part 0 in slot 1 of the
+// CTA before, the others in slots 0 from this CTA on): o = sum 2^(lg_p - lg) o_p.
 template <int DIM, int R>
 __global__ void __launch_bounds__(8 * DIM) join_kernel(const AttendArgs g) {
   __shared__ float s_wt[8][kMaxCtas];
-  __shared__ float s_tot[8][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 j0 = g.joins[2 * blockIdx.x], j1 = g.joins[2 * blockIdx.x + 1];
   const int parts = j0.x;
   if (parts <= 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int c0 = blockIdx.x, first = blockIdx.y * 8;
-  auto slot = [&](int p) { return p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + p - 1); };
+  auto slot = [&](int p) {
+    return static_cast<size_t>(p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + p - 1));
+  };
   const int rows = static_cast<int>(
       min(static_cast<long long>(R), static_cast<long long>(j0.z) * g.G - j1.x));
   if (warp < 8 && first + warp < rows) {
     const int r = first + warp;
-    float m = kUnset, w = kUnset;
+    float m = -INFINITY;
     for (int p = lane; p < parts; p += 32) {
-      const float4 s = g.stats[static_cast<size_t>(slot(p)) * R + r];
-      m = fmaxf(m, s.x);
-      w = fmaxf(w, s.z);
-    }
-    m = warp_max(m);
-    w = warp_max(w);
-    float l = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-      const float4 s = g.stats[static_cast<size_t>(slot(p)) * R + r];
-      l += s.y * ex2_approx(s.x - m);
-      s_wt[warp][p] = ex2_approx(s.z - w);
+      const float x = g.stats[slot(p) * R + r];
+      m = x > m || x != x ? x : m;
     }
 #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, m, o);
+      m = x > m || x != x ? x : m;  // NaN stays
+    }
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int p = lane; p < parts; p += 32) l += exp2f(g.stats[slot(p) * R + r] - ref);
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) {
-      s_tot[warp][0] = l == 0.f ? 0.f : 1.f / l;
-      s_tot[warp][1] = exp2f(w - kShiftW - m);
-      if (g.lse != nullptr) {
-        const int i = (j1.x + r) / g.G, hq = j0.w * g.G + (j1.x + r) % g.G;
-        g.lse[static_cast<size_t>(hq) * g.T + j0.y + i] = (m + log2f(l)) * kLn2;
-      }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int p = lane; p < parts; p += 32)
+      s_wt[warp][p] = exp2f(g.stats[slot(p) * R + r] - ref) * inv;
+    if (lane == 0 && g.lse != nullptr) {
+      const int i = (j1.x + r) / g.G, hq = j0.w * g.G + (j1.x + r) % g.G;
+      g.lse[static_cast<size_t>(hq) * g.T + j0.y + i] = (ref + log2f(l)) * kLn2;
     }
   }
   __syncthreads();
@@ -875,11 +1036,9 @@ __global__ void __launch_bounds__(8 * DIM) join_kernel(const AttendArgs g) {
   if (r >= rows) return;
   float acc = 0.f;
 #pragma unroll 8
-  for (int p = 0; p < parts; ++p)
-    acc += s_wt[rl][p] * g.partial[(static_cast<size_t>(slot(p)) * R + r) * DIM + dd];
+  for (int p = 0; p < parts; ++p) acc += s_wt[rl][p] * g.partial[(slot(p) * R + r) * DIM + dd];
   const int i = (j1.x + r) / g.G, hq = j0.w * g.G + (j1.x + r) % g.G;
-  g.o[(static_cast<size_t>(j0.y + i) * g.H + hq) * DIM + dd] =
-      __float2bfloat16(s_tot[rl][0] == 0.f ? 0.f : acc * s_tot[rl][0] * s_tot[rl][1]);
+  g.o[(static_cast<size_t>(j0.y + i) * g.H + hq) * DIM + dd] = __float2bfloat16(acc);
 }
 
 // ------------------------------------------------------------------ host
@@ -899,7 +1058,7 @@ Workspace layout(int R, int d) {
   Workspace w;
   w.joins = 0;
   w.stats = align_up(sizeof(int4) * 2 * kMaxCtas, 256);
-  w.partial = w.stats + align_up(sizeof(float4) * static_cast<size_t>(kSlots) * R, 256);
+  w.partial = w.stats + align_up(sizeof(float) * static_cast<size_t>(kSlots) * R, 256);
   w.total = w.partial + sizeof(float) * static_cast<size_t>(kSlots) * R * d;
   return w;
 }
@@ -926,12 +1085,15 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
   if (!make_page_map(&mk, c->k_codes, c) || !make_page_map(&mv, c->v_codes, c))
     return FLAMIA_ERR_CUDA;
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM, R>)) + 1024;
+  static_assert(Cfg<DIM, R>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
   if (cudaFuncSetAttribute(attend_kernel<DIM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem) != cudaSuccess)
     return FLAMIA_ERR_CUDA;
   const int grid = min(kMaxCtas, num_sms() * Cfg<DIM, R>::kCtas);
-  attend_kernel<DIM, R><<<grid, kThreads, smem, s>>>(mk, mv, g);
+  attend_kernel<DIM, R><<<grid, Cfg<DIM, R>::kThreads, smem, s>>>(mk, mv, g);
   if (cudaGetLastError() != cudaSuccess) return FLAMIA_ERR_CUDA;
+  count_launches(1);
+  if (g.whole) return FLAMIA_OK;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, R / 8);
   cfg.blockDim = dim3(8 * DIM);
@@ -942,7 +1104,7 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, join_kernel<DIM, R>, g) != cudaSuccess) return FLAMIA_ERR_CUDA;
-  count_launches(2);
+  count_launches(1);
   return FLAMIA_OK;
 }
 
@@ -969,7 +1131,7 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   if (st != FLAMIA_OK) return st;
   if (!valid_batch(T, ndocs) || table_stride <= 0 || H <= 0 || H > 4096 || H % cache->H_kv != 0 ||
       !(softmax_scale > 0.f) || std::isinf(softmax_scale) || window < 0 || sinks < 0 ||
-      (sinks > 0 && window == 0) || static_cast<long long>(T) * H >= (1ll << 31))
+      (sinks > 0 && window == 0) || static_cast<long long>(T) * H >= (1ll << 31) - 64)
     return FLAMIA_ERR_INVALID_ARG;
   if (T == 0) return FLAMIA_OK;
   if (!valid_rows(q_bf16, q_stride) || o_bf16 == nullptr || !aligned(o_bf16, 16) ||
@@ -990,7 +1152,7 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   g.starts = starts;
   g.table = page_table;
   g.joins = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + w.joins);
-  g.stats = reinterpret_cast<float4*>(static_cast<uint8_t*>(ws) + w.stats);
+  g.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.stats);
   g.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.partial);
   g.status = dev_status;
   g.q_stride = q_stride;
@@ -1005,6 +1167,7 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   // positions stay below 2^30: larger windows and first tokens see the same
   g.window = window < kMaxPos ? window : kMaxPos;
   g.sinks = sinks < kMaxPos ? sinks : kMaxPos;
+  g.whole = static_cast<long long>(table_stride) * cache->page_size <= 128 * kWholeTiles;
   g.scale_log2 = softmax_scale * 1.44269504088896340736f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 128)
