@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t finite_mag(uint32_t w) {
 }
 
 template <int DIM, bool TOK>
-__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheArgs g) {
+__global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const CacheArgs g) {
   constexpr int LPR = DIM / 8;   // lanes per row: 8 elements each
   constexpr int RPI = 32 / LPR;  // rows per warp-wide access
   constexpr int NLD = 32 / RPI;  // accesses per block
