@@ -8,8 +8,8 @@
 // and float32 weights become sums of E4M3 terms instead, side by side in N:
 //   q 2^-e = h + 2^-4 l              (e per row; exact for the elements above
 //                                     2^-14 of the row's largest),
-//   w      = h + 2^-5 m + 2^-10 l    (relative error 2^-14, floor 2^-24 of the
-//                                     largest weight),
+//   w      = h + 2^-5 m + 2^-10 l    (relative error at most 2^-11, floor 2^-24
+//                                     of the largest weight),
 // which costs N = 2 R and 3 R columns of a product that reads M = 128 rows of
 // shared memory in any case.
 //
@@ -51,11 +51,9 @@ constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for 
 constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
-constexpr int kItemCost = 2;    // an item's own steps (queries, output) in tiles
+constexpr int kItemCost = 4;    // an item's own steps (queries, output) in tiles
 constexpr int kWholeTiles = 4;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kShift = 4.f;   // weights are 2^kShift at the reference and at
-constexpr float kSlack = 4.f;   // most 2^(kShift + kSlack) = 256 < 448
 constexpr float kUnset = 1e30f; // -reference of a row that has seen no key yet
 constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
 constexpr int kLow = 60;
@@ -115,6 +113,34 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
+}
+
+// A pair of floats rounded to FP16; FP16 pairs to E4M3 / E5M2 codes; 32 (w - code)
+// of an FP16 pair (exact).
+__device__ __forceinline__ uint32_t half2_of(float2 a) {
+  const __half2 h = __floats2half2_rn(a.x, a.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t e5m2x2_of_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t residual32(uint32_t w, uint32_t code) {
+  uint32_t c, r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"(static_cast<uint16_t>(code)));
+  const uint32_t p32 = 0x50005000u, n32 = 0xD000D000u;  // 32, -32
+  asm("{\n\t.reg .b32 t;\n\t"
+      "mul.rn.f16x2 t, %1, %2;\n\t"
+      "fma.rn.f16x2 %0, %3, %4, t;\n\t}"
+      : "=r"(r)
+      : "r"(w), "r"(p32), "r"(c), "r"(n32));
+  return r;
 }
 
 __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
@@ -181,11 +207,26 @@ struct Cfg {
   static constexpr int kSoftmax = 128 * kHalves;    // softmax threads
   static constexpr int kThreads = kSoftmax + 64;
   static constexpr int kCtas = R == 8 ? 3 : 2;      // resident CTAs per SM
-  static constexpr int kStages = (R == 16 ? 3 : 2) * (128 / DIM);
+  // Stages.  32 rows: K is read once its scores are there and V a softmax later,
+  // so each has a ring of its own, and the scale bytes (and which pieces were
+  // loaded) one that is two longer, as the softmax of a tile is done two score
+  // products later (a chunk of 512 tokens over 8,192: 284 -> 257 us).  With
+  // fewer rows, where HBM sets the pace, K, V and scales of a tile share a stage
+  // and a barrier (96 ragged contexts: 102 us against 128).
+  static constexpr bool kSplit = R == 32;
+  static constexpr int kKS = (R == 8 ? 2 : 3) * (128 / DIM);
+  static constexpr int kVS = (R == 16 ? 3 : 2) * (128 / DIM);
+  static constexpr int kSS = kSplit ? kKS + 2 : kKS;
+  static_assert(kSplit || kKS == kVS, "one ring");
   static constexpr int kTileBytes = 128 * DIM;
+  // 32 rows are bound by the softmax warps: their weights go through FP16
+  // (relative error 2^-11) and keep the last term in E5M2, whose range leaves
+  // room for references that move seldom
+  static constexpr bool kHalfWeights = R == 32;
+  static constexpr float kShift = kHalfWeights ? 0.f : 4.f;  // log2 of a weight at the reference
+  static constexpr float kSlack = 8.f - kShift;              // weights <= 2^8 < 448
   static constexpr int kNS = 2 * R;                 // columns of S^T
   static constexpr int kNO = R == 8 ? 32 : 3 * R;   // columns of O^T
-  static constexpr int kPBufs = R == 32 ? 2 : 1;
   static constexpr int kAtoms = (kNO + 31) / 32;    // P^T: 32 columns x 128 keys each
   static constexpr uint32_t kColO = 2 * kNS;
   static constexpr uint32_t kCols = R == 8 ? 64 : R == 16 ? 128 : 256;
@@ -195,12 +236,12 @@ struct Cfg {
 template <int DIM, int R>
 struct Smem {
   using C = Cfg<DIM, R>;
-  alignas(1024) uint8_t v[C::kStages][C::kTileBytes];
-  alignas(1024) uint8_t k[C::kStages][C::kTileBytes];
-  alignas(1024) uint8_t p[C::kPBufs][C::kAtoms * 4096];
+  alignas(1024) uint8_t v[C::kVS][C::kTileBytes];
+  alignas(1024) uint8_t k[C::kKS][C::kTileBytes];
+  alignas(1024) uint8_t p[C::kAtoms * 4096];
   alignas(1024) uint8_t q[2 * R * DIM];
-  alignas(128) uint8_t ks[C::kStages][128];
-  alignas(128) uint8_t vs[C::kStages][128];
+  alignas(128) uint8_t ks[C::kSS][128];
+  alignas(128) uint8_t vs[C::kSS][128];
   alignas(16) float qf[R];      // 2^e of a row x softmax scale x log2 e
   alignas(16) float nref[R];    // kShift - reference
   alignas(16) float fac[R], facl[R];  // changes of scale of O^T and l
@@ -209,12 +250,13 @@ struct Smem {
   alignas(16) int orow[R];      // its row of o, -1: none
   float red[4][R];
   int rede[C::kSoftmax / 32];
-  uint64_t full[C::kStages], empty[C::kStages];
+  uint64_t k_full[C::kKS], k_empty[C::kKS], v_full[C::kVS], v_empty[C::kVS];
+  uint64_t sc_full[C::kSS];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t q_full, o_empty;
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Segment seg[kSegSlots];
-  int loaded[C::kStages];       // pieces of the tile that were loaded
+  int loaded[C::kSS];           // pieces of the tile that were loaded
   int plan_b;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
@@ -361,18 +403,23 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(smem_u32(&sm.full[i]), 1);
-      mbar_init(smem_u32(&sm.empty[i]), 1);
+    for (int i = 0; i < C::kKS; ++i) {
+      mbar_init(smem_u32(&sm.k_full[i]), 1);
+      mbar_init(smem_u32(&sm.k_empty[i]), 1);
+    }
+    for (int i = 0; i < C::kSS; ++i) mbar_init(smem_u32(&sm.sc_full[i]), 1);
+    for (int i = 0; i < C::kVS; ++i) {
+      mbar_init(smem_u32(&sm.v_full[i]), 1);
+      mbar_init(smem_u32(&sm.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.p_full[i]), C::kSoftmax);
+      mbar_init(smem_u32(&sm.p_full[i]), C::kSoftmax / 32);
       mbar_init(smem_u32(&sm.pv_done[i]), 1);
       sm.stop[i] = 0;
     }
-    mbar_init(smem_u32(&sm.q_full), C::kSoftmax);
-    mbar_init(smem_u32(&sm.o_empty), C::kSoftmax);
+    mbar_init(smem_u32(&sm.q_full), C::kSoftmax / 32);
+    mbar_init(smem_u32(&sm.o_empty), C::kSoftmax / 32);
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(smem_u32(&sm.seg_full[i]), 1);
       mbar_init(smem_u32(&sm.seg_empty[i]), kProducer + 1);  // softmax warps, MMA issuer
@@ -400,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       prefetch_tensormap(&map_k);
       prefetch_tensormap(&map_v);
     }
-    int b = sm.plan_b, tc = 0, nseg = 0;
+    int b = sm.plan_b, tc = 0, kc = 0, vc = 0, nseg = 0;  // kc, vc: tiles of K and V issued
     long long u = u0;
     bool ok = true, first = true;
     int4 join0 = make_int4(0, 0, 0, 0), join1 = make_int4(0, 0, 0, 0);
@@ -506,24 +553,55 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (i + 1 < sg.i1) page = entry(i + 1, need, in_page);
         if (nd && !good) report(g.status, FLAMIA_DEV_BAD_PAGE);
         const unsigned mask = __ballot_sync(0xffffffffu, good);
-        const int st = tc % C::kStages;
-        if (tc >= C::kStages)
-          ok = mbar_wait_w_ab(smem_u32(&sm.empty[st]), ((tc / C::kStages) - 1) & 1, &sm.abort);
-        if (!ok) break;
-        const uint32_t bar = smem_u32(&sm.full[st]);
-        if (lane == 0) {
-          sm.loaded[st] = static_cast<int>(mask);
-          mbar_arrive_expect_tx(bar, __popc(mask) * (2 * piece * DIM + 2 * piece));
-        }
-        __syncwarp();
-        if (good) {
-          const int pr = lane * piece;  // first key of the piece inside the tile
-          const int prow = pg * g.H_kv + sg.hk;
-          const long long sc = static_cast<long long>(prow) * g.page_size + ip;
-          tma_load_3d(smem_u32(sm.k[st]) + pr * DIM, &map_k, bar, 0, ip, prow);
-          bulk_load(smem_u32(sm.ks[st]) + pr, g.k_scales + sc, piece, bar);
-          tma_load_3d(smem_u32(sm.v[st]) + pr * DIM, &map_v, bar, 0, ip, prow);
-          bulk_load(smem_u32(sm.vs[st]) + pr, g.v_scales + sc, piece, bar);
+        const int n = __popc(mask), pr = lane * piece;  // first key of the piece in the tile
+        const int prow = pg * g.H_kv + sg.hk;
+        const long long sc = static_cast<long long>(prow) * g.page_size + ip;
+        const int kt = tc % C::kKS, vt = tc % C::kVS, ss = tc % C::kSS;
+        auto wait_v_slot = [&]() {
+          return tc < C::kVS ||
+                 mbar_wait_w_ab(smem_u32(&sm.v_empty[vt]), ((tc / C::kVS) - 1) & 1, &sm.abort);
+        };
+        auto load_k = [&](uint32_t bar, uint32_t sc_bar) {
+          tma_load_3d(smem_u32(sm.k[kt]) + pr * DIM, &map_k, bar, 0, ip, prow);
+          bulk_load(smem_u32(sm.ks[ss]) + pr, g.k_scales + sc, piece, sc_bar);
+          bulk_load(smem_u32(sm.vs[ss]) + pr, g.v_scales + sc, piece, sc_bar);
+        };
+        auto load_v = [&](uint32_t bar) {
+          tma_load_3d(smem_u32(sm.v[vt]) + pr * DIM, &map_v, bar, 0, ip, prow);
+        };
+        const uint32_t kbar = smem_u32(&sm.k_full[kt]);
+        if constexpr (C::kSplit) {
+          if (tc >= C::kKS)
+            ok = mbar_wait_w_ab(smem_u32(&sm.k_empty[kt]), ((tc / C::kKS) - 1) & 1, &sm.abort);
+          if (!ok) break;
+          const uint32_t sbar = smem_u32(&sm.sc_full[ss]), vbar = smem_u32(&sm.v_full[vt]);
+          if (lane == 0) {
+            sm.loaded[ss] = static_cast<int>(mask);
+            mbar_arrive_expect_tx(sbar, n * 2 * piece);
+            mbar_arrive_expect_tx(kbar, n * piece * DIM);
+          }
+          __syncwarp();
+          if (good) load_k(kbar, sbar);
+          ++kc;
+          ok = wait_v_slot();
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(vbar, n * piece * DIM);
+          __syncwarp();
+          if (good) load_v(vbar);
+          ++vc;
+        } else {
+          ok = wait_v_slot();
+          if (!ok) break;
+          if (lane == 0) {
+            sm.loaded[ss] = static_cast<int>(mask);
+            mbar_arrive_expect_tx(kbar, n * (2 * piece * DIM + 2 * piece));
+          }
+          __syncwarp();
+          if (good) {
+            load_k(kbar, kbar);
+            load_v(kbar);
+          }
+          ++kc;
         }
         __syncwarp();
       }
@@ -534,24 +612,30 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       g.joins[2 * blockIdx.x + 1] = join1;
     }
     // every issued copy has landed before the CTA can exit
-    for (int j = max(0, tc - C::kStages); j < tc; ++j)
-      ok &= mbar_wait_w(smem_u32(&sm.full[j % C::kStages]), (j / C::kStages) & 1);
+    for (int j = max(0, kc - C::kKS); j < kc; ++j)
+      ok &= mbar_wait_w(smem_u32(&sm.k_full[j % C::kKS]), (j / C::kKS) & 1) &&
+            (!C::kSplit || mbar_wait_w(smem_u32(&sm.sc_full[j % C::kSS]), (j / C::kSS) & 1));
+    for (int j = max(0, vc - C::kVS); j < vc; ++j)
+      ok &= mbar_wait_w(smem_u32(&sm.v_full[j % C::kVS]), (j / C::kVS) & 1);
     if (!ok) sm.abort = 1;
   } else if (warp == kIssuer) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t lay = DIM == 128 ? kLayoutSW128 : kLayoutSW64;
     constexpr uint32_t sbo = 8 * DIM;
     const uint32_t id_s = idesc_f8(128, C::kNS, 0, 0);
-    const uint32_t id_o = idesc_f8(128, C::kNO, 1, 1);
+    // weights: all terms at once, or the last one apart (E5M2: bit 10)
+    const uint32_t id_o = idesc_f8(128, C::kHalfWeights ? 2 * R : C::kNO, 1, 1);
+    const uint32_t id_lo = idesc_f8(128, R < 16 ? 16 : R, 1, 1) | (1u << 10);
     const uint64_t dk0 = smem_desc(smem_u32(sm.k[0]), 0, sbo, lay);
     const uint64_t dq = smem_desc(smem_u32(sm.q), 0, sbo, lay);
-    // head dim 64: M = 128 takes a second 64-row atom; it reads the tile of K
-    // that lies behind V's, into lanes 64 .. 127 of O^T, which nobody reads
-    const uint64_t dv0 = smem_desc(
-        smem_u32(sm.v[0]), DIM == 64 ? smem_u32(sm.k[0]) - smem_u32(sm.v[0]) : 0, sbo, lay);
+    // head dim 64: M = 128 takes a second 64-row atom; it reads the bytes one
+    // tile on (V's next stage or K's first), into lanes 64 .. 127 of O^T, which
+    // nobody reads
+    const uint64_t dv0 =
+        smem_desc(smem_u32(sm.v[0]), DIM == 64 ? C::kTileBytes : 0, sbo, lay);
     // P^T: MN-major, atoms of 32 columns x 8 keys, 4,096 bytes from one set of
     // 32 columns to the next
-    const uint64_t dp0 = smem_desc(smem_u32(sm.p[0]), 4096, 256, kLayoutSW32);
+    const uint64_t dp0 = smem_desc(smem_u32(sm.p), 4096, 256, kLayoutSW32);
     constexpr uint32_t kStep = C::kTileBytes / 16;
     int tc = 0, nlive = 0;
     bool ok = true;
@@ -566,18 +650,18 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       if (nt <= 0) continue;
       // S^T of tile t of the segment
       auto issue_s = [&](int t) {
-        const int st = (tc + t) % C::kStages, sb = (tc + t) & 1;
+        const int x = tc + t, st = x % C::kKS, sb = x & 1;
 #pragma unroll
         for (int ks = 0; ks < DIM / 32; ++ks)
           mma_f8_w(tmem + sb * C::kNS, dk0 + st * kStep + 2 * ks, dq + 2 * ks, id_s, ks > 0);
         tc_commit_w(smem_u32(&sm.s_full[sb]));
+        if (C::kSplit) tc_commit_w(smem_u32(&sm.k_empty[st]));
       };
-      auto wait_full = [&](int t) {
+      auto wait_k = [&](int t) {
         const int x = tc + t;
-        return mbar_wait_w_ab(smem_u32(&sm.full[x % C::kStages]), (x / C::kStages) & 1,
-                              &sm.abort);
+        return mbar_wait_w_ab(smem_u32(&sm.k_full[x % C::kKS]), (x / C::kKS) & 1, &sm.abort);
       };
-      ok = mbar_wait_w_ab(smem_u32(&sm.q_full), nlive & 1, &sm.abort) && wait_full(0);
+      ok = mbar_wait_w_ab(smem_u32(&sm.q_full), nlive & 1, &sm.abort) && wait_k(0);
       if (!ok) break;
       tc_fence_after();
       issue_s(0);
@@ -586,30 +670,34 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         bool ahead = false;
         if (t + 1 < nt) {
           const int x = tc + t + 1;
-          ahead = __all_sync(0xffffffffu, mbar_test(smem_u32(&sm.full[x % C::kStages]),
-                                                    (x / C::kStages) & 1));
+          ahead = __all_sync(0xffffffffu,
+                             mbar_test(smem_u32(&sm.k_full[x % C::kKS]), (x / C::kKS) & 1));
           if (ahead) {
             tc_fence_after();
             issue_s(t + 1);
           }
         }
-        const int x = tc + t;
+        const int x = tc + t, st = x % C::kVS;
         ok = mbar_wait_w_ab(smem_u32(&sm.p_full[x & 1]), (x >> 1) & 1, &sm.abort);
+        if (C::kSplit && ok)
+          ok = mbar_wait_w_ab(smem_u32(&sm.v_full[st]), (x / C::kVS) & 1, &sm.abort);
         // O^T of the segment before has been read
         if (ok && t == 0 && nlive > 0)
           ok = mbar_wait_w_ab(smem_u32(&sm.o_empty), (nlive - 1) & 1, &sm.abort);
         if (!ok) break;
         tc_fence_after();
-        const int st = x % C::kStages;
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_f8_w(tmem + C::kColO, dv0 + st * kStep + ks * (32 * DIM / 16),
-                   dp0 + (x % C::kPBufs) * (C::kAtoms * 4096 / 16) + ks * (1024 / 16), id_o,
-                   t > 0 || ks > 0);
-        tc_commit_w(smem_u32(&sm.empty[st]));
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint64_t dv = dv0 + st * kStep + ks * (32 * DIM / 16);
+          const uint64_t dp = dp0 + ks * (1024 / 16);
+          mma_f8_w(tmem + C::kColO, dv, dp, id_o, t > 0 || ks > 0);
+          if (C::kHalfWeights)
+            mma_f8_w(tmem + C::kColO + 2 * R, dv, dp + 2 * (4096 / 16), id_lo, t > 0 || ks > 0);
+        }
         tc_commit_w(smem_u32(&sm.pv_done[x & 1]));
+        tc_commit_w(smem_u32(&sm.v_empty[st]));
         if (t + 1 < nt && !ahead) {
-          ok = wait_full(t + 1);
+          ok = wait_k(t + 1);
           if (!ok) break;
           tc_fence_after();
           issue_s(t + 1);
@@ -658,13 +746,14 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const bool live = tid < rows;
         sm.pos[tid] = live ? sg.start + i : -1;
         sm.orow[tid] = live ? (sg.s + i) * g.H + hq : -1;
-        sm.nref[tid] = kShift;
+        sm.nref[tid] = C::kShift;
         sm.has[tid] = 0;
       }
       if (nt > 0) {
         queries.split(sm.q, sm.qf, g.scale_log2, tid);
         fence_proxy_async_smem();
-        mbar_arrive(smem_u32(&sm.q_full));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
       sync();  // row tables
       float2 l[RW / 2];
@@ -676,23 +765,29 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       const int all_pieces = g.page_size >= 128 ? 1 : (1 << (128 / g.page_size)) - 1;
 
       for (int t = 0; t < nt; ++t, ++tc) {
-        const int st = tc % C::kStages, buf = tc & 1;
+        const int ss = tc % C::kSS, buf = tc & 1;
         const int k0 = tile_of(sg, sg.i0 + t) * 128, key = k0 + key_in;
         ok = mbar_wait_w_ab(smem_u32(&sm.s_full[buf]), (tc >> 1) & 1, &sm.abort);
-        // the scale bytes: landed before the scores could be computed
-        ok = ok && mbar_wait_w_ab(smem_u32(&sm.full[st]), (tc / C::kStages) & 1, &sm.abort);
+        // the scale bytes (a split ring's K barrier may be two phases on by now)
+        ok = ok && mbar_wait_w_ab(smem_u32(C::kSplit ? &sm.sc_full[ss] : &sm.k_full[ss]),
+                                  (tc / C::kSS) & 1, &sm.abort);
+        const int eb = sm.vs[ss][key_in];
+        const float kf = pow2_byte(sm.ks[ss][key_in]);
+        const int loaded = sm.loaded[ss];
         if (!ok) sm.stop[buf] = 1;
         tc_fence_after();
-        const int eb = sm.vs[st][key_in];
-        const float kf = pow2_byte(sm.ks[st][key_in]);
         // keys that not every row sees
-        const int loaded = sm.loaded[st];
         const bool whole = loaded == all_pieces && k0 + 127 <= pf &&
                            (g.window == 0 || k0 > pl - g.window || k0 + 127 < g.sinks);
         bool any = true;        // some row sees the key
         uint32_t seen = ~0u;    // of this thread's rows
         bool nan = false;
         if (!whole) {
+          const int st = tc % C::kVS;
+          if (C::kSplit && !mbar_wait_w_ab(smem_u32(&sm.v_full[st]), (tc / C::kVS) & 1, &sm.abort)) {
+            ok = false;
+            sm.stop[buf] = 1;
+          }
           const bool here = (loaded >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
           const bool first = g.window == 0 || key < g.sinks;
           any = here && key <= pl && (first || key > pf - g.window);
@@ -730,70 +825,83 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const int ev = any ? eb - 127 : -127;
         int evc = max(ev, e0 - kLow);
         float2 y[RW / 2];
-        auto scores = [&]() {
-          const float2 kf2 = make_float2(kf, kf);
-          const float evf = static_cast<float>(evc);
-          const float2 ev2 = make_float2(evf, evf), lo2 = make_float2(0.0625f, 0.0625f);
+        // Usually one pass over the scores and a vote that the references hold.
+        // If they do not, or on an item's first tile, E0 moves (before pass 1)
+        // and then the rows' references (before pass 2), and the scores are
+        // taken again.
+        int rise = 0;
+        bool broken = false;
+#pragma unroll 1
+        for (int pass = t == 0 ? 1 : 0;; ++pass) {
+          if (pass == 1) {
+            if (t == 0) {
+              vote(false);
+              if (sm.stop[buf]) {
+                broken = true;
+                break;
+              }
+            }
+            const int em = __reduce_max_sync(0xffffffffu, ev + 127);
+            if (lane == 0) sm.rede[warp] = em;
+            // rows without a reference are measured from 0
+            if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = C::kShift;
+            sync();
+            int top = -127;
 #pragma unroll
-          for (int c = 0; c < RW; c += 8) {
-            uint32_t h[8], lo[8];
-            tmem_ld8(tmem + lanes + buf * C::kNS + r0 + c, h);
-            tmem_ld8(tmem + lanes + buf * C::kNS + R + r0 + c, lo);
-            tmem_ld_wait();
+            for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
+            if (t == 0) {
+              e0 = top;
+            } else if (top > e0 + kHigh) {
+              rise = top - e0;
+              e0 = top;
+            }
+            evc = max(ev, e0 - kLow);
+          }
+          {
+            const float2 kf2 = make_float2(kf, kf);
+            const float evf = static_cast<float>(evc);
+            const float2 ev2 = make_float2(evf, evf), lo2 = make_float2(0.0625f, 0.0625f);
 #pragma unroll
-            for (int r = 0; r < 8; r += 4) {
-              const float4 qf = *reinterpret_cast<const float4*>(sm.qf + r0 + c + r);
-              const float4 nr = *reinterpret_cast<const float4*>(sm.nref + r0 + c + r);
-              const float2 a = __ffma2_rn(as_f2(lo[r], lo[r + 1]), lo2, as_f2(h[r], h[r + 1]));
-              const float2 b =
-                  __ffma2_rn(as_f2(lo[r + 2], lo[r + 3]), lo2, as_f2(h[r + 2], h[r + 3]));
-              y[(c + r) / 2] = __ffma2_rn(a, __fmul2_rn(kf2, make_float2(qf.x, qf.y)),
-                                          __fadd2_rn(ev2, make_float2(nr.x, nr.y)));
-              y[(c + r) / 2 + 1] = __ffma2_rn(b, __fmul2_rn(kf2, make_float2(qf.z, qf.w)),
-                                              __fadd2_rn(ev2, make_float2(nr.z, nr.w)));
+            for (int c = 0; c < RW; c += 8) {
+              uint32_t h[8], lo[8];
+              tmem_ld8(tmem + lanes + buf * C::kNS + r0 + c, h);
+              tmem_ld8(tmem + lanes + buf * C::kNS + R + r0 + c, lo);
+              tmem_ld_wait();
+#pragma unroll
+              for (int r = 0; r < 8; r += 4) {
+                const float4 qf = *reinterpret_cast<const float4*>(sm.qf + r0 + c + r);
+                const float4 nr = *reinterpret_cast<const float4*>(sm.nref + r0 + c + r);
+                const float2 a = __ffma2_rn(as_f2(lo[r], lo[r + 1]), lo2, as_f2(h[r], h[r + 1]));
+                const float2 b =
+                    __ffma2_rn(as_f2(lo[r + 2], lo[r + 3]), lo2, as_f2(h[r + 2], h[r + 3]));
+                y[(c + r) / 2] = __ffma2_rn(a, __fmul2_rn(kf2, make_float2(qf.x, qf.y)),
+                                            __fadd2_rn(ev2, make_float2(nr.x, nr.y)));
+                y[(c + r) / 2 + 1] = __ffma2_rn(b, __fmul2_rn(kf2, make_float2(qf.z, qf.w)),
+                                                __fadd2_rn(ev2, make_float2(nr.z, nr.w)));
+              }
+            }
+            if (!whole) {
+              const float nv = __uint_as_float(0x7FC00000u);
+#pragma unroll
+              for (int r = 0; r < RW; r += 2) {
+                y[r / 2].x = !((seen >> r) & 1) ? -INFINITY : nan ? nv : y[r / 2].x;
+                y[r / 2].y = !((seen >> (r + 1)) & 1) ? -INFINITY : nan ? nv : y[r / 2].y;
+              }
             }
           }
-          if (!whole) {
-            const float nv = __uint_as_float(0x7FC00000u);
+          if (pass == 2) break;
+          if (pass == 0) {
+            float mx = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < RW; r += 2) {
-              y[r / 2].x = !((seen >> r) & 1) ? -INFINITY : nan ? nv : y[r / 2].x;
-              y[r / 2].y = !((seen >> (r + 1)) & 1) ? -INFINITY : nan ? nv : y[r / 2].y;
+            for (int r = 0; r < RW / 2; ++r) mx = fmax3(mx, y[r].x, y[r].y);
+            const bool move = vote(mx > C::kShift + C::kSlack || ev > e0 + kHigh);
+            if (sm.stop[buf]) {  // the same for all: written before the barrier
+              broken = true;
+              break;
             }
+            if (!move) break;
+            continue;
           }
-        };
-        // do the references hold?
-        bool over = t == 0;
-        if (t > 0) {
-          scores();
-          float mx = -INFINITY;
-#pragma unroll
-          for (int r = 0; r < RW / 2; ++r) mx = fmax3(mx, y[r].x, y[r].y);
-          over = mx > kShift + kSlack || ev > e0 + kHigh;
-        }
-        const bool move = vote(over);
-        if (sm.stop[buf]) {  // the same for all: written before the barrier
-          ok = false;
-          break;
-        }
-        if (move) {
-          // E0, then the rows' references
-          const int em = __reduce_max_sync(0xffffffffu, ev + 127);
-          if (lane == 0) sm.rede[warp] = em;
-          // rows without a reference are measured from 0
-          if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = kShift;
-          sync();
-          int top = -127, rise = 0;
-#pragma unroll
-          for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
-          if (t == 0) {
-            e0 = top;
-          } else if (top > e0 + kHigh) {
-            rise = top - e0;
-            e0 = top;
-          }
-          evc = max(ev, e0 - kLow);
-          scores();
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             const float a = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
@@ -806,17 +914,17 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             // A row keeps its reference while it holds; one that has seen
             // nothing (or nothing but NaN) has none.  If E0 rose by more than
             // 40, the references follow, so that l (whose terms are at most
-            // 2^(kShift + kSlack + kLow + rise)) stays inside float32.
+            // 2^(8 + kLow + rise)) stays inside float32.
             const float n0 = sm.nref[tid];
             float n1 = n0, f = 1.f, fl = 1.f;
             if (tid >= rows) {
               n1 = -kUnset;
             } else if (!sm.has[tid]) {
               const bool now = a > -INFINITY;
-              n1 = now ? n0 - ceilf(a - kShift) : kUnset;
+              n1 = now ? n0 - ceilf(a - C::kShift) : kUnset;
               sm.has[tid] = now;
             } else {
-              const float up = fmaxf(a > kShift + kSlack ? ceilf(a - kShift) : 0.f,
+              const float up = fmaxf(a > C::kShift + C::kSlack ? ceilf(a - C::kShift) : 0.f,
                                      static_cast<float>(rise - 40));
               const float by = fmaxf(up, 0.f);
               n1 = n0 - by;
@@ -840,23 +948,23 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               sm.stop[buf ^ 1] = 1;
             }
             tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 3 * RW; c += 8) {
+              const int col = c / RW * R + r0 + c % RW;
+              uint32_t a[8];
+              tmem_ld8(tmem + lanes + C::kColO + col, a);
+              tmem_ld_wait();
 #pragma unroll
-            for (int term = 0; term < 3; ++term) {
-#pragma unroll
-              for (int c = 0; c < RW; c += 8) {
-                uint32_t a[8];
-                const uint32_t at = tmem + lanes + C::kColO + term * R + r0 + c;
-                tmem_ld8(at, a);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  a[i] = __float_as_uint(__uint_as_float(a[i]) * sm.fac[r0 + c + i]);
-                tmem_st8(at, a);
-              }
+              for (int i = 0; i < 8; ++i)
+                a[i] = __float_as_uint(__uint_as_float(a[i]) * sm.fac[r0 + c % RW + i]);
+              tmem_st8(tmem + lanes + C::kColO + col, a);
             }
             tmem_st_wait();
           }
-          scores();
+        }
+        if (broken) {
+          ok = false;
+          break;
         }
         // weights and their E4M3 terms, 4 rows a word
         const float gl = ex2_approx(static_cast<float>(e0 - evc));
@@ -875,27 +983,37 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             b.x *= z;
             b.y *= z;
           }
-          const float2 n32 = make_float2(-32.f, -32.f), p32 = make_float2(32.f, 32.f);
+          if constexpr (C::kHalfWeights) {
+            uint32_t ha = half2_of(a), hb = half2_of(b);
 #pragma unroll
-          for (int term = 0; term < 3; ++term) {
-            const uint32_t ca = cvt_e4m3x2(a.x, a.y), cb = cvt_e4m3x2(b.x, b.y);
-            tw[term][r / 4] = ca | (cb << 16);
-            if (term < 2) {  // 32 (w - h), exact
-              a = __ffma2_rn(e4m3x2_to_float2(ca), n32, __fmul2_rn(a, p32));
-              b = __ffma2_rn(e4m3x2_to_float2(cb), n32, __fmul2_rn(b, p32));
+            for (int term = 0; term < 2; ++term) {
+              const uint32_t ca = e4m3x2_of_half2(ha), cb = e4m3x2_of_half2(hb);
+              tw[term][r / 4] = ca | (cb << 16);
+              ha = residual32(ha, ca);
+              hb = residual32(hb, cb);
+            }
+            tw[2][r / 4] = e5m2x2_of_half2(ha) | (e5m2x2_of_half2(hb) << 16);
+          } else {
+            const float2 n32 = make_float2(-32.f, -32.f), p32 = make_float2(32.f, 32.f);
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              const uint32_t ca = cvt_e4m3x2(a.x, a.y), cb = cvt_e4m3x2(b.x, b.y);
+              tw[term][r / 4] = ca | (cb << 16);
+              if (term < 2) {  // 32 (w - h), exact
+                a = __ffma2_rn(e4m3x2_to_float2(ca), n32, __fmul2_rn(a, p32));
+                b = __ffma2_rn(e4m3x2_to_float2(cb), n32, __fmul2_rn(b, p32));
+              }
             }
           }
         }
-        // the product that last read this buffer of P^T
-        if (tc >= C::kPBufs) {
-          const int x = tc - C::kPBufs;
-          if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[x & 1]), (x >> 1) & 1, &sm.abort)) {
-            late = true;
-            sm.stop[buf ^ 1] = 1;
-          }
+        // the product before has read P^T
+        if (tc >= 1 &&
+            !mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort)) {
+          late = true;
+          sm.stop[buf ^ 1] = 1;
         }
         // P^T: key rows of 32 columns (32 bytes), 16-byte chunks swizzled
-        const uint32_t pb = smem_u32(sm.p[tc % C::kPBufs]) + key_in * 32;
+        const uint32_t pb = smem_u32(sm.p) + key_in * 32;
         const uint32_t sw = ((key_in >> 2) & 1) * 16;
         if constexpr (R == 8) {
           sts128(pb + sw, tw[0][0], tw[0][1], tw[1][0], tw[1][1]);
@@ -910,7 +1028,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(smem_u32(&sm.p_full[buf]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[buf]));
       }
       if (!ok) break;
 
@@ -972,11 +1091,11 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           }
         }
       }
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[ns % kSegSlots]));
-      if (nt > 0) {
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sm.o_empty));
+      if (lane == 0) {
+        if (nt > 0) mbar_arrive(smem_u32(&sm.o_empty));
+        mbar_arrive(smem_u32(&sm.seg_empty[ns % kSegSlots]));
       }
     }
     if (!ok) sm.abort = 1;
@@ -992,53 +1111,65 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 
 // Joins the parts of an item that several CTAs shared (part 0 in slot 1 of the
 // CTA before, the others in slots 0 from this CTA on): o = sum 2^(lg_p - lg) o_p.
+// One warp a row, without shared memory, so that blocks fit beside the first
+// kernel's CTAs and are there when it ends.
 template <int DIM, int R>
-__global__ void __launch_bounds__(8 * DIM) join_kernel(const AttendArgs g) {
-  __shared__ float s_wt[8][kMaxCtas];
+__global__ void __launch_bounds__(256) join_kernel(const AttendArgs g) {
+  constexpr int E = DIM / 32;  // elements a lane
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 j0 = g.joins[2 * blockIdx.x], j1 = g.joins[2 * blockIdx.x + 1];
   const int parts = j0.x;
-  if (parts <= 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x, first = blockIdx.y * 8;
-  auto slot = [&](int p) {
-    return static_cast<size_t>(p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + p - 1));
+  if (parts <= 0 || r >= static_cast<long long>(j0.z) * g.G - j1.x) return;
+  const int c0 = blockIdx.x;
+  auto at = [&](int p) {  // the part's row
+    return static_cast<size_t>(p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + p - 1)) * R + r;
   };
-  const int rows = static_cast<int>(
-      min(static_cast<long long>(R), static_cast<long long>(j0.z) * g.G - j1.x));
-  if (warp < 8 && first + warp < rows) {
-    const int r = first + warp;
-    float m = -INFINITY;
-    for (int p = lane; p < parts; p += 32) {
-      const float x = g.stats[slot(p) * R + r];
-      m = x > m || x != x ? x : m;
-    }
+  float m = -INFINITY;
+  for (int p = lane; p < parts; p += 32) {
+    const float x = g.stats[at(p)];
+    m = x > m || x != x ? x : m;
+  }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float x = __shfl_xor_sync(0xffffffffu, m, o);
-      m = x > m || x != x ? x : m;  // NaN stays
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int p = lane; p < parts; p += 32) l += exp2f(g.stats[slot(p) * R + r] - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int p = lane; p < parts; p += 32)
-      s_wt[warp][p] = exp2f(g.stats[slot(p) * R + r] - ref) * inv;
-    if (lane == 0 && g.lse != nullptr) {
-      const int i = (j1.x + r) / g.G, hq = j0.w * g.G + (j1.x + r) % g.G;
-      g.lse[static_cast<size_t>(hq) * g.T + j0.y + i] = (ref + log2f(l)) * kLn2;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, m, o);
+    m = x > m || x != x ? x : m;  // NaN stays
+  }
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[E] = {};
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    const float wt = p0 + lane < parts ? exp2f(g.stats[at(p0 + lane)] - ref) : 0.f;
+    l += wt;
+    const int n = min(32, parts - p0);
+#pragma unroll 8
+    for (int p = 0; p < n; ++p) {
+      const float w = __shfl_sync(0xffffffffu, wt, p);
+      const float* x = g.partial + at(p0 + p) * DIM + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(x);
+        acc[0] = fmaf(w, v.x, acc[0]);
+        acc[1] = fmaf(w, v.y, acc[1]);
+        acc[2] = fmaf(w, v.z, acc[2]);
+        acc[3] = fmaf(w, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(x);
+        acc[0] = fmaf(w, v.x, acc[0]);
+        acc[1] = fmaf(w, v.y, acc[1]);
+      }
     }
   }
-  __syncthreads();
-  const int rl = threadIdx.x / DIM, dd = threadIdx.x % DIM, r = first + rl;
-  if (r >= rows) return;
-  float acc = 0.f;
-#pragma unroll 8
-  for (int p = 0; p < parts; ++p) acc += s_wt[rl][p] * g.partial[(slot(p) * R + r) * DIM + dd];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = (j1.x + r) / g.G, hq = j0.w * g.G + (j1.x + r) % g.G;
-  g.o[(static_cast<size_t>(j0.y + i) * g.H + hq) * DIM + dd] = __float2bfloat16(acc);
+  if (lane == 0 && g.lse != nullptr)
+    g.lse[static_cast<size_t>(hq) * g.T + j0.y + i] = (ref + log2f(l)) * kLn2;
+  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(
+      g.o + (static_cast<size_t>(j0.y + i) * g.H + hq) * DIM + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    out[e / 2] = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e] * inv,
+                                       inv == 0.f ? 0.f : acc[e + 1] * inv);
 }
 
 // ------------------------------------------------------------------ host
@@ -1096,7 +1227,7 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
   if (g.whole) return FLAMIA_OK;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, R / 8);
-  cfg.blockDim = dim3(8 * DIM);
+  cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

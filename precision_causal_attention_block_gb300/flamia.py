@@ -240,45 +240,59 @@ def flamia_attn_bwd_gqa(q: QTensor, k: QTensor, v: QTensor, dout: QTensor, D, ls
                                       _stream()), "flamia_attn_bwd_gqa")
 
 
-def _rows(x, name, heads=None, d=None, out=False):
+_BF16, _I32 = torch.bfloat16, torch.int32
+
+
+def _current():
+    """(device index, raw stream) that a call's tensors have to be on and its work goes to."""
+    if not torch.cuda.is_initialized():
+        return -2, 0  # no tensor is there (CPU tensors answer -1)
+    d = torch._C._cuda_getDevice()
+    return d, torch._C._cuda_getCurrentRawStream(d)
+
+
+def _elsewhere(name):
+    raise RuntimeError(f"{name}: flamia needs tensors on the current CUDA device")
+
+
+def _rows(x, name, T, heads, d, dev, out=False):
     """(pointer, token stride in elements) of BF16 rows [T, heads, d]: any
     token stride, the heads of a token side by side."""
-    if x.dtype is not torch.bfloat16 or x.dim() != 3:
+    if x.dtype is not _BF16 or x.dim() != 3:
         raise RuntimeError(f"{name}: flamia needs BF16 rows [T, heads, d]")
-    T, h, n = x.shape
-    if (heads is not None and h != heads) or (d is not None and n != d):
-        raise RuntimeError(f"{name}: shape {tuple(x.shape)}, expected [T, {heads}, {d}]")
-    stride, sh, sd = x.stride()
-    if sd != 1 or (h > 1 and sh != n):
+    t, h, n = x.shape
+    if t != T or h != heads or n != d:
+        raise RuntimeError(f"{name}: shape {tuple(x.shape)}, expected {(T, heads, d)}")
+    stride = h * n
+    if t > 1 and not x.is_contiguous():
+        stride, sh, sd = x.stride()
+        if sd != 1 or (h > 1 and sh != n):
+            raise RuntimeError(f"{name}: the heads of a token must be contiguous")
+        if out and stride < h * n:
+            raise RuntimeError(f"{name}: an output's rows must not overlap")
+    elif t <= 1 and not x.is_contiguous():  # (whatever the stride of a single token)
         raise RuntimeError(f"{name}: the heads of a token must be contiguous")
-    if T <= 1:
-        stride = h * n
-    elif out and stride < h * n:
-        raise RuntimeError(f"{name}: an output's rows must not overlap")
-    return _on_device(x, name), stride
+    if x.get_device() != dev:
+        _elsewhere(name)
+    return x.data_ptr(), stride
 
 
-def _on_device(t, name):
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise RuntimeError(f"{name}: flamia needs tensors on the current CUDA device")
-    return t.data_ptr()
-
-
-def _ints(t, name, numel=None):
+def _ints(t, name, numel, dev):
     """Pointer of a contiguous int32 tensor (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not torch.int32 or not t.is_contiguous():
-        raise RuntimeError(f"{name}: flamia needs contiguous int32 tensors")
-    if numel is not None and t.numel() != numel:
-        raise RuntimeError(f"{name}: {t.numel()} entries, expected {numel}")
-    return _on_device(t, name)
+    if t.dtype is not _I32 or not t.is_contiguous() or (numel and t.numel() != numel):
+        raise RuntimeError(f"{name}: expected a contiguous int32 tensor"
+                           + (f" of {numel} entries" if numel else ""))
+    if t.get_device() != dev:
+        _elsewhere(name)
+    return t.data_ptr()
 
 
-def _page_table(t, nseq):
+def _page_table(t, nseq, dev):
     if t.dim() != 2 or t.shape[0] != nseq:
         raise RuntimeError(f"page_table: shape {tuple(t.shape)}, expected [{nseq}, pages]")
-    return _ints(t, "page_table")
+    return _ints(t, "page_table", 0, dev)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0,
@@ -338,24 +352,27 @@ class Rotary:
 
 def flamia_rope(q_in, q_out, k_in, k_out, rotary: Rotary, cu_seqlens, starts=None,
                 inverse: bool = False, dev_status=None):
+    dev, stream = _current()
+    if q_in.dim() != 3:
+        raise RuntimeError("q_in: flamia needs BF16 rows [T, heads, d]")
     T, H, d = q_in.shape
-    qi, qis = _rows(q_in, "q_in")
-    qo, qos = _rows(q_out, "q_out", H, d, out=True)
+    qi, qis = _rows(q_in, "q_in", T, H, d, dev)
+    qo, qos = _rows(q_out, "q_out", T, H, d, dev, True)
     H_kv, ki, kis, ko, kos = 0, None, 0, None, 0
-    if q_out.shape[0] != T:
-        raise RuntimeError("q_out: another number of rows than q_in")
     if k_in is not None:
         H_kv = k_in.shape[1]
-        ki, kis = _rows(k_in, "k_in", H_kv, d)
-        ko, kos = _rows(k_out, "k_out", H_kv, d, out=True)
-        if k_in.shape[0] != T or k_out.shape[0] != T:
-            raise RuntimeError("k: another number of rows than q")
+        ki, kis = _rows(k_in, "k_in", T, H_kv, d, dev)
+        ko, kos = _rows(k_out, "k_out", T, H_kv, d, dev, True)
     n = cu_seqlens.numel() - 1
-    _check(load().flamia_rope(
-        qi, qo, qis, qos, ki, ko, kis, kos, T, H, H_kv, d, _on_device(rotary.turns, "turns"),
+    if rotary.turns.get_device() != dev:
+        _elsewhere("turns")
+    st = (_LIB or load()).flamia_rope(
+        qi, qo, qis, qos, ki, ko, kis, kos, T, H, H_kv, d, rotary.turns.data_ptr(),
         rotary.rot_dim, rotary.mscale, rotary.flags | (FLAG_ROPE_INVERSE if inverse else 0),
-        _ints(cu_seqlens, "cu_seqlens"), n, _ints(starts, "starts", n),
-        _ints(dev_status, "dev_status"), _stream()), "flamia_rope")
+        _ints(cu_seqlens, "cu_seqlens", 0, dev), n, _ints(starts, "starts", n, dev),
+        _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_rope")
 
 
 class KVCache:
@@ -398,7 +415,9 @@ class KVCache:
                                      v_scales.data_ptr(), self.num_pages, self.page_size,
                                      self.H_kv, self.d)
         self._ref = ctypes.byref(self._struct)
-        self._ws = None
+        self.device_index = k_codes.get_device()
+        # attend's workspace, and the sizes that it was last found large enough for
+        self._ws, self._ws_key = None, None
 
     def write(self, k, v, cu_seqlens, starts, page_table, dev_status=None):
         """Quantises rows k, v [T, H_kv, d] into positions starts[b] .. of each
@@ -427,10 +446,13 @@ class KVCache:
         if lse is None:
             lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         if ws is None:
-            need = flamia_attn_cache_workspace_bytes(T, cu_seqlens.numel() - 1, H, self.H_kv,
-                                                     self.d)
-            if self._ws is None or self._ws.numel() < need:
-                self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
+            key = (T, cu_seqlens.numel(), H)
+            if key != self._ws_key:
+                need = flamia_attn_cache_workspace_bytes(T, cu_seqlens.numel() - 1, H, self.H_kv,
+                                                         self.d)
+                if self._ws is None or self._ws.numel() < need:
+                    self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
+                self._ws_key = key
             ws = self._ws
         flamia_attn_cache(self, q, cu_seqlens, starts, page_table, softmax_scale, window, sinks, o,
                           lse, ws, dev_status)
@@ -438,31 +460,35 @@ class KVCache:
 
 
 def flamia_cache_write(cache: KVCache, k, v, cu_seqlens, starts, page_table, dev_status=None):
-    kp, ks = _rows(k, "k", cache.H_kv, cache.d)
-    vp, vs = _rows(v, "v", cache.H_kv, cache.d)
-    n = cu_seqlens.numel() - 1
-    if v.shape[0] != k.shape[0]:
-        raise RuntimeError("v: another number of rows than k")
-    _on_device(cache.k_codes, "cache")
-    _check(load().flamia_cache_write(
-        cache._ref, kp, ks, vp, vs, k.shape[0], _ints(cu_seqlens, "cu_seqlens"), n,
-        _ints(starts, "starts", n), _page_table(page_table, n), page_table.shape[1],
+    dev, stream = _current()
+    T, n = k.shape[0], cu_seqlens.numel() - 1
+    kp, ks = _rows(k, "k", T, cache.H_kv, cache.d, dev)
+    vp, vs = _rows(v, "v", T, cache.H_kv, cache.d, dev)
+    if cache.device_index != dev:
+        _elsewhere("cache")
+    st = (_LIB or load()).flamia_cache_write(
+        cache._ref, kp, ks, vp, vs, T, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
+        _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
         FORMAT_TOKEN_SCALES if cache.token_scales else FORMAT_MXFP8,
-        _ints(dev_status, "dev_status"), _stream()), "flamia_cache_write")
+        _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_cache_write")
 
 
 def flamia_cache_read(cache: KVCache, k_out, v_out, cu_seqlens, starts, page_table,
                       dev_status=None):
-    kp, ks = _rows(k_out, "k_out", cache.H_kv, cache.d, out=True)
-    vp, vs = _rows(v_out, "v_out", cache.H_kv, cache.d, out=True)
-    n = cu_seqlens.numel() - 1
-    if v_out.shape[0] != k_out.shape[0]:
-        raise RuntimeError("v_out: another number of rows than k_out")
-    _on_device(cache.k_codes, "cache")
-    _check(load().flamia_cache_read(
-        cache._ref, kp, ks, vp, vs, k_out.shape[0], _ints(cu_seqlens, "cu_seqlens"), n,
-        _ints(starts, "starts", n), _page_table(page_table, n), page_table.shape[1],
-        _ints(dev_status, "dev_status"), _stream()), "flamia_cache_read")
+    dev, stream = _current()
+    T, n = k_out.shape[0], cu_seqlens.numel() - 1
+    kp, ks = _rows(k_out, "k_out", T, cache.H_kv, cache.d, dev, True)
+    vp, vs = _rows(v_out, "v_out", T, cache.H_kv, cache.d, dev, True)
+    if cache.device_index != dev:
+        _elsewhere("cache")
+    st = (_LIB or load()).flamia_cache_read(
+        cache._ref, kp, ks, vp, vs, T, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
+        _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
+        _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_cache_read")
 
 
 def flamia_attn_cache_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: int) -> int:
@@ -471,21 +497,30 @@ def flamia_attn_cache_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: 
 
 def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax_scale, window,
                       sinks, o, lse, ws, dev_status=None):
+    dev, stream = _current()
+    if q.dim() != 3:
+        raise RuntimeError("q: flamia needs BF16 rows [T, heads, d]")
     T, H, d = q.shape
-    qp, qs = _rows(q, "q", None, cache.d)
+    qp, qs = _rows(q, "q", T, H, cache.d, dev)
     n = cu_seqlens.numel() - 1
-    if o.dtype is not torch.bfloat16 or o.shape != q.shape or not o.is_contiguous():
+    if o.dtype is not _BF16 or o.shape != q.shape or not o.is_contiguous():
         raise RuntimeError("o: expected contiguous BF16 of q's shape")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (H, T)
-                            or not lse.is_contiguous()):
-        raise RuntimeError("lse: expected contiguous float32 [H, T]")
-    _on_device(cache.k_codes, "cache")
-    _check(load().flamia_attn_cache(
-        cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens"), n, _ints(starts, "starts", n),
-        _page_table(page_table, n), page_table.shape[1], softmax_scale, window, sinks,
-        _on_device(o, "o"), None if lse is None else _on_device(lse, "lse"),
-        _on_device(ws, "ws"), ws.numel() * ws.element_size(), _ints(dev_status, "dev_status"),
-        _stream()), "flamia_attn_cache")
+    lp = None
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
+            raise RuntimeError("lse: expected contiguous float32 [H, T]")
+        lp = lse.data_ptr()
+        if lse.get_device() != dev:
+            _elsewhere("lse")
+    if cache.device_index != dev or o.get_device() != dev or ws.get_device() != dev:
+        _elsewhere("cache, o and ws")
+    st = (_LIB or load()).flamia_attn_cache(
+        cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
+        _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
+        softmax_scale, window, sinks, o.data_ptr(), lp, ws.data_ptr(), ws.nbytes,
+        _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_attn_cache")
 
 
 def flamia_debug_tmem_ldred(x, vals, mx):

@@ -78,17 +78,25 @@ class Pair:
                 assert np.array_equal(got, want[:n]), (name, b)
 
 
-def attend_tolerance(q, k, v, scale, n_keys, o):
+def weight_error(T, nseq, G):
+    """Relative rounding of a softmax weight: three E4M3 terms of 4 bits hold it
+    to 2^-14; items of 32 rows (more than 16 rows a sequence and K / V head on
+    average) round it to FP16 first, half a step of which is 2^-11, and its terms
+    hold those 11 bits (E4M3, E4M3 and the 3 bits of E5M2)."""
+    return 2.0 ** -11 if -(-T // nseq) * G > 16 else 2.0 ** -14
+
+
+def attend_tolerance(q, k, v, scale, n_keys, o, weight):
     """How far an output of the cached attention may be off, elementwise: its BF16
     rounding (half a step, 2^-8 of the value) and, times the largest value seen,
     the relative error of the softmax weights.  A score is off by at most
     2^-19.5 + 2^-17 of scale |q| |k| (the query's split into E4M3 terms; float32
-    sums of d exact products), taken as 2^-16; a weight by twice that, 2^-14 for
-    its own split into E4M3 terms and 2^-24 of the largest weight for each key
+    sums of d exact products), taken as 2^-16; a weight by twice that, by `weight`
+    (its own split into terms) and 2^-24 of the largest weight for each key
     below their range, and 2^-20 for exp2 and the sums."""
     qn = np.sqrt((q ** 2).sum(-1)).max()
     kn = np.sqrt((k ** 2).sum(-1)).max()
-    rel = 2 * 2.0 ** -16 * scale * qn * kn + 2.0 ** -14 + n_keys * 2.0 ** -24 + 2.0 ** -20
+    rel = 2 * 2.0 ** -16 * scale * qn * kn + weight + n_keys * 2.0 ** -24 + 2.0 ** -20
     return 2.0 ** -8 * np.abs(o) + 2 * rel * np.abs(v).max()
 
 
@@ -108,7 +116,8 @@ def check_attend(o, lse, pair, q, n, starts, scale, window=0, sinks=0):
         qb = q[at:at + c].double().cpu().numpy()
         k, v = pair.k.values(b)[:max(starts[b], 0) + c], pair.v.values(b)[:max(starts[b], 0) + c]
         ro, rl = S.attend(qb, k, v, starts[b], scale, window, sinks)
-        tol = attend_tolerance(qb, k, v, scale, len(k), ro)
+        tol = attend_tolerance(qb, k, v, scale, len(k), ro,
+                               weight_error(len(q), len(n), q.shape[1] // pair.gpu.H_kv))
         got, gl = o[at:at + c], lse[:, at:at + c]
         assert np.isfinite(got).all(), ("o", b)
         worst = np.max(np.abs(got - ro) / tol)

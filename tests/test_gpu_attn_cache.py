@@ -260,3 +260,61 @@ def test_rows_beyond_32_bits_of_a_large_cache(lib):
                    cache.read(offsets([600]), None, table, 600))
     for a, b in zip(*res):
         assert torch.equal(a, b)
+
+
+LONG_RUNS = [
+    # sequences, longest context, new tokens, H, H_kv, d, page, window, sinks
+    (120, 2500, 1, 16, 8, 128, 64, 0, 0),
+    (120, 2500, 1, 16, 16, 64, 32, 0, 0),
+    (90, 2500, 2, 16, 4, 128, 128, 0, 0),
+    (90, 2500, 4, 8, 2, 64, 64, 700, 4),
+    (40, 2500, 40, 8, 4, 128, 256, 0, 0),
+    (30, 2500, 70, 8, 8, 64, 64, 300, 130),
+]
+
+
+@pytest.mark.parametrize("nseq,longest,new,H,H_kv,d,page,window,sinks", LONG_RUNS)
+def test_many_tiles_a_cta(lib, nseq, longest, new, H, H_kv, d, page, window, sinks):
+    """Batches that give every CTA a run of many key tiles and several items, against
+    float64 attention (torch) of the values read back from the cache."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    from tests.serving_helpers import attend_tolerance, lse_tolerance, page_table, weight_error
+    rng = np.random.default_rng(nseq + d + new)
+    lens = [int(x) for x in np.exp(rng.uniform(np.log(new), np.log(longest), nseq))]
+    n = [int(min(c, rng.integers(1, new + 1))) for c in lens]
+    starts = [c - m for c, m in zip(lens, n)]
+    t, pages = page_table(rng, lens, page)
+    table = torch.from_numpy(t).to(DEV)
+    cache = fl.KVCache(pages, page, H_kv, d)
+    L, T = sum(lens), sum(n)
+    g = torch.Generator(device=DEV).manual_seed(nseq)
+    new_rows = lambda rows, h: torch.randn(rows, h, d, generator=g, device=DEV).to(torch.bfloat16)
+    cache.write(new_rows(L, H_kv), new_rows(L, H_kv), offsets(lens), None, table)
+    k, v = cache.read(offsets(lens), None, table, L)
+    q = new_rows(T, H)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, lse = cache.attend(q, offsets(n), i32(starts), table, d ** -0.5, window=window, sinks=sinks,
+                          dev_status=st)
+    assert int(st.item()) == 0
+    weight = weight_error(T, nseq, H // H_kv)
+    at = base = 0
+    for b in range(nseq):
+        qb = q[at:at + n[b]].double()
+        kb, vb = k[base:base + lens[b]].double(), v[base:base + lens[b]].double()
+        p = torch.arange(starts[b], lens[b], device=DEV)[:, None]
+        j = torch.arange(lens[b], device=DEV)
+        seen = j <= p
+        if window:
+            seen &= (j > p - window) | (j < sinks)
+        x = torch.einsum("ihd,jhd->hij", qb, kb.repeat_interleave(H // H_kv, 1)) * d ** -0.5
+        x = x.masked_fill(~seen, -torch.inf)
+        ref = torch.einsum("hij,jhd->ihd", torch.softmax(x, 2), vb.repeat_interleave(H // H_kv, 1))
+        rl = torch.logsumexp(x, 2).cpu().numpy()
+        qn, kn, vn, rn = (y.cpu().numpy() for y in (qb, kb, vb, ref))
+        tol = attend_tolerance(qn, kn, vn, d ** -0.5, lens[b], rn, weight)
+        err = np.abs(o[at:at + n[b]].double().cpu().numpy() - rn)
+        assert (err <= tol).all(), (b, (err / tol).max())
+        err = np.abs(lse[:, at:at + n[b]].double().cpu().numpy() - rl)
+        assert (err <= lse_tolerance(qn, kn, d ** -0.5, rl)).all(), b
+        at += n[b]
+        base += lens[b]
