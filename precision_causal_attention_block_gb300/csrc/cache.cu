@@ -36,10 +36,16 @@ struct CacheArgs {
 struct Block {
   int lo, hi;
   int h, kv;          // head, 0 = K / 1 = V
-  long long row;      // first row of the block in the codes / scales arrays
+  int page, in_page;  // its page (-1: none) and first row in it
   long long token;    // packed row of offset 0 (may lie before the document)
+  // first row in the codes / scales arrays
+  __device__ __forceinline__ long long row(const CacheArgs& g) const {
+    return (static_cast<long long>(page) * g.H_kv + h) * g.page_size + in_page;
+  }
 };
 
+// The page is looked up but not checked: a caller can have the rows' loads
+// under way before it looks (valid_page).
 __device__ __forceinline__ bool find_block(const CacheArgs& g, long long unit, int lane,
                                            Block& blk) {
   const int per = 2 * g.H_kv;
@@ -49,8 +55,8 @@ __device__ __forceinline__ bool find_block(const CacheArgs& g, long long unit, i
   blk.h = hk - blk.kv * g.H_kv;
   const int b = warp_last_not_above(
       g.ndocs, vb, lane, [&](int i) { return (__ldg(g.cu + i) >> 5) + 2 * i; });
-  const DocRange r = doc_range(g.cu, b, g.T);
   const int start = g.starts != nullptr ? __ldg(g.starts + b) : 0;
+  const DocRange r = doc_range(g.cu, b, g.T);
   if (r.e <= r.s) return false;
   if (start < 0) {
     if (lane == 0) report(g.status, FLAMIA_DEV_BAD_PAGE);
@@ -63,35 +69,55 @@ __device__ __forceinline__ bool find_block(const CacheArgs& g, long long unit, i
   blk.lo = j == 0 ? lead : 0;
   blk.hi = static_cast<int>(min(32ll, static_cast<long long>(start) + n - p0));
   const long long slot = p0 / g.page_size;
-  int page = -1;
+  blk.page = -1;
   if (slot < g.table_stride)
-    page = __ldg(g.table + static_cast<long long>(b) * g.table_stride + slot);
-  if (page < 0 || page >= g.num_pages) {
-    if (lane == 0) report(g.status, FLAMIA_DEV_BAD_PAGE);
-    return false;
-  }
-  blk.row = (static_cast<long long>(page) * g.H_kv + blk.h) * g.page_size + (p0 - slot * g.page_size);
+    blk.page = __ldg(g.table + static_cast<long long>(b) * g.table_stride + slot);
+  blk.in_page = static_cast<int>(p0 - slot * g.page_size);
   blk.token = r.s + p0 - start;
   return true;
 }
 
-// A BF16 pair with infinities turned into NaN.
-__device__ __forceinline__ float2 finite_or_nan(uint32_t w) {
-  float a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xFFFF0000u);
-  if ((w & 0x7F80u) == 0x7F80u) a = __uint_as_float(0x7FC00000u);
-  if ((w & 0x7F800000u) == 0x7F800000u) b = __uint_as_float(0x7FC00000u);
-  return make_float2(a, b);
+__device__ __forceinline__ bool valid_page(const CacheArgs& g, const Block& blk, int lane) {
+  const bool ok = blk.page >= 0 && blk.page < g.num_pages;
+  if (!ok && lane == 0) report(g.status, FLAMIA_DEV_BAD_PAGE);
+  return ok;
 }
 
 // Magnitudes of a BF16 pair as two 16-bit integers (their order is the
-// values'), non-finite ones as 0.
-__device__ __forceinline__ uint32_t finite_mag(uint32_t w) {
-  uint32_t m = w & 0x7FFF7FFFu;
-  if ((m & 0x7F80u) == 0x7F80u) m &= 0xFFFF0000u;
-  if ((m & 0x7F800000u) == 0x7F800000u) m &= 0x0000FFFFu;
-  return m;
+// values'); 0x7F80 and above are infinities and NaN.
+__device__ __forceinline__ uint32_t mag(uint32_t w) { return w & 0x7FFF7FFFu; }
+__device__ __forceinline__ uint32_t mag(const uint4& x) {
+  return __vmaxu2(__vmaxu2(mag(x.x), mag(x.y)), __vmaxu2(mag(x.z), mag(x.w)));
+}
+// Non-finite elements of a BF16 pair become NaN (their codes then, too); clear:
+// become 0 (for the maximum).
+__device__ __forceinline__ uint32_t mark(uint32_t w, bool clear) {
+  const uint32_t n = clear ? 0u : 0x7FC0u;
+  if ((w & 0x7F80u) == 0x7F80u) w = (w & 0xFFFF0000u) | n;
+  if ((w & 0x7F800000u) == 0x7F800000u) w = (w & 0x0000FFFFu) | (n << 16);
+  return w;
+}
+__device__ __forceinline__ uint4 mark(const uint4& x, bool clear) {
+  return make_uint4(mark(x.x, clear), mark(x.y, clear), mark(x.z, clear), mark(x.w, clear));
 }
 
+// 8 BF16 elements times inv, as E4M3 codes.
+__device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  const float2 f = make_float2(inv, inv);
+  float2 v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    v[j] = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), f);
+  return make_uint2(cvt_e4m3x4(v[0].x, v[0].y, v[1].x, v[1].y),
+                    cvt_e4m3x4(v[2].x, v[2].y, v[3].x, v[3].y));
+}
+
+// Instructions, not HBM, would set the pace of a plain loop here: maxima run on
+// packed 16-bit integers, products on float pairs, and infinities and NaN are
+// looked for once a block (a maximum of 0x7F80 or more) instead of at each
+// element.  58,918 tokens x 16 heads x 128: 510 us with a check at each element
+// and 178 registers.
 template <int DIM, bool TOK>
 __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const CacheArgs g) {
   constexpr int LPR = DIM / 8;   // lanes per row: 8 elements each
@@ -106,46 +132,82 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
   Block blk;
   if (unit >= g.units || !find_block(g, unit, lane, blk)) return;
   const int sub = lane / LPR, chunk = lane % LPR;
-  const __nv_bfloat16* rows = blk.kv ? g.rows[1] : g.rows[0];
   const long long stride = blk.kv ? g.stride[1] : g.stride[0];
-  uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + blk.row * DIM;
-  uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + blk.row;
+  const __nv_bfloat16* src =
+      (blk.kv ? g.rows[1] : g.rows[0]) + (blk.token + sub) * stride + blk.h * DIM + chunk * 8;
+  const bool full = blk.lo == 0 && blk.hi == 32;
 
   uint4 x[NLD];
+  if (full) {
 #pragma unroll
-  for (int i = 0; i < NLD; ++i) {
-    const int r = i * RPI + sub;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r >= blk.lo && r < blk.hi)
-      x[i] = __ldg(reinterpret_cast<const uint4*>(rows + (blk.token + r) * stride + blk.h * DIM +
-                                                  chunk * 8));
+    for (int i = 0; i < NLD; ++i)
+      x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPI * stride));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int r = i * RPI + sub;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r >= blk.lo && r < blk.hi)
+        x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPI * stride));
+    }
   }
+  if (!valid_page(g, blk, lane)) return;
+  const long long row = blk.row(g);
+  uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + row * DIM;
+  uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + row;
   // what the block holds before the call keeps its exponent, or a larger one
   int held = -127;
   if (!TOK && blk.lo > 0) held = static_cast<int>(scales[0]) - 127;
 
-  // maxima as 16-bit integers
-  uint32_t m[NLD];
   uint32_t all = 0;
 #pragma unroll
-  for (int i = 0; i < NLD; ++i) {
-    const uint32_t a = __vmaxu2(finite_mag(x[i].x), finite_mag(x[i].y));
-    const uint32_t b = __vmaxu2(finite_mag(x[i].z), finite_mag(x[i].w));
-    const uint32_t c = __vmaxu2(a, b);
-    m[i] = max(c & 0xFFFFu, c >> 16);
-    all = max(all, m[i]);
+  for (int i = 0; i < NLD; ++i) all = __vmaxu2(all, mag(x[i]));
+  all = __reduce_max_sync(0xffffffffu, max(all & 0xFFFFu, all >> 16));
+  if (all >= 0x7F80u) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      a = __vmaxu2(a, mag(mark(x[i], true)));
+      x[i] = mark(x[i], false);
+    }
+    all = __reduce_max_sync(0xffffffffu, max(a & 0xFFFFu, a >> 16));
   }
-  int e = 0;
-  if (!TOK) {
-    all = __reduce_max_sync(0xffffffffu, all);
-    e = max(held, roundup_exponent(__uint_as_float(all << 16)));
-    if (blk.lo > 0 && e > held) {
-      // the held codes are rounded again under the larger exponent
-      const float f = held - e < -126 ? 0.f : exp2i(held - e);
-#pragma unroll 4
+  uint2* out = reinterpret_cast<uint2*>(codes + sub * DIM) + chunk;
+  if constexpr (TOK) {
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int r = i * RPI + sub;
+      uint32_t m = mag(mark(x[i], true));
+      m = max(m & 0xFFFFu, m >> 16);
+#pragma unroll
+      for (int off = LPR / 2; off > 0; off >>= 1)
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      const int e = roundup_exponent(__uint_as_float(m << 16));
+      if (r >= blk.lo && r < blk.hi) {
+        out[i * RPI * (DIM / 8)] = encode(x[i], exp2i(-e));
+        if (chunk == 0) scales[r] = static_cast<uint8_t>(e + 127);
+      }
+    }
+  } else {
+    const int e = max(held, roundup_exponent(__uint_as_float(all << 16)));
+    const float inv = exp2i(-e);  // e in [-127, 120]: 2^-e is a normal float
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < NLD; ++i) out[i * RPI * (DIM / 8)] = encode(x[i], inv);
+      scales[lane] = static_cast<uint8_t>(e + 127);
+    } else {
+#pragma unroll
       for (int i = 0; i < NLD; ++i) {
         const int r = i * RPI + sub;
-        if (r < blk.lo) {
+        if (r >= blk.lo && r < blk.hi) out[i * RPI * (DIM / 8)] = encode(x[i], inv);
+      }
+      const bool grew = blk.lo > 0 && e > held;
+      if (lane < blk.hi && (lane >= blk.lo || grew)) scales[lane] = static_cast<uint8_t>(e + 127);
+      if (grew) {
+        // the held codes are rounded again under the larger exponent
+        const float f = held - e < -126 ? 0.f : exp2i(held - e);
+#pragma unroll 1
+        for (int r = sub; r < blk.lo; r += RPI) {
           uint2* at = reinterpret_cast<uint2*>(codes + r * DIM) + chunk;
           uint2 c = *at;
           const float2 v0 = e4m3x2_to_float2(c.x & 0xFFFFu), v1 = e4m3x2_to_float2(c.x >> 16);
@@ -155,29 +217,6 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
           *at = c;
         }
       }
-      if (lane < blk.lo) scales[lane] = static_cast<uint8_t>(e + 127);
-    }
-    if (lane >= blk.lo && lane < blk.hi) scales[lane] = static_cast<uint8_t>(e + 127);
-  }
-#pragma unroll
-  for (int i = 0; i < NLD; ++i) {
-    const int r = i * RPI + sub;
-    if (TOK) {
-      uint32_t mm = m[i];
-#pragma unroll
-      for (int off = LPR / 2; off > 0; off >>= 1)
-        mm = max(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-      e = roundup_exponent(__uint_as_float(mm << 16));
-    }
-    const float inv = exp2i(-e);  // e in [-127, 120]: 2^-e is a normal float
-    if (r >= blk.lo && r < blk.hi) {
-      const float2 v0 = finite_or_nan(x[i].x), v1 = finite_or_nan(x[i].y);
-      const float2 v2 = finite_or_nan(x[i].z), v3 = finite_or_nan(x[i].w);
-      uint2 c;
-      c.x = cvt_e4m3x4(v0.x * inv, v0.y * inv, v1.x * inv, v1.y * inv);
-      c.y = cvt_e4m3x4(v2.x * inv, v2.y * inv, v3.x * inv, v3.y * inv);
-      reinterpret_cast<uint2*>(codes + r * DIM)[chunk] = c;
-      if (TOK && chunk == 0) scales[r] = static_cast<uint8_t>(e + 127);
     }
   }
 }
@@ -194,12 +233,13 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheAr
                 static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x,
                 static_cast<long long>(gridDim.x) * kCacheThreads, g.status);
   Block blk;
-  if (unit >= g.units || !find_block(g, unit, lane, blk)) return;
+  if (unit >= g.units || !find_block(g, unit, lane, blk) || !valid_page(g, blk, lane)) return;
   const int sub = lane / LPR, chunk = lane % LPR;
   __nv_bfloat16* rows = blk.kv ? g.rows[1] : g.rows[0];
   const long long stride = blk.kv ? g.stride[1] : g.stride[0];
-  const uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + blk.row * DIM;
-  const uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + blk.row;
+  const long long row = blk.row(g);
+  const uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + row * DIM;
+  const uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + row;
   uint2 x[NLD];
 #pragma unroll
   for (int i = 0; i < NLD; ++i) {
