@@ -446,7 +446,7 @@ flamia_status flamia_attn_bwd_gqa(const flamia_qtensor* q, const flamia_qtensor*
  *  turns        device uint64[rot_dim / 2].  rot_dim: a multiple of 16, 16 .. d.
  *  starts       device int32[ndocs] or NULL.
  *  cu_seqlens   as elsewhere, but it may end before T (a padded batch): rows
- *               behind the last document are neither read nor written.
+ *               behind the last document are not written.
  *  flags        FLAMIA_FLAG_ROPE_INTERLEAVED | FLAMIA_FLAG_ROPE_INVERSE.
  * T == 0 enqueues nothing.  ndocs <= 2^20.
  */

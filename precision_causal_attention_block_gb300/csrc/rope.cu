@@ -9,7 +9,8 @@
 // A CTA takes kTok tokens: its threads work out the tokens' cosines and sines
 // once, pass them through shared memory, and each keeps those of one 16-element
 // unit of the row (8 pairs) in registers while it walks the heads of Q and K.
-// HBM-bound: 2 bytes read and 2 written per element.
+// HBM-bound: 2 bytes read and 2 written per element.  131,072 tokens x 64 heads of
+// 64: 304 us, 7.0 TB/s of reads and writes.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -63,6 +64,37 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
   __shared__ int s_pos[kTok];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int t0 = blockIdx.x * kTok;
+  const int unit = tid % kUnits, hl = (tid / kUnits) % kLanes, tk = tid / (kUnits * kLanes);
+  const int t = t0 + tk;
+  const bool turn = unit * 16 < g.rot;
+  const int half = g.rot / 2;
+  // the unit's two 8-element chunks: both halves of its pairs, or 16
+  // neighbouring elements (interleaved pairs, or the part that is copied)
+  const int c0 = (INTER || !turn) ? unit * 16 : unit * 8;
+  const int c1 = (INTER || !turn) ? c0 + 8 : c0 + half;
+  const int heads = g.H + g.H_kv;
+  // kBatch heads at a time: all their loads before the first store (the
+  // compiler cannot move loads over stores that may alias them).  With one
+  // token a CTA, where latency counts, those of the first batch come before the
+  // positions and angles are worked out (a decode step of 16 tokens: 3.0 -> 2.7
+  // us; with four, other CTAs fill the wait, and registers count: 16,384 tokens
+  // x 32 heads 45.5 us without, 47.3 with it).
+  constexpr int kBatch = 4;
+  uint4 w0[kBatch], w1[kBatch];
+  auto load = [&](int h0) {
+    const __nv_bfloat16* qi = g.q_in + t * g.q_in_stride;
+    const __nv_bfloat16* ki = g.k_in + t * g.k_in_stride;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * kLanes;
+      if (h < heads) {
+        const __nv_bfloat16* in = h < g.H ? qi + h * DIM : ki + (h - g.H) * DIM;
+        w0[j] = *reinterpret_cast<const uint4*>(in + c0);
+        w1[j] = *reinterpret_cast<const uint4*>(in + c1);
+      }
+    }
+  };
+  if (kTok == 1 && t < g.T) load(hl);
 
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * kRopeThreads + tid,
                 static_cast<long long>(gridDim.x) * kRopeThreads, g.status);
@@ -78,7 +110,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
     if (lane == 0) s_pos[warp] = pos;
   }
   __syncthreads();
-  const int half = g.rot / 2;
   for (int i = tid; i < kTok * half; i += kRopeThreads) {
     const int tk = i / half, pair = i - tk * half;
     const unsigned long long ph =
@@ -89,14 +120,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
   }
   __syncthreads();
 
-  const int unit = tid % kUnits, hl = (tid / kUnits) % kLanes, tk = tid / (kUnits * kLanes);
-  const int t = t0 + tk;
   if (s_pos[tk] == INT_MIN) return;
-  const bool turn = unit * 16 < g.rot;
-  // the unit's two 8-element chunks: both halves of its pairs, or 16
-  // neighbouring elements (interleaved pairs, or the part that is copied)
-  const int c0 = (INTER || !turn) ? unit * 16 : unit * 8;
-  const int c1 = (INTER || !turn) ? c0 + 8 : c0 + half;
   float cs[8], sn[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -104,51 +128,50 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
     cs[i] = w.x;
     sn[i] = w.y;
   }
-  const __nv_bfloat16* qi = g.q_in + t * g.q_in_stride;
   __nv_bfloat16* qo = g.q_out + t * g.q_out_stride;
-  const __nv_bfloat16* ki = g.k_in + t * g.k_in_stride;
   __nv_bfloat16* ko = g.k_out + t * g.k_out_stride;
-  const int heads = g.H + g.H_kv;
-#pragma unroll 2
-  for (int h = hl; h < heads; h += kLanes) {
-    const bool isq = h < g.H;
-    const __nv_bfloat16* in = isq ? qi + h * DIM : ki + (h - g.H) * DIM;
-    __nv_bfloat16* out = isq ? qo + h * DIM : ko + (h - g.H) * DIM;
-    const uint4 w0 = *reinterpret_cast<const uint4*>(in + c0);
-    const uint4 w1 = *reinterpret_cast<const uint4*>(in + c1);
-    uint4 r0 = w0, r1 = w1;
-    if (turn) {
-      float x[8], y[8], u[8], v[8];
-      unpack(w0, x);
-      unpack(w1, y);
-      if (INTER) {
+  for (int h0 = hl; h0 < heads; h0 += kBatch * kLanes) {
+    if (kTok != 1 || h0 != hl) load(h0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
-          u[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
-          v[2 * i] = y[2 * i] * cs[4 + i] - y[2 * i + 1] * sn[4 + i];
-          v[2 * i + 1] = y[2 * i] * sn[4 + i] + y[2 * i + 1] * cs[4 + i];
-        }
-      } else {
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = h0 + j * kLanes;
+      if (h >= heads) break;
+      __nv_bfloat16* out = h < g.H ? qo + h * DIM : ko + (h - g.H) * DIM;
+      if (turn) {
+        float x[8], y[8], u[8], v[8];
+        unpack(w0[j], x);
+        unpack(w1[j], y);
+        if (INTER) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          u[i] = x[i] * cs[i] - y[i] * sn[i];
-          v[i] = x[i] * sn[i] + y[i] * cs[i];
+          for (int i = 0; i < 4; ++i) {
+            u[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
+            u[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
+            v[2 * i] = y[2 * i] * cs[4 + i] - y[2 * i + 1] * sn[4 + i];
+            v[2 * i + 1] = y[2 * i] * sn[4 + i] + y[2 * i + 1] * cs[4 + i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            u[i] = x[i] * cs[i] - y[i] * sn[i];
+            v[i] = x[i] * sn[i] + y[i] * cs[i];
+          }
         }
+        w0[j] = pack(u);
+        w1[j] = pack(v);
       }
-      r0 = pack(u);
-      r1 = pack(v);
+      *reinterpret_cast<uint4*>(out + c0) = w0[j];
+      *reinterpret_cast<uint4*>(out + c1) = w1[j];
     }
-    *reinterpret_cast<uint4*>(out + c0) = r0;
-    *reinterpret_cast<uint4*>(out + c1) = r1;
   }
 }
 
 template <int DIM>
 void launch(const RopeArgs& g, bool inter, cudaStream_t s) {
-  // four tokens a CTA share its set-up; with few tokens one each, so that a
-  // decode step's heads spread over the GPU
-  const bool few = g.T < 4 * 2 * 152;
+  // Four tokens a CTA share its set-up; with few tokens one each, so that a
+  // decode step's heads spread over the GPU (40 heads of 128, one against four:
+  // 300 tokens 2.9 us against 3.4, 600 tokens 3.8 against 3.6, 4,800 tokens 21.4
+  // against 15.8).
+  const bool few = g.T < 3 * 152;
   const int tok = few ? 1 : 4;
   const int grid = (g.T + tok - 1) / tok;
   auto kern = few ? (inter ? rope_kernel<DIM, 1, true> : rope_kernel<DIM, 1, false>)
