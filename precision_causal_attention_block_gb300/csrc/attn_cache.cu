@@ -53,6 +53,7 @@ constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
 constexpr int kItemCost = 4;    // an item's own steps (queries, output) in tiles
 constexpr int kWholeTiles = 4;
+constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kUnset = 1e30f; // -reference of a row that has seen no key yet
 constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
@@ -108,39 +109,60 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                       uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
-               : "memory");
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// A pair of floats rounded to FP16; FP16 pairs to E4M3 / E5M2 codes; 32 (w - code)
-// of an FP16 pair (exact).
+// A pair of floats rounded to FP16.
 __device__ __forceinline__ uint32_t half2_of(float2 a) {
   const __half2 h = __floats2half2_rn(a.x, a.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t e5m2x2_of_half2(uint32_t h) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t residual32(uint32_t w, uint32_t code) {
-  uint32_t c, r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(c) : "h"(static_cast<uint16_t>(code)));
+// Four FP16 weights (two pairs): their E4M3 codes in one word, and 32 (w - code)
+// in place of the weights (exact).
+__device__ __forceinline__ uint32_t take_term(uint32_t& a, uint32_t& b) {
+  uint32_t w;
   const uint32_t p32 = 0x50005000u, n32 = 0xD000D000u;  // 32, -32
-  asm("{\n\t.reg .b32 t;\n\t"
-      "mul.rn.f16x2 t, %1, %2;\n\t"
-      "fma.rn.f16x2 %0, %3, %4, t;\n\t}"
-      : "=r"(r)
-      : "r"(w), "r"(p32), "r"(c), "r"(n32));
-  return r;
+  asm("{\n\t.reg .b16 ca, cb;\n\t.reg .b32 ha, hb, ta, tb;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 ca, %0;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 cb, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 ha, ca;\n\t"
+      "cvt.rn.f16x2.e4m3x2 hb, cb;\n\t"
+      "mul.rn.f16x2 ta, %0, %3;\n\t"
+      "mul.rn.f16x2 tb, %1, %3;\n\t"
+      "fma.rn.f16x2 %0, ha, %4, ta;\n\t"
+      "fma.rn.f16x2 %1, hb, %4, tb;\n\t"
+      "mov.b32 %2, {ca, cb};\n\t}"
+      : "+r"(a), "+r"(b), "=r"(w)
+      : "r"(p32), "r"(n32));
+  return w;
+}
+// Four FP16 values as E5M2 codes.
+__device__ __forceinline__ uint32_t e5m2x4_of_half(uint32_t a, uint32_t b) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 ca, cb;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 ca, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 cb, %2;\n\t"
+      "mov.b32 %0, {ca, cb};\n\t}"
+      : "=r"(w)
+      : "r"(a), "r"(b));
+  return w;
+}
+// The same with float32 weights.
+__device__ __forceinline__ uint32_t take_term(float2& a, float2& b) {
+  uint32_t w, ha, hb;
+  asm("{\n\t.reg .b16 ca, cb;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 ca, %4, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 cb, %6, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, ca;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, cb;\n\t"
+      "mov.b32 %0, {ca, cb};\n\t}"
+      : "=r"(w), "=r"(ha), "=r"(hb)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  const float2 n32 = make_float2(-32.f, -32.f), p32 = make_float2(32.f, 32.f);
+  a = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&ha)), n32, __fmul2_rn(a, p32));
+  b = __ffma2_rn(__half22float2(*reinterpret_cast<const __half2*>(&hb)), n32, __fmul2_rn(b, p32));
+  return w;
 }
 
 __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
@@ -202,27 +224,27 @@ __device__ __forceinline__ int tile_of(const Segment& g, int i) {
 
 template <int DIM, int R>
 struct Cfg {
-  static constexpr int kHalves = R == 32 ? 2 : 1;   // softmax warpgroups
+  static constexpr int kHalves = R == 8 ? 1 : 2;     // softmax warpgroups
   static constexpr int kRows = R / kHalves;         // rows of a softmax thread
   static constexpr int kSoftmax = 128 * kHalves;    // softmax threads
   static constexpr int kThreads = kSoftmax + 64;
   static constexpr int kCtas = R == 8 ? 3 : 2;      // resident CTAs per SM
   // Stages.  32 rows: K is read once its scores are there and V a softmax later,
   // so each has a ring of its own, and the scale bytes (and which pieces were
-  // loaded) one that is two longer, as the softmax of a tile is done two score
-  // products later (a chunk of 512 tokens over 8,192: 284 -> 257 us).  With
+  // loaded) one that is at least two longer, as the softmax of a tile is done two
+  // score products later (a chunk of 512 tokens over 8,192: 284 -> 257 us).  With
   // fewer rows, where HBM sets the pace, K, V and scales of a tile share a stage
   // and a barrier (96 ragged contexts: 102 us against 128).
   static constexpr bool kSplit = R == 32;
   static constexpr int kKS = (R == 8 ? 2 : 3) * (128 / DIM);
   static constexpr int kVS = (R == 16 ? 3 : 2) * (128 / DIM);
-  static constexpr int kSS = kSplit ? kKS + 2 : kKS;
-  static_assert(kSplit || kKS == kVS, "one ring");
+  static constexpr int kSS = kSplit ? 8 : kKS;
+  static_assert(kSplit ? kSS >= kKS + 2 : kKS == kVS, "rings");
   static constexpr int kTileBytes = 128 * DIM;
-  // 32 rows are bound by the softmax warps: their weights go through FP16
+  // 16 and 32 rows are bound by the softmax warps: their weights go through FP16
   // (relative error 2^-11) and keep the last term in E5M2, whose range leaves
   // room for references that move seldom
-  static constexpr bool kHalfWeights = R == 32;
+  static constexpr bool kHalfWeights = R >= 16;
   static constexpr float kShift = kHalfWeights ? 0.f : 4.f;  // log2 of a weight at the reference
   static constexpr float kSlack = 8.f - kShift;              // weights <= 2^8 < 448
   static constexpr int kNS = 2 * R;                 // columns of S^T
@@ -246,6 +268,7 @@ struct Smem {
   alignas(16) float nref[R];    // kShift - reference
   alignas(16) float fac[R], facl[R];  // changes of scale of O^T and l
   int has[R];                   // the row has a reference
+  bool nan[2][128];  // a half-seen key's value holds a NaN (by tile parity)
   alignas(16) int pos[R];       // position of a row's token, -1: no such row
   alignas(16) int orow[R];      // its row of o, -1: none
   float red[4][R];
@@ -256,7 +279,7 @@ struct Smem {
   uint64_t q_full, o_empty;
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Segment seg[kSegSlots];
-  int loaded[C::kSS];           // pieces of the tile that were loaded
+  int2 tile[C::kSS];            // first key; pieces that were loaded, kWhole
   int plan_b;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     }
     while (ok) {
       Segment sg{};
-      int hi = 0, wlo = 0;
+      int hi = 0, wlo = 0, pf = 0, pl = 0;  // pf, pl: positions of the first and last row
       if (u >= u1) {
         sg.s = -1;
       } else {
@@ -476,9 +499,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sg.start = w.start;
         sg.hk = hk;
         sg.row0 = rt * R;
-        // positions of the row tile's first and last token
-        const int pf = w.start + sg.row0 / g.G;
-        const int pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
+        pf = w.start + sg.row0 / g.G;
+        pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
                                                       static_cast<long long>(sg.row0) + R - 1) /
                                                   g.G);
         hi = max(pl + 1, 0);
@@ -557,6 +579,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const int prow = pg * g.H_kv + sg.hk;
         const long long sc = static_cast<long long>(prow) * g.page_size + ip;
         const int kt = tc % C::kKS, vt = tc % C::kVS, ss = tc % C::kSS;
+        const int k0 = tile_of(sg, i) * 128;
+        const bool whole = n == pieces && k0 + 127 <= pf &&
+                           (g.window == 0 || k0 > pl - g.window || k0 + 127 < g.sinks);
+        const int2 info = make_int2(k0, static_cast<int>(mask) | (whole ? kWhole : 0));
         auto wait_v_slot = [&]() {
           return tc < C::kVS ||
                  mbar_wait_w_ab(smem_u32(&sm.v_empty[vt]), ((tc / C::kVS) - 1) & 1, &sm.abort);
@@ -576,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           if (!ok) break;
           const uint32_t sbar = smem_u32(&sm.sc_full[ss]), vbar = smem_u32(&sm.v_full[vt]);
           if (lane == 0) {
-            sm.loaded[ss] = static_cast<int>(mask);
+            sm.tile[ss] = info;
             mbar_arrive_expect_tx(sbar, n * 2 * piece);
             mbar_arrive_expect_tx(kbar, n * piece * DIM);
           }
@@ -593,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           ok = wait_v_slot();
           if (!ok) break;
           if (lane == 0) {
-            sm.loaded[ss] = static_cast<int>(mask);
+            sm.tile[ss] = info;
             mbar_arrive_expect_tx(kbar, n * (2 * piece * DIM + 2 * piece));
           }
           __syncwarp();
@@ -625,7 +651,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     const uint32_t id_s = idesc_f8(128, C::kNS, 0, 0);
     // weights: all terms at once, or the last one apart (E5M2: bit 10)
     const uint32_t id_o = idesc_f8(128, C::kHalfWeights ? 2 * R : C::kNO, 1, 1);
-    const uint32_t id_lo = idesc_f8(128, R < 16 ? 16 : R, 1, 1) | (1u << 10);
+    const uint32_t id_lo = idesc_f8(128, R < 16 ? 16 : R, 1, 1) | (1u << 10);  // (R = 8: unused)
     const uint64_t dk0 = smem_desc(smem_u32(sm.k[0]), 0, sbo, lay);
     const uint64_t dq = smem_desc(smem_u32(sm.q), 0, sbo, lay);
     // head dim 64: M = 128 takes a second 64-row atom; it reads the bytes one
@@ -692,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           const uint64_t dp = dp0 + ks * (1024 / 16);
           mma_f8_w(tmem + C::kColO, dv, dp, id_o, t > 0 || ks > 0);
           if (C::kHalfWeights)
-            mma_f8_w(tmem + C::kColO + 2 * R, dv, dp + 2 * (4096 / 16), id_lo, t > 0 || ks > 0);
+            mma_f8_w(tmem + C::kColO + 2 * R, dv, dp + (2 * R / 32) * (4096 / 16), id_lo, t > 0 || ks > 0);
         }
         tc_commit_w(smem_u32(&sm.pv_done[x & 1]));
         tc_commit_w(smem_u32(&sm.v_empty[st]));
@@ -715,7 +741,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     auto vote = [&](bool p) { return softmax_vote<C::kSoftmax>(p); };
     auto sync = [&]() { named_barrier_sync(1, C::kSoftmax); };
-    int tc = 0;
+    int tc = 0, ss = 0, sph = 0;  // tiles so far; their place and phase in the ring of scales
     bool ok = true, late = false;  // late: a wait ran out where the warps cannot part
     // a segment's queries are loaded while the one before ends; its ring slot is
     // free again when the segment is done
@@ -760,152 +786,134 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 #pragma unroll
       for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
       int e0 = -127;
-      const int pf = sg.start + sg.row0 / g.G;               // positions of the first
-      const int pl = sg.start + (sg.row0 + rows - 1) / g.G;  // and the last row
-      const int all_pieces = g.page_size >= 128 ? 1 : (1 << (128 / g.page_size)) - 1;
-
       for (int t = 0; t < nt; ++t, ++tc) {
-        const int ss = tc % C::kSS, buf = tc & 1;
-        const int k0 = tile_of(sg, sg.i0 + t) * 128, key = k0 + key_in;
+        const int buf = tc & 1;
         ok = mbar_wait_w_ab(smem_u32(&sm.s_full[buf]), (tc >> 1) & 1, &sm.abort);
         // the scale bytes (a split ring's K barrier may be two phases on by now)
         ok = ok && mbar_wait_w_ab(smem_u32(C::kSplit ? &sm.sc_full[ss] : &sm.k_full[ss]),
-                                  (tc / C::kSS) & 1, &sm.abort);
-        const int eb = sm.vs[ss][key_in];
-        const float kf = pow2_byte(sm.ks[ss][key_in]);
-        const int loaded = sm.loaded[ss];
+                                  sph, &sm.abort);
         if (!ok) sm.stop[buf] = 1;
         tc_fence_after();
-        // keys that not every row sees
-        const bool whole = loaded == all_pieces && k0 + 127 <= pf &&
-                           (g.window == 0 || k0 > pl - g.window || k0 + 127 < g.sinks);
-        bool any = true;        // some row sees the key
-        uint32_t seen = ~0u;    // of this thread's rows
-        bool nan = false;
-        if (!whole) {
-          const int st = tc % C::kVS;
-          if (C::kSplit && !mbar_wait_w_ab(smem_u32(&sm.v_full[st]), (tc / C::kVS) & 1, &sm.abort)) {
-            ok = false;
+        int ev = sm.vs[ss][key_in] - 127;  // V's exponent
+        const float kf = pow2_byte(sm.ks[ss][key_in]);
+        const bool whole = (sm.tile[ss].y & kWhole) != 0;
+        if (!whole) {  // some rows do not see some keys
+          const int2 info = sm.tile[ss];
+          const int st = tc % C::kVS, key = info.x + key_in;
+          if (C::kSplit &&
+              !mbar_wait_w_ab(smem_u32(&sm.v_full[st]), (tc / C::kVS) & 1, &sm.abort))
             sm.stop[buf] = 1;
-          }
-          const bool here = (loaded >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
+          const int pf = sg.start + sg.row0 / g.G;               // positions of the first
+          const int pl = sg.start + (sg.row0 + rows - 1) / g.G;  // and the last row
+          const bool here = (info.y >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
           const bool first = g.window == 0 || key < g.sinks;
-          any = here && key <= pl && (first || key > pf - g.window);
+          const bool any = here && key <= pl && (first || key > pf - g.window);
           const bool every = here && key <= pf && (first || key > pl - g.window) && rows == R;
-          if (!every) {
-            seen = 0;
-#pragma unroll
-            for (int r = 0; r < RW; ++r) {
-              const int p = sm.pos[r0 + r];
-              if (here && key <= p && (first || key > p - g.window)) seen |= 1u << r;
-            }
-          }
+          if (!any) ev = -127;  // neutral
           // A value that some rows see and others do not must not reach the
-          // others: 0 x NaN is NaN.  Unseen rows of V are cleared; a NaN in a
-          // half-seen one moves into the weights of those that see it.
-          if (any && !every) {
-            const uint4* vr = reinterpret_cast<const uint4*>(sm.v[st] + key_in * DIM);
-#pragma unroll 4
-            for (int i = 0; i < DIM / 16; ++i) {
-              const uint4 a = vr[i];
-              const uint32_t aa[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                nan |= ((((aa[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
-            }
-          }
-          if (C::kHalves > 1) sync();  // both halves have looked
-          if ((!any || nan) && half == 0) {
+          // others: 0 x NaN is NaN.  Unseen rows of V are cleared, and half-seen
+          // ones that hold a NaN, which moves into the weights of the rows that
+          // see them.  (The first half looks; the vote orders the second.)
+          if (half == 0) {
             uint4* vr = reinterpret_cast<uint4*>(sm.v[st] + key_in * DIM);
+            bool nan = false;
+            if (any && !every) {
 #pragma unroll 4
-            for (int i = 0; i < DIM / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < DIM / 16; ++i) {
+                const uint4 a = vr[i];
+                const uint32_t aa[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  nan |= ((((aa[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
+              }
+            }
+            sm.nan[buf][key_in] = nan;
+            if (!any || nan) {
+#pragma unroll 4
+              for (int i = 0; i < DIM / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+            }
           }
         }
-        // V's exponent; what nobody sees has the neutral one
-        const int ev = any ? eb - 127 : -127;
         int evc = max(ev, e0 - kLow);
-        float2 y[RW / 2];
-        // Usually one pass over the scores and a vote that the references hold.
-        // If they do not, or on an item's first tile, E0 moves (before pass 1)
-        // and then the rows' references (before pass 2), and the scores are
-        // taken again.
-        int rise = 0;
-        bool broken = false;
+        // x + eV - ref + kShift of rows r0 + c .. + 7.  They are taken anew from
+        // tensor memory where they are needed (for the vote, the references, the
+        // weights): held in registers over the vote they cost more, in spills.
+        auto scores = [&](const int c, float2 (&y)[4]) {
+          const float2 kf2 = make_float2(kf, kf);
+          const float evf = static_cast<float>(evc);
+          const float2 ev2 = make_float2(evf, evf), lo2 = make_float2(0.0625f, 0.0625f);
+          uint32_t h[8], lo[8];
+          tmem_ld8(tmem + lanes + buf * C::kNS + r0 + c, h);
+          tmem_ld8(tmem + lanes + buf * C::kNS + R + r0 + c, lo);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < 8; r += 4) {
+            const float4 qf = *reinterpret_cast<const float4*>(sm.qf + r0 + c + r);
+            const float4 nr = *reinterpret_cast<const float4*>(sm.nref + r0 + c + r);
+            const float2 a = __ffma2_rn(as_f2(lo[r], lo[r + 1]), lo2, as_f2(h[r], h[r + 1]));
+            const float2 b =
+                __ffma2_rn(as_f2(lo[r + 2], lo[r + 3]), lo2, as_f2(h[r + 2], h[r + 3]));
+            y[r / 2] = __ffma2_rn(a, __fmul2_rn(kf2, make_float2(qf.x, qf.y)),
+                                  __fadd2_rn(ev2, make_float2(nr.x, nr.y)));
+            y[r / 2 + 1] = __ffma2_rn(b, __fmul2_rn(kf2, make_float2(qf.z, qf.w)),
+                                      __fadd2_rn(ev2, make_float2(nr.z, nr.w)));
+          }
+          if (!whole) {
+            const int2 info = sm.tile[ss];
+            const int key = info.x + key_in;
+            const bool here = (info.y >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
+            const bool first = g.window == 0 || key < g.sinks;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const int p = sm.pos[r0 + c + r];
+              if (!(here && key <= p && (first || key > p - g.window)))
+                (r & 1 ? y[r / 2].y : y[r / 2].x) = -INFINITY;
+            }
+          }
+        };
+        // Do the references hold?  On an item's first tile there are none.
+        bool move = true;
+        if (t > 0) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < RW; c += 8) {
+            float2 y[4];
+            scores(c, y);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmax3(mx, y[r].x, y[r].y);
+          }
+          move = mx > C::kShift + C::kSlack || ev > e0 + kHigh;
+        }
+        move = vote(move);
+        if (sm.stop[buf]) {  // the same for all: written before the barrier
+          ok = false;
+          break;
+        }
+        if (move) {  // E0, then the rows' references
+          const int em = __reduce_max_sync(0xffffffffu, ev + 127);
+          if (lane == 0) sm.rede[warp] = em;
+          // rows without a reference are measured from 0
+          if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = C::kShift;
+          sync();
+          int top = -127, rise = 0;
+#pragma unroll
+          for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
+          if (t == 0) {
+            e0 = top;
+          } else if (top > e0 + kHigh) {
+            rise = top - e0;
+            e0 = top;
+          }
+          evc = max(ev, e0 - kLow);
 #pragma unroll 1
-        for (int pass = t == 0 ? 1 : 0;; ++pass) {
-          if (pass == 1) {
-            if (t == 0) {
-              vote(false);
-              if (sm.stop[buf]) {
-                broken = true;
-                break;
-              }
+          for (int c = 0; c < RW; c += 8) {
+            float2 y[4];
+            scores(c, y);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              const float a = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
+              if (lane == 0) sm.red[warp & 3][r0 + c + r] = a;
             }
-            const int em = __reduce_max_sync(0xffffffffu, ev + 127);
-            if (lane == 0) sm.rede[warp] = em;
-            // rows without a reference are measured from 0
-            if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = C::kShift;
-            sync();
-            int top = -127;
-#pragma unroll
-            for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
-            if (t == 0) {
-              e0 = top;
-            } else if (top > e0 + kHigh) {
-              rise = top - e0;
-              e0 = top;
-            }
-            evc = max(ev, e0 - kLow);
-          }
-          {
-            const float2 kf2 = make_float2(kf, kf);
-            const float evf = static_cast<float>(evc);
-            const float2 ev2 = make_float2(evf, evf), lo2 = make_float2(0.0625f, 0.0625f);
-#pragma unroll
-            for (int c = 0; c < RW; c += 8) {
-              uint32_t h[8], lo[8];
-              tmem_ld8(tmem + lanes + buf * C::kNS + r0 + c, h);
-              tmem_ld8(tmem + lanes + buf * C::kNS + R + r0 + c, lo);
-              tmem_ld_wait();
-#pragma unroll
-              for (int r = 0; r < 8; r += 4) {
-                const float4 qf = *reinterpret_cast<const float4*>(sm.qf + r0 + c + r);
-                const float4 nr = *reinterpret_cast<const float4*>(sm.nref + r0 + c + r);
-                const float2 a = __ffma2_rn(as_f2(lo[r], lo[r + 1]), lo2, as_f2(h[r], h[r + 1]));
-                const float2 b =
-                    __ffma2_rn(as_f2(lo[r + 2], lo[r + 3]), lo2, as_f2(h[r + 2], h[r + 3]));
-                y[(c + r) / 2] = __ffma2_rn(a, __fmul2_rn(kf2, make_float2(qf.x, qf.y)),
-                                            __fadd2_rn(ev2, make_float2(nr.x, nr.y)));
-                y[(c + r) / 2 + 1] = __ffma2_rn(b, __fmul2_rn(kf2, make_float2(qf.z, qf.w)),
-                                                __fadd2_rn(ev2, make_float2(nr.z, nr.w)));
-              }
-            }
-            if (!whole) {
-              const float nv = __uint_as_float(0x7FC00000u);
-#pragma unroll
-              for (int r = 0; r < RW; r += 2) {
-                y[r / 2].x = !((seen >> r) & 1) ? -INFINITY : nan ? nv : y[r / 2].x;
-                y[r / 2].y = !((seen >> (r + 1)) & 1) ? -INFINITY : nan ? nv : y[r / 2].y;
-              }
-            }
-          }
-          if (pass == 2) break;
-          if (pass == 0) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int r = 0; r < RW / 2; ++r) mx = fmax3(mx, y[r].x, y[r].y);
-            const bool move = vote(mx > C::kShift + C::kSlack || ev > e0 + kHigh);
-            if (sm.stop[buf]) {  // the same for all: written before the barrier
-              broken = true;
-              break;
-            }
-            if (!move) break;
-            continue;
-          }
-#pragma unroll
-          for (int r = 0; r < RW; ++r) {
-            const float a = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
-            if (lane == 0) sm.red[warp & 3][r0 + r] = a;
           }
           sync();
           if (tid < R) {
@@ -962,74 +970,69 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             tmem_st_wait();
           }
         }
-        if (broken) {
-          ok = false;
-          break;
-        }
-        // weights and their E4M3 terms, 4 rows a word
+        // weights and their 8-bit terms
         const float gl = ex2_approx(static_cast<float>(e0 - evc));
         const float2 g2 = make_float2(gl, gl);
         const float z = ev < evc ? ex2_approx(static_cast<float>(max(ev - evc, -126))) : 1.f;
-        uint32_t tw[3][RW / 4];
 #pragma unroll
-        for (int r = 0; r < RW; r += 4) {
-          float2 a = make_float2(ex2_approx(y[r / 2].x), ex2_approx(y[r / 2].y));
-          float2 b = make_float2(ex2_approx(y[r / 2 + 1].x), ex2_approx(y[r / 2 + 1].y));
-          l[r / 2] = __ffma2_rn(a, g2, l[r / 2]);
-          l[r / 2 + 1] = __ffma2_rn(b, g2, l[r / 2 + 1]);
-          if (ev < evc) {
-            a.x *= z;
-            a.y *= z;
-            b.x *= z;
-            b.y *= z;
-          }
-          if constexpr (C::kHalfWeights) {
-            uint32_t ha = half2_of(a), hb = half2_of(b);
+        for (int c = 0; c < RW; c += 8) {
+          float2 y[4];
+          scores(c, y);
+          if (!whole && sm.nan[buf][key_in]) {
+            const float nv = __uint_as_float(0x7FC00000u);
 #pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const uint32_t ca = e4m3x2_of_half2(ha), cb = e4m3x2_of_half2(hb);
-              tw[term][r / 4] = ca | (cb << 16);
-              ha = residual32(ha, ca);
-              hb = residual32(hb, cb);
-            }
-            tw[2][r / 4] = e5m2x2_of_half2(ha) | (e5m2x2_of_half2(hb) << 16);
-          } else {
-            const float2 n32 = make_float2(-32.f, -32.f), p32 = make_float2(32.f, 32.f);
-#pragma unroll
-            for (int term = 0; term < 3; ++term) {
-              const uint32_t ca = cvt_e4m3x2(a.x, a.y), cb = cvt_e4m3x2(b.x, b.y);
-              tw[term][r / 4] = ca | (cb << 16);
-              if (term < 2) {  // 32 (w - h), exact
-                a = __ffma2_rn(e4m3x2_to_float2(ca), n32, __fmul2_rn(a, p32));
-                b = __ffma2_rn(e4m3x2_to_float2(cb), n32, __fmul2_rn(b, p32));
-              }
+            for (int r = 0; r < 4; ++r) {
+              if (y[r].x != -INFINITY) y[r].x = nv;
+              if (y[r].y != -INFINITY) y[r].y = nv;
             }
           }
-        }
-        // the product before has read P^T
-        if (tc >= 1 &&
-            !mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort)) {
-          late = true;
-          sm.stop[buf ^ 1] = 1;
-        }
-        // P^T: key rows of 32 columns (32 bytes), 16-byte chunks swizzled
-        const uint32_t pb = smem_u32(sm.p) + key_in * 32;
-        const uint32_t sw = ((key_in >> 2) & 1) * 16;
-        if constexpr (R == 8) {
-          sts128(pb + sw, tw[0][0], tw[0][1], tw[1][0], tw[1][1]);
-          sts128(pb + (sw ^ 16), tw[2][0], tw[2][1], 0, 0);
-        } else {
+          uint32_t tw[3][2];
+#pragma unroll
+          for (int r = 0; r < 8; r += 4) {
+            float2 a = make_float2(ex2_approx(y[r / 2].x), ex2_approx(y[r / 2].y));
+            float2 b = make_float2(ex2_approx(y[r / 2 + 1].x), ex2_approx(y[r / 2 + 1].y));
+            l[(c + r) / 2] = __ffma2_rn(a, g2, l[(c + r) / 2]);
+            l[(c + r) / 2 + 1] = __ffma2_rn(b, g2, l[(c + r) / 2 + 1]);
+            if (ev < evc) {
+              a.x *= z;
+              a.y *= z;
+              b.x *= z;
+              b.y *= z;
+            }
+            if constexpr (C::kHalfWeights) {
+              uint32_t ha = half2_of(a), hb = half2_of(b);
+              tw[0][r / 4] = take_term(ha, hb);
+              tw[1][r / 4] = take_term(ha, hb);
+              tw[2][r / 4] = e5m2x4_of_half(ha, hb);
+            } else {
+              tw[0][r / 4] = take_term(a, b);
+              tw[1][r / 4] = take_term(a, b);
+              tw[2][r / 4] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
+            }
+          }
+          // the product before has read P^T
+          if (c == 0 && tc >= 1 &&
+              !mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort)) {
+            late = true;
+            sm.stop[buf ^ 1] = 1;
+          }
+          // P^T: key rows of 32 columns (32 bytes), 16-byte chunks swizzled
 #pragma unroll
           for (int term = 0; term < 3; ++term) {
-            const int n = term * R + r0;  // first column: a multiple of 16
-            sts128(pb + (n / 32) * 4096 + (sw ^ (n & 16)), tw[term][0], tw[term][1], tw[term][2],
-                   tw[term][3]);
+            const int n = term * R + c, col = n + r0;  // column of the first row
+            const uint32_t at = smem_u32(sm.p) + (R == 32 ? term : n / 32) * 4096 + key_in * 32 +
+                                ((((key_in >> 2) & 1) * 16) ^ (col & 16)) + (col & 8);
+            sts64(at, tw[term][0], tw[term][1]);
           }
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[buf]));
+        if (++ss == C::kSS) {
+          ss = 0;
+          sph ^= 1;
+        }
       }
       if (!ok) break;
 
