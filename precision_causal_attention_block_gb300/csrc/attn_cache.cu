@@ -40,6 +40,7 @@
 // lane); then one TMA producer warp and one MMA issuer warp.
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "paged.cuh"
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   Smem<DIM, R>& sm = *reinterpret_cast<Smem<DIM, R>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  start_next();
 
   if (tid == 0) {
     for (int i = 0; i < C::kKS; ++i) {
@@ -454,6 +455,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     tmem_alloc(smem_u32(&sm.tmem_base), C::kCols);
     tmem_relinquish();
   }
+  wait_for_previous();
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
                 static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   tc_fence_before();
@@ -1120,7 +1122,9 @@ template <int DIM, int R>
 __global__ void __launch_bounds__(256) join_kernel(const AttendArgs g) {
   constexpr int E = DIM / 32;  // elements a lane
   const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (no start_next here: the next call's CTAs, let in among these, made that
+  // call slower by up to 20%)
+  wait_for_previous();
   const int4 j0 = g.joins[2 * blockIdx.x], j1 = g.joins[2 * blockIdx.x + 1];
   const int parts = j0.x;
   if (parts <= 0 || r >= static_cast<long long>(j0.z) * g.G - j1.x) return;
@@ -1220,26 +1224,29 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
     return FLAMIA_ERR_CUDA;
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM, R>)) + 1024;
   static_assert(Cfg<DIM, R>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(attend_kernel<DIM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem) != cudaSuccess)
-    return FLAMIA_ERR_CUDA;
   const int grid = min(kMaxCtas, num_sms() * Cfg<DIM, R>::kCtas);
-  attend_kernel<DIM, R><<<grid, Cfg<DIM, R>::kThreads, smem, s>>>(mk, mv, g);
-  if (cudaGetLastError() != cudaSuccess) return FLAMIA_ERR_CUDA;
-  count_launches(1);
+  auto go = [&]() {
+    return launch_after(attend_kernel<DIM, R>, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk, mv,
+                        g);
+  };
+  // The kernel's shared-memory limit is raised once on a device; again if a
+  // launch fails (a new context does not have it).
+  static std::atomic<unsigned long long> raised{0};
+  auto raise = [&]() {
+    return cudaFuncSetAttribute(attend_kernel<DIM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                smem) == cudaSuccess;
+  };
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FLAMIA_ERR_CUDA;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(raised.load(std::memory_order_relaxed) & bit)) {
+    if (!raise()) return FLAMIA_ERR_CUDA;
+    raised.fetch_or(bit, std::memory_order_relaxed);
+  }
+  if (!go() && (!raise() || !go())) return FLAMIA_ERR_CUDA;
   if (g.whole) return FLAMIA_OK;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, R / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<DIM, R>, g) != cudaSuccess) return FLAMIA_ERR_CUDA;
-  count_launches(1);
-  return FLAMIA_OK;
+  return launch_after(join_kernel<DIM, R>, dim3(grid, R / 8), 256, 0, s, g) ? FLAMIA_OK
+                                                                           : FLAMIA_ERR_CUDA;
 }
 
 }  // namespace

@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
   const int lane = threadIdx.x & 31;
   const long long unit =
       static_cast<long long>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  start_next();
+  wait_for_previous();
   check_offsets(g.cu, g.ndocs, g.T,
                 static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x,
                 static_cast<long long>(gridDim.x) * kCacheThreads, g.status);
@@ -229,6 +231,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheAr
   const int lane = threadIdx.x & 31;
   const long long unit =
       static_cast<long long>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  start_next();
+  wait_for_previous();
   check_offsets(g.cu, g.ndocs, g.T,
                 static_cast<long long>(blockIdx.x) * kCacheThreads + threadIdx.x,
                 static_cast<long long>(gridDim.x) * kCacheThreads, g.status);
@@ -303,9 +307,9 @@ flamia_status fill_args(CacheArgs& g, const flamia_kvcache* cache, const void* k
 flamia_status launch(void (*kern)(const CacheArgs), const CacheArgs& g, cudaStream_t s) {
   const long long blocks = (g.units * 32 + kCacheThreads - 1) / kCacheThreads;
   if (blocks >= (1ll << 31)) return FLAMIA_ERR_INVALID_ARG;
-  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, s>>>(g);
-  count_launches(1);
-  return cudaGetLastError() == cudaSuccess ? FLAMIA_OK : FLAMIA_ERR_CUDA;
+  return launch_after(kern, dim3(static_cast<unsigned>(blocks)), kCacheThreads, 0, s, g)
+             ? FLAMIA_OK
+             : FLAMIA_ERR_CUDA;
 }
 
 }  // namespace

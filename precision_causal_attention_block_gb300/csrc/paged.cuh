@@ -53,6 +53,40 @@ __device__ __forceinline__ void check_offsets(const int32_t* __restrict__ cu, in
     report(status, FLAMIA_DEV_BAD_SEQLENS);
 }
 
+// Programmatic dependent launch: the serving kernels follow one another closely
+// (rotary, cache write, attention, join), so each is launched with
+// launch_after, which lets its CTAs start while the kernel before it in the
+// stream drains, and begins with wait_for_previous: nothing is read or written
+// before that kernel has completed.  start_next lets the kernel behind it do the
+// same.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void start_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... P, class... A>
+inline bool launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
+    cudaGetLastError();  // (not left behind for the caller's next check)
+    return false;
+  }
+  count_launches(1);
+  return true;
+}
+
 // Host checks shared by the cache calls.
 inline flamia_status check_cache(const flamia_kvcache* c) {
   if (c == nullptr || c->k_codes == nullptr || c->k_scales == nullptr || c->v_codes == nullptr ||

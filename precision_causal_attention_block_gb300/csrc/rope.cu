@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
       }
     }
   };
+  start_next();
+  wait_for_previous();
   if (kTok == 1 && t < g.T) load(hl);
 
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * kRopeThreads + tid,
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
 }
 
 template <int DIM>
-void launch(const RopeArgs& g, bool inter, cudaStream_t s) {
+bool launch(const RopeArgs& g, bool inter, cudaStream_t s) {
   // Four tokens a CTA share its set-up; with few tokens one each, so that a
   // decode step's heads spread over the GPU (40 heads of 128, one against four:
   // 300 tokens 2.9 us against 3.4, 600 tokens 3.8 against 3.6, 4,800 tokens 21.4
@@ -176,7 +178,7 @@ void launch(const RopeArgs& g, bool inter, cudaStream_t s) {
   const int grid = (g.T + tok - 1) / tok;
   auto kern = few ? (inter ? rope_kernel<DIM, 1, true> : rope_kernel<DIM, 1, false>)
                   : (inter ? rope_kernel<DIM, 4, true> : rope_kernel<DIM, 4, false>);
-  kern<<<grid, kRopeThreads, 0, s>>>(g);
+  return launch_after(kern, dim3(grid), kRopeThreads, 0, s, g);
 }
 
 }  // namespace
@@ -231,10 +233,6 @@ extern "C" flamia_status flamia_rope(const void* q_in, void* q_out, int64_t q_in
   g.sign = (flags & FLAMIA_FLAG_ROPE_INVERSE) ? -1.f : 1.f;
   const bool inter = (flags & FLAMIA_FLAG_ROPE_INTERLEAVED) != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (d == 128)
-    launch<128>(g, inter, s);
-  else
-    launch<64>(g, inter, s);
-  count_launches(1);
-  return cudaGetLastError() == cudaSuccess ? FLAMIA_OK : FLAMIA_ERR_CUDA;
+  return (d == 128 ? launch<128>(g, inter, s) : launch<64>(g, inter, s)) ? FLAMIA_OK
+                                                                        : FLAMIA_ERR_CUDA;
 }
