@@ -52,7 +52,7 @@ constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for 
 constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
-constexpr int kItemCost = 4;    // an item's own steps (queries, output) in tiles
+constexpr int kItemCost = 3;    // an item's own steps (queries, output) in tiles
 constexpr int kWholeTiles = 4;
 constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -221,6 +221,12 @@ __device__ __forceinline__ int tile_of(const Segment& g, int i) {
   return i < g.ns ? i : i - g.ns + g.wt;
 }
 
+// The piece of a tile (a page of less than 128 rows, or the whole tile) that
+// holds one of its keys.
+__device__ __forceinline__ int piece_of(int key_in, int page_size) {
+  return page_size == 32 ? key_in >> 5 : page_size == 64 ? key_in >> 6 : 0;
+}
+
 // ------------------------------------------------------------------ kernel
 
 template <int DIM, int R>
@@ -282,6 +288,7 @@ struct Smem {
   Segment seg[kSegSlots];
   int2 tile[C::kSS];            // first key; pieces that were loaded, kWhole
   int plan_b;
+  SeqWork plan_seq;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
   uint32_t tmem_base;
@@ -289,10 +296,22 @@ struct Smem {
   volatile int abort;
 };
 
+// a * b / c and a / c for a, b, c >= 0, in 32 bits where they suffice (a 64-bit
+// division takes some hundred cycles, and the first copies wait for it).
+__device__ __forceinline__ long long mul_div(long long a, long long b, long long c) {
+  const long long ab = a * b;
+  if (((ab | c) >> 32) == 0)
+    return static_cast<uint32_t>(ab) / static_cast<uint32_t>(c);
+  return ab / c;
+}
+__device__ __forceinline__ long long div_up(long long a, long long c) {
+  return mul_div(a + c - 1, 1, c);
+}
+
 // CTAs that get a run: at least two tiles each, as far as there are any.
 __device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long total) {
   const int least = g.whole ? 1 : kItemCost + 2;
-  return min(static_cast<long long>(gridDim.x), (total + least - 1) / least);
+  return min(static_cast<long long>(gridDim.x), div_up(total, least));
 }
 
 // Total units, and this CTA's run of them: [u0, u1), starting at unit `off` of
@@ -322,8 +341,8 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   }
   const long long ctas = active_ctas(g, total);
   const long long c = blockIdx.x;
-  const long long u0 = c < ctas ? total * c / ctas : total;
-  const long long u1 = c < ctas ? total * (c + 1) / ctas : total;
+  const long long u0 = c < ctas ? mul_div(total, c, ctas) : total;
+  const long long u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;
   if (tid == 0) {
     sm.plan_u0 = u0;
     sm.plan_u1 = u1;
@@ -332,12 +351,13 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   if (u0 < u1 && before <= u0 && u0 < before + sum) {
     long long off = u0 - before;
     int b = b0;
-    for (; b < b1 - 1; ++b) {
-      const long long u = seq_work<R>(g, b).total(g.H_kv);
-      if (off < u) break;
-      off -= u;
+    SeqWork w = seq_work<R>(g, b);
+    while (b < b1 - 1 && off >= w.total(g.H_kv)) {
+      off -= w.total(g.H_kv);
+      w = seq_work<R>(g, ++b);
     }
     sm.plan_b = b;
+    sm.plan_seq = w;
     sm.plan_off = off;
   }
   __syncthreads();
@@ -480,10 +500,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     SeqWork w{};
     int hk = 0, rt = 0, o = 0;
     if (u < u1) {
-      w = seq_work<R>(g, b);
-      const long long item = sm.plan_off / w.units;
+      w = sm.plan_seq;
+      const long long item = mul_div(sm.plan_off, 1, w.units);
       o = static_cast<int>(sm.plan_off - item * w.units);
-      hk = static_cast<int>(item / w.row_tiles);
+      hk = static_cast<int>(mul_div(item, 1, w.row_tiles));
       rt = static_cast<int>(item - static_cast<long long>(hk) * w.row_tiles);
     }
     while (ok) {
@@ -521,8 +541,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           // the second CTA of an item has it joined: parts are the CTA before
           // this one (slot 1) and slots 0 from here on
           const long long ctas = active_ctas(g, total), c = blockIdx.x, ui = u0 - o;
-          if (c > 0 && total * (c - 1) / ctas <= ui + kItemCost) {
-            const long long last = ((ui + w.units) * ctas + total - 1) / total - 1;
+          if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost) {
+            const long long last = div_up((ui + w.units) * ctas, total) - 1;
             join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, hk);
             join1 = make_int4(sg.row0, 0, 0, 0);
           }
@@ -807,7 +827,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             sm.stop[buf] = 1;
           const int pf = sg.start + sg.row0 / g.G;               // positions of the first
           const int pl = sg.start + (sg.row0 + rows - 1) / g.G;  // and the last row
-          const bool here = (info.y >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
+          const bool here = (info.y >> piece_of(key_in, g.page_size)) & 1;
           const bool first = g.window == 0 || key < g.sinks;
           const bool any = here && key <= pl && (first || key > pf - g.window);
           const bool every = here && key <= pf && (first || key > pl - g.window) && rows == R;
@@ -817,12 +837,15 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           // ones that hold a NaN, which moves into the weights of the rows that
           // see them.  (The first half looks; the vote orders the second.)
           if (half == 0) {
+            // (each thread starts at another 16 bytes of its row: no bank conflicts)
             uint4* vr = reinterpret_cast<uint4*>(sm.v[st] + key_in * DIM);
+            constexpr int kChunks = DIM / 16;
+            const int turn = key_in / (128 / DIM);
             bool nan = false;
             if (any && !every) {
 #pragma unroll 4
-              for (int i = 0; i < DIM / 16; ++i) {
-                const uint4 a = vr[i];
+              for (int i = 0; i < kChunks; ++i) {
+                const uint4 a = vr[(i + turn) % kChunks];
                 const uint32_t aa[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -832,7 +855,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             sm.nan[buf][key_in] = nan;
             if (!any || nan) {
 #pragma unroll 4
-              for (int i = 0; i < DIM / 16; ++i) vr[i] = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < kChunks; ++i) vr[(i + turn) % kChunks] = make_uint4(0, 0, 0, 0);
             }
           }
         }
@@ -863,7 +886,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           if (!whole) {
             const int2 info = sm.tile[ss];
             const int key = info.x + key_in;
-            const bool here = (info.y >> (g.page_size >= 128 ? 0 : key_in / g.page_size)) & 1;
+            const bool here = (info.y >> piece_of(key_in, g.page_size)) & 1;
             const bool first = g.window == 0 || key < g.sinks;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
