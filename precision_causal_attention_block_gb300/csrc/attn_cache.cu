@@ -52,7 +52,7 @@ constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for 
 constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
-constexpr int kItemCost = 3;    // an item's own steps (queries, output) in tiles
+constexpr int kItemCost = 2;    // an item's own steps (queries, output) in tiles
 constexpr int kWholeTiles = 4;
 constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -714,18 +714,28 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       tc_fence_after();
       issue_s(0);
       for (int t = 0; t < nt && ok; ++t) {
-        // the next scores first, if their keys are here already
+        // the next scores first, if their keys come before this tile's weights
+        const int x = tc + t, st = x % C::kVS;
         bool ahead = false;
         if (t + 1 < nt) {
-          const int x = tc + t + 1;
-          ahead = __all_sync(0xffffffffu,
-                             mbar_test(smem_u32(&sm.k_full[x % C::kKS]), (x / C::kKS) & 1));
-          if (ahead) {
-            tc_fence_after();
-            issue_s(t + 1);
+          const int y = x + 1;
+          const uint64_t t0 = globaltimer_ns();
+          for (int spin = 0;; ++spin) {
+            if (__all_sync(0xffffffffu,
+                           mbar_test(smem_u32(&sm.k_full[y % C::kKS]), (y / C::kKS) & 1))) {
+              tc_fence_after();
+              issue_s(t + 1);
+              ahead = true;
+              break;
+            }
+            if (__all_sync(0xffffffffu, mbar_test(smem_u32(&sm.p_full[x & 1]), (x >> 1) & 1)))
+              break;
+            // (bounded: the wait below reports)
+            if ((spin & 63) == 63 && __any_sync(0xffffffffu, sm.abort || globaltimer_ns() - t0 >
+                                                                             kWaitTimeoutNs))
+              break;
           }
         }
-        const int x = tc + t, st = x % C::kVS;
         ok = mbar_wait_w_ab(smem_u32(&sm.p_full[x & 1]), (x >> 1) & 1, &sm.abort);
         if (C::kSplit && ok)
           ok = mbar_wait_w_ab(smem_u32(&sm.v_full[st]), (x / C::kVS) & 1, &sm.abort);
@@ -830,7 +840,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           const bool here = (info.y >> piece_of(key_in, g.page_size)) & 1;
           const bool first = g.window == 0 || key < g.sinks;
           const bool any = here && key <= pl && (first || key > pf - g.window);
-          const bool every = here && key <= pf && (first || key > pl - g.window) && rows == R;
+          const bool every = here && key <= pf && (first || key > pl - g.window);
           if (!any) ev = -127;  // neutral
           // A value that some rows see and others do not must not reach the
           // others: 0 x NaN is NaN.  Unseen rows of V are cleared, and half-seen
