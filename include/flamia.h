@@ -429,7 +429,7 @@ flamia_status flamia_attn_bwd_gqa(const flamia_qtensor* q, const flamia_qtensor*
  * to dQ and dK after the backward.
  *
  * Token t of document b stands at position p = starts[b] + t - cu_seqlens[b]
- * (starts NULL: 0).  Pair i < rot_dim / 2 of every head's row is turned by the
+ * (starts NULL: 0; p is an int32).  Pair i < rot_dim / 2 of every head's row is turned by the
  * angle 2 pi frac(p * turns[i] / 2^64) and multiplied by mscale:
  *   (x, y) -> mscale (x cos - y sin, x sin + y cos);
  * FLAMIA_FLAG_ROPE_INVERSE turns the other way (the transpose, mscale kept).
@@ -491,6 +491,8 @@ typedef struct {
  * starts 0 gets the codes and scale bytes that flamia_quantize_tokenblock
  * gives it, bit for bit, and a call repeated on the same tokens changes nothing.
  * FLAMIA_FORMAT_TOKEN_SCALES OR-ed in: one exponent per token and head.
+ * A sequence is written in one of the two formats throughout (what is held is
+ * taken as the same one); readers take either.
  * Infinities and NaN become NaN codes and do not enter the block maximum.
  * Positions behind the last new token keep what they held.
  *
@@ -527,7 +529,12 @@ flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16, int64
  *   values code * 2^e; lse = log sum exp of the scaled scores (natural log).
  * A query that sees no key (p < 0) gets o = 0 and lse = -inf.  A NaN key or
  * value that a query sees makes its output NaN; one that it does not see, and
- * whatever lies behind a sequence's last token, changes nothing.
+ * whatever lies behind a sequence's last token, changes nothing.  Scores and sums
+ * are float32; a softmax weight is rounded to 2^-14 of itself (to FP16, 2^-11,
+ * with more than 8 query rows a sequence and K / V head on average) or 2^-24 of
+ * the row's largest weight times value scale, whichever is more (scales more than
+ * 2^60 below the largest seen count as 2^-60 of it here).  Positions stay
+ * below 2^30.
  * Query head h reads K / V head h / (H / H_kv).
  *
  *  q_bf16     BF16 rows [T][H][d], token stride in elements (multiple of 8).

@@ -92,21 +92,30 @@ def seen_keys(p, L, window=0, sinks=0):
     return m
 
 
-def attend(q, k, v, start, scale, window=0, sinks=0):
+def attend(q, k, v, start, scale, window=0, sinks=0, v_exponents=None):
     """(o [n, H, d], lse [H, n]) of one sequence: queries q [n, H, d] at
-    positions start .. over cached values k, v [L, H_kv, d]."""
+    positions start .. over cached values k, v [L, H_kv, d].
+
+    With v_exponents [L, H_kv] (those of v's scales) also what an error bound
+    needs: mass [n, H, d] = sum p |v|, and top [n, H], the largest p 448 2^e of a
+    seen key, exponents more than 60 below the largest seen counting as that."""
     q = np.asarray(q, dtype=np.float64)
     n, H, d = q.shape
     G = H // k.shape[1]
     o, lse = np.zeros((n, H, d)), np.full((H, n), -math.inf)
+    mass, top = np.zeros((n, H, d)), np.zeros((n, H))
     for i in range(n):
         m = seen_keys(start + i, len(k), window, sinks)
         if not m.any():
             continue
         for h in range(H):
             x = k[m, h // G] @ q[i, h] * scale
-            top = x.max()
-            w = np.exp(x - top)
+            high = x.max()
+            w = np.exp(x - high)
             o[i, h] = w @ v[m, h // G] / w.sum()
-            lse[h, i] = top + math.log(w.sum())
-    return o, lse
+            lse[h, i] = high + math.log(w.sum())
+            if v_exponents is not None:
+                e = v_exponents[m, h // G].astype(np.float64)
+                mass[i, h] = w @ np.abs(v[m, h // G]) / w.sum()
+                top[i, h] = (w * np.exp2(np.maximum(e, e.max() - 60))).max() * 448 / w.sum()
+    return (o, lse) if v_exponents is None else (o, lse, mass, top)

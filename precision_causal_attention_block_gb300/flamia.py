@@ -416,8 +416,10 @@ class KVCache:
                                      self.H_kv, self.d)
         self._ref = ctypes.byref(self._struct)
         self.device_index = k_codes.get_device()
-        # attend's workspace, and the sizes that it was last found large enough for
-        self._ws, self._ws_key = None, None
+        # attend's workspace, large enough for every call: it never moves, so a
+        # captured call keeps pointing at it
+        self._ws = torch.empty(flamia_attn_cache_workspace_bytes(1 << 10, 1, 1, 1, self.d),
+                               dtype=torch.uint8, device=k_codes.device)
 
     def write(self, k, v, cu_seqlens, starts, page_table, dev_status=None):
         """Quantises rows k, v [T, H_kv, d] into positions starts[b] .. of each
@@ -445,17 +447,8 @@ class KVCache:
             o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-        if ws is None:
-            key = (T, cu_seqlens.numel(), H)
-            if key != self._ws_key:
-                need = flamia_attn_cache_workspace_bytes(T, cu_seqlens.numel() - 1, H, self.H_kv,
-                                                         self.d)
-                if self._ws is None or self._ws.numel() < need:
-                    self._ws = torch.empty(need, dtype=torch.uint8, device=self.k_codes.device)
-                self._ws_key = key
-            ws = self._ws
         flamia_attn_cache(self, q, cu_seqlens, starts, page_table, softmax_scale, window, sinks, o,
-                          lse, ws, dev_status)
+                          lse, self._ws if ws is None else ws, dev_status)
         return o, lse
 
 
@@ -658,8 +651,9 @@ class TrainingCall:
 
 class DecodeCall:
     """Buffers and the sequence of C-ABI calls of one serving step over a
-    KVCache (rotary positions -> cache write -> attention) for up to T new
-    tokens of nseq sequences.  The calls read cu_seqlens, starts and page_table
+    KVCache (rotary positions -> cache write -> attention) for T rows of new
+    tokens of nseq sequences (cu_seqlens may end before T: the rows behind are
+    padding, and sequences may be empty).  The calls read cu_seqlens, starts and page_table
     on the device, so a captured step can be replayed while the caller updates
     them in place."""
 

@@ -86,18 +86,19 @@ def weight_error(T, nseq, G):
     return 2.0 ** -11 if -(-T // nseq) * G > 8 else 2.0 ** -14
 
 
-def attend_tolerance(q, k, v, scale, n_keys, o, weight):
+def attend_tolerance(q, k, scale, n_keys, o, weight, mass, top):
     """How far an output of the cached attention may be off, elementwise: its BF16
-    rounding (half a step, 2^-8 of the value) and, times the largest value seen,
-    the relative error of the softmax weights.  A score is off by at most
-    2^-19.5 + 2^-17 of scale |q| |k| (the query's split into E4M3 terms; float32
-    sums of d exact products), taken as 2^-16; a weight by twice that, by `weight`
-    (its own split into terms) and 2^-24 of the largest weight for each key
-    below their range, and 2^-20 for exp2 and the sums."""
+    rounding (half a step, 2^-8 of the value), the relative error of the softmax
+    weights (twice: the sum that divides them has it too) times mass = sum p |v|,
+    and 2^-24 of the largest weight times value scale (top) for each key below
+    the weights' range.  A score is off by at most 2^-19.5 + 2^-17 of scale |q| |k|
+    (the query's split into E4M3 terms; float32 sums of d exact products), taken
+    as 2^-16; a weight by twice that, by `weight` (its own split into terms) and
+    2^-20 for exp2 and the sums."""
     qn = np.sqrt((q ** 2).sum(-1)).max()
     kn = np.sqrt((k ** 2).sum(-1)).max()
-    rel = 2 * 2.0 ** -16 * scale * qn * kn + weight + n_keys * 2.0 ** -24 + 2.0 ** -20
-    return 2.0 ** -8 * np.abs(o) + 2 * rel * np.abs(v).max()
+    rel = 2 * 2.0 ** -16 * scale * qn * kn + weight + 2.0 ** -20
+    return 2.0 ** -8 * np.abs(o) + 2 * rel * mass + 2 * n_keys * 2.0 ** -24 * top
 
 
 def lse_tolerance(q, k, scale, lse):
@@ -115,12 +116,14 @@ def check_attend(o, lse, pair, q, n, starts, scale, window=0, sinks=0):
             continue
         qb = q[at:at + c].double().cpu().numpy()
         k, v = pair.k.values(b)[:max(starts[b], 0) + c], pair.v.values(b)[:max(starts[b], 0) + c]
-        ro, rl = S.attend(qb, k, v, starts[b], scale, window, sinks)
-        tol = attend_tolerance(qb, k, v, scale, len(k), ro,
-                               weight_error(len(q), len(n), q.shape[1] // pair.gpu.H_kv))
+        e = pair.v.scales[b][:len(k)].astype(int) - 127
+        ro, rl, mass, top = S.attend(qb, k, v, starts[b], scale, window, sinks, e)
+        tol = attend_tolerance(qb, k, scale, len(k), ro,
+                               weight_error(len(q), len(n), q.shape[1] // pair.gpu.H_kv), mass,
+                               top[..., None])
         got, gl = o[at:at + c], lse[:, at:at + c]
         assert np.isfinite(got).all(), ("o", b)
-        worst = np.max(np.abs(got - ro) / tol)
+        worst = np.max(np.abs(got - ro) / np.maximum(tol, 2.0 ** -133))  # (BF16's smallest step)
         assert worst <= 1, ("o", b, worst, np.abs(got - ro).max())
         none = rl == -math.inf
         assert np.array_equal(none, gl == -math.inf)

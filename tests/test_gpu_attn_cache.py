@@ -105,6 +105,109 @@ def test_first_token_of_zero_value_takes_the_weight(lib):
             check_attend(o, lse, pair, q, [1], [L - 1], d ** -0.5)
 
 
+def _ramp(rng, L, H_kv, d, k_of, v_of):
+    k, v = bf16(rng, (L, H_kv, d)).double(), bf16(rng, (L, H_kv, d)).double()
+    p = torch.arange(L, dtype=torch.float64)[:, None, None]
+    return (k * k_of(p)).to(torch.bfloat16), (v * v_of(p)).to(torch.bfloat16)
+
+
+RAMPS = {
+    # keys that grow along the sequence: the references move again and again
+    "growing keys": (lambda p: 0.05 + p / 120, lambda p: 1.0 + 0 * p),
+    "shrinking keys": (lambda p: 12 - p / 120, lambda p: 1.0 + 0 * p),
+    # values whose exponents climb or fall by more than their references' range
+    "climbing values": (lambda p: 1.0 + 0 * p, lambda p: 10.0 ** (-30 + p / 20)),
+    "falling values": (lambda p: 1.0 + 0 * p, lambda p: 10.0 ** (30 - p / 20)),
+    "a step up": (lambda p: 1.0 + 0 * p, lambda p: torch.where(p < 700, 1e-25, 1e12)),
+    "a step down": (lambda p: 1.0 + 0 * p, lambda p: torch.where(p < 700, 1e12, 1e-25)),
+}
+
+
+@pytest.mark.parametrize("name", sorted(RAMPS))
+@pytest.mark.parametrize("n,H,H_kv,d", [(1, 2, 2, 128), (1, 2, 1, 64), (6, 4, 2, 128),
+                                        (40, 2, 2, 64)])
+def test_changing_magnitudes_along_a_sequence(lib, name, n, H, H_kv, d):
+    """Several tiles an item (many sequences share the CTAs), scores or value
+    exponents that change by far more than the slack of the running references."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(len(name) + n)
+    L, nseq = 1230, 150
+    pair = Pair(fl, rng, [L], 64, H_kv, d)
+    k, v = _ramp(rng, L, H_kv, d, *RAMPS[name])
+    pair.write(k, v, [L], [0])
+    table = pair.table.expand(nseq, -1).contiguous()  # the same pages in every sequence
+    q1 = bf16(rng, (n, H, d))
+    q = q1.repeat(nseq, 1, 1).to(DEV)
+    o, lse = pair.gpu.attend(q, offsets([n] * nseq), i32([L - n] * nseq), table, d ** -0.5)
+    # the same sequence everywhere; cut into parts at different places
+    check_attend(o[:n], lse[:, :n].contiguous(), pair, q[:n], [n], [L - n], d ** -0.5)
+    far = (o.view(nseq, n, H, d).float() - o[:n].float()).abs().max()
+    assert float(far) <= 2.0 ** -6 * float(o[:n].float().abs().max())
+
+
+def test_nan_and_infinite_queries_touch_their_row_only(lib):
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(41)
+    for n, H in ((1, 4), (3, 4), (9, 4)):
+        pair = Pair(fl, rng, [300, 300], 64, 2, 64)
+        pair.write(bf16(rng, (600, 2, 64)), bf16(rng, (600, 2, 64)), [300, 300], [0, 0])
+        q = bf16(rng, (2 * n, H, 64)).to(DEV)
+        args = (offsets([n, n]), i32([300 - n] * 2), pair.table, 0.125)
+        good, _ = pair.gpu.attend(q, *args)
+        q[0, 1, 5] = float("nan")
+        q[n, 3, 0] = float("-inf")
+        bad, _ = pair.gpu.attend(q, *args)
+        hit = torch.zeros(2 * n, H, dtype=torch.bool, device=DEV)
+        hit[0, 1] = hit[n, 3] = True
+        assert bool(torch.isnan(bad[hit]).all()) and torch.equal(bad[~hit], good[~hit])
+
+
+def test_workspace_of_a_cache_never_moves(lib):
+    """A captured call stays valid when later calls have more rows an item."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(42)
+    pair = Pair(fl, rng, [900] * 4, 64, 1, 64)
+    pair.write(bf16(rng, (3600, 1, 64)), bf16(rng, (3600, 1, 64)), [900] * 4, [0] * 4)
+    q = bf16(rng, (4, 1, 64)).to(DEV)
+    cu, st = offsets([1] * 4), i32([899] * 4)
+    o, lse = torch.zeros_like(q), torch.zeros(1, 4, device=DEV)
+    run = lambda: pair.gpu.attend(q, cu, st, pair.table, 0.125, o=o, lse=lse)
+    run()
+    want = o.clone()
+    at = pair.gpu._ws.data_ptr()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    big = bf16(rng, (160, 8, 64)).to(DEV)
+    pair.gpu.attend(big, offsets([40] * 4), i32([860] * 4), pair.table, 0.125)
+    assert pair.gpu._ws.data_ptr() == at
+    o.zero_()
+    g.replay()
+    assert torch.equal(o, want)
+
+
+def test_no_tokens(lib):
+    from precision_causal_attention_block_gb300 import flamia as fl
+    c = fl.KVCache(2, 32, 1, 64)
+    z = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device=DEV)
+    t = torch.zeros(2, 1, dtype=torch.int32, device=DEV)
+    cu = i32([0, 0, 0])
+    before = lib.flamia_debug_launch_count()
+    c.write(z, z, cu, None, t)
+    k, _ = c.read(cu, None, t, 0)
+    o, lse = c.attend(z, cu, None, t, 0.125)
+    fl.Rotary(fl.rope_frequencies(64))(z, z, cu)
+    assert k.shape == (0, 1, 64) and o.shape == (0, 1, 64) and lse.shape == (1, 0)
+    assert lib.flamia_debug_launch_count() == before
+    # and sequences that are all idle in a padded batch
+    x = torch.ones(3, 1, 64, dtype=torch.bfloat16, device=DEV)
+    o = torch.full_like(x, 5.0)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c.write(x, x, cu, None, t, dev_status=st)
+    c.attend(x, cu, None, t, 0.125, o=o, dev_status=st)
+    assert bool((o == 5.0).all()) and not bool(c.k_codes.any()) and int(st.item()) == 0
+
+
 def test_nan_stays_where_it_is_seen(lib):
     """NaN keys and values outside the window, behind the end or in other
     sequences change nothing; a query that sees one gives NaN, its neighbours do not."""
@@ -301,17 +404,21 @@ def test_many_tiles_a_cta(lib, nseq, longest, new, H, H_kv, d, page, window, sin
     for b in range(nseq):
         qb = q[at:at + n[b]].double()
         kb, vb = k[base:base + lens[b]].double(), v[base:base + lens[b]].double()
-        p = torch.arange(starts[b], lens[b], device=DEV)[:, None]
+        i = torch.arange(starts[b], lens[b], device=DEV)[:, None]
         j = torch.arange(lens[b], device=DEV)
-        seen = j <= p
+        seen = j <= i
         if window:
-            seen &= (j > p - window) | (j < sinks)
+            seen &= (j > i - window) | (j < sinks)
         x = torch.einsum("ihd,jhd->hij", qb, kb.repeat_interleave(H // H_kv, 1)) * d ** -0.5
         x = x.masked_fill(~seen, -torch.inf)
-        ref = torch.einsum("hij,jhd->ihd", torch.softmax(x, 2), vb.repeat_interleave(H // H_kv, 1))
+        p = torch.softmax(x, 2)
+        vb = vb.repeat_interleave(H // H_kv, 1)
+        ref, mass = torch.einsum("hij,jhd->ihd", p, vb), torch.einsum("hij,jhd->ihd", p, vb.abs())
+        # a block's scale is at most 2 / 448 of its largest value
+        top = 2 * p.amax(2).t()[..., None] * vb.abs().max()
         rl = torch.logsumexp(x, 2).cpu().numpy()
-        qn, kn, vn, rn = (y.cpu().numpy() for y in (qb, kb, vb, ref))
-        tol = attend_tolerance(qn, kn, vn, d ** -0.5, lens[b], rn, weight)
+        qn, kn, rn, mass, top = (y.cpu().numpy() for y in (qb, kb, ref, mass, top))
+        tol = attend_tolerance(qn, kn, d ** -0.5, lens[b], rn, weight, mass, top)
         err = np.abs(o[at:at + n[b]].double().cpu().numpy() - rn)
         assert (err <= tol).all(), (b, (err / tol).max())
         err = np.abs(lse[:, at:at + n[b]].double().cpu().numpy() - rl)
