@@ -52,7 +52,7 @@ constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for 
 constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
-constexpr int kItemCost = 2;    // an item's own steps (queries, output) in tiles
+constexpr int kItemCost = 3;    // an item's own steps (queries, output) in tiles
 constexpr int kWholeTiles = 4;
 constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -86,6 +86,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
+}
+
+// Two bounded waits of a converged warp whose latencies overlap: a wait for a
+// phase that is long complete still takes some 150 cycles.  (From 16 rows on;
+// with 8, where HBM sets the pace, it measured slower: 99 us against 97 on 96
+// ragged contexts.)
+__device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
+                                          uint32_t parity1, const volatile int* abort) {
+  const bool a = mbar_try_wait(bar0, parity0);
+  const bool b = mbar_try_wait(bar1, parity1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return mbar_wait_w_ab(bar0, parity0, abort) && mbar_wait_w_ab(bar1, parity1, abort);
 }
 
 // Barrier of the N threads of the softmax warps that also ORs a predicate over
@@ -292,7 +304,6 @@ struct Smem {
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
   uint32_t tmem_base;
-  int stop[2];                  // softmax warps: a wait ran out (by tile parity)
   volatile int abort;
 };
 
@@ -460,7 +471,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       mbar_init(smem_u32(&sm.s_full[i]), 1);
       mbar_init(smem_u32(&sm.p_full[i]), C::kSoftmax / 32);
       mbar_init(smem_u32(&sm.pv_done[i]), 1);
-      sm.stop[i] = 0;
     }
     mbar_init(smem_u32(&sm.q_full), C::kSoftmax / 32);
     mbar_init(smem_u32(&sm.o_empty), C::kSoftmax / 32);
@@ -699,11 +709,14 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       // S^T of tile t of the segment
       auto issue_s = [&](int t) {
         const int x = tc + t, st = x % C::kKS, sb = x & 1;
+        if (lane == 0) {
 #pragma unroll
-        for (int ks = 0; ks < DIM / 32; ++ks)
-          mma_f8_w(tmem + sb * C::kNS, dk0 + st * kStep + 2 * ks, dq + 2 * ks, id_s, ks > 0);
-        tc_commit_w(smem_u32(&sm.s_full[sb]));
-        if (C::kSplit) tc_commit_w(smem_u32(&sm.k_empty[st]));
+          for (int ks = 0; ks < DIM / 32; ++ks)
+            mma_f8(tmem + sb * C::kNS, dk0 + st * kStep + 2 * ks, dq + 2 * ks, id_s, ks > 0);
+          tc_commit(smem_u32(&sm.s_full[sb]));
+          if (C::kSplit) tc_commit(smem_u32(&sm.k_empty[st]));
+        }
+        __syncwarp();
       };
       auto wait_k = [&](int t) {
         const int x = tc + t;
@@ -744,16 +757,20 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           ok = mbar_wait_w_ab(smem_u32(&sm.o_empty), (nlive - 1) & 1, &sm.abort);
         if (!ok) break;
         tc_fence_after();
+        if (lane == 0) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint64_t dv = dv0 + st * kStep + ks * (32 * DIM / 16);
-          const uint64_t dp = dp0 + ks * (1024 / 16);
-          mma_f8_w(tmem + C::kColO, dv, dp, id_o, t > 0 || ks > 0);
-          if (C::kHalfWeights)
-            mma_f8_w(tmem + C::kColO + 2 * R, dv, dp + (2 * R / 32) * (4096 / 16), id_lo, t > 0 || ks > 0);
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t dv = dv0 + st * kStep + ks * (32 * DIM / 16);
+            const uint64_t dp = dp0 + ks * (1024 / 16);
+            mma_f8(tmem + C::kColO, dv, dp, id_o, t > 0 || ks > 0);
+            if (C::kHalfWeights)
+              mma_f8(tmem + C::kColO + 2 * R, dv, dp + (2 * R / 32) * (4096 / 16), id_lo,
+                     t > 0 || ks > 0);
+          }
+          tc_commit(smem_u32(&sm.pv_done[x & 1]));
+          tc_commit(smem_u32(&sm.v_empty[st]));
         }
-        tc_commit_w(smem_u32(&sm.pv_done[x & 1]));
-        tc_commit_w(smem_u32(&sm.v_empty[st]));
+        __syncwarp();
         if (t + 1 < nt && !ahead) {
           ok = wait_k(t + 1);
           if (!ok) break;
@@ -768,13 +785,17 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   } else {
     // ------------------------------------------------------------ softmax
     constexpr int RW = C::kRows;
-    const int half = warp >> 2, r0 = half * RW;     // this thread's rows r0 ..
+    const int half = C::kHalves == 1 ? 0 : warp >> 2, r0 = half * RW;     // this thread's rows r0 ..
     const int key_in = tid & 127;                   // its key inside a tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     auto vote = [&](bool p) { return softmax_vote<C::kSoftmax>(p); };
     auto sync = [&]() { named_barrier_sync(1, C::kSoftmax); };
     int tc = 0, ss = 0, sph = 0;  // tiles so far; their place and phase in the ring of scales
     bool ok = true, late = false;  // late: a wait ran out where the warps cannot part
+    auto fail = [&]() {
+      late = true;
+      sm.abort = 1;
+    };
     // a segment's queries are loaded while the one before ends; its ring slot is
     // free again when the segment is done
     Queries<DIM, R> queries;
@@ -818,13 +839,18 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 #pragma unroll
       for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
       int e0 = -127;
+#pragma unroll 1
       for (int t = 0; t < nt; ++t, ++tc) {
         const int buf = tc & 1;
-        ok = mbar_wait_w_ab(smem_u32(&sm.s_full[buf]), (tc >> 1) & 1, &sm.abort);
-        // the scale bytes (a split ring's K barrier may be two phases on by now)
-        ok = ok && mbar_wait_w_ab(smem_u32(C::kSplit ? &sm.sc_full[ss] : &sm.k_full[ss]),
-                                  sph, &sm.abort);
-        if (!ok) sm.stop[buf] = 1;
+        // the scores and the scale bytes (a split ring's K barrier may be two phases
+        // on by now).  A wait that runs out ends the other roles' waits and this
+        // role at the next segment: until then all softmax warps keep step.
+        const uint32_t sbar = smem_u32(&sm.s_full[buf]);
+        const uint32_t cbar = smem_u32(C::kSplit ? &sm.sc_full[ss] : &sm.k_full[ss]);
+        if (R == 8 ? !mbar_wait_w_ab(sbar, (tc >> 1) & 1, &sm.abort) ||
+                         !mbar_wait_w_ab(cbar, sph, &sm.abort)
+                   : !wait_both(sbar, (tc >> 1) & 1, cbar, sph, &sm.abort))
+          fail();
         tc_fence_after();
         int ev = sm.vs[ss][key_in] - 127;  // V's exponent
         const float kf = pow2_byte(sm.ks[ss][key_in]);
@@ -834,7 +860,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           const int st = tc % C::kVS, key = info.x + key_in;
           if (C::kSplit &&
               !mbar_wait_w_ab(smem_u32(&sm.v_full[st]), (tc / C::kVS) & 1, &sm.abort))
-            sm.stop[buf] = 1;
+            fail();
           const int pf = sg.start + sg.row0 / g.G;               // positions of the first
           const int pl = sg.start + (sg.row0 + rows - 1) / g.G;  // and the last row
           const bool here = (info.y >> piece_of(key_in, g.page_size)) & 1;
@@ -920,10 +946,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           move = mx > C::kShift + C::kSlack || ev > e0 + kHigh;
         }
         move = vote(move);
-        if (sm.stop[buf]) {  // the same for all: written before the barrier
-          ok = false;
-          break;
-        }
         if (move) {  // E0, then the rows' references
           const int em = __reduce_max_sync(0xffffffffu, ev + 127);
           if (lane == 0) sm.rede[warp] = em;
@@ -986,10 +1008,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
           }
           if (t > 0) {  // O^T, once the product before has added to it
-            if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort)) {
-              late = true;
-              sm.stop[buf ^ 1] = 1;
-            }
+            if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort))
+              fail();
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 3 * RW; c += 8) {
@@ -1005,6 +1025,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             tmem_st_wait();
           }
         }
+        // (whether the product before has read P^T is asked here and looked at
+        // when the first weights are there)
+        const bool p_free =
+            tc == 0 || mbar_test(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1);
         // weights and their 8-bit terms
         const float gl = ex2_approx(static_cast<float>(e0 - evc));
         const float2 g2 = make_float2(gl, gl);
@@ -1045,12 +1069,9 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               tw[2][r / 4] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
             }
           }
-          // the product before has read P^T
-          if (c == 0 && tc >= 1 &&
-              !mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort)) {
-            late = true;
-            sm.stop[buf ^ 1] = 1;
-          }
+          if (c == 0 && !__all_sync(0xffffffffu, p_free) &&
+              !mbar_wait_w_ab(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1, &sm.abort))
+            fail();
           // P^T: key rows of 32 columns (32 bytes), 16-byte chunks swizzled
 #pragma unroll
           for (int term = 0; term < 3; ++term) {
@@ -1069,14 +1090,13 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           sph ^= 1;
         }
       }
-      if (!ok) break;
 
       // the next segment's queries come while this one's last product runs
       ok = await(ns + 1);
       // ---------------------------------------------------------- epilogue
       if (nt > 0) {
         const int x = tc - 1;
-        if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[x & 1]), (x >> 1) & 1, &sm.abort)) late = true;
+        if (!mbar_wait_w_ab(smem_u32(&sm.pv_done[x & 1]), (x >> 1) & 1, &sm.abort)) fail();
         tc_fence_after();
       }
       const int slot = sg.slot;
