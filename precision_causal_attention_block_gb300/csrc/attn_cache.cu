@@ -36,8 +36,16 @@
 // kWholeTiles tiles an item, items stay whole and the second kernel is not
 // launched.
 //
-// Warps 0-3 (R = 32: 0-7, two halves of the rows): softmax (thread = key = TMEM
-// lane); then one TMA producer warp and one MMA issuer warp.
+// Warps 0-3 (16 and 32 rows: 0-7, two halves of the rows): softmax (thread = key =
+// TMEM lane); then one TMA producer warp and one MMA issuer warp.
+//
+// Measured: 96 sequences with one new token over 16 .. 16,384 cached (32 / 8 heads
+// of 128) 98 us, 5.9 TB/s of codes and scales; one token over 131,072 (32 heads of
+// 64) 97 us, 5.6 TB/s; 48 sequences with 4 drafted tokens, a window of 4,096 (16 /
+// 4 heads of 128) 52 us, 3.8 TB/s; 505 tokens over 7,866 (16 heads of 128, two
+// sequences) 224 us, 280 TFLOP/s.  HBM bounds the first two, the softmax warps'
+// work and waits for a tile (some 2,500 cycles with 8 or 16 rows, 4,000 with 32,
+// two or three tiles at a time on an SM) the others.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -52,7 +60,11 @@ constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for 
 constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
-constexpr int kItemCost = 3;    // an item's own steps (queries, output) in tiles
+// An item's own steps (queries, first references, output) in tiles: 2 .. 6 are
+// within 4% of one another on the ragged and the windowed batch.
+constexpr int kItemCost = 3;
+// Items of at most so many tiles stay whole: 64 sequences over 512 tokens 19.6 us
+// whole, 21.7 cut and joined; over 1,024 tokens 36.9 against 34.2.
 constexpr int kWholeTiles = 4;
 constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -1235,8 +1247,10 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendArgs g) {
 // ------------------------------------------------------------------ host
 
 // Query rows side by side in one item: those of a K / V head's mean number of
-// new tokens, up to 32 (more rows reuse a K / V tile more often, but each costs
-// its share of the softmax warps' time).
+// new tokens, up to 32.  More rows than there are cost softmax time and resident
+// CTAs (4 rows a head: 98, 104, 158 us with 8, 16, 32; one row: 97, 125, 184), fewer
+// read K and V again for each item (16 rows a head: 70, 52, 73 us; 505 rows: 375,
+// 268, 224).
 int rows_per_item(int T, int ndocs, int G) {
   const long long rows = ((static_cast<long long>(T) + ndocs - 1) / ndocs) * G;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;

