@@ -84,6 +84,7 @@ struct AttendArgs {
   int* status;
   long long q_stride;
   int T, H, H_kv, G, ndocs, table_stride, num_pages, page_size, window, sinks;
+  int cap;           // positions that the page table has room for
   int whole;         // items stay whole
   float scale_log2;
 };
@@ -222,7 +223,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
   if (w.start > kMaxPos - w.n) w.start = -w.n;  // reported by the producer
   w.start = max(w.start, -kMaxPos);
   w.row_tiles = static_cast<int>((static_cast<long long>(w.n) * g.G + R - 1) / R);
-  const int end = max(w.start + w.n, 0);
+  // (no further than the page table: a wild first position costs no endless walk)
+  const int end = min(max(w.start + w.n, 0), g.cap);
   int tiles = (end + 127) >> 7;
   if (g.window > 0)
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         }
         if (lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
           const int raw = g.starts != nullptr ? __ldg(g.starts + b) : 0;
-          if (raw > kMaxPos - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
+          if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
         }
         first = false;
         u += take;
@@ -1375,7 +1377,9 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   // positions stay below 2^30: larger windows and first tokens see the same
   g.window = window < kMaxPos ? window : kMaxPos;
   g.sinks = sinks < kMaxPos ? sinks : kMaxPos;
-  g.whole = static_cast<long long>(table_stride) * cache->page_size <= 128 * kWholeTiles;
+  const long long cap = static_cast<long long>(table_stride) * cache->page_size;
+  g.cap = static_cast<int>(cap < kMaxPos ? cap : kMaxPos);
+  g.whole = cap <= 128 * kWholeTiles;
   g.scale_log2 = softmax_scale * 1.44269504088896340736f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 128)

@@ -322,6 +322,34 @@ def test_bad_pages_are_reported(lib):
         assert int(st.item()) & fl.DEV_BAD_SEQLENS, cu
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 0), (70, 1 << 29)])
+@pytest.mark.parametrize("pages", [4, 40])
+def test_first_positions_far_outside_the_table(lib, window, sinks, pages):
+    """They are reported, the walk over keys ends with the page table (a walk to the
+    position would be 2^22 tiles, seconds), and the other sequence is served."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(33)
+    pair = Pair(fl, rng, [128, 128], 32, 2, 64)
+    pair.write(bf16(rng, (256, 2, 64)), bf16(rng, (256, 2, 64)), [128, 128], [0, 0])
+    table = torch.zeros(2, pages, dtype=torch.int32, device=DEV)
+    table[:, :4] = pair.table
+    table[1, 4:] = pair.table[1, 0]
+    q = bf16(rng, (2, 2, 64)).to(DEV)
+    cu = offsets([1, 1])
+    good, _ = pair.gpu.attend(q, cu, i32([127, 127]), table, 0.125, window, sinks)
+    for start in (1 << 29, (1 << 30) - 1, 1 << 30, (1 << 31) - 1):
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        starts = i32([127, start])
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        o, _ = pair.gpu.attend(q, cu, starts, table, 0.125, window, sinks, dev_status=st)
+        end.record()
+        torch.cuda.synchronize()
+        assert int(st.item()) == fl.DEV_BAD_PAGE, start
+        assert torch.equal(o[0], good[0]) and bool(torch.isfinite(o[1].float()).all()), start
+        assert begin.elapsed_time(end) < 500.0, start
+
+
 def test_repeatable_and_two_streams(lib):
     """The same call twice gives the same bits; two calls at once on two streams, a
     workspace each, too."""
