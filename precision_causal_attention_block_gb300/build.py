@@ -19,6 +19,7 @@ LIB = os.path.join(BUILD, "libflamia.so")
 SOURCES = ["abi.cu", "quantize.cu", "worklist.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd128.cu",
            "attn_short.cu",
            "attn_bwd_pair.cu", "rope.cu", "cache.cu", "attn_cache.cu",
+           "attn_cache_rows.cu",
            "probe_mma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

@@ -39,55 +39,25 @@
 // Warps 0-3 (16 and 32 rows: 0-7, two halves of the rows): softmax (thread = key =
 // TMEM lane); then one TMA producer warp and one MMA issuer warp.
 //
+// (More query rows than 128 a K / V head: attn_cache_rows.cu.)
+//
 // Measured: 96 sequences with one new token over 16 .. 16,384 cached (32 / 8 heads
 // of 128) 98 us, 5.9 TB/s of codes and scales; one token over 131,072 (32 heads of
 // 64) 97 us, 5.6 TB/s; 48 sequences with 4 drafted tokens, a window of 4,096 (16 /
-// 4 heads of 128) 52 us, 3.8 TB/s; 505 tokens over 7,866 (16 heads of 128, two
-// sequences) 224 us, 280 TFLOP/s.  HBM bounds the first two, the softmax warps'
+// 4 heads of 128) 52 us, 3.8 TB/s.  HBM bounds the first two, the softmax warps'
 // work and waits for a tile (some 2,500 cycles with 8 or 16 rows, 4,000 with 32,
-// two or three tiles at a time on an SM) the others.
+// two or three tiles at a time on an SM) the last.
 #include <cuda_bf16.h>
 
-#include <atomic>
 #include <cmath>
 
-#include "paged.cuh"
+#include "attend.cuh"
 
 namespace flamia {
 namespace {
 
-constexpr int kMaxCtas = 512;   // runs of a launch (the workspace is sized for it)
-constexpr int kSlots = 2 * kMaxCtas;  // partial results
-constexpr int kSegSlots = 4;
-constexpr int kMaxPos = 1 << 30;
-// An item's own steps (queries, first references, output) in tiles: 2 .. 6 are
-// within 4% of one another on the ragged and the windowed batch.
-constexpr int kItemCost = 3;
-// Items of at most so many tiles stay whole: 64 sequences over 512 tokens 19.6 us
-// whole, 21.7 cut and joined; over 1,024 tokens 36.9 against 34.2.
-constexpr int kWholeTiles = 4;
-constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kUnset = 1e30f; // -reference of a row that has seen no key yet
-constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
-constexpr int kLow = 60;
-
-struct AttendArgs {
-  const uint8_t *k_scales, *v_scales;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* o;
-  float* lse;
-  const int32_t *cu, *starts, *table;
-  int4* joins;       // [kMaxCtas][2]: items to join
-  float* stats;      // [kSlots][R] log2 sum 2^x
-  float* partial;    // [kSlots][R][d] o
-  int* status;
-  long long q_stride;
-  int T, H, H_kv, G, ndocs, table_stride, num_pages, page_size, window, sinks;
-  int cap;           // positions that the page table has room for
-  int whole;         // items stay whole
-  float scale_log2;
-};
+constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 
 // ------------------------------------------------------------------ PTX
 
@@ -99,18 +69,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
           dst),
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
-}
-
-// Two bounded waits of a converged warp whose latencies overlap: a wait for a
-// phase that is long complete still takes some 150 cycles.  (From 16 rows on;
-// with 8, where HBM sets the pace, it measured slower: 99 us against 97 on 96
-// ragged contexts.)
-__device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t parity0, uint32_t bar1,
-                                          uint32_t parity1, const volatile int* abort) {
-  const bool a = mbar_try_wait(bar0, parity0);
-  const bool b = mbar_try_wait(bar1, parity1);
-  if (__all_sync(0xffffffffu, a && b)) return true;
-  return mbar_wait_w_ab(bar0, parity0, abort) && mbar_wait_w_ab(bar1, parity1, abort);
 }
 
 // Barrier of the N threads of the softmax warps that also ORs a predicate over
@@ -139,11 +97,6 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// A pair of floats rounded to FP16.
-__device__ __forceinline__ uint32_t half2_of(float2 a) {
-  const __half2 h = __floats2half2_rn(a.x, a.y);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // Four FP16 weights (two pairs): their E4M3 codes in one word, and 32 (w - code)
 // in place of the weights (exact).
 __device__ __forceinline__ uint32_t take_term(uint32_t& a, uint32_t& b) {
@@ -193,64 +146,6 @@ __device__ __forceinline__ uint32_t take_term(float2& a, float2& b) {
 
 __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
-}
-
-__device__ __forceinline__ float pow2_byte(int byte) {
-  return byte > 0 ? __uint_as_float(static_cast<uint32_t>(byte) << 23) : 0x1p-127f;
-}
-
-// ------------------------------------------------------------------ work
-
-// Sequence b's share of the work: row tiles x K / V heads items of `tiles` key
-// tiles (an upper bound over its row tiles: a segment that runs past its item's
-// last tile is cut there).  An item is `units` long: kItemCost, then a unit
-// for each tile; one unit if items stay whole.
-struct SeqWork {
-  int s, n, start;     // packed rows [s, s + n) at positions start ..
-  int row_tiles, tiles, units;
-  __device__ __forceinline__ long long total(int H_kv) const {
-    return static_cast<long long>(row_tiles) * H_kv * units;
-  }
-};
-
-template <int R>
-__device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
-  SeqWork w;
-  const DocRange r = doc_range(g.cu, b, g.T);
-  w.s = r.s;
-  w.n = r.e - r.s;
-  w.start = g.starts != nullptr ? __ldg(g.starts + b) : 0;
-  if (w.start > kMaxPos - w.n) w.start = -w.n;  // reported by the producer
-  w.start = max(w.start, -kMaxPos);
-  w.row_tiles = static_cast<int>((static_cast<long long>(w.n) * g.G + R - 1) / R);
-  // (no further than the page table: a wild first position costs no endless walk)
-  const int end = min(max(w.start + w.n, 0), g.cap);
-  int tiles = (end + 127) >> 7;
-  if (g.window > 0)
-    tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
-                           ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);
-  w.tiles = max(tiles, 1);
-  w.units = g.whole ? 1 : w.tiles + kItemCost;
-  return w;
-}
-
-// A run of one item's key tiles, handed from the producer to the other roles.
-struct Segment {
-  int s, n, start;  // as SeqWork; s < 0: no more work
-  int hk, row0;     // K / V head; first row (token-major, then query head)
-  int i0, i1;       // its key tiles: list positions i0 .. i1 - 1
-  int ns, wt;       // list position i is key tile i (i < ns) or i - ns + wt
-  int slot;         // partial result slot, or -1: the whole item
-};
-
-__device__ __forceinline__ int tile_of(const Segment& g, int i) {
-  return i < g.ns ? i : i - g.ns + g.wt;
-}
-
-// The piece of a tile (a page of less than 128 rows, or the whole tile) that
-// holds one of its keys.
-__device__ __forceinline__ int piece_of(int key_in, int page_size) {
-  return page_size == 32 ? key_in >> 5 : page_size == 64 ? key_in >> 6 : 0;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -320,73 +215,6 @@ struct Smem {
   uint32_t tmem_base;
   volatile int abort;
 };
-
-// a * b / c and a / c for a, b, c >= 0, in 32 bits where they suffice (a 64-bit
-// division takes some hundred cycles, and the first copies wait for it).
-__device__ __forceinline__ long long mul_div(long long a, long long b, long long c) {
-  const long long ab = a * b;
-  if (((ab | c) >> 32) == 0)
-    return static_cast<uint32_t>(ab) / static_cast<uint32_t>(c);
-  return ab / c;
-}
-__device__ __forceinline__ long long div_up(long long a, long long c) {
-  return mul_div(a + c - 1, 1, c);
-}
-
-// CTAs that get a run: at least two tiles each, as far as there are any.
-__device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long total) {
-  const int least = g.whole ? 1 : kItemCost + 2;
-  return min(static_cast<long long>(gridDim.x), div_up(total, least));
-}
-
-// Total units, and this CTA's run of them: [u0, u1), starting at unit `off` of
-// sequence b.  Every thread sums a stretch of sequences; the one whose stretch
-// holds u0 walks it.
-template <int R, int kThreads, class Sm>
-__device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (g.ndocs + kThreads - 1) / kThreads;
-  const int b0 = min(tid * each, g.ndocs), b1 = min(b0 + each, g.ndocs);
-  long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_work<R>(g, b).total(g.H_kv);
-  long long inc = sum;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += y;
-  }
-  if (lane == 31) sm.scan[warp] = inc;
-  if (tid == 0) sm.plan_b = g.ndocs;
-  __syncthreads();
-  long long before = inc - sum, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sm.scan[w];
-    total += sm.scan[w];
-  }
-  const long long ctas = active_ctas(g, total);
-  const long long c = blockIdx.x;
-  const long long u0 = c < ctas ? mul_div(total, c, ctas) : total;
-  const long long u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;
-  if (tid == 0) {
-    sm.plan_u0 = u0;
-    sm.plan_u1 = u1;
-    sm.plan_total = total;
-  }
-  if (u0 < u1 && before <= u0 && u0 < before + sum) {
-    long long off = u0 - before;
-    int b = b0;
-    SeqWork w = seq_work<R>(g, b);
-    while (b < b1 - 1 && off >= w.total(g.H_kv)) {
-      off -= w.total(g.H_kv);
-      w = seq_work<R>(g, ++b);
-    }
-    sm.plan_b = b;
-    sm.plan_seq = w;
-    sm.plan_off = off;
-  }
-  __syncthreads();
-}
 
 // The queries of a segment held by one softmax thread: 16-byte chunks of rows
 // r0 + tid / (d / 8), r0 = 0, kPer, 2 kPer, ...
@@ -1181,81 +1009,21 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   }
 }
 
-// Joins the parts of an item that several CTAs shared (part 0 in slot 1 of the
-// CTA before, the others in slots 0 from this CTA on): o = sum 2^(lg_p - lg) o_p.
-// One warp a row, without shared memory, so that blocks fit beside the first
-// kernel's CTAs and are there when it ends.
-template <int DIM, int R>
-__global__ void __launch_bounds__(256) join_kernel(const AttendArgs g) {
-  constexpr int E = DIM / 32;  // elements a lane
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  // (no start_next here: the next call's CTAs, let in among these, made that
-  // call slower by up to 20%)
-  wait_for_previous();
-  const int4 j0 = g.joins[2 * blockIdx.x], j1 = g.joins[2 * blockIdx.x + 1];
-  const int parts = j0.x;
-  if (parts <= 0 || r >= static_cast<long long>(j0.z) * g.G - j1.x) return;
-  const int c0 = blockIdx.x;
-  auto at = [&](int p) {  // the part's row
-    return static_cast<size_t>(p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 + p - 1)) * R + r;
-  };
-  float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) {
-    const float x = g.stats[at(p)];
-    m = x > m || x != x ? x : m;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float x = __shfl_xor_sync(0xffffffffu, m, o);
-    m = x > m || x != x ? x : m;  // NaN stays
-  }
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[E] = {};
-  for (int p0 = 0; p0 < parts; p0 += 32) {
-    const float wt = p0 + lane < parts ? exp2f(g.stats[at(p0 + lane)] - ref) : 0.f;
-    l += wt;
-    const int n = min(32, parts - p0);
-#pragma unroll 8
-    for (int p = 0; p < n; ++p) {
-      const float w = __shfl_sync(0xffffffffu, wt, p);
-      const float* x = g.partial + at(p0 + p) * DIM + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(x);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(x);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int i = (j1.x + r) / g.G, hq = j0.w * g.G + (j1.x + r) % g.G;
-  if (lane == 0 && g.lse != nullptr)
-    g.lse[static_cast<size_t>(hq) * g.T + j0.y + i] = (ref + log2f(l)) * kLn2;
-  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(
-      g.o + (static_cast<size_t>(j0.y + i) * g.H + hq) * DIM + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    out[e / 2] = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e] * inv,
-                                       inv == 0.f ? 0.f : acc[e + 1] * inv);
-}
-
 // ------------------------------------------------------------------ host
 
 // Query rows side by side in one item: those of a K / V head's mean number of
-// new tokens, up to 32.  More rows than there are cost softmax time and resident
-// CTAs (4 rows a head: 98, 104, 158 us with 8, 16, 32; one row: 97, 125, 184), fewer
-// read K and V again for each item (16 rows a head: 70, 52, 73 us; 505 rows: 375,
-// 268, 224).
+// new tokens, up to 32, or 256 (attn_cache_rows.cu).  More rows than there are cost
+// softmax time and resident CTAs (4 rows a head: 98, 104, 158 us with 8, 16, 32; one
+// row: 97, 125, 184), fewer read K and V again for each item (16 rows a head: 70,
+// 52, 73 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 54 and
+// 70 us, 96 rows 70 and 73, 128 rows 89 and 77; one sequence over 4,096, 128 rows 32
+// and 38, 256 rows 46 and 52; 64 sequences over 100, 400 rows 66 and 42; 505 rows over
+// 7,866 224 and 137.
+constexpr int kManyRows = 256;
+
 int rows_per_item(int T, int ndocs, int G) {
   const long long rows = ((static_cast<long long>(T) + ndocs - 1) / ndocs) * G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 32 : kManyRows;
 }
 
 struct Workspace {
@@ -1263,10 +1031,11 @@ struct Workspace {
 };
 Workspace layout(int R, int d) {
   Workspace w;
+  const size_t slots = R == kManyRows ? 2 * kRowsCtas : kSlots;
   w.joins = 0;
   w.stats = align_up(sizeof(int4) * 2 * kMaxCtas, 256);
-  w.partial = w.stats + align_up(sizeof(float) * static_cast<size_t>(kSlots) * R, 256);
-  w.total = w.partial + sizeof(float) * static_cast<size_t>(kSlots) * R * d;
+  w.partial = w.stats + align_up(sizeof(float) * slots * R, 256);
+  w.total = w.partial + sizeof(float) * slots * R * d;
   return w;
 }
 
@@ -1294,28 +1063,12 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM, R>)) + 1024;
   static_assert(Cfg<DIM, R>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
   const int grid = min(kMaxCtas, num_sms() * Cfg<DIM, R>::kCtas);
-  auto go = [&]() {
-    return launch_after(attend_kernel<DIM, R>, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk, mv,
-                        g);
-  };
-  // The kernel's shared-memory limit is raised once on a device; again if a
-  // launch fails (a new context does not have it).
   static std::atomic<unsigned long long> raised{0};
-  auto raise = [&]() {
-    return cudaFuncSetAttribute(attend_kernel<DIM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                smem) == cudaSuccess;
-  };
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FLAMIA_ERR_CUDA;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(raised.load(std::memory_order_relaxed) & bit)) {
-    if (!raise()) return FLAMIA_ERR_CUDA;
-    raised.fetch_or(bit, std::memory_order_relaxed);
-  }
-  if (!go() && (!raise() || !go())) return FLAMIA_ERR_CUDA;
-  if (g.whole) return FLAMIA_OK;
-  return launch_after(join_kernel<DIM, R>, dim3(grid, R / 8), 256, 0, s, g) ? FLAMIA_OK
-                                                                           : FLAMIA_ERR_CUDA;
+  return launch_large(attend_kernel<DIM, R>, raised, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk,
+                      mv, g) &&
+                 (g.whole || launch_join<DIM, R>(grid, s, g))
+             ? FLAMIA_OK
+             : FLAMIA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1382,6 +1135,7 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   g.whole = cap <= 128 * kWholeTiles;
   g.scale_log2 = softmax_scale * 1.44269504088896340736f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (R == kManyRows) return attend_rows(cache, g, s);
   if (d == 128)
     return R == 8 ? launch<128, 8>(cache, g, s)
                   : R == 16 ? launch<128, 16>(cache, g, s) : launch<128, 32>(cache, g, s);

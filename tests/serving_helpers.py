@@ -82,7 +82,8 @@ def weight_error(T, nseq, G):
     """Relative rounding of a softmax weight: three E4M3 terms of 4 bits hold it
     to 2^-14; items of 16 or 32 rows (more than 8 rows a sequence and K / V head on
     average) round it to FP16 first, half a step of which is 2^-11, and its terms
-    hold those 11 bits (E4M3, E4M3 and the 3 bits of E5M2)."""
+    hold those 11 bits (E4M3, E4M3 and the 3 bits of E5M2); items of 256 rows multiply
+    it as FP16."""
     return 2.0 ** -11 if -(-T // nseq) * G > 8 else 2.0 ** -14
 
 
