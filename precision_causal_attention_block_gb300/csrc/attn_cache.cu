@@ -39,7 +39,7 @@
 // Warps 0-3 (16 and 32 rows: 0-7, two halves of the rows): softmax (thread = key =
 // TMEM lane); then one TMA producer warp and one MMA issuer warp.
 //
-// (More query rows than 128 a K / V head: attn_cache_rows.cu.)
+// (More query rows than 96 a K / V head: attn_cache_rows.cu.)
 //
 // Measured: 96 sequences with one new token over 16 .. 16,384 cached (32 / 8 heads
 // of 128) 98 us, 5.9 TB/s of codes and scales; one token over 131,072 (32 heads of
@@ -1016,14 +1016,14 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 // softmax time and resident CTAs (4 rows a head: 98, 104, 158 us with 8, 16, 32; one
 // row: 97, 125, 184), fewer read K and V again for each item (16 rows a head: 70,
 // 52, 73 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 54 and
-// 70 us, 96 rows 70 and 73, 128 rows 89 and 77; one sequence over 4,096, 128 rows 32
-// and 38, 256 rows 46 and 52; 64 sequences over 100, 400 rows 66 and 42; 505 rows over
-// 7,866 224 and 137.
+// 61 us, 96 rows 70 and 64, 128 rows 89 and 67; one sequence over 4,096, 64 rows 26
+// and 33, 128 rows 32 and 35; 64 sequences over 100, 400 rows 66 and 41; 505 rows over
+// 7,866 224 and 122.
 constexpr int kManyRows = 256;
 
 int rows_per_item(int T, int ndocs, int G) {
   const long long rows = ((static_cast<long long>(T) + ndocs - 1) / ndocs) * G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 32 : kManyRows;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 96 ? 32 : kManyRows;
 }
 
 struct Workspace {

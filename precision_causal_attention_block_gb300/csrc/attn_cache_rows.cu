@@ -23,13 +23,13 @@
 // tile's softmax runs the tensor core works for the other.  Runs of key tiles, parts
 // and joins are those of attend.cuh.
 //
-// Measured: 505 tokens over 7,866 (16 heads of 128, two sequences) 137 us, 460
-// TFLOP/s (32 rows an item: 224 us, 280 TFLOP/s).  A key tile takes some 5,600 cycles
-// where the tensor core is busy for 2,300: the softmax of a row tile (2,800) and its
-// two products (2,000 with their issue) follow one another, and the other row
-// tile fills the gaps only in part.  A CTA's first scores come 16,000 cycles after its
+// Measured: 505 tokens over 7,866 (16 heads of 128, two sequences) 122 us, 515
+// TFLOP/s (32 rows an item: 224 us, 280 TFLOP/s); 512 over 8,000 (32 / 8 heads, four
+// sequences) 340 us.  A key tile takes some 5,000 cycles where the tensor core is
+// busy for 2,300: the softmax of a row tile (2,800) and its two products follow one
+// another, and the other row tile fills the gaps only in part.  A CTA's first scores come 16,000 cycles after its
 // start (plan, queries), its output takes 5,000.  Scores of 64 keys in two buffers,
-// so that the softmax does not wait for them, took longer (150 us: twice the
+// so that the softmax does not wait for them, took longer (146 us: twice the
 // products to issue); K and V loaded and converted side by side, 139 registers
 // and more code, too (181: spills, and misses in the instruction cache).
 #include <cmath>
@@ -110,31 +110,32 @@ __device__ __forceinline__ bool group_vote(int id, bool p) {
 // D (+)= A * B, FP16 x FP16 -> F32: A and B in shared memory, or A in tensor
 // memory (two elements a 32-bit column).  idesc_f8's fields serve: the operand
 // formats are 0 for FP16, too.  Descriptors come as their low words (the address)
-// and one high word.
+// and one high word.  Issued by one elected thread of a converged warp: under a
+// branch for one lane the eight products of a tile took 850 cycles to issue
+// (505 tokens over 7,866: 137 us against 122).
 __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t hi,
                                         uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
       "mov.b64 da, {%1, %3};\n\t"
       "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
                                            uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
       "setp.ne.b32 p, %5, 0;\n\t"
       "mov.b64 db, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
-// Keeps the compiler from holding every product's operands in registers.
-__device__ __forceinline__ void opaque(uint32_t& x) { asm volatile("" : "+r"(x)); }
 
 // A warpgroup's registers a thread from here on.  The kernel starts with 128 each;
 // 2 x 168 + 112 + 64 is what four warpgroups then had.
@@ -897,18 +898,15 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (s < 0) break;
         if (nt <= 0) continue;
         auto issue_s = [&](int y, int w) {  // scores of row tile w and key tile y
-          if (lane == 0) {
-              uint32_t a = q0 + w * kStep, b = k0 + (y & 1) * kStep;
-            opaque(a);
-            opaque(b);
+          const uint32_t a = q0 + w * kStep, b = k0 + (y & 1) * kStep;
+          __syncwarp();
 #pragma unroll
-            for (int ks = 0; ks < DIM / 16; ++ks) {
-              const uint32_t at = (ks >> 2) * (C::kBlock / 16) + (ks & 3) * 2;
-              mma_f16(tmem + w * 128, a + at, b + at, hi, id_s, ks > 0);
-            }
-            tc_commit(smem_u32(&sm.s_full[w]));
-            if (w == tiles - 1) tc_commit(smem_u32(&sm.k_empty[y & 1]));
+          for (int ks = 0; ks < DIM / 16; ++ks) {
+            const uint32_t at = (ks >> 2) * (C::kBlock / 16) + (ks & 3) * 2;
+            mma_f16(tmem + w * 128, a + at, b + at, hi, id_s, ks > 0);
           }
+          tc_commit_w(smem_u32(&sm.s_full[w]));
+          if (w == tiles - 1) tc_commit_w(smem_u32(&sm.k_empty[y & 1]));
           __syncwarp();
         };
         auto wait_k = [&](int y) {
@@ -933,17 +931,14 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
             if (!ok) break;
             ++x[w];
             tc_fence_after();
-            if (lane == 0) {
-                uint32_t a = tmem + w * 128, b = v0 + (y & 1) * kStep;
-              opaque(a);
-              opaque(b);
+            __syncwarp();
+            const uint32_t a = tmem + w * 128, b = v0 + (y & 1) * kStep;
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                mma_f16_ts(tmem + C::kColO + w * DIM, a + ks * 8, b + ks * (2048 / 16), hi, id_o,
-                           t > 0 || ks > 0);
-              tc_commit(smem_u32(&sm.pv_done[w]));
-              if (w == tiles - 1) tc_commit(smem_u32(&sm.v_empty[y & 1]));
-            }
+            for (int ks = 0; ks < 8; ++ks)
+              mma_f16_ts(tmem + C::kColO + w * DIM, a + ks * 8, b + ks * (2048 / 16), hi, id_o,
+                         t > 0 || ks > 0);
+            tc_commit_w(smem_u32(&sm.pv_done[w]));
+            if (w == tiles - 1) tc_commit_w(smem_u32(&sm.v_empty[y & 1]));
             __syncwarp();
             if (t + 1 < nt) issue_s(y + 1, w);
           }
@@ -953,8 +948,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
       if (!ok) {
         sm.abort = 1;
         // what was issued ends before shared memory and tensor memory go
-        if (lane == 0) tc_commit(smem_u32(&sm.drained));
         __syncwarp();
+        tc_commit_w(smem_u32(&sm.drained));
         mbar_wait_w(smem_u32(&sm.drained), 0);
       }
     }
