@@ -297,8 +297,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   Smem<DIM, R>& sm = *reinterpret_cast<Smem<DIM, R>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  start_next();
-
   if (tid == 0) {
     for (int i = 0; i < C::kKS; ++i) {
       mbar_init(smem_u32(&sm.k_full[i]), 1);
@@ -326,6 +324,9 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   if (warp == kIssuer) {
     tmem_alloc(smem_u32(&sm.tmem_base), C::kCols);
     tmem_relinquish();
+    // (only now: the next kernel's CTAs, which wait for this one's end, must not hold
+    // tensor memory that a CTA of this one still asks for)
+    start_next();
   }
   wait_for_previous();
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,

@@ -416,8 +416,8 @@ class KVCache:
                                      self.H_kv, self.d)
         self._ref = ctypes.byref(self._struct)
         self.device_index = k_codes.get_device()
-        # attend's workspace, large enough for every call: it never moves, so a
-        # captured call keeps pointing at it
+        # attend's workspace, large enough for every call (42 MB, 21 with heads of 64):
+        # it never moves, so a captured call keeps pointing at it
         self._ws = torch.empty(flamia_attn_cache_workspace_bytes(1 << 10, 1, 1, 1, self.d),
                                dtype=torch.uint8, device=k_codes.device)
 
