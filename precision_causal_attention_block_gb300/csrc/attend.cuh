@@ -17,9 +17,11 @@ constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kRowsCtas = 160;        // the same with 256 rows an item
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
-// An item's own steps (queries, first references, output) in tiles: 2 .. 6 are
-// within 4% of one another on the ragged and the windowed batch.
-constexpr int kItemCost = 3;
+// An item's own steps (queries, first references, output) in tiles.  2 .. 6 are
+// within 4% of one another on the ragged and the windowed batch; with 256 rows an
+// item, 505 tokens over 7,866: 124, 121, 118, 120, 119 us with 1, 3, 5, 7, 9.
+template <int R>
+constexpr int kItemCost = R == 256 ? 5 : 3;
 // Items of at most so many tiles stay whole: 64 sequences over 512 tokens 19.6 us
 // whole, 21.7 cut and joined; over 1,024 tokens 36.9 against 34.2.
 constexpr int kWholeTiles = 4;
@@ -96,7 +98,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
                            ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);
   w.tiles = max(tiles, 1);
-  w.units = g.whole ? 1 : w.tiles + kItemCost;
+  w.units = g.whole ? 1 : w.tiles + kItemCost<R>;
   return w;
 }
 
@@ -132,8 +134,9 @@ __device__ __forceinline__ long long div_up(long long a, long long c) {
 }
 
 // CTAs that get a run: at least two tiles each, as far as there are any.
+template <int R>
 __device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long total) {
-  const int least = g.whole ? 1 : kItemCost + 2;
+  const int least = g.whole ? 1 : kItemCost<R> + 2;
   return min(static_cast<long long>(gridDim.x), div_up(total, least));
 }
 
@@ -162,7 +165,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
   }
-  const long long ctas = active_ctas(g, total);
+  const long long ctas = active_ctas<R>(g, total);
   const long long c = blockIdx.x;
   const long long u0 = c < ctas ? mul_div(total, c, ctas) : total;
   const long long u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;

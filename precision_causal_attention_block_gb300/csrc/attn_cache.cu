@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sg.s = -1;
       } else {
         const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
-        const int cost = g.whole ? 0 : kItemCost;
+        const int cost = g.whole ? 0 : kItemCost<R>;
         const int i0 = max(o - cost, 0);
         const int i1 = g.whole ? w.tiles : max(o + take - cost, 0);
         sg.s = w.s;
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (first && i0 > 0) {
           // the second CTA of an item has it joined: parts are the CTA before
           // this one (slot 1) and slots 0 from here on
-          const long long ctas = active_ctas(g, total), c = blockIdx.x, ui = u0 - o;
-          if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost) {
+          const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
+          if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost<R>) {
             const long long last = div_up((ui + w.units) * ctas, total) - 1;
             join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, hk);
             join1 = make_int4(sg.row0, 0, 0, 0);
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 // 52, 73 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 54 and
 // 61 us, 96 rows 70 and 64, 128 rows 89 and 67; one sequence over 4,096, 64 rows 26
 // and 33, 128 rows 32 and 35; 64 sequences over 100, 400 rows 66 and 41; 505 rows over
-// 7,866 224 and 122.
+// 7,866 224 and 118.
 constexpr int kManyRows = 256;
 
 int rows_per_item(int T, int ndocs, int G) {

@@ -23,7 +23,7 @@
 // tile's softmax runs the tensor core works for the other.  Runs of key tiles, parts
 // and joins are those of attend.cuh.
 //
-// Measured: 505 tokens over 7,866 (16 heads of 128, two sequences) 122 us, 515
+// Measured: 505 tokens over 7,866 (16 heads of 128, two sequences) 118 us, 530
 // TFLOP/s (32 rows an item: 224 us, 280 TFLOP/s); 512 over 8,000 (32 / 8 heads, four
 // sequences) 340 us.  A key tile takes some 5,000 cycles where the tensor core is
 // busy for 2,300: the softmax of a row tile (2,800) and its two products follow one
@@ -235,7 +235,7 @@ struct Walk {
     RowSegment sg{};
     while (u < u1) {
       const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
-      const int cost = g.whole ? 0 : kItemCost;
+      const int cost = g.whole ? 0 : kItemCost<R>;
       const int i0 = max(o - cost, 0);
       const int i1 = g.whole ? w.tiles : max(o + take - cost, 0);
       sg.seq = b;
@@ -263,8 +263,8 @@ struct Walk {
       if (first && i0 > 0) {
         // the second CTA of an item has it joined: parts are the CTA before this
         // one (slot 1) and slots 0 from here on
-        const long long ctas = active_ctas(g, total), c = blockIdx.x, ui = u0 - o;
-        if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost) {
+        const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
+        if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost<R>) {
           const long long last = div_up((ui + w.units) * ctas, total) - 1;
           join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, hk);
           join1 = make_int4(sg.row0, 0, 0, 0);
