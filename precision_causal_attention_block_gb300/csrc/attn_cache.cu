@@ -18,9 +18,12 @@
 //   w = 2^(x + eV - ref + kShift),   l = sum w 2^(E0 - eV),
 //   o = O^T 2^E0 / l,   log2 sum 2^x = ref - kShift - E0 + log2 l,
 // with one integer reference a row (a running maximum of x + eV) and one
-// integer E0 (a running maximum of eV) for all rows.  Keys whose values are
-// more than 2^kLow below E0 (zero values under a heavy first token) enter the
-// references with eV raised to E0 - kLow and have their weight lowered
+// integer E0 (a running maximum of eV) for all rows.  When E0 rises, l is put by as
+// log2 sum 2^x of the keys so far and starts anew: lifted to the new E0 it could
+// leave float32 (values that climb while scores fall), and a reference that moved
+// along would push the next weights, which count as much, under their range.  Keys
+// whose values are more than 2^kLow below E0 (zero values under a heavy first token)
+// enter the references with eV raised to E0 - kLow and have their weight lowered
 // afterwards, so that l keeps them and stays inside float32.  References move
 // only when a tile exceeds them by more than kSlack, which the one barrier of
 // a tile votes on; O^T is then rescaled in tensor memory.
@@ -194,7 +197,9 @@ struct Smem {
   alignas(128) uint8_t vs[C::kSS][128];
   alignas(16) float qf[R];      // 2^e of a row x softmax scale x log2 e
   alignas(16) float nref[R];    // kShift - reference
-  alignas(16) float fac[R], facl[R];  // changes of scale of O^T and l
+  alignas(16) float fac[R];     // change of scale of O^T and l
+  float ve[R];                  // 2^E0 for o
+  float past[R];                // log2 sum 2^x before E0 last rose, -inf: none
   int has[R];                   // the row has a reference
   bool nan[2][128];  // a half-seen key's value holds a NaN (by tile parity)
   alignas(16) int pos[R];       // position of a row's token, -1: no such row
@@ -670,6 +675,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sm.orow[tid] = live ? (sg.s + i) * g.H + hq : -1;
         sm.nref[tid] = C::kShift;
         sm.has[tid] = 0;
+        sm.past[tid] = -INFINITY;
       }
       if (nt > 0) {
         queries.split(sm.q, sm.qf, g.scale_log2, tid);
@@ -681,6 +687,19 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       float2 l[RW / 2];
 #pragma unroll
       for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
+      // l of a row over the keys (threads); the caller's barrier, then sum_of(row)
+      auto sum_keys = [&]() {
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+          float s = r & 1 ? l[r / 2].y : l[r / 2].x;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          if (lane == 0) sm.red[warp & 3][r0 + r] = s;
+        }
+      };
+      auto sum_of = [&](int r) {
+        return (sm.red[0][r] + sm.red[1][r]) + (sm.red[2][r] + sm.red[3][r]);
+      };
       int e0 = -127;
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, ++tc) {
@@ -795,13 +814,20 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           // rows without a reference are measured from 0
           if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = C::kShift;
           sync();
-          int top = -127, rise = 0;
+          int top = -127;
 #pragma unroll
           for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
           if (t == 0) {
             e0 = top;
-          } else if (top > e0 + kHigh) {
-            rise = top - e0;
+          } else if (top > e0 + kHigh) {  // (the same in all warps)
+            sum_keys();
+            sync();
+            if (tid < R)
+              sm.past[tid] = log2_add(sm.past[tid], __log2f(sum_of(tid)) - sm.nref[tid] -
+                                                        static_cast<float>(e0));
+            sync();
+#pragma unroll
+            for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
             e0 = top;
           }
           evc = max(ev, e0 - kLow);
@@ -820,33 +846,27 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             const float a = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
                                   fmaxf(sm.red[2][tid], sm.red[3][tid]));
             // A row keeps its reference while it holds; one that has seen
-            // nothing (or nothing but NaN) has none.  If E0 rose by more than
-            // 40, the references follow, so that l (whose terms are at most
-            // 2^(8 + kLow + rise)) stays inside float32.
+            // nothing (or nothing but NaN) has none.
             const float n0 = sm.nref[tid];
-            float n1 = n0, f = 1.f, fl = 1.f;
+            float n1 = n0, f = 1.f;
             if (tid >= rows) {
               n1 = -kUnset;
             } else if (!sm.has[tid]) {
               const bool now = a > -INFINITY;
               n1 = now ? n0 - ceilf(a - C::kShift) : kUnset;
               sm.has[tid] = now;
-            } else {
-              const float up = fmaxf(a > C::kShift + C::kSlack ? ceilf(a - C::kShift) : 0.f,
-                                     static_cast<float>(rise - 40));
-              const float by = fmaxf(up, 0.f);
+            } else if (a > C::kShift + C::kSlack) {
+              const float by = ceilf(a - C::kShift);
               n1 = n0 - by;
               f = ex2_approx(-by);
-              fl = ex2_approx(static_cast<float>(rise) - by);
             }
             sm.nref[tid] = n1;
             sm.fac[tid] = f;
-            sm.facl[tid] = fl;
           }
           sync();
 #pragma unroll
           for (int r = 0; r < RW; r += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sm.facl + r0 + r);
+            const float4 f = *reinterpret_cast<const float4*>(sm.fac + r0 + r);
             l[r / 2] = __fmul2_rn(l[r / 2], make_float2(f.x, f.y));
             l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
           }
@@ -943,20 +963,19 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         tc_fence_after();
       }
       const int slot = sg.slot;
-      // l over the keys (threads)
-#pragma unroll
-      for (int r = 0; r < RW; ++r) {
-        float s = r & 1 ? l[r / 2].y : l[r / 2].x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) sm.red[warp & 3][r0 + r] = s;
-      }
+      sum_keys();
       sync();
       if (tid < rows) {
-        const float s = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
-        sm.fac[tid] = s == 0.f ? 0.f : 1.f / s;  // nothing seen: l = 0
-        const float lg = s == 0.f ? -INFINITY
-                                  : log2f(s) - sm.nref[tid] - static_cast<float>(e0);
+        const float s = sum_of(tid), past = sm.past[tid];
+        float lg = s == 0.f ? -INFINITY : log2f(s) - sm.nref[tid] - static_cast<float>(e0);
+        if (past == -INFINITY) {
+          sm.fac[tid] = s == 0.f ? 0.f : 1.f / s;  // nothing seen: l = 0
+          sm.ve[tid] = e0 < -126 ? 0x1p-127f : exp2i(e0);
+        } else {
+          lg = log2_add(past, lg);
+          sm.fac[tid] = exp2f(-sm.nref[tid] - lg);
+          sm.ve[tid] = 1.f;
+        }
         const int orow = sm.orow[tid];
         if (slot >= 0)
           g.stats[static_cast<size_t>(slot) * R + tid] = lg;
@@ -964,7 +983,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           g.lse[static_cast<size_t>(orow % g.H) * g.T + orow / g.H] = lg * kLn2;
       }
       sync();
-      const float ve = e0 < -126 ? 0x1p-127f : exp2i(e0);
       const bool active = DIM == 128 || key_in < DIM;
 #pragma unroll
       for (int c = 0; c < RW; c += 8) {
@@ -984,7 +1002,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             float v = 0.f;
             if (nt > 0 && f != 0.f)
               v = fmaf(fmaf(__uint_as_float(lo[i]), 0x1p-5f, __uint_as_float(m[i])), 0x1p-5f,
-                       __uint_as_float(h[i])) * f * ve;
+                       __uint_as_float(h[i])) * f * sm.ve[r];
             if (slot >= 0)
               g.partial[(static_cast<size_t>(slot) * R + r) * DIM + key_in] = v;
             else

@@ -11,8 +11,9 @@
 // enter the scores of a key, as in attn_cache.cu:
 //   w = 2^(x + eV - ref),  l = sum w 2^(E0 - eV),
 //   o = O 2^E0 / l,        log2 sum 2^x = ref - E0 + log2 l,
-// but a thread owns a row here, so maxima and sums need no other thread.  A row's
-// reference is an integer that moves when a tile exceeds it by more than kSlack;
+// l put by when E0 rises, as there; but a thread owns a row here, so maxima and sums
+// need no other thread.  A row's reference is an integer that moves when a tile
+// exceeds it by more than kSlack;
 // where 32 keys have one K and one V exponent (always, with exponents of 32-token
 // blocks) their largest score comes with a load from tensor memory.
 //
@@ -609,6 +610,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 
       float l = 0.f, nref = 0.f;  // nref: -reference
       bool has = false;           // the row has a reference
+      float past = -INFINITY;     // log2 sum 2^x before E0 last rose
       int e0 = -127;
 #pragma unroll 1
       for (int t = 0; t < (active ? nt : 0); ++t, ++x) {
@@ -620,11 +622,11 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         tc_fence_after();
         const int top = max(max(sm.col[ss][0].top, sm.col[ss][1].top),
                             max(sm.col[ss][2].top, sm.col[ss][3].top));
-        int rise = 0;
         if (t == 0) {
           e0 = top;
-        } else if (top > e0 + kHigh) {
-          rise = top - e0;
+        } else if (top > e0 + kHigh) {  // (as in attn_cache.cu)
+          past = log2_add(past, __log2f(l) - nref - static_cast<float>(e0));
+          l = 0.f;
           e0 = top;
         }
         const int k0 = tile_of(sg, sg.i0 + t) * 128;
@@ -696,9 +698,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
             for (int j = 0; j < 32; j += 2) mx = fmax3(mx, y[j], y[j + 1]);
           }
         }
-        // Where it does not, or there is none yet, it moves.  If E0 rose by more than
-        // 40 the references follow, so that l stays inside float32.
-        const bool need = has ? mx > kSlack || rise > 0 : mx > -INFINITY;
+        // Where it does not, or there is none yet, it moves.
+        const bool need = has ? mx > kSlack : mx > -INFINITY;
         if (__any_sync(0xffffffffu, need)) {
           float f = 1.f;
           if (need) {
@@ -706,11 +707,10 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
               nref -= ceilf(mx);
               has = true;
             } else {
-              const float by = fmaxf(mx > kSlack ? ceilf(mx) : 0.f,
-                                     static_cast<float>(max(rise - 40, 0)));
+              const float by = ceilf(mx);
               nref -= by;
               f = ex2_approx(-by);
-              l *= ex2_approx(static_cast<float>(rise) - by);
+              l *= f;
             }
           }
           if (t > 0) {  // O, once the product before has added to it
@@ -800,9 +800,14 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           if (!mbar_wait_w_ab(obar, (x - 1) & 1, &sm.abort)) fail();
           tc_fence_after();
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: l = 0
-        const float lg = l == 0.f ? -INFINITY : log2f(l) - nref - static_cast<float>(e0);
-        const float ve = e0 < -126 ? 0x1p-127f : exp2i(e0);
+        float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: l = 0
+        float lg = l == 0.f ? -INFINITY : log2f(l) - nref - static_cast<float>(e0);
+        float ve = e0 < -126 ? 0x1p-127f : exp2i(e0);
+        if (past != -INFINITY) {
+          lg = log2_add(past, lg);
+          inv = exp2f(-nref - lg);
+          ve = 1.f;
+        }
         const size_t out = static_cast<size_t>(sg.s + tok) * g.H + hq;
         if (live) {
           if (slot >= 0)
