@@ -486,10 +486,11 @@ typedef struct {
  * format FLAMIA_FORMAT_MXFP8: one exponent per 32-token block (positions 32 i ..
  * 32 i + 31) and head, the rule of flamia_quantize_tokenblock over the new
  * tokens of the block; where the block already holds tokens (starts[b] inside
- * it) the exponent is the larger of that and the held one, and if it grew the
- * held codes c become RNE_E4M3(c 2^(e_old - e)).  So a prompt written at
- * starts 0 gets the codes and scale bytes that flamia_quantize_tokenblock
- * gives it, bit for bit, and a call repeated on the same tokens changes nothing.
+ * it) the exponent is the larger of that and the largest held one, and the codes c
+ * of held tokens with a smaller one become RNE_E4M3(c 2^(e_old - e)).  So a prompt
+ * written at starts 0 gets the codes and scale bytes that flamia_quantize_tokenblock
+ * gives it, bit for bit, and a call repeated at once on the same tokens changes
+ * nothing.
  * FLAMIA_FORMAT_TOKEN_SCALES OR-ed in: one exponent per token and head.
  * A sequence is written in one of the two formats throughout (what is held is
  * taken as the same one); readers take either.

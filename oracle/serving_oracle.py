@@ -60,16 +60,16 @@ class Cache:
             end = min(p0 + size, start + n)
             new = x[p - start:end - start]
             e = O.roundup_exponent(np.abs(new).max(axis=(0, 2)))  # [H]
-            if p > p0:
-                was = scales[p0].astype(int) - 127
-                e = np.maximum(e, was)
-                for h in np.nonzero(e > was)[0]:
-                    held = codes[p0:p, h]
+            if p > p0:  # (rows that were written again may have exponents of their own)
+                was = scales[p0:p].astype(int) - 127  # [held, H]
+                e = np.maximum(e, was.max(axis=0))
+                for r, h in np.argwhere(was < e):
+                    held = codes[p0 + r, h]
                     nan = (held & 0x7F) == 0x7F
                     value = np.where(nan, 0.0, O.e4m3_decode(np.where(nan, 0, held)))
-                    again = O.e4m3_encode(value * 2.0 ** float(was[h] - e[h]))
-                    codes[p0:p, h] = np.where(nan, 0x7F, again)
-                    scales[p0:p, h] = e[h] + 127
+                    again = O.e4m3_encode(value * 2.0 ** float(was[r, h] - e[h]))
+                    codes[p0 + r, h] = np.where(nan, 0x7F, again)
+                    scales[p0 + r, h] = e[h] + 127
             c = O.e4m3_encode(new * np.ldexp(1.0, -e)[None, :, None])
             codes[p:end] = np.where(bad[p - start:end - start], 0x7F, c)
             scales[p:end] = (e + 127).astype(np.uint8)

@@ -157,9 +157,10 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
   const long long row = blk.row(g);
   uint8_t* codes = (blk.kv ? g.codes[1] : g.codes[0]) + row * DIM;
   uint8_t* scales = (blk.kv ? g.scales[1] : g.scales[0]) + row;
-  // what the block holds before the call keeps its exponent, or a larger one
+  // what the block holds before the call (a lane's row) keeps its exponent, or a larger
+  // one; rows that were written again may have exponents of their own
   int held = -127;
-  if (!TOK && blk.lo > 0) held = static_cast<int>(scales[0]) - 127;
+  if (!TOK && lane < blk.lo) held = static_cast<int>(scales[lane]) - 127;
 
   uint32_t all = 0;
 #pragma unroll
@@ -191,7 +192,8 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
       }
     }
   } else {
-    const int e = max(held, roundup_exponent(__uint_as_float(all << 16)));
+    int e = roundup_exponent(__uint_as_float(all << 16));
+    if (blk.lo > 0) e = max(e, __reduce_max_sync(0xffffffffu, held));
     const float inv = exp2i(-e);  // e in [-127, 120]: 2^-e is a normal float
     if (full) {
 #pragma unroll
@@ -203,20 +205,25 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
         const int r = i * RPI + sub;
         if (r >= blk.lo && r < blk.hi) out[i * RPI * (DIM / 8)] = encode(x[i], inv);
       }
-      const bool grew = blk.lo > 0 && e > held;
+      const bool grew = lane < blk.lo && e > held;
       if (lane < blk.hi && (lane >= blk.lo || grew)) scales[lane] = static_cast<uint8_t>(e + 127);
-      if (grew) {
-        // the held codes are rounded again under the larger exponent
-        const float f = held - e < -126 ? 0.f : exp2i(held - e);
+      const unsigned again = __ballot_sync(0xffffffffu, grew);
+      if (again) {
+        // held codes are rounded again under a larger exponent
 #pragma unroll 1
-        for (int r = sub; r < blk.lo; r += RPI) {
-          uint2* at = reinterpret_cast<uint2*>(codes + r * DIM) + chunk;
-          uint2 c = *at;
-          const float2 v0 = e4m3x2_to_float2(c.x & 0xFFFFu), v1 = e4m3x2_to_float2(c.x >> 16);
-          const float2 v2 = e4m3x2_to_float2(c.y & 0xFFFFu), v3 = e4m3x2_to_float2(c.y >> 16);
-          c.x = cvt_e4m3x4(v0.x * f, v0.y * f, v1.x * f, v1.y * f);
-          c.y = cvt_e4m3x4(v2.x * f, v2.y * f, v3.x * f, v3.y * f);
-          *at = c;
+        for (int r0 = 0; r0 < blk.lo; r0 += RPI) {
+          const int r = r0 + sub;  // (below 32)
+          const int by = __shfl_sync(0xffffffffu, held, r) - e;
+          if ((again >> r) & 1) {
+            const float f = by < -126 ? 0.f : exp2i(by);
+            uint2* at = reinterpret_cast<uint2*>(codes + r * DIM) + chunk;
+            uint2 c = *at;
+            const float2 v0 = e4m3x2_to_float2(c.x & 0xFFFFu), v1 = e4m3x2_to_float2(c.x >> 16);
+            const float2 v2 = e4m3x2_to_float2(c.y & 0xFFFFu), v3 = e4m3x2_to_float2(c.y >> 16);
+            c.x = cvt_e4m3x4(v0.x * f, v0.y * f, v1.x * f, v1.y * f);
+            c.y = cvt_e4m3x4(v2.x * f, v2.y * f, v3.x * f, v3.y * f);
+            *at = c;
+          }
         }
       }
     }
