@@ -94,7 +94,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
   const DocRange r = doc_range(g.cu, b, g.T);
   w.s = r.s;
   w.n = r.e - r.s;
-  w.start = g.starts != nullptr ? __ldg(g.starts + b) : 0;
+  w.start = g.starts != nullptr ? g.starts[b] : 0;
   if (w.start > kMaxPos - w.n) w.start = -w.n;  // reported by the producer
   w.start = max(w.start, -kMaxPos);
   w.row_tiles = static_cast<int>((static_cast<long long>(w.n) * g.G + R - 1) / R);

@@ -238,9 +238,9 @@ struct Queries {
       w[it] = make_uint4(0, 0, 0, 0);
       if (r < R && row < static_cast<long long>(sg.n) * g.G) {
         const int i = row / g.G, hq = sg.hk * g.G + row - i * g.G;
-        w[it] = __ldg(reinterpret_cast<const uint4*>(g.q + (sg.s + i) * g.q_stride +
-                                                     static_cast<long long>(hq) * DIM +
-                                                     tid % kLanes * 8));
+        w[it] = *reinterpret_cast<const uint4*>(g.q + (sg.s + i) * g.q_stride +
+                                                static_cast<long long>(hq) * DIM +
+                                                tid % kLanes * 8);
       }
     }
   }
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           }
         }
         if (lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
-          const int raw = g.starts != nullptr ? __ldg(g.starts + b) : 0;
+          const int raw = g.starts != nullptr ? g.starts[b] : 0;
           if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
         }
         first = false;
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
                (g.window == 0 || kp + piece > wlo || kp < g.sinks);
         const int slot = kp / g.page_size;
         in_page = kp - slot * g.page_size;
-        return need && slot < g.table_stride ? __ldg(row + slot) : -1;
+        return need && slot < g.table_stride ? row[slot] : -1;
       };
       bool need;
       int in_page;

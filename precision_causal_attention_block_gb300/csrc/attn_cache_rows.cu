@@ -272,7 +272,7 @@ struct Walk {
         }
       }
       if (reports && hk == 0 && rt == 0 && i0 == 0) {
-        const int raw = g.starts != nullptr ? __ldg(g.starts + b) : 0;
+        const int raw = g.starts != nullptr ? g.starts[b] : 0;
         if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
       }
       first = false;
@@ -311,7 +311,7 @@ struct Block32 {
     for (int it = 0; it < kIters; ++it) {
       w[it] = make_uint4(0, 0, 0, 0);
       if ((seen >> (it * kPer + lane / kLanes)) & 1)
-        w[it] = __ldg(reinterpret_cast<const uint4*>(src + it * kPer * DIM));
+        w[it] = *reinterpret_cast<const uint4*>(src + it * kPer * DIM);
     }
   }
   // As FP16 into rows row0 .. of an operand tile.
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         const int key0 = tile_of(sg, i) * 128 + cw * 32, slot = key0 / g.page_size;
         const bool need = i < sg.i1 && key0 < hi &&
                           (g.window == 0 || key0 + 32 > wlo || key0 < g.sinks);
-        const int page = need && slot < g.table_stride ? __ldg(table + slot) : -1;
+        const int page = need && slot < g.table_stride ? table[slot] : -1;
         const bool there = page >= 0 && page < g.num_pages;
         if (need && !there) report(g.status, FLAMIA_DEV_BAD_PAGE);
         // (a cache that fits the memory has fewer than 2^31 of them)
@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         next.seen = __ballot_sync(0xffffffffu,
                                   row >= 0 && any(tile_of(sg, i) * 128 + cw * 32 + lane));
         const long long at = static_cast<long long>(max(row, 0)) * 32 + lane;
-        kbyte1 = __ldg(g.k_scales + at);
-        vbyte1 = __ldg(g.v_scales + at);
+        kbyte1 = g.k_scales[at];
+        vbyte1 = g.v_scales[at];
       };
       auto load_codes = [&](const uint8_t* codes) {
         next.load(codes + static_cast<long long>(max(row, 0)) * 32 * DIM, lane);

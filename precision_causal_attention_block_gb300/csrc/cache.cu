@@ -54,8 +54,8 @@ __device__ __forceinline__ bool find_block(const CacheArgs& g, long long unit, i
   blk.kv = hk >= g.H_kv;
   blk.h = hk - blk.kv * g.H_kv;
   const int b = warp_last_not_above(
-      g.ndocs, vb, lane, [&](int i) { return (__ldg(g.cu + i) >> 5) + 2 * i; });
-  const int start = g.starts != nullptr ? __ldg(g.starts + b) : 0;
+      g.ndocs, vb, lane, [&](int i) { return (g.cu[i] >> 5) + 2 * i; });
+  const int start = g.starts != nullptr ? g.starts[b] : 0;
   const DocRange r = doc_range(g.cu, b, g.T);
   if (r.e <= r.s) return false;
   if (start < 0) {
@@ -71,7 +71,7 @@ __device__ __forceinline__ bool find_block(const CacheArgs& g, long long unit, i
   const long long slot = p0 / g.page_size;
   blk.page = -1;
   if (slot < g.table_stride)
-    blk.page = __ldg(g.table + static_cast<long long>(b) * g.table_stride + slot);
+    blk.page = g.table[static_cast<long long>(b) * g.table_stride + slot];
   blk.in_page = static_cast<int>(p0 - slot * g.page_size);
   blk.token = r.s + p0 - start;
   return true;
@@ -143,14 +143,14 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
   if (full) {
 #pragma unroll
     for (int i = 0; i < NLD; ++i)
-      x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPI * stride));
+      x[i] = *reinterpret_cast<const uint4*>(src + i * RPI * stride);
   } else {
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
       const int r = i * RPI + sub;
       x[i] = make_uint4(0, 0, 0, 0);
       if (r >= blk.lo && r < blk.hi)
-        x[i] = __ldg(reinterpret_cast<const uint4*>(src + i * RPI * stride));
+        x[i] = *reinterpret_cast<const uint4*>(src + i * RPI * stride);
     }
   }
   if (!valid_page(g, blk, lane)) return;
@@ -257,9 +257,9 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheAr
   for (int i = 0; i < NLD; ++i) {
     const int r = i * RPI + sub;
     x[i] = make_uint2(0, 0);
-    if (r >= blk.lo && r < blk.hi) x[i] = __ldg(reinterpret_cast<const uint2*>(codes + r * DIM) + chunk);
+    if (r >= blk.lo && r < blk.hi) x[i] = reinterpret_cast<const uint2*>(codes + r * DIM)[chunk];
   }
-  const int sc = __ldg(scales + lane);
+  const int sc = scales[lane];
 #pragma unroll
   for (int i = 0; i < NLD; ++i) {
     const int r = i * RPI + sub;

@@ -15,10 +15,10 @@ constexpr int kMaxSeqs = 1 << 20;
 struct DocRange {
   int s, e;
 };
-__device__ __forceinline__ DocRange doc_range(const int32_t* __restrict__ cu, int b, int T) {
+__device__ __forceinline__ DocRange doc_range(const int32_t* cu, int b, int T) {
   DocRange r;
-  r.s = min(max(__ldg(cu + b), 0), T);
-  r.e = min(max(__ldg(cu + b + 1), r.s), T);
+  r.s = min(max(cu[b], 0), T);
+  r.e = min(max(cu[b + 1], r.s), T);
   return r;
 }
 
@@ -45,11 +45,11 @@ __device__ __forceinline__ int warp_last_not_above(int n, int x, int lane, Key k
 }
 
 // Light validation of cu_seqlens, spread over a grid's threads.
-__device__ __forceinline__ void check_offsets(const int32_t* __restrict__ cu, int ndocs, int T,
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int ndocs, int T,
                                               long long thread, long long nthreads, int* status) {
   for (long long i = thread; i < ndocs; i += nthreads)
-    if (__ldg(cu + i) > __ldg(cu + i + 1)) report(status, FLAMIA_DEV_BAD_SEQLENS);
-  if (thread == 0 && (__ldg(cu) != 0 || __ldg(cu + ndocs) > T))
+    if (cu[i] > cu[i + 1]) report(status, FLAMIA_DEV_BAD_SEQLENS);
+  if (thread == 0 && (cu[0] != 0 || cu[ndocs] > T))
     report(status, FLAMIA_DEV_BAD_SEQLENS);
 }
 
@@ -58,7 +58,10 @@ __device__ __forceinline__ void check_offsets(const int32_t* __restrict__ cu, in
 // launch_after, which lets its CTAs start while the kernel before it in the
 // stream drains, and begins with wait_for_previous: nothing is read or written
 // before that kernel has completed.  start_next lets the kernel behind it do the
-// same.
+// same.  A kernel's lifetime then begins before the end of the one that writes its
+// inputs, so all of them (rows, codes, scales, offsets, positions, page tables) are
+// read by ordinary loads behind the wait and through pointers without __restrict__,
+// never as read-only data (__ldg), which neither the wait nor its clobber binds.
 __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

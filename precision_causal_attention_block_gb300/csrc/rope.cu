@@ -105,9 +105,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
     const int t = t0 + warp;
     int pos = INT_MIN;
     if (t < g.T) {
-      const int b = warp_last_not_above(g.ndocs, t, lane, [&](int i) { return __ldg(g.cu + i); });
+      const int b = warp_last_not_above(g.ndocs, t, lane, [&](int i) { return g.cu[i]; });
       const DocRange r = doc_range(g.cu, b, g.T);
-      if (t >= r.s && t < r.e) pos = (g.starts != nullptr ? __ldg(g.starts + b) : 0) + t - r.s;
+      if (t >= r.s && t < r.e) pos = (g.starts != nullptr ? g.starts[b] : 0) + t - r.s;
     }
     if (lane == 0) s_pos[warp] = pos;
   }
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
   for (int i = tid; i < kTok * half; i += kRopeThreads) {
     const int tk = i / half, pair = i - tk * half;
     const unsigned long long ph =
-        static_cast<unsigned long long>(static_cast<long long>(s_pos[tk])) * __ldg(g.turns + pair);
+        static_cast<unsigned long long>(static_cast<long long>(s_pos[tk])) * g.turns[pair];
     float sn, cs;
     sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f, &sn, &cs);
     s_trig[tk][pair] = make_float2(cs * g.mscale, sn * g.mscale * g.sign);
