@@ -542,7 +542,8 @@ flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16, int64
  *  o_bf16     [T, H, d] BF16.   lse  float [H, T], or NULL.
  *  window     0: every earlier key.   sinks  >= 0; needs window > 0 if > 0.
  *  ws         flamia_attn_cache_workspace_bytes bytes, 256-byte aligned; calls
- *             that may overlap need one each.  Nothing is kept in it.
+ *             that may overlap (on two streams, in two graphs, from two threads on
+ *             one stream: a call is two kernels) need one each.  Nothing is kept in it.
  * cu_seqlens may end before T: rows behind the last sequence are not written
  * (lse columns neither).  T == 0 enqueues nothing.
  */

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 
 import torch
 
@@ -416,10 +417,10 @@ class KVCache:
                                      self.H_kv, self.d)
         self._ref = ctypes.byref(self._struct)
         self.device_index = k_codes.get_device()
-        # attend's workspace, large enough for every call (42 MB, 21 with heads of 64):
-        # it never moves, so a captured call keeps pointing at it
-        self._ws = torch.empty(flamia_attn_cache_workspace_bytes(1 << 10, 1, 1, 1, self.d),
-                               dtype=torch.uint8, device=k_codes.device)
+
+    @property
+    def _ws(self):  # (of eager calls)
+        return _eager_workspace(*_current())[0]
 
     def write(self, k, v, cu_seqlens, starts, page_table, dev_status=None):
         """Quantises rows k, v [T, H_kv, d] into positions starts[b] .. of each
@@ -440,16 +441,38 @@ class KVCache:
     def attend(self, q, cu_seqlens, starts, page_table, softmax_scale: float, window: int = 0,
                sinks: int = 0, o=None, lse=None, ws=None, dev_status=None):
         """(o, lse) of queries q [T, H, d] at positions starts[b] .. over the
-        cache.  ws None: a workspace that the cache keeps, for calls that do
-        not overlap."""
+        cache.  ws None: the workspace of the current stream and thread (42 MB, made
+        by their first call, shared by all caches), or, while a graph is captured, one
+        that belongs to the graph: calls that overlap never share one."""
         T, H = q.shape[0], q.shape[1]
         if o is None:
             o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         flamia_attn_cache(self, q, cu_seqlens, starts, page_table, softmax_scale, window, sinks, o,
-                          lse, self._ws if ws is None else ws, dev_status)
+                          lse, ws, dev_status)
         return o, lse
+
+
+class _Held(threading.local):
+    """Workspaces of a thread's eager attend calls, (tensor, pointer, bytes) by (device,
+    stream).  Nothing is kept in one, so calls that follow one another share it; two
+    threads on one stream do not, as one's kernels may come between the other's."""
+
+    def __init__(self):
+        self.ws = {}
+
+
+_HELD = _Held()
+
+
+def _eager_workspace(dev, stream):
+    held = _HELD.ws.get((dev, stream))
+    if held is None:
+        size = flamia_attn_cache_workspace_bytes(1 << 10, 1, 1, 1, 128)  # enough for all calls
+        t = torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", dev))
+        held = _HELD.ws[dev, stream] = t, t.data_ptr(), size
+    return held
 
 
 def flamia_cache_write(cache: KVCache, k, v, cu_seqlens, starts, page_table, dev_status=None):
@@ -489,7 +512,7 @@ def flamia_attn_cache_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: 
 
 
 def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax_scale, window,
-                      sinks, o, lse, ws, dev_status=None):
+                      sinks, o, lse, ws=None, dev_status=None):
     dev, stream = _current()
     if q.dim() != 3:
         raise RuntimeError("q: flamia needs BF16 rows [T, heads, d]")
@@ -505,12 +528,24 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
         lp = lse.data_ptr()
         if lse.get_device() != dev:
             _elsewhere("lse")
-    if cache.device_index != dev or o.get_device() != dev or ws.get_device() != dev:
-        _elsewhere("cache, o and ws")
+    if cache.device_index != dev or o.get_device() != dev:
+        _elsewhere("cache and o")
+    if ws is None:
+        if torch._C._cuda_isCurrentStreamCapturing():
+            # from the graph's pool: replays of two graphs may overlap
+            ws = torch.empty(flamia_attn_cache_workspace_bytes(T, n, H, cache.H_kv, cache.d),
+                             dtype=torch.uint8, device=q.device)
+            wp, wn = ws.data_ptr(), ws.nbytes
+        else:
+            _, wp, wn = _eager_workspace(dev, stream)
+    else:
+        wp, wn = ws.data_ptr(), ws.nbytes
+        if ws.get_device() != dev:
+            _elsewhere("ws")
     st = (_LIB or load()).flamia_attn_cache(
         cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
         _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
-        softmax_scale, window, sinks, o.data_ptr(), lp, ws.data_ptr(), ws.nbytes,
+        softmax_scale, window, sinks, o.data_ptr(), lp, wp, wn,
         _ints(dev_status, "dev_status", 0, dev), stream)
     if st:
         _check(st, "flamia_attn_cache")
