@@ -540,6 +540,8 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
             _, wp, wn = _eager_workspace(dev, stream)
     else:
         wp, wn = ws.data_ptr(), ws.nbytes
+        if not ws.is_contiguous():
+            raise RuntimeError("ws: expected a contiguous tensor")
         if ws.get_device() != dev:
             _elsewhere("ws")
     st = (_LIB or load()).flamia_attn_cache(

@@ -1,0 +1,45 @@
+"""What the Python binding hands to the cached attention (no GPU: the library's entry
+point is replaced, and CPU tensors count as being on the current device)."""
+import types
+
+import pytest
+import torch
+
+
+@pytest.fixture
+def attend(monkeypatch):
+    from precision_causal_attention_block_gb300 import flamia as fl
+    calls = []
+
+    class Lib:
+        def flamia_attn_cache(self, *a):
+            calls.append(a)
+            return 0
+
+    monkeypatch.setattr(fl, "_LIB", Lib())
+    monkeypatch.setattr(fl, "_current", lambda: (-1, 0))
+    cache = types.SimpleNamespace(d=64, H_kv=2, device_index=-1, _ref=None)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    cu = torch.tensor([0, 3], dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    big = torch.zeros(4096, dtype=torch.uint8)
+
+    def run(scale=0.125, window=0, sinks=0, ws=big):
+        fl.flamia_attn_cache(cache, q, cu, None, table, scale, window, sinks, torch.empty_like(q),
+                             None, ws)
+        return calls[-1]
+
+    run.calls = calls
+    run.big = big
+    return run
+
+
+def test_a_workspace_is_one_piece_of_memory(attend):
+    """An expanded tensor has as many bytes as its shape says and owns one of them."""
+    a = attend()
+    assert a[15] == attend.big.data_ptr() and a[16] == 4096
+    n = len(attend.calls)
+    for ws in (attend.big[:1].expand(1 << 26), attend.big[::2], attend.big.view(64, 64).t()):
+        with pytest.raises(RuntimeError, match="ws"):
+            attend(ws=ws)
+    assert len(attend.calls) == n
