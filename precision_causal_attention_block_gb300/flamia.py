@@ -242,6 +242,7 @@ def flamia_attn_bwd_gqa(q: QTensor, k: QTensor, v: QTensor, dout: QTensor, D, ls
 
 
 _BF16, _I32 = torch.bfloat16, torch.int32
+_INT_MAX = (1 << 31) - 1
 
 
 def _current():
@@ -544,10 +545,13 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
             raise RuntimeError("ws: expected a contiguous tensor")
         if ws.get_device() != dev:
             _elsewhere("ws")
+    if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
+        # (ctypes would keep the low 32 bits; positions end before, negative ones are refused)
+        window, sinks = (max(-1, min(x, _INT_MAX)) for x in (window, sinks))
     st = (_LIB or load()).flamia_attn_cache(
         cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
         _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
-        softmax_scale, window, sinks, o.data_ptr(), lp, wp, wn,
+        float(softmax_scale), window, sinks, o.data_ptr(), lp, wp, wn,
         _ints(dev_status, "dev_status", 0, dev), stream)
     if st:
         _check(st, "flamia_attn_cache")

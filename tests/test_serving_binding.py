@@ -2,6 +2,7 @@
 point is replaced, and CPU tensors count as being on the current device)."""
 import types
 
+import numpy as np
 import pytest
 import torch
 
@@ -43,3 +44,19 @@ def test_a_workspace_is_one_piece_of_memory(attend):
         with pytest.raises(RuntimeError, match="ws"):
             attend(ws=ws)
     assert len(attend.calls) == n
+
+
+def test_windows_and_first_tokens_beyond_32_bits(attend):
+    """They see the same as the largest of 32 bits; negative ones stay negative."""
+    top = (1 << 31) - 1
+    for given, want in ((0, 0), (5, 5), (top, top), (top + 1, top), ((1 << 32) + 5, top),
+                        (1 << 63, top), (-1, -1), (-(1 << 32), -1), (5 - (1 << 32), -1)):
+        a = attend(window=given, sinks=0)
+        assert (a[11], a[12]) == (want, 0), given
+        a = attend(window=7, sinks=given)
+        assert (a[11], a[12]) == (7, want), given
+
+
+def test_any_number_is_a_scale(attend):
+    for s in (0.25, 1, np.float32(0.25), np.float64(0.25), torch.tensor(0.25)):
+        assert type(attend(scale=s)[10]) is float
