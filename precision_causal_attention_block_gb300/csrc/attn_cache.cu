@@ -209,7 +209,7 @@ struct Smem {
   uint64_t k_full[C::kKS], k_empty[C::kKS], v_full[C::kVS], v_empty[C::kVS];
   uint64_t sc_full[C::kSS];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t q_full, o_empty;
+  uint64_t q_full, o_empty, drained;
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Segment seg[kSegSlots];
   int2 tile[C::kSS];            // first key; pieces that were loaded, kWhole
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     }
     mbar_init(smem_u32(&sm.q_full), C::kSoftmax / 32);
     mbar_init(smem_u32(&sm.o_empty), C::kSoftmax / 32);
+    mbar_init(smem_u32(&sm.drained), 1);
     for (int i = 0; i < kSegSlots; ++i) {
       mbar_init(smem_u32(&sm.seg_full[i]), 1);
       mbar_init(smem_u32(&sm.seg_empty[i]), kProducer + 1);  // softmax warps, MMA issuer
@@ -629,7 +630,13 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       tc += nt;
       ++nlive;
     }
-    if (!ok) sm.abort = 1;
+    if (!ok) {
+      sm.abort = 1;
+      // what was issued ends before shared memory and tensor memory go
+      if (lane == 0) tc_commit(smem_u32(&sm.drained));
+      __syncwarp();
+      mbar_wait_w(smem_u32(&sm.drained), 0);
+    }
   } else {
     // ------------------------------------------------------------ softmax
     constexpr int RW = C::kRows;

@@ -32,3 +32,14 @@ def test_every_kernel_waits_for_the_one_before():
             end = body.find("__global__ void", 1)
             body = body[:end] if end > 0 else body
             assert "wait_for_previous();" in body, (name, body[:120])
+
+
+@pytest.mark.parametrize("name", ["attn_cache.cu", "attn_cache_rows.cu"])
+def test_products_in_flight_end_before_their_memory_goes(name):
+    """A CTA whose waits run out frees its tensor memory and exits: the issuer's way out
+    commits what it issued to a barrier and waits there, with a limit."""
+    code = _code(name)
+    failed = [code[m.end():m.end() + 400] for m in re.finditer(r"if \(!ok\) \{", code)]
+    assert any(re.search(r"tc_commit(_w)?\(smem_u32\(&sm\.drained\)\);.*"
+                         r"mbar_wait_w\(smem_u32\(&sm\.drained\), 0\);", f, re.S) for f in failed)
+    assert "mbar_init(smem_u32(&sm.drained), 1);" in code
