@@ -594,8 +594,8 @@ class TrainingCall:
                  hadamard: bool = False, causal: bool = True, H_kv=None,
                  deterministic_dq: bool = False, dq_accum: str = "fp32", schedule: str = "dynamic",
                  ds_rows: bool = False, token_scales: bool = False,
-                 ds_zero_count: bool = False, bwd_ctas: str = "rule", rope: Rotary = None,
-                 device="cuda"):
+                 ds_zero_count: bool = False, bwd_ctas: str = "rule", device="cuda",
+                 rope: Rotary = None):
         self.T, self.H, self.d = T, H, d
         self.H_kv = H if H_kv is None else H_kv
         self.scale = softmax_scale

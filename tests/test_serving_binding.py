@@ -60,3 +60,13 @@ def test_windows_and_first_tokens_beyond_32_bits(attend):
 def test_any_number_is_a_scale(attend):
     for s in (0.25, 1, np.float32(0.25), np.float64(0.25), torch.tensor(0.25)):
         assert type(attend(scale=s)[10]) is float
+
+
+def test_arguments_by_position_keep_their_places():
+    """What a training call took by position before it knew rotary positions."""
+    import inspect
+    from precision_causal_attention_block_gb300 import flamia as fl
+    names = list(inspect.signature(fl.TrainingCall).parameters)
+    assert names[:17] == ["T", "H", "d", "cu_seqlens", "softmax_scale", "nvfp4_qk", "hadamard", "causal",
+                          "H_kv", "deterministic_dq", "dq_accum", "schedule", "ds_rows", "token_scales",
+                          "ds_zero_count", "bwd_ctas", "device"]
