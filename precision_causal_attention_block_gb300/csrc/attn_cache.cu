@@ -8,8 +8,9 @@
 // and float32 weights become sums of E4M3 terms instead, side by side in N:
 //   q 2^-e = h + 2^-4 l              (e per row; exact for the elements above
 //                                     2^-14 of the row's largest),
-//   w      = h + 2^-5 m + 2^-10 l    (relative error at most 2^-11, floor 2^-24
-//                                     of the largest weight),
+//   w      = h + 2^-5 m + 2^-10 l    (relative error at most 2^-14, floor 2^-23
+//                                     of the largest weight; with 16 and 32 rows of
+//                                     w rounded to FP16, 2^-11),
 // which costs N = 2 R and 3 R columns of a product that reads M = 128 rows of
 // shared memory in any case.
 //
@@ -119,12 +120,12 @@ __device__ __forceinline__ uint32_t take_term(uint32_t& a, uint32_t& b) {
       : "r"(p32), "r"(n32));
   return w;
 }
-// Four FP16 values as E5M2 codes.
-__device__ __forceinline__ uint32_t e5m2x4_of_half(uint32_t a, uint32_t b) {
+// Four FP16 values as E4M3 codes.
+__device__ __forceinline__ uint32_t e4m3x4_of_half(uint32_t a, uint32_t b) {
   uint32_t w;
   asm("{\n\t.reg .b16 ca, cb;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 ca, %1;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 cb, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 ca, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 cb, %2;\n\t"
       "mov.b32 %0, {ca, cb};\n\t}"
       : "=r"(w)
       : "r"(a), "r"(b));
@@ -173,11 +174,12 @@ struct Cfg {
   static_assert(kSplit ? kSS >= kKS + 2 : kKS == kVS, "rings");
   static constexpr int kTileBytes = 128 * DIM;
   // 16 and 32 rows are bound by the softmax warps: their weights go through FP16
-  // (relative error 2^-11) and keep the last term in E5M2, whose range leaves
-  // room for references that move seldom
+  // (relative error 2^-11)
   static constexpr bool kHalfWeights = R >= 16;
-  static constexpr float kShift = kHalfWeights ? 0.f : 4.f;  // log2 of a weight at the reference
-  static constexpr float kSlack = 8.f - kShift;              // weights <= 2^8 < 448
+  // The last term ends 2^-20 below 1 (half of E4M3's smallest step, twice 2^-5 down),
+  // and the largest weight is between 2^(kShift - 1) and 2^(kShift + kSlack)
+  static constexpr float kShift = 4.f;           // log2 of a weight at the reference
+  static constexpr float kSlack = 8.f - kShift;  // weights <= 2^8 < 448
   static constexpr int kNS = 2 * R;                 // columns of S^T
   static constexpr int kNO = R == 8 ? 32 : 3 * R;   // columns of O^T
   static constexpr int kAtoms = (kNO + 31) / 32;    // P^T: 32 columns x 128 keys each
@@ -530,9 +532,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     constexpr uint32_t lay = DIM == 128 ? kLayoutSW128 : kLayoutSW64;
     constexpr uint32_t sbo = 8 * DIM;
     const uint32_t id_s = idesc_f8(128, C::kNS, 0, 0);
-    // weights: all terms at once, or the last one apart (E5M2: bit 10)
-    const uint32_t id_o = idesc_f8(128, C::kHalfWeights ? 2 * R : C::kNO, 1, 1);
-    const uint32_t id_lo = idesc_f8(128, R < 16 ? 16 : R, 1, 1) | (1u << 10);  // (R = 8: unused)
+    const uint32_t id_o = idesc_f8(128, C::kNO, 1, 1);
     const uint64_t dk0 = smem_desc(smem_u32(sm.k[0]), 0, sbo, lay);
     const uint64_t dq = smem_desc(smem_u32(sm.q), 0, sbo, lay);
     // head dim 64: M = 128 takes a second 64-row atom; it reads the bytes one
@@ -610,11 +610,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             const uint64_t dv = dv0 + st * kStep + ks * (32 * DIM / 16);
-            const uint64_t dp = dp0 + ks * (1024 / 16);
-            mma_f8(tmem + C::kColO, dv, dp, id_o, t > 0 || ks > 0);
-            if (C::kHalfWeights)
-              mma_f8(tmem + C::kColO + 2 * R, dv, dp + (2 * R / 32) * (4096 / 16), id_lo,
-                     t > 0 || ks > 0);
+            mma_f8(tmem + C::kColO, dv, dp0 + ks * (1024 / 16), id_o, t > 0 || ks > 0);
           }
           tc_commit(smem_u32(&sm.pv_done[x & 1]));
           tc_commit(smem_u32(&sm.v_empty[st]));
@@ -932,7 +928,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               uint32_t ha = half2_of(a), hb = half2_of(b);
               tw[0][r / 4] = take_term(ha, hb);
               tw[1][r / 4] = take_term(ha, hb);
-              tw[2][r / 4] = e5m2x4_of_half(ha, hb);
+              tw[2][r / 4] = e4m3x4_of_half(ha, hb);
             } else {
               tw[0][r / 4] = take_term(a, b);
               tw[1][r / 4] = take_term(a, b);
