@@ -533,8 +533,7 @@ flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16, int64
  * whatever lies behind a sequence's last token, changes nothing.  Scores and sums
  * are float32; a softmax weight is rounded to 2^-14 of itself (to FP16, 2^-11,
  * with more than 8 query rows a sequence and K / V head on average) or 2^-23 of
- * the row's largest weight times value scale, whichever is more (scales more than
- * 2^60 below the largest seen count as 2^-60 of it here).  Positions stay
+ * the row's largest weight times value scale, whichever is more.  Positions stay
  * below 2^30.
  * Query head h reads K / V head h / (H / H_kv).
  *

@@ -27,7 +27,7 @@ constexpr int kItemCost = R == 256 ? 5 : 3;
 constexpr int kWholeTiles = 4;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
-constexpr int kLow = 60;
+constexpr int kLow = 60;        // keys whose eV lies further below E0 are summed apart
 
 struct AttendArgs {
   const uint8_t *k_scales, *v_scales;
@@ -63,13 +63,28 @@ __device__ __forceinline__ uint32_t half2_of(float2 a) {
   const __half2 h = __floats2half2_rn(a.x, a.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// log2(2^a + 2^b); -infinity: nothing.  NaN stays.  (The hardware's functions, to 2^-22:
-// the float32 logarithms that they are added to hold no more.  log2f and exp2f here
-// made the 256-row kernel's loop longer: a prompt chunk 121 us against 120.)
-__device__ __forceinline__ float log2_add(float a, float b) {
-  const float m = fmaxf(a, b), ref = m == -INFINITY ? 0.f : m;
-  return ref + __log2f(ex2_approx(a - ref) + ex2_approx(b - ref));
-}
+// A sum m 2^e of softmax weights 2^x with an exponent of its own (a whole number), for
+// what a row's running sum cannot hold; m = 0: nothing.  NaN stays.
+struct Sum {
+  float m, e;
+  __device__ __forceinline__ void add(float qm, float qe) {
+    if (qm == 0.f) return;
+    if (m == 0.f) {
+      m = qm;
+      e = qe;
+      return;
+    }
+    const float top = fmaxf(e, qe);
+    auto scaled = [&](float x, float ex) {
+      return ldexpf(x, max(static_cast<int>(ex - top), -400));
+    };
+    m = scaled(m, e) + scaled(qm, qe);
+    e = top;
+  }
+};
+constexpr float kNoExponent = -1e30f;
+// 2^k, k cut to the exponents of normal floats.
+__device__ __forceinline__ float pow2_within(int k) { return exp2i(min(max(k, -126), 127)); }
 __device__ __forceinline__ float pow2_byte(int byte) {
   return byte > 0 ? __uint_as_float(static_cast<uint32_t>(byte) << 23) : 0x1p-127f;
 }

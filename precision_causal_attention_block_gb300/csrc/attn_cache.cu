@@ -19,15 +19,14 @@
 //   w = 2^(x + eV - ref + kShift),   l = sum w 2^(E0 - eV),
 //   o = O^T 2^E0 / l,   log2 sum 2^x = ref - kShift - E0 + log2 l,
 // with one integer reference a row (a running maximum of x + eV) and one
-// integer E0 (a running maximum of eV) for all rows.  When E0 rises, l is put by as
-// log2 sum 2^x of the keys so far and starts anew: lifted to the new E0 it could
-// leave float32 (values that climb while scores fall), and a reference that moved
-// along would push the next weights, which count as much, under their range.  Keys
-// whose values are more than 2^kLow below E0 (zero values under a heavy first token)
-// enter the references with eV raised to E0 - kLow and have their weight lowered
-// afterwards, so that l keeps them and stays inside float32.  References move
-// only when a tile exceeds them by more than kSlack, which the one barrier of
-// a tile votes on; O^T is then rescaled in tensor memory.
+// integer E0 (a running maximum of eV) for all rows.  What float32 cannot hold beside
+// the rest of l goes to a sum with an exponent of its own, kept a row in shared memory
+// (Sum): l itself whenever E0 rises (lifted to the new E0 it could leave float32, and
+// a reference that moved along would push the next weights, which count as much, under
+// their range), and the keys whose values are more than 2^kLow below E0 (zero values
+// under a heavy first token; or rows that do not see the large value beside them).
+// References move only when a tile exceeds them by more than kSlack, which the one
+// barrier of a tile votes on; O^T is then rescaled in tensor memory.
 //
 // Work: the key tiles of all (sequence, K / V head, row tile) items are laid end
 // to end, with kItemCost tiles' worth for each item's own steps, and cut into
@@ -61,6 +60,7 @@ namespace flamia {
 namespace {
 
 constexpr float kUnset = 1e30f; // -reference of a row that has seen no key yet
+constexpr int kUnseen = -200;   // eV of a key that no row sees
 constexpr int kWhole = 1 << 8;  // every row sees every key of a tile
 
 // ------------------------------------------------------------------ PTX
@@ -95,6 +95,10 @@ __device__ __forceinline__ float warp_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
+}
+
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
 }
 
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
@@ -200,14 +204,15 @@ struct Smem {
   alignas(16) float qf[R];      // 2^e of a row x softmax scale x log2 e
   alignas(16) float nref[R];    // kShift - reference
   alignas(16) float fac[R];     // change of scale of O^T and l
-  float ve[R];                  // 2^E0 for o
-  float past[R];                // log2 sum 2^x before E0 last rose, -inf: none
+  float ve[R];                  // for o
+  Sum past[R];                  // sum 2^x of what is not in l
+  float far[4][R], fare[4][R];  // a tile's share of it, by warp
   int has[R];                   // the row has a reference
   bool nan[2][128];  // a half-seen key's value holds a NaN (by tile parity)
   alignas(16) int pos[R];       // position of a row's token, -1: no such row
   alignas(16) int orow[R];      // its row of o, -1: none
   float red[4][R];
-  int rede[C::kSoftmax / 32];
+  int2 rede[C::kSoftmax / 32];
   uint64_t k_full[C::kKS], k_empty[C::kKS], v_full[C::kVS], v_empty[C::kVS];
   uint64_t sc_full[C::kSS];
   uint64_t s_full[2], p_full[2], pv_done[2];
@@ -678,7 +683,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sm.orow[tid] = live ? (sg.s + i) * g.H + hq : -1;
         sm.nref[tid] = C::kShift;
         sm.has[tid] = 0;
-        sm.past[tid] = -INFINITY;
+        sm.past[tid] = Sum{0.f, kNoExponent};
       }
       if (nt > 0) {
         queries.split(sm.q, sm.qf, g.scale_log2, tid);
@@ -717,7 +722,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
                    : !wait_both(sbar, (tc >> 1) & 1, cbar, sph, &sm.abort))
           fail();
         tc_fence_after();
-        int ev = sm.vs[ss][key_in] - 127;  // V's exponent
+        int ev = sm.vs[ss][key_in] - 127;  // V's exponent; kUnseen
         const float kf = pow2_byte(sm.ks[ss][key_in]);
         const bool whole = (sm.tile[ss].y & kWhole) != 0;
         if (!whole) {  // some rows do not see some keys
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           const bool first = g.window == 0 || key < g.sinks;
           const bool any = here && key <= pl && (first || key > pf - g.window);
           const bool every = here && key <= pf && (first || key > pl - g.window);
-          if (!any) ev = -127;  // neutral
+          if (!any) ev = kUnseen;
           // A value that some rows see and others do not must not reach the
           // others: 0 x NaN is NaN.  Unseen rows of V are cleared, and half-seen
           // ones that hold a NaN, which moves into the weights of the rows that
@@ -760,13 +765,12 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             }
           }
         }
-        int evc = max(ev, e0 - kLow);
         // x + eV - ref + kShift of rows r0 + c .. + 7.  They are taken anew from
         // tensor memory where they are needed (for the vote, the references, the
         // weights): held in registers over the vote they cost more, in spills.
         auto scores = [&](const int c, float2 (&y)[4]) {
           const float2 kf2 = make_float2(kf, kf);
-          const float evf = static_cast<float>(evc);
+          const float evf = static_cast<float>(ev);
           const float2 ev2 = make_float2(evf, evf), lo2 = make_float2(0.0625f, 0.0625f);
           uint32_t h[8], lo[8];
           tmem_ld8(tmem + lanes + buf * C::kNS + r0 + c, h);
@@ -808,32 +812,57 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 #pragma unroll
             for (int r = 0; r < 4; ++r) mx = fmax3(mx, y[r].x, y[r].y);
           }
-          move = mx > C::kShift + C::kSlack || ev > e0 + kHigh;
+          move = mx > C::kShift + C::kSlack || ev > e0 + kHigh || (ev < e0 - kLow && ev != kUnseen);
         }
         move = vote(move);
         if (move) {  // E0, then the rows' references
-          const int em = __reduce_max_sync(0xffffffffu, ev + 127);
-          if (lane == 0) sm.rede[warp] = em;
+          const int em = __reduce_max_sync(0xffffffffu, ev);
+          const int el = __reduce_min_sync(0xffffffffu, ev == kUnseen ? 127 : ev);
+          if (lane == 0) sm.rede[warp] = make_int2(em, el);
           // rows without a reference are measured from 0
           if (tid < R && sm.nref[tid] == kUnset) sm.nref[tid] = C::kShift;
           sync();
-          int top = -127;
+          int top = -127, low = 127;
 #pragma unroll
-          for (int w = 0; w < C::kSoftmax / 32; ++w) top = max(top, sm.rede[w] - 127);
+          for (int w = 0; w < C::kSoftmax / 32; ++w) {
+            top = max(top, sm.rede[w].x);
+            low = min(low, sm.rede[w].y);
+          }
           if (t == 0) {
             e0 = top;
           } else if (top > e0 + kHigh) {  // (the same in all warps)
             sum_keys();
             sync();
-            if (tid < R)
-              sm.past[tid] = log2_add(sm.past[tid], __log2f(sum_of(tid)) - sm.nref[tid] -
-                                                        static_cast<float>(e0));
+            if (tid < R) sm.past[tid].add(sum_of(tid), -sm.nref[tid] - static_cast<float>(e0));
             sync();
 #pragma unroll
             for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
             e0 = top;
           }
-          evc = max(ev, e0 - kLow);
+          const bool apart = low < e0 - kLow;
+          if (apart) {  // keys that l does not hold (short code: the tile's has to stay so)
+            const bool far = ev < e0 - kLow && ev != kUnseen;
+#pragma unroll 1
+            for (int r = r0; r < r0 + RW; ++r) {
+              uint32_t h, lo;
+              const int key = sm.tile[ss].x + key_in;
+              const bool first = g.window == 0 || key < g.sinks;
+              tmem_ld1(tmem + lanes + buf * C::kNS + r, h);
+              tmem_ld1(tmem + lanes + buf * C::kNS + R + r, lo);
+              tmem_ld_wait();
+              const int p = sm.pos[r];
+              float x = fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(h)) * (kf * sm.qf[r]);
+              if (!(far && key <= p && (first || key > p - g.window))) x = -INFINITY;
+              const float m = ceilf(fmaxf(warp_max(x), kNoExponent));
+              float s = ex2_approx(x - m);
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+              if (lane == 0) {
+                sm.far[warp & 3][r] = s;
+                sm.fare[warp & 3][r] = m;
+              }
+            }
+          }
 #pragma unroll 1
           for (int c = 0; c < RW; c += 8) {
             float2 y[4];
@@ -852,6 +881,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             // nothing (or nothing but NaN) has none.
             const float n0 = sm.nref[tid];
             float n1 = n0, f = 1.f;
+            if (apart)
+              for (int w = 0; w < 4; ++w) sm.past[tid].add(sm.far[w][tid], sm.fare[w][tid]);
             if (tid >= rows) {
               n1 = -kUnset;
             } else if (!sm.has[tid]) {
@@ -896,9 +927,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const bool p_free =
             tc == 0 || mbar_test(smem_u32(&sm.pv_done[buf ^ 1]), ((tc - 1) >> 1) & 1);
         // weights and their 8-bit terms
-        const float gl = ex2_approx(static_cast<float>(e0 - evc));
+        const float gl = ev < e0 - kLow ? 0.f : exp2i(e0 - ev);
         const float2 g2 = make_float2(gl, gl);
-        const float z = ev < evc ? ex2_approx(static_cast<float>(max(ev - evc, -126))) : 1.f;
 #pragma unroll
         for (int c = 0; c < RW; c += 8) {
           float2 y[4];
@@ -918,12 +948,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             float2 b = make_float2(ex2_approx(y[r / 2 + 1].x), ex2_approx(y[r / 2 + 1].y));
             l[(c + r) / 2] = __ffma2_rn(a, g2, l[(c + r) / 2]);
             l[(c + r) / 2 + 1] = __ffma2_rn(b, g2, l[(c + r) / 2 + 1]);
-            if (ev < evc) {
-              a.x *= z;
-              a.y *= z;
-              b.x *= z;
-              b.y *= z;
-            }
             if constexpr (C::kHalfWeights) {
               uint32_t ha = half2_of(a), hb = half2_of(b);
               tw[0][r / 4] = take_term(ha, hb);
@@ -969,16 +993,13 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       sum_keys();
       sync();
       if (tid < rows) {
-        const float s = sum_of(tid), past = sm.past[tid];
-        float lg = s == 0.f ? -INFINITY : log2f(s) - sm.nref[tid] - static_cast<float>(e0);
-        if (past == -INFINITY) {
-          sm.fac[tid] = s == 0.f ? 0.f : 1.f / s;  // nothing seen: l = 0
-          sm.ve[tid] = e0 < -126 ? 0x1p-127f : exp2i(e0);
-        } else {
-          lg = log2_add(past, lg);
-          sm.fac[tid] = exp2f(-sm.nref[tid] - lg);
-          sm.ve[tid] = 1.f;
-        }
+        Sum all = sm.past[tid];
+        all.add(sum_of(tid), -sm.nref[tid] - static_cast<float>(e0));
+        const float lg = all.m == 0.f ? -INFINITY : log2f(all.m) + all.e;
+        // o = O^T 2^(ref - kShift) / sum, the power of two in two halves
+        const int k = static_cast<int>(-sm.nref[tid] - all.e);
+        sm.fac[tid] = all.m == 0.f ? 0.f : pow2_within(k / 2) / all.m;  // (0: nothing seen)
+        sm.ve[tid] = pow2_within(k - k / 2);
         const int orow = sm.orow[tid];
         if (slot >= 0)
           g.stats[static_cast<size_t>(slot) * R + tid] = lg;

@@ -11,8 +11,8 @@
 // enter the scores of a key, as in attn_cache.cu:
 //   w = 2^(x + eV - ref),  l = sum w 2^(E0 - eV),
 //   o = O 2^E0 / l,        log2 sum 2^x = ref - E0 + log2 l,
-// l put by when E0 rises, as there; but a thread owns a row here, so maxima and sums
-// need no other thread.  A row's reference is an integer that moves when a tile
+// and a Sum for what l cannot hold, as there; but a thread owns a row here, so maxima
+// and sums need no other thread.  A row's reference is an integer that moves when a tile
 // exceeds it by more than kSlack;
 // where 32 keys have one K and one V exponent (always, with exponents of 32-token
 // blocks) their largest score comes with a load from tensor memory.
@@ -45,6 +45,7 @@ constexpr float kSlack = 8.f;
 constexpr int kUniform = 1;   // one K and one V exponent
 constexpr int kEvery = 2;     // every row sees every key
 constexpr int kHere = 4;      // there is a page
+constexpr int kLowShift = 8;  // from here on: the byte of the smallest eV that a row sees
 
 // A row of 32 keys' exponents.
 struct alignas(16) Keys32 {
@@ -79,6 +80,7 @@ struct Smem {
   alignas(16) int ev[4][128];     // the softmax is done two score products later
   Keys32 col[4][4];
   uint32_t nan[4][4];             // half-seen keys whose value holds a NaN
+  Sum past[C::kRows];             // sum 2^x of what is not in a row's l
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4];
   uint64_t s_full[2], p_full[2], pv_done[2];  // by row tile
   uint64_t q_full[2], drained;
@@ -337,6 +339,38 @@ struct Block32 {
   }
 };
 
+// Adds 2^x of a tile's keys whose eV lies below floor_ev to a row's sum.  (Not inlined:
+// rare, and inside the tile's code it made a prompt chunk 139 us against 119.)
+__device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev,
+                                       const Keys32* col, const uint32_t* nan, uint32_t t_s,
+                                       float qf, int floor_ev, int k0, int pos, int window,
+                                       int sinks) {
+  float top = kNoExponent, sum = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {  // the largest, then the sum
+    const int at = (i & 15) * 8, flags = col[at / 32].flags;
+    uint32_t s[8];
+    tmem_ld8(t_s + at, s);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int key = k0 + at + j;
+      const bool seen =
+          (flags & kEvery) ||
+          ((flags & kHere) && key <= pos && (window == 0 || key < sinks || key > pos - window));
+      float x = __uint_as_float(s[j]) * (kf[at + j] * qf);
+      if (!(flags & kEvery) && (nan[at / 32] >> ((at + j) & 31)) & 1) x = __uint_as_float(0x7FC00000u);
+      if (!seen || ev[at + j] >= floor_ev) x = -INFINITY;
+      if (i < 16)
+        top = fmaxf(top, x);
+      else
+        sum += ex2_approx(x - top);
+    }
+    if (i == 15) top = ceilf(top);
+  }
+  past.add(sum, top);
+}
+
 template <int DIM>
 __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(const AttendArgs g,
                                                                            const uint8_t* k_codes,
@@ -472,12 +506,13 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           const int kx = seen ? kbyte : kb0, vx = seen ? vbyte : vb0;
           const bool uniform = __all_sync(0xffffffffu, kx == kb0 && vx == vb0);
           const int top = __reduce_max_sync(0xffffffffu, vx);
+          const int low = live ? __reduce_min_sync(0xffffffffu, vx) : 255;
           sm.kf[ss][cw * 32 + lane] = pow2_byte(kx);
           sm.ev[ss][cw * 32 + lane] = vx - 127;
           if (lane == 0)
             sm.col[ss][cw] = Keys32{pow2_byte(kb0), vb0 - 127, live ? top - 127 : -127,
                                     (uniform ? kUniform : 0) | (half ? 0 : kEvery) |
-                                        (good ? kHere : 0)};
+                                        (good ? kHere : 0) | (low << kLowShift)};
         } else if (half) {
           // A value that some rows see and others do not must not reach the others:
           // one that holds a NaN is cleared, and the NaN moves into the weights of
@@ -610,7 +645,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 
       float l = 0.f, nref = 0.f;  // nref: -reference
       bool has = false;           // the row has a reference
-      float past = -INFINITY;     // log2 sum 2^x before E0 last rose
+      sm.past[r] = Sum{0.f, kNoExponent};
       int e0 = -127;
 #pragma unroll 1
       for (int t = 0; t < (active ? nt : 0); ++t, ++x) {
@@ -625,23 +660,25 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (t == 0) {
           e0 = top;
         } else if (top > e0 + kHigh) {  // (as in attn_cache.cu)
-          past = log2_add(past, __log2f(l) - nref - static_cast<float>(e0));
+          sm.past[r].add(l, -nref - static_cast<float>(e0));
           l = 0.f;
           e0 = top;
         }
         const int k0 = tile_of(sg, sg.i0 + t) * 128;
         const int floor_ev = e0 - kLow;
-        // 32 keys with one K and one V exponent: y = x kq + (evc + nref)
-        float kq[4], evc[4];
-        int flags = kUniform | kEvery;
+        // 32 keys with one K and one V exponent: y = x kq + (eV + nref)
+        float kq[4], evf[4];
+        int flags = kUniform | kEvery, low = 127;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const Keys32 kc = sm.col[ss][c];
           kq[c] = kc.kf * qf;
-          evc[c] = static_cast<float>(max(kc.ev, floor_ev));
+          evf[c] = static_cast<float>(kc.ev);
           flags &= kc.flags;
+          low = min(low, (kc.flags >> kLowShift) - 127);
         }
-        const bool plain = flags == (kUniform | kEvery);
+        const bool apart = low < floor_ev;  // some keys are not in l
+        const bool plain = flags == (kUniform | kEvery) && !apart;
         if (!(flags & kEvery) &&  // half-seen keys: V has been searched for NaN
             !mbar_wait_w_ab(smem_u32(&sm.v_full[(tc + t) & 1]), ((tc + t) >> 1) & 1, &sm.abort))
           fail();
@@ -670,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float v = fmaf(__uint_as_float(s[j + i]), kk[i] * qf,
-                             static_cast<float>(max(ee[i], floor_ev)) + nref);
+                             static_cast<float>(ee[i]) + nref);
               if ((nan >> (j + i)) & 1) v = __uint_as_float(0x7FC00000u);
               y[j + i] = (m >> (j + i)) & 1 ? v : -INFINITY;
             }
@@ -684,11 +721,11 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           tmem_ld32_max(t_s + 64, s0, m0);
           tmem_ld32_max(t_s + 96, s1, m1);
           tmem_ld_wait();
-          mx = fmaxf(fmaf(m0, kq[2], evc[2] + nref), fmaf(m1, kq[3], evc[3] + nref));
+          mx = fmaxf(fmaf(m0, kq[2], evf[2] + nref), fmaf(m1, kq[3], evf[3] + nref));
           tmem_ld32_max(t_s, s0, m0);
           tmem_ld32_max(t_s + 32, s1, m1);
           tmem_ld_wait();
-          mx = fmax3(mx, fmaf(m0, kq[0], evc[0] + nref), fmaf(m1, kq[1], evc[1] + nref));
+          mx = fmax3(mx, fmaf(m0, kq[0], evf[0] + nref), fmaf(m1, kq[1], evf[1] + nref));
         } else {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -733,8 +770,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (plain) {
           auto weights = [&](int c, const uint32_t (&s)[32]) {
             const Keys32 kc = sm.col[ss][c];
-            const int ev = kc.ev, evc = max(ev, floor_ev);
-            const float kq = kc.kf * qf, add = static_cast<float>(evc) + nref;
+            const float kq = kc.kf * qf, add = static_cast<float>(kc.ev) + nref;
             const float2 kq2 = make_float2(kq, kq), add2 = make_float2(add, add);
             float2 y[16];
 #pragma unroll
@@ -750,12 +786,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
               b = __fadd2_rn(b, y[j + 1]);
             }
             a = __fadd2_rn(a, b);
-            l = fmaf(a.x + a.y, exp2i(e0 - evc), l);
-            if (ev < evc) {
-              const float z = exp2i(max(ev - evc, -126));
-#pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = __fmul2_rn(y[j], make_float2(z, z));
-            }
+            l = fmaf(a.x + a.y, exp2i(e0 - kc.ev), l);
             uint32_t p[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) p[j] = half2_of(y[j]);
@@ -770,6 +801,9 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
             tmem_ld_wait();
           }
         } else {
+          if (apart)
+            sum_apart(sm.past[r], sm.kf[ss], sm.ev[ss], sm.col[ss], sm.nan[ss], t_s, qf, floor_ev,
+                      k0, pos, g.window, g.sinks);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float y[32];
@@ -777,10 +811,9 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
             uint32_t p[16];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const int ev = sm.ev[ss][c * 32 + j], evc = max(ev, floor_ev);
+              const int ev = sm.ev[ss][c * 32 + j];
               y[j] = ex2_approx(y[j]);
-              l = fmaf(y[j], exp2i(e0 - evc), l);
-              if (ev < evc) y[j] *= exp2i(max(ev - evc, -126));
+              l = fmaf(y[j], ev < floor_ev ? 0.f : exp2i(e0 - ev), l);
               if (j & 1) p[j / 2] = half2_of(make_float2(y[j - 1], y[j]));
             }
             tmem_st16(t_s + c * 16, p);
@@ -800,14 +833,12 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           if (!mbar_wait_w_ab(obar, (x - 1) & 1, &sm.abort)) fail();
           tc_fence_after();
         }
-        float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: l = 0
-        float lg = l == 0.f ? -INFINITY : log2f(l) - nref - static_cast<float>(e0);
-        float ve = e0 < -126 ? 0x1p-127f : exp2i(e0);
-        if (past != -INFINITY) {
-          lg = log2_add(past, lg);
-          inv = exp2f(-nref - lg);
-          ve = 1.f;
-        }
+        Sum past = sm.past[r];
+        past.add(l, -nref - static_cast<float>(e0));
+        const float lg = past.m == 0.f ? -INFINITY : log2f(past.m) + past.e;
+        const int k = static_cast<int>(-nref - past.e);  // (as in attn_cache.cu)
+        const float inv = past.m == 0.f ? 0.f : pow2_within(k / 2) / past.m;
+        const float ve = pow2_within(k - k / 2);
         const size_t out = static_cast<size_t>(sg.s + tok) * g.H + hq;
         if (live) {
           if (slot >= 0)
