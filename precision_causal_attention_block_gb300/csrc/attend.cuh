@@ -212,7 +212,8 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
 }
 
 // Joins the parts of an item that several CTAs shared (part 0 in slot 1 of the
-// CTA before, the others in slots 0 from this CTA on): o = sum 2^(lg_p - lg) o_p.
+// CTA before, the others in slots 0 from this CTA on): o = sum 2^(lg_p - lg) o_p, the
+// weights in two halves, as a small one may meet large values (2^-150 x 2^100).
 // One warp a row, without shared memory, so that blocks fit beside the first
 // kernel's CTAs and are there when it ends.
 template <int DIM, int R>
@@ -242,8 +243,8 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendArgs g) {
   const float ref = m == -INFINITY ? 0.f : m;
   float l = 0.f, acc[E] = {};
   for (int p0 = 0; p0 < parts; p0 += 32) {
-    const float wt = p0 + lane < parts ? exp2f(g.stats[at(p0 + lane)] - ref) : 0.f;
-    l += wt;
+    const float wt = p0 + lane < parts ? exp2f(0.5f * (g.stats[at(p0 + lane)] - ref)) : 0.f;
+    l = fmaf(wt, wt, l);
     const int n = min(32, parts - p0);
 #pragma unroll 8
     for (int p = 0; p < n; ++p) {
@@ -253,14 +254,14 @@ __global__ void __launch_bounds__(256) join_kernel(const AttendArgs g) {
                                          : at(p0 + p) * DIM + lane * E);
       if constexpr (E == 4) {
         const float4 v = *reinterpret_cast<const float4*>(x);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
+        acc[0] = fmaf(w, w * v.x, acc[0]);
+        acc[1] = fmaf(w, w * v.y, acc[1]);
+        acc[2] = fmaf(w, w * v.z, acc[2]);
+        acc[3] = fmaf(w, w * v.w, acc[3]);
       } else {
         const float2 v = *reinterpret_cast<const float2*>(x);
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
+        acc[0] = fmaf(w, w * v.x, acc[0]);
+        acc[1] = fmaf(w, w * v.y, acc[1]);
       }
     }
   }

@@ -77,8 +77,9 @@ def test_scores_and_value_exponents_that_move_apart(lib, name, n, H, H_kv, d, ns
                              dev_status=st)
     assert int(st.item()) == 0
     qn, kn, vn = q1.double().numpy(), pair.k.values(0), pair.v.values(0)
-    ro, rl, mass, top = S.attend(qn, kn, vn, L - n, d ** -0.5,
-                                 v_exponents=pair.v.scales[0].astype(int) - 127)
+    e = pair.v.scales[0].astype(int) - 127
+    ro, rl, mass, _ = S.attend(qn, kn, vn, L - n, d ** -0.5, v_exponents=e)
+    top = largest_weight(qn, kn, L - n, d ** -0.5, e)
     tol = attend_tolerance(qn, kn, d ** -0.5, L, ro, weight_error(n, 1, H // H_kv), mass,
                            top[..., None])
     got = o.view(nseq, n, H, d).double().cpu().numpy()
