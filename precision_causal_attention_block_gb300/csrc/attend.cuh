@@ -63,8 +63,9 @@ __device__ __forceinline__ uint32_t half2_of(float2 a) {
   const __half2 h = __floats2half2_rn(a.x, a.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// A sum m 2^e of softmax weights 2^x with an exponent of its own (a whole number), for
-// what a row's running sum cannot hold; m = 0: nothing.  NaN stays.
+// A sum m 2^e of softmax weights 2^(x - ref) with an exponent of its own (a whole
+// number; it moves with the reference), for what a row's running sum cannot hold; m =
+// 0: nothing.  NaN stays.
 struct Sum {
   float m, e;
   __device__ __forceinline__ void add(float qm, float qe) {
@@ -83,6 +84,24 @@ struct Sum {
   }
 };
 constexpr float kNoExponent = -1e30f;
+
+// References beyond kLarge, where float32 begins to lose fractions of the scores: a
+// reference set from a row's largest score could leave that one above it by many units
+// (weights past their range) or below it (none at all).  So it is set some steps of
+// float32 too low, what exceeds it by no more than room(-ref) does not move it, and
+// weights above the largest are cut to that (scores that close count as equal).
+constexpr float kLarge = 65536.f;
+__device__ __forceinline__ float lowered(float nref) {
+  return fabsf(nref) > kLarge ? nref + ceilf(fabsf(nref) * 0x1p-21f) : nref;
+}
+__device__ __forceinline__ float room(float nref) {
+  return fabsf(nref) > kLarge ? fabsf(nref) * 0x1p-19f : 0.f;
+}
+__device__ __forceinline__ float cut(float y, float most) {  // (NaN stays)
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(most));
+  return r;
+}
 // 2^k, k cut to the exponents of normal floats.
 __device__ __forceinline__ float pow2_within(int k) { return exp2i(min(max(k, -126), 127)); }
 __device__ __forceinline__ float pow2_byte(int byte) {

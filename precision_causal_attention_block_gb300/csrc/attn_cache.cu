@@ -205,9 +205,10 @@ struct Smem {
   alignas(16) float nref[R];    // kShift - reference
   alignas(16) float fac[R];     // change of scale of O^T and l
   float ve[R];                  // for o
-  Sum past[R];                  // sum 2^x of what is not in l
+  Sum past[R];                  // sum 2^(x + nref) of what is not in l
   float far[4][R], fare[4][R];  // a tile's share of it, by warp
   int has[R];                   // the row has a reference
+  int large;                    // some row's is beyond kLarge
   bool nan[2][128];  // a half-seen key's value holds a NaN (by tile parity)
   alignas(16) int pos[R];       // position of a row's token, -1: no such row
   alignas(16) int orow[R];      // its row of o, -1: none
@@ -685,6 +686,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sm.has[tid] = 0;
         sm.past[tid] = Sum{0.f, kNoExponent};
       }
+      if (tid == 0) sm.large = 0;
       if (nt > 0) {
         queries.split(sm.q, sm.qf, g.scale_log2, tid);
         fence_proxy_async_smem();
@@ -709,6 +711,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         return (sm.red[0][r] + sm.red[1][r]) + (sm.red[2][r] + sm.red[3][r]);
       };
       int e0 = -127;
+      bool large = false;
 #pragma unroll 1
       for (int t = 0; t < nt; ++t, ++tc) {
         const int buf = tc & 1;
@@ -833,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           } else if (top > e0 + kHigh) {  // (the same in all warps)
             sum_keys();
             sync();
-            if (tid < R) sm.past[tid].add(sum_of(tid), -sm.nref[tid] - static_cast<float>(e0));
+            if (tid < R) sm.past[tid].add(sum_of(tid), -static_cast<float>(e0));
             sync();
 #pragma unroll
             for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
@@ -851,7 +854,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               tmem_ld1(tmem + lanes + buf * C::kNS + R + r, lo);
               tmem_ld_wait();
               const int p = sm.pos[r];
-              float x = fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(h)) * (kf * sm.qf[r]);
+              float x = fmaf(fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(h)),
+                             kf * sm.qf[r], sm.nref[r]);
               if (!(far && key <= p && (first || key > p - g.window))) x = -INFINITY;
               const float m = ceilf(fmaxf(warp_max(x), kNoExponent));
               float s = ex2_approx(x - m);
@@ -887,17 +891,20 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               n1 = -kUnset;
             } else if (!sm.has[tid]) {
               const bool now = a > -INFINITY;
-              n1 = now ? n0 - ceilf(a - C::kShift) : kUnset;
+              n1 = now ? lowered(n0 - ceilf(a - C::kShift)) : kUnset;
+              if (now) sm.past[tid].e += n1 - n0;
               sm.has[tid] = now;
-            } else if (a > C::kShift + C::kSlack) {
-              const float by = ceilf(a - C::kShift);
-              n1 = n0 - by;
-              f = ex2_approx(-by);
+            } else if (a > C::kShift + C::kSlack + room(n0)) {
+              n1 = lowered(n0 - ceilf(a - C::kShift));
+              f = ex2_approx(n1 - n0);
+              sm.past[tid].e += n1 - n0;
             }
+            if (tid < rows && n1 != kUnset && fabsf(n1) > kLarge) sm.large = 1;
             sm.nref[tid] = n1;
             sm.fac[tid] = f;
           }
           sync();
+          large = sm.large;
 #pragma unroll
           for (int r = 0; r < RW; r += 4) {
             const float4 f = *reinterpret_cast<const float4*>(sm.fac + r0 + r);
@@ -940,6 +947,11 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               if (y[r].x != -INFINITY) y[r].x = nv;
               if (y[r].y != -INFINITY) y[r].y = nv;
             }
+          }
+          if (large) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              y[r] = make_float2(cut(y[r].x, C::kShift + C::kSlack), cut(y[r].y, C::kShift + C::kSlack));
           }
           uint32_t tw[3][2];
 #pragma unroll
@@ -994,10 +1006,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       sync();
       if (tid < rows) {
         Sum all = sm.past[tid];
-        all.add(sum_of(tid), -sm.nref[tid] - static_cast<float>(e0));
-        const float lg = all.m == 0.f ? -INFINITY : log2f(all.m) + all.e;
+        all.add(sum_of(tid), -static_cast<float>(e0));
+        const float lg = all.m == 0.f ? -INFINITY : log2f(all.m) + all.e - sm.nref[tid];
         // o = O^T 2^(ref - kShift) / sum, the power of two in two halves
-        const int k = static_cast<int>(-sm.nref[tid] - all.e);
+        const int k = static_cast<int>(-all.e);
         sm.fac[tid] = all.m == 0.f ? 0.f : pow2_within(k / 2) / all.m;  // (0: nothing seen)
         sm.ve[tid] = pow2_within(k - k / 2);
         const int orow = sm.orow[tid];

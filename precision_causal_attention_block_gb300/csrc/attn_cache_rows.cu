@@ -80,7 +80,7 @@ struct Smem {
   alignas(16) int ev[4][128];     // the softmax is done two score products later
   Keys32 col[4][4];
   uint32_t nan[4][4];             // half-seen keys whose value holds a NaN
-  Sum past[C::kRows];             // sum 2^x of what is not in a row's l
+  Sum past[C::kRows];             // sum 2^(x + nref) of what is not in a row's l
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4];
   uint64_t s_full[2], p_full[2], pv_done[2];  // by row tile
   uint64_t q_full[2], drained;
@@ -339,12 +339,12 @@ struct Block32 {
   }
 };
 
-// Adds 2^x of a tile's keys whose eV lies below floor_ev to a row's sum.  (Not inlined:
+// Adds 2^(x + nref) of a tile's keys whose eV lies below floor_ev to a row's sum.  (Not inlined:
 // rare, and inside the tile's code it made a prompt chunk 139 us against 119.)
 __device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev,
                                        const Keys32* col, const uint32_t* nan, uint32_t t_s,
-                                       float qf, int floor_ev, int k0, int pos, int window,
-                                       int sinks) {
+                                       float qf, float nref, int floor_ev, int k0, int pos,
+                                       int window, int sinks) {
   float top = kNoExponent, sum = 0.f;
 #pragma unroll 1
   for (int i = 0; i < 32; ++i) {  // the largest, then the sum
@@ -358,7 +358,7 @@ __device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev
       const bool seen =
           (flags & kEvery) ||
           ((flags & kHere) && key <= pos && (window == 0 || key < sinks || key > pos - window));
-      float x = __uint_as_float(s[j]) * (kf[at + j] * qf);
+      float x = fmaf(__uint_as_float(s[j]), kf[at + j] * qf, nref);
       if (!(flags & kEvery) && (nan[at / 32] >> ((at + j) & 31)) & 1) x = __uint_as_float(0x7FC00000u);
       if (!seen || ev[at + j] >= floor_ev) x = -INFINITY;
       if (i < 16)
@@ -645,6 +645,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 
       float l = 0.f, nref = 0.f;  // nref: -reference
       bool has = false;           // the row has a reference
+      bool large = false;         // some row's of the warp is beyond kLarge
       sm.past[r] = Sum{0.f, kNoExponent};
       int e0 = -127;
 #pragma unroll 1
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (t == 0) {
           e0 = top;
         } else if (top > e0 + kHigh) {  // (as in attn_cache.cu)
-          sm.past[r].add(l, -nref - static_cast<float>(e0));
+          sm.past[r].add(l, -static_cast<float>(e0));
           l = 0.f;
           e0 = top;
         }
@@ -736,20 +737,20 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           }
         }
         // Where it does not, or there is none yet, it moves.
-        const bool need = has ? mx > kSlack : mx > -INFINITY;
+        const bool need = has ? mx > kSlack + room(nref) : mx > -INFINITY;
         if (__any_sync(0xffffffffu, need)) {
           float f = 1.f;
           if (need) {
-            if (!has) {
-              nref -= ceilf(mx);
-              has = true;
-            } else {
-              const float by = ceilf(mx);
-              nref -= by;
-              f = ex2_approx(-by);
+            const float by = lowered(nref - ceilf(mx)) - nref;
+            if (has) {
+              f = ex2_approx(by);
               l *= f;
             }
+            nref += by;
+            sm.past[r].e += by;
+            has = true;
           }
+          large = __any_sync(0xffffffffu, fabsf(nref) > kLarge);
           if (t > 0) {  // O, once the product before has added to it
             if (!mbar_wait_w_ab(obar, (x - 1) & 1, &sm.abort)) fail();
             tc_fence_after();
@@ -767,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         }
         // Weights.  Those of 32 keys take half of the scores' columns, and none whose
         // scores are still to be read.
-        if (plain) {
+        if (plain && !large) {
           auto weights = [&](int c, const uint32_t (&s)[32]) {
             const Keys32 kc = sm.col[ss][c];
             const float kq = kc.kf * qf, add = static_cast<float>(kc.ev) + nref;
@@ -802,8 +803,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           }
         } else {
           if (apart)
-            sum_apart(sm.past[r], sm.kf[ss], sm.ev[ss], sm.col[ss], sm.nan[ss], t_s, qf, floor_ev,
-                      k0, pos, g.window, g.sinks);
+            sum_apart(sm.past[r], sm.kf[ss], sm.ev[ss], sm.col[ss], sm.nan[ss], t_s, qf, nref,
+                      floor_ev, k0, pos, g.window, g.sinks);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float y[32];
@@ -812,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int ev = sm.ev[ss][c * 32 + j];
-              y[j] = ex2_approx(y[j]);
+              y[j] = ex2_approx(cut(y[j], kSlack));
               l = fmaf(y[j], ev < floor_ev ? 0.f : exp2i(e0 - ev), l);
               if (j & 1) p[j / 2] = half2_of(make_float2(y[j - 1], y[j]));
             }
@@ -834,9 +835,9 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           tc_fence_after();
         }
         Sum past = sm.past[r];
-        past.add(l, -nref - static_cast<float>(e0));
-        const float lg = past.m == 0.f ? -INFINITY : log2f(past.m) + past.e;
-        const int k = static_cast<int>(-nref - past.e);  // (as in attn_cache.cu)
+        past.add(l, -static_cast<float>(e0));
+        const float lg = past.m == 0.f ? -INFINITY : log2f(past.m) + past.e - nref;
+        const int k = static_cast<int>(-past.e);  // (as in attn_cache.cu)
         const float inv = past.m == 0.f ? 0.f : pow2_within(k / 2) / past.m;
         const float ve = pow2_within(k - k / 2);
         const size_t out = static_cast<size_t>(sg.s + tok) * g.H + hq;
