@@ -97,10 +97,6 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
-__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-}
-
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -843,30 +839,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             e0 = top;
           }
           const bool apart = low < e0 - kLow;
-          if (apart) {  // keys that l does not hold (short code: the tile's has to stay so)
-            const bool far = ev < e0 - kLow && ev != kUnseen;
-#pragma unroll 1
-            for (int r = r0; r < r0 + RW; ++r) {
-              uint32_t h, lo;
-              const int key = sm.tile[ss].x + key_in;
-              const bool first = g.window == 0 || key < g.sinks;
-              tmem_ld1(tmem + lanes + buf * C::kNS + r, h);
-              tmem_ld1(tmem + lanes + buf * C::kNS + R + r, lo);
-              tmem_ld_wait();
-              const int p = sm.pos[r];
-              float x = fmaf(fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(h)),
-                             kf * sm.qf[r], sm.nref[r]);
-              if (!(far && key <= p && (first || key > p - g.window))) x = -INFINITY;
-              const float m = ceilf(fmaxf(warp_max(x), kNoExponent));
-              float s = ex2_approx(x - m);
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-              if (lane == 0) {
-                sm.far[warp & 3][r] = s;
-                sm.fare[warp & 3][r] = m;
-              }
-            }
-          }
 #pragma unroll 1
           for (int c = 0; c < RW; c += 8) {
             float2 y[4];
@@ -875,6 +847,21 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             for (int r = 0; r < 8; ++r) {
               const float a = warp_max(r & 1 ? y[r / 2].y : y[r / 2].x);
               if (lane == 0) sm.red[warp & 3][r0 + c + r] = a;
+            }
+            if (apart) {  // keys that l does not hold
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                const float x =
+                    ev < e0 - kLow ? (r & 1 ? y[r / 2].y : y[r / 2].x) - static_cast<float>(ev) : -INFINITY;
+                const float m = ceilf(fmaxf(warp_max(x), kNoExponent));
+                float s = ex2_approx(x - m);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) {
+                  sm.far[warp & 3][r0 + c + r] = s;
+                  sm.fare[warp & 3][r0 + c + r] = m;
+                }
+              }
             }
           }
           sync();
