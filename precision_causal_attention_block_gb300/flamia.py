@@ -336,7 +336,7 @@ class Rotary:
         self.rot_dim, self.interleaved, self.mscale = 2 * len(w), bool(interleaved), float(mscale)
         if not all(math.isfinite(f) for f in w):
             raise ValueError("frequencies must be finite")
-        steps = [int(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for f in w]
+        steps = [round(f / (2 * math.pi) * 2.0 ** 64) % (1 << 64) for f in w]
         self.turns = torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps],
                                   dtype=torch.int64, device=device)
         self.flags = FLAG_ROPE_INTERLEAVED if interleaved else 0

@@ -70,3 +70,15 @@ def test_arguments_by_position_keep_their_places():
     assert names[:17] == ["T", "H", "d", "cu_seqlens", "softmax_scale", "nvfp4_qk", "hadamard", "causal",
                           "H_kv", "deterministic_dq", "dq_accum", "schedule", "ds_rows", "token_scales",
                           "ds_zero_count", "bwd_ctas", "device"]
+
+
+def test_turns_are_rounded():
+    """round(2^64 w / 2 pi), as the C header has it, for slow pairs too."""
+    from fractions import Fraction
+    from precision_causal_attention_block_gb300 import flamia as fl
+    import math
+    w = [1e-9, 3e-12, 7.7e-15, 0.01]
+    r = fl.Rotary(w, device="cpu")
+    for f, t in zip(w, r.turns.tolist()):
+        x = Fraction(f / (2 * math.pi)) * 2 ** 64
+        assert abs(t - x) <= Fraction(1, 2), f
