@@ -530,11 +530,13 @@ flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16, int64
  *   values code * 2^e; lse = log sum exp of the scaled scores (natural log).
  * A query that sees no key (p < 0) gets o = 0 and lse = -inf.  A NaN key or
  * value that a query sees makes its output NaN; one that it does not see, and
- * whatever lies behind a sequence's last token, changes nothing.  Scores and sums
- * are float32; a softmax weight is rounded to 2^-14 of itself (to FP16, 2^-11,
- * with more than 8 query rows a sequence and K / V head on average) or 2^-23 of
- * the row's largest weight times value scale, whichever is more; scores beyond
- * 2^16 within 2^-19 of one another may count as equal.  Positions stay below 2^30.
+ * whatever lies behind a sequence's last token, changes nothing.  Queries enter
+ * exactly but for elements below 2^-13 of their row's largest, which are rounded to
+ * 2^-21 of that.  Scores and sums are float32; a softmax weight is rounded to 2^-14
+ * of itself (to FP16, 2^-11, with more than 8 query rows a sequence and K / V head
+ * on average) or 2^-23 of the row's largest weight times value scale, whichever is
+ * more; scores beyond 2^16 within 2^-19 of one another may count as equal.  Positions
+ * stay below 2^30.
  * Query head h reads K / V head h / (H / H_kv).
  *
  *  q_bf16     BF16 rows [T][H][d], token stride in elements (multiple of 8).

@@ -18,12 +18,14 @@ constexpr int kRowsCtas = 160;        // the same with 256 rows an item
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
 // An item's own steps (queries, first references, output) in tiles.  2 .. 6 are
-// within 4% of one another on the ragged and the windowed batch; with 256 rows an
-// item, 505 tokens over 7,866: 124, 121, 118, 120, 119 us with 1, 3, 5, 7, 9.
+// within 3% of one another on the ragged and the windowed batch; with 256 rows an
+// item, 505 tokens over 7,866: 116, 113, 112, 113, 113 us with 1, 3, 5, 7, 9; 4,096
+// tokens over none: 198, 198, 201, 203, 208.
 template <int R>
 constexpr int kItemCost = R == 256 ? 5 : 3;
-// Items of at most so many tiles stay whole: 64 sequences over 512 tokens 19.6 us
-// whole, 21.7 cut and joined; over 1,024 tokens 36.9 against 34.2.
+// Items of at most so many tiles (as the page table's width bounds them) stay whole: 64
+// sequences over 512 tokens 19.9 us whole, 23.7 cut and joined; over 1,024 tokens 38.9
+// against 37.9.
 constexpr int kWholeTiles = 4;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
@@ -111,8 +113,10 @@ __device__ __forceinline__ float pow2_byte(int byte) {
 // ------------------------------------------------------------------ work
 
 // Sequence b's share of the work: row tiles x K / V heads items of `tiles` key
-// tiles (an upper bound over its row tiles: a segment that runs past its item's
-// last tile is cut there).  An item is `units` long: kItemCost, then a unit
+// tiles (an upper bound over its row tiles, the last one's: a segment that runs past
+// its item's last tile is cut there.  So the first row tiles of a prompt count for more
+// than they have: 4,096 tokens over none take 197 us, at 349 TFLOP/s, where 505 over
+// 7,361 run at 563).  An item is `units` long: kItemCost, then a unit
 // for each tile; one unit if items stay whole.
 struct SeqWork {
   int s, n, start;     // packed rows [s, s + n) at positions start ..

@@ -7,7 +7,7 @@
 // holds, V read MN-major, so nothing converts or transposes them; BF16 queries
 // and float32 weights become sums of E4M3 terms instead, side by side in N:
 //   q 2^-e = h + 2^-4 l              (e per row; exact for the elements above
-//                                     2^-14 of the row's largest),
+//                                     2^-13 of the row's largest),
 //   w      = h + 2^-5 m + 2^-10 l    (relative error at most 2^-14, floor 2^-23
 //                                     of the largest weight; with 16 and 32 rows of
 //                                     w rounded to FP16, 2^-11),
@@ -31,7 +31,8 @@
 // Work: the key tiles of all (sequence, K / V head, row tile) items are laid end
 // to end, with kItemCost tiles' worth for each item's own steps, and cut into
 // equal runs, one for each resident CTA, so that a batch of ragged lengths keeps
-// every SM reading until the end.  A CTA finishes the items that lie whole
+// every SM reading until the end (single and drafted tokens, chunks of a long prompt;
+// a prompt's early row tiles end before their share, see seq_work).  A CTA finishes the items that lie whole
 // inside its run; of the (at most two) it shares it leaves o and log2 sum 2^x
 // in the workspace, and a second small kernel, launched with programmatic
 // dependent launch, joins them in order of position (no atomics: results do not
@@ -45,9 +46,9 @@
 // (More query rows than 96 a K / V head: attn_cache_rows.cu.)
 //
 // Measured: 96 sequences with one new token over 16 .. 16,384 cached (32 / 8 heads
-// of 128) 98 us, 5.9 TB/s of codes and scales; one token over 131,072 (32 heads of
-// 64) 97 us, 5.6 TB/s; 48 sequences with 4 drafted tokens, a window of 4,096 (16 /
-// 4 heads of 128) 52 us, 3.8 TB/s.  HBM bounds the first two, the softmax warps'
+// of 128) 100 us, 5.75 TB/s of codes and scales; one token over 131,072 (32 heads of
+// 64) 100 us, 5.45 TB/s; 48 sequences with 4 drafted tokens, a window of 4,096 (16 /
+// 4 heads of 128) 54 us, 3.7 TB/s.  HBM bounds the first two, the softmax warps'
 // work and waits for a tile (some 2,500 cycles with 8 or 16 rows, 4,000 with 32,
 // two or three tiles at a time on an SM) the last.
 #include <cuda_bf16.h>
@@ -1055,12 +1056,14 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 
 // Query rows side by side in one item: those of a K / V head's mean number of
 // new tokens, up to 32, or 256 (attn_cache_rows.cu).  More rows than there are cost
-// softmax time and resident CTAs (4 rows a head: 98, 104, 158 us with 8, 16, 32; one
-// row: 97, 125, 184), fewer read K and V again for each item (16 rows a head: 70,
-// 52, 73 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 54 and
-// 61 us, 96 rows 70 and 64, 128 rows 89 and 67; one sequence over 4,096, 64 rows 26
-// and 33, 128 rows 32 and 35; 64 sequences over 100, 400 rows 66 and 41; 505 rows over
-// 7,866 224 and 118.
+// softmax time and resident CTAs (4 rows a head: 101, 109, 161 us with 8, 16, 32; one
+// row: 98, 127, 196), fewer read K and V again for each item (16 rows a head: 74,
+// 56, 80 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 55 and
+// 58 us, 96 rows 72 and 60, 128 rows 90 and 63; one sequence over 4,096, 64 rows 28
+// and 35, 128 rows 33 and 36; 64 sequences over 100, 400 rows 73 and 40; 505 rows over
+// 7,300 206 and 105.  The mean is of the whole call: prompts beside single tokens
+// give both the same rows (2,048 tokens over none and 63 single ones over 8,192, 32 /
+// 8 heads of 128: 613 us, apart 120 and 169).
 constexpr int kManyRows = 256;
 
 int rows_per_item(int T, int ndocs, int G) {

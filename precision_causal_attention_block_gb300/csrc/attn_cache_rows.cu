@@ -24,13 +24,15 @@
 // tile's softmax runs the tensor core works for the other.  Runs of key tiles, parts
 // and joins are those of attend.cuh.
 //
-// Measured: 505 tokens over 7,866 (16 heads of 128, two sequences) 118 us, 530
-// TFLOP/s (32 rows an item: 224 us, 280 TFLOP/s); 512 over 8,000 (32 / 8 heads, four
-// sequences) 340 us.  A key tile takes some 5,000 cycles where the tensor core is
-// busy for 2,300: the softmax of a row tile (2,800) and its two products follow one
-// another, and the other row tile fills the gaps only in part.  A CTA's first scores come 16,000 cycles after its
-// start (plan, queries), its output takes 5,000.  Scores of 64 keys in two buffers,
-// so that the softmax does not wait for them, took longer (146 us: twice the
+// Measured: 505 tokens over 7,866 (16 heads of 128, two sequences) 112 us, 560
+// TFLOP/s; 512 over 8,000 (32 / 8 heads, four sequences) 332 us (32 rows an item: 824).
+// With an exponent a token every tile takes the slow body: 505 over 7,361 246 us
+// against 112.  Clock stamps, when the first of these took 118 us: a key tile takes
+// some 5,000 cycles where the tensor core is busy for 2,300, as the softmax of a row
+// tile (2,800) and its two products follow one another and the other row tile fills
+// the gaps only in part; a CTA's first scores come 16,000 cycles after its start (plan,
+// queries), its output takes 5,000.  Scores of 64 keys in two buffers, so that the
+// softmax does not wait for them, took longer (146 us against 122 then: twice the
 // products to issue); K and V loaded and converted side by side, 139 registers
 // and more code, too (181: spills, and misses in the instruction cache).
 #include <cmath>

@@ -117,7 +117,8 @@ __device__ __forceinline__ uint2 encode(const uint4& x, float inv) {
 // packed 16-bit integers, products on float pairs, and infinities and NaN are
 // looked for once a block (a maximum of 0x7F80 or more) instead of at each
 // element.  58,918 tokens x 16 heads x 128: 103 us, 7.0 TB/s (510 us with a check
-// at each element and 178 registers, 199 with 96 registers).
+// at each element and 178 registers, 199 with 96 registers).  With an exponent a
+// token, 3 or 4 shuffles an access come on top: 142 us.
 template <int DIM, bool TOK>
 __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const CacheArgs g) {
   constexpr int LPR = DIM / 8;   // lanes per row: 8 elements each
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kCacheThreads, 5) cache_write_kernel(const Cac
   }
 }
 
-// 79,477 tokens x 16 heads x 128: 145 us, 6.7 TB/s.
+// 79,477 tokens x 16 heads x 128: 144 us, 6.8 TB/s.
 template <int DIM>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheArgs g) {
   constexpr int LPR = DIM / 8;
