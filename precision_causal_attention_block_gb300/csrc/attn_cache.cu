@@ -31,12 +31,12 @@
 // Work: the key tiles of all (sequence, K / V head, row tile) items are laid end
 // to end, with kItemCost tiles' worth for each item's own steps, and cut into
 // equal runs, one for each resident CTA, so that a batch of ragged lengths keeps
-// every SM reading until the end (single and drafted tokens, chunks of a long prompt;
-// a prompt's early row tiles end before their share, see seq_work).  A CTA finishes the items that lie whole
-// inside its run; of the (at most two) it shares it leaves o and log2 sum 2^x
-// in the workspace, and a second small kernel, launched with programmatic
-// dependent launch, joins them in order of position (no atomics: results do not
-// depend on timing).  Where the page table is too narrow for more than
+// every SM reading until the end (single and drafted tokens, chunks of a long
+// prompt; the early row tiles of a prompt end before their share, see seq_work).  A
+// CTA finishes the items that lie whole inside its run; of the (at most two) it shares
+// it leaves o and log2 sum 2^x in the workspace, and a second small kernel, launched
+// with programmatic dependent launch, joins them in order of position (no atomics:
+// results do not depend on timing).  Where the page table is too narrow for more than
 // kWholeTiles tiles an item, items stay whole and the second kernel is not
 // launched.
 //
@@ -812,7 +812,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 #pragma unroll
             for (int r = 0; r < 4; ++r) mx = fmax3(mx, y[r].x, y[r].y);
           }
-          move = mx > C::kShift + C::kSlack || ev > e0 + kHigh || (ev < e0 - kLow && ev != kUnseen);
+          move = mx > C::kShift + C::kSlack || ev > e0 + kHigh ||
+                 (ev < e0 - kLow && ev != kUnseen);
         }
         move = vote(move);
         if (move) {  // E0, then the rows' references
@@ -852,8 +853,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             if (apart) {  // keys that l does not hold
 #pragma unroll
               for (int r = 0; r < 8; ++r) {
-                const float x =
-                    ev < e0 - kLow ? (r & 1 ? y[r / 2].y : y[r / 2].x) - static_cast<float>(ev) : -INFINITY;
+                float x = (r & 1 ? y[r / 2].y : y[r / 2].x) - static_cast<float>(ev);
+                if (ev >= e0 - kLow) x = -INFINITY;
                 const float m = ceilf(fmaxf(warp_max(x), kNoExponent));
                 float s = ex2_approx(x - m);
 #pragma unroll
@@ -939,7 +940,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           if (large) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              y[r] = make_float2(cut(y[r].x, C::kShift + C::kSlack), cut(y[r].y, C::kShift + C::kSlack));
+              y[r] = make_float2(cut(y[r].x, C::kShift + C::kSlack),
+                                 cut(y[r].y, C::kShift + C::kSlack));
           }
           uint32_t tw[3][2];
 #pragma unroll

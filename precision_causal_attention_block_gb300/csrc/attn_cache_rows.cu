@@ -361,7 +361,8 @@ __device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev
           (flags & kEvery) ||
           ((flags & kHere) && key <= pos && (window == 0 || key < sinks || key > pos - window));
       float x = fmaf(__uint_as_float(s[j]), kf[at + j] * qf, nref);
-      if (!(flags & kEvery) && (nan[at / 32] >> ((at + j) & 31)) & 1) x = __uint_as_float(0x7FC00000u);
+      if (!(flags & kEvery) && (nan[at / 32] >> ((at + j) & 31)) & 1)
+        x = __uint_as_float(0x7FC00000u);
       if (!seen || ev[at + j] >= floor_ev) x = -INFINITY;
       if (i < 16)
         top = fmaxf(top, x);
