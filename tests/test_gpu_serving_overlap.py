@@ -59,3 +59,47 @@ def test_replayed_steps(lib, n, first, H, H_kv, d, page, token):
                      (caches[0].k_scales, want.k_scales), (caches[0].v_scales, want.v_scales)):
             assert torch.equal(a, b), i
     step.check_status()
+
+
+def test_beside_a_training_call(lib):
+    """Decode steps and prompts on two streams while a third trains: each gives the bits
+    that it gives alone (the kernels share the SMs' tensor memory, nothing else)."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(91)
+    d, H, H_kv, T = 128, 8, 2, 1500
+    cu = offsets([1000, 500])
+    x = [bf16(rng, (T, h, d)).to(DEV) for h in (H, H_kv, H_kv, H)]
+    rot = fl.Rotary(fl.rope_frequencies(d))
+    train = fl.TrainingCall(T, H, d, cu, d ** -0.5, H_kv=H_kv, deterministic_dq=True, rope=rot)
+    jobs = []
+    for n, first in (([1] * 40, 1200), ([300, 211], 700)):
+        nseq, m = len(n), sum(n)
+        t, pages = page_table(rng, [first + c for c in n], 64)
+        cache = fl.KVCache(pages, 64, H_kv, d)
+        table = torch.from_numpy(t).to(DEV)
+        k, v = (bf16(rng, (first * nseq, H_kv, d)).to(DEV) for _ in range(2))
+        cache.write(k, v, offsets([first] * nseq), None, table)
+        step = fl.DecodeCall(cache, m, nseq, H, d ** -0.5, rope=rot)
+        args = ([bf16(rng, (m, h, d)).to(DEV) for h in (H, H_kv, H_kv)] +
+                [offsets(n), i32([first] * nseq), table])
+        jobs.append((step, args))
+    want = [[y.clone() for y in train(*x)] + [train.o.clone()]]
+    for step, args in jobs:
+        step(*args)
+        want.append([step.o.clone(), step.lse.clone()])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(12):
+        with torch.cuda.stream(streams[0]):
+            train(*x)
+        for s, (step, args) in zip(streams[1:], jobs):
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    step(*args)
+    torch.cuda.synchronize()
+    got = [[train.dq, train.dk, train.dv, train.o]] + [[step.o, step.lse] for step, _ in jobs]
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    train.check_status()
+    for step, _ in jobs:
+        step.check_status()
