@@ -52,15 +52,17 @@ typedef enum {
 
 /* Bits OR-ed into *dev_status by the kernels. */
 #define FLAMIA_DEV_BAD_SEQLENS 0x1  /* cu_seqlens not monotone or not ending at T */
-#define FLAMIA_DEV_CAPACITY    0x2  /* more work items than the buffer holds      */
+#define FLAMIA_DEV_CAPACITY    0x2  /* more work items than the buffer holds, or
+                                       more pages asked for than are free        */
 #define FLAMIA_DEV_TIMEOUT     0x4  /* a bounded wait gave up; outputs invalid    */
 #define FLAMIA_DEV_RANGE       0x8  /* a scale exponent left the E8M0 range a mode
                                        supports (per-token operand scales with
                                        |V| near 2^96 or beyond); outputs invalid */
 #define FLAMIA_DEV_BAD_PAGE    0x10 /* a page-table entry that a call needs lies outside
                                        [0, num_pages), or a sequence's positions
-                                       outside its table; that page is neither read
-                                       nor written                               */
+                                       outside its table, or a sequence outside the
+                                       page table; that page is neither read nor
+                                       written                                   */
 
 /* Quantiser output formats. */
 #define FLAMIA_FORMAT_MXFP8       0 /* E4M3 codes + per-token E8M0 scales          */
@@ -458,6 +460,27 @@ flamia_status flamia_rope(const void* q_in, void* q_out, int64_t q_in_stride,
                           int* dev_status, void* stream);
 
 /*
+ * Rotary positions with several axes (time, height and width of the patches of an
+ * image or a video; text moves along all of them together): flamia_rope with the
+ * position of pair i of token t taken from positions[axes[i] * pos_stride + t].
+ * The caller gives all positions, so there are no starts; a position may be negative.
+ *
+ *  axes       device uint8[rot_dim / 2]: the axis of each pair (naxes - 1 at most;
+ *             larger entries count as that).
+ *  positions  device int32, naxes rows of T entries, pos_stride entries apart.
+ *  naxes      1 .. rot_dim / 2.
+ * Everything else as for flamia_rope (tokens behind the last document are not
+ * written; FLAMIA_FLAG_ROPE_INVERSE turns gradients back).
+ */
+flamia_status flamia_rope_axes(const void* q_in, void* q_out, int64_t q_in_stride,
+                               int64_t q_out_stride, const void* k_in, void* k_out,
+                               int64_t k_in_stride, int64_t k_out_stride, int T, int H, int H_kv,
+                               int d, const uint64_t* turns, const uint8_t* axes, int rot_dim,
+                               float mscale, int flags, const int32_t* positions,
+                               int64_t pos_stride, int naxes, const int32_t* cu_seqlens,
+                               int ndocs, int* dev_status, void* stream);
+
+/*
  * Paged key-value cache: the K and V of running sequences in the quantiser's
  * format, for the calls below.  All device pointers, owned by the caller.
  *  k_codes, v_codes    u8 [num_pages][H_kv][page_size][d]  E4M3 codes.
@@ -519,6 +542,82 @@ flamia_status flamia_cache_read(const flamia_kvcache* cache, void* k_bf16, int64
                                 void* v_bf16, int64_t v_stride, int T, const int32_t* cu_seqlens,
                                 int ndocs, const int32_t* starts, const int32_t* page_table,
                                 int table_stride, int* dev_status, void* stream);
+
+/*
+ * Pages of the cache: the books that say who uses which, kept on the device so that a
+ * captured step can hand out its own pages.
+ *  page_table  device int32 [nseq][table_stride], as above: a row a sequence, -1
+ *              where it has no page.  1 <= nseq <= 65,536, nseq * table_stride < 2^31.
+ *  refs        device int32 [num_pages]: how many slots of the page table hold each
+ *              page; 0: free.  A fresh pool has zeros here and -1 in the table; the
+ *              calls keep the two in line, and both are the caller's to read.
+ * Calls on one pool must not overlap one another, nor calls that use its pages.
+ * What they decide does not depend on timing.  A sequence outside the table or a page
+ * outside the pool sets FLAMIA_DEV_BAD_PAGE and is left alone.
+ */
+
+/*
+ * Copies pages: page dst[i] of `to` becomes page src[i] of `from` (K and V, codes and
+ * scale bytes).  The two caches have the same page_size, H_kv and d, and may be one;
+ * no page may then be both source and target, and in any case none a target twice.
+ * Pairs with a negative entry are left out.  The page table and refs are not touched.
+ *  src, dst   device int32[n].   n == 0 enqueues nothing.
+ */
+flamia_status flamia_pages_copy(const flamia_kvcache* from, const flamia_kvcache* to,
+                                const int32_t* src, const int32_t* dst, int n, int* dev_status,
+                                void* stream);
+
+/*
+ * Sequence children[i] goes on from where parents[i] stands: it gives its pages back,
+ * takes those that hold the first lens[parents[i]] tokens of the parent, shared with it
+ * (refs counted), and that length.  parents[i] < 0, or parents NULL: it only gives
+ * its pages back and has length 0 then.  All parents are read before any child is
+ * written, so children may be parents (beams put in a new order); a sequence that is
+ * its own parent gives back the pages behind its length.  children[i] < 0: nothing.  Of
+ * entries with the same child the last one counts.  No page is copied: see
+ * flamia_pages_reserve.
+ *  parents, children  device int32[n], n <= nseq.   n == 0 enqueues nothing.
+ *  lens       device int32 [nseq]: tokens that each sequence holds (its next starts).
+ *  ws         flamia_pages_fork_workspace_bytes(n, table_stride) bytes, 256-byte aligned.
+ */
+size_t flamia_pages_fork_workspace_bytes(int n, int table_stride);
+flamia_status flamia_pages_fork(int32_t* refs, int num_pages, int32_t* page_table,
+                                int table_stride, int nseq, int page_size,
+                                const int32_t* parents, const int32_t* children, int n,
+                                int32_t* lens, void* ws, size_t ws_bytes, int* dev_status,
+                                void* stream);
+
+/*
+ * Pages for the new tokens of a call: afterwards every slot that positions starts[b] ..
+ * starts[b] + n_b - 1 of sequence b fall into (n_b = cu_seqlens[b + 1] - cu_seqlens[b])
+ * holds a page that no other slot holds.  In order of sequence and slot: one without a page takes
+ * the lowest free one; one whose page has other users takes the lowest free one, to which
+ * the rows of positions below starts[b] are copied, and leaves the old one; if all the
+ * users of a page are among the call's slots, the last of them keeps it.  If there are not
+ * as many free pages, nothing is changed and FLAMIA_DEV_CAPACITY is set.  A sequence
+ * whose positions lie outside its row gets none.
+ * cu_seqlens and starts as for flamia_cache_write (cu_seqlens may end before T).
+ * T == 0 enqueues nothing.
+ *  ws         flamia_pages_reserve_workspace_bytes(T, nseq, table_stride, page_size)
+ *             bytes, 256-byte aligned.
+ */
+size_t flamia_pages_reserve_workspace_bytes(int T, int nseq, int table_stride, int page_size);
+flamia_status flamia_pages_reserve(const flamia_kvcache* cache, int32_t* refs,
+                                   int32_t* page_table, int table_stride, int nseq, int T,
+                                   const int32_t* cu_seqlens, const int32_t* starts, void* ws,
+                                   size_t ws_bytes, int* dev_status, void* stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with `live` of them, the k-th used
+ * page from page `live` on is copied to the k-th free one before it, and the page table
+ * and refs follow.  Other records of page numbers are the caller's to change.
+ *  live       device int32[1], or NULL: the number of pages in use.
+ *  ws         flamia_pages_compact_workspace_bytes(num_pages) bytes, 256-byte aligned.
+ */
+size_t flamia_pages_compact_workspace_bytes(int num_pages);
+flamia_status flamia_pages_compact(const flamia_kvcache* cache, int32_t* refs,
+                                   int32_t* page_table, int table_stride, int nseq, int32_t* live,
+                                   void* ws, size_t ws_bytes, int* dev_status, void* stream);
 
 /*
  * Attention of new tokens over the cache (single tokens, drafted tokens or

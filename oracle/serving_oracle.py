@@ -3,8 +3,8 @@
 TEST INFRASTRUCTURE ONLY, like flamia_oracle (whose E4M3 / E8M0 formats it
 uses): rotary positions, the cache write (one exponent per 32-token block and
 head, held codes rounded again where it grows; or one per token and head), the
-read-back, and softmax attention over cached values with a window and first
-tokens.  Sequences are walked one at a time over plain arrays: the cache is a
+read-back, softmax attention over cached values with a window and first
+tokens, and the books of a pool of pages.  Sequences are walked one at a time over plain arrays: the cache is a
 dict from (sequence, position) to rows, with no pages.
 """
 from __future__ import annotations
@@ -30,6 +30,94 @@ def rope(x, pos, freqs, interleaved=False, mscale=1.0, inverse=False):
     y[..., a] = x[..., a] * c - x[..., b] * s
     y[..., b] = x[..., a] * s + x[..., b] * c
     return y
+
+
+def rope_axes(x, pos, axes, freqs, interleaved=False, mscale=1.0, inverse=False):
+    """Rows x [T, H, d]: pair i turned by pos[axes[i]] * freqs[i], pos [axes, T].  Pairs of
+    one axis are turned together, by rope with the other pairs' frequencies 0 (and their
+    scale taken back)."""
+    x = np.asarray(x, dtype=np.float64)
+    axes, freqs = np.asarray(axes), np.asarray(freqs, dtype=np.float64)
+    r = 2 * len(freqs)
+    y = x.copy()
+    for a in range(axes.max() + 1):
+        z = rope(x, pos[a], np.where(axes == a, freqs, 0.0), interleaved, mscale, inverse)
+        for i in np.nonzero(axes == a)[0]:
+            for e in ((2 * i, 2 * i + 1) if interleaved else (i, i + r // 2)):
+                y[..., e] = z[..., e]
+    return y
+
+
+class Pages:
+    """A pool's books and the arrays of its pages (numpy, first index the page), with
+    the calls that change them, written as one step after another."""
+
+    def __init__(self, page_size, table, refs, arrays):
+        self.page, self.table, self.refs = page_size, np.array(table), np.array(refs)
+        self.arrays = arrays
+
+    def _use(self, p, by):
+        if p >= 0:
+            self.refs[p] += by
+
+    def copy(self, src, dst):
+        for a, b in zip(src, dst):
+            if a >= 0 and b >= 0:
+                for x in self.arrays:
+                    x[b] = x[a]
+
+    def fork(self, parents, children, lens):
+        last = {c: (p, i) for i, (p, c) in enumerate(zip(parents, children)) if c >= 0}
+        rows = {}
+        for c, (p, _) in last.items():
+            n = lens[p] if p >= 0 else 0
+            row = np.full(self.table.shape[1], -1)
+            need = -(-n // self.page)
+            if need:
+                row[:need] = self.table[p, :need]
+            rows[c] = row, n
+        for c, (row, n) in rows.items():
+            for was, now in zip(self.table[c], row):
+                self._use(was, -1)
+                self._use(now, 1)
+            self.table[c], lens[c] = row, n
+
+    def reserve(self, n, starts):
+        """False: not enough free pages (nothing changes)."""
+        slots = [(b, j) for b, (c, s) in enumerate(zip(n, starts)) if c > 0
+                 for j in range(s // self.page, (s + c - 1) // self.page + 1)]
+        table, refs, copies = self.table.copy(), self.refs.copy(), []
+        free = [p for p in range(len(refs)) if refs[p] == 0]
+        # of a page whose users are all here the last one keeps it
+        for b, j in slots:
+            p = table[b, j]
+            users = [s for s in slots if self.table[s] == p]
+            keeps = p >= 0 and (self.refs[p] <= 1 or
+                                (len(users) == self.refs[p] and users[-1] == (b, j)))
+            if keeps:
+                continue
+            if not free:
+                return False
+            q = free.pop(0)
+            if p >= 0:
+                refs[p] -= 1
+                copies.append((p, q, max(starts[b] - j * self.page, 0)))
+            table[b, j], refs[q] = q, 1
+        self.table, self.refs = table, refs
+        for a, b, rows in copies:
+            for x in self.arrays:
+                x[b, :, :rows] = x[a, :, :rows]
+        return True
+
+    def compact(self):
+        live = int((self.refs > 0).sum())
+        for p in range(live, len(self.refs)):
+            if self.refs[p] > 0:
+                q = int(np.nonzero(self.refs == 0)[0][0])
+                self.copy([p], [q])
+                self.refs[q], self.refs[p] = self.refs[p], 0
+                self.table[self.table == p] = q
+        return live
 
 
 class Cache:

@@ -11,6 +11,10 @@
 // unit of the row (8 pairs) in registers while it walks the heads of Q and K.
 // HBM-bound: 2 bytes read and 2 written per element.  131,072 tokens x 64 heads of
 // 64: 300 us, 7.1 TB/s of reads and writes.
+//
+// With several axes (time, height, width of a picture's patches) each pair takes the
+// position of its own axis, and the caller gives the positions of every token: no
+// document has to be looked for, and the rest is the same.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -32,8 +36,11 @@ struct RopeArgs {
   const unsigned long long* turns;
   const int32_t* cu;
   const int32_t* starts;
+  const uint8_t* axes;       // of each pair, with positions [naxes][pos_stride]
+  const int32_t* positions;
+  long long pos_stride;
   int* status;
-  int T, H, H_kv, ndocs, rot;
+  int T, H, H_kv, ndocs, rot, naxes;
   float mscale, sign;
 };
 
@@ -56,7 +63,7 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
   return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-template <int DIM, int kTok, bool INTER>
+template <int DIM, int kTok, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
   constexpr int kUnits = DIM / 16;                       // 16-element units of a row
   constexpr int kLanes = kRopeThreads / kUnits / kTok;   // heads walked side by side
@@ -100,11 +107,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
 
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * kRopeThreads + tid,
                 static_cast<long long>(gridDim.x) * kRopeThreads, g.status);
-  // position of each token (INT_MIN: in no document)
+  // position of each token (INT_MIN: in no document; with axes 0 stands for its own)
   if (warp < kTok) {
     const int t = t0 + warp;
     int pos = INT_MIN;
-    if (t < g.T) {
+    if (AXES) {
+      if (t < min(g.cu[g.ndocs], g.T)) pos = 0;
+    } else if (t < g.T) {
       const int b = warp_last_not_above(g.ndocs, t, lane, [&](int i) { return g.cu[i]; });
       const DocRange r = doc_range(g.cu, b, g.T);
       if (t >= r.s && t < r.e) pos = (g.starts != nullptr ? g.starts[b] : 0) + t - r.s;
@@ -114,8 +123,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
   __syncthreads();
   for (int i = tid; i < kTok * half; i += kRopeThreads) {
     const int tk = i / half, pair = i - tk * half;
+    int pos = s_pos[tk];
+    if (AXES && pos != INT_MIN)
+      pos = g.positions[min(static_cast<int>(g.axes[pair]), g.naxes - 1) * g.pos_stride + t0 + tk];
     const unsigned long long ph =
-        static_cast<unsigned long long>(static_cast<long long>(s_pos[tk])) * g.turns[pair];
+        static_cast<unsigned long long>(static_cast<long long>(pos)) * g.turns[pair];
     float sn, cs;
     sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f, &sn, &cs);
     s_trig[tk][pair] = make_float2(cs * g.mscale, sn * g.mscale * g.sign);
@@ -167,7 +179,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs g) {
   }
 }
 
-template <int DIM>
+template <int DIM, bool AXES>
 bool launch(const RopeArgs& g, bool inter, cudaStream_t s) {
   // Four tokens a CTA share its set-up; with few tokens one each, so that a
   // decode step's heads spread over the GPU (40 heads of 128, one against four:
@@ -176,9 +188,64 @@ bool launch(const RopeArgs& g, bool inter, cudaStream_t s) {
   const bool few = g.T < 3 * 152;
   const int tok = few ? 1 : 4;
   const int grid = (g.T + tok - 1) / tok;
-  auto kern = few ? (inter ? rope_kernel<DIM, 1, true> : rope_kernel<DIM, 1, false>)
-                  : (inter ? rope_kernel<DIM, 4, true> : rope_kernel<DIM, 4, false>);
+  auto kern = few ? (inter ? rope_kernel<DIM, 1, true, AXES> : rope_kernel<DIM, 1, false, AXES>)
+                  : (inter ? rope_kernel<DIM, 4, true, AXES> : rope_kernel<DIM, 4, false, AXES>);
   return launch_after(kern, dim3(grid), kRopeThreads, 0, s, g);
+}
+
+// Both entry points: `g` holds the positions (or starts) already.
+template <bool AXES>
+flamia_status rope(RopeArgs g, const void* q_in, void* q_out, int64_t q_in_stride,
+                   int64_t q_out_stride, const void* k_in, void* k_out, int64_t k_in_stride,
+                   int64_t k_out_stride, int T, int H, int H_kv, int d, const uint64_t* turns,
+                   int rot_dim, float mscale, int flags, const int32_t* cu_seqlens, int ndocs,
+                   int* dev_status, void* stream) {
+  if (!supported_dim(d)) return FLAMIA_ERR_UNSUPPORTED;
+  if (flags & ~(FLAMIA_FLAG_ROPE_INTERLEAVED | FLAMIA_FLAG_ROPE_INVERSE))
+    return FLAMIA_ERR_UNSUPPORTED;
+  if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return FLAMIA_ERR_UNSUPPORTED;
+  if (!valid_batch(T, ndocs) || H <= 0 || H > 4096 || H_kv < 0 || H_kv > 4096 ||
+      !std::isfinite(mscale))
+    return FLAMIA_ERR_INVALID_ARG;
+  if (AXES && (g.naxes < 1 || g.naxes > rot_dim / 2 || g.pos_stride < 0 ||
+               g.pos_stride >= (1ll << 40)))
+    return FLAMIA_ERR_INVALID_ARG;
+  if (T == 0) return FLAMIA_OK;
+  if (turns == nullptr || cu_seqlens == nullptr || !aligned(turns, 8))
+    return FLAMIA_ERR_INVALID_ARG;
+  if (AXES && (g.axes == nullptr || g.positions == nullptr || !aligned(g.positions, 4)))
+    return FLAMIA_ERR_INVALID_ARG;
+  if (!valid_rows(q_in, q_in_stride) || !valid_rows(q_out, q_out_stride) ||
+      (T > 1 && q_out_stride < static_cast<int64_t>(H) * d) ||
+      (q_in == q_out && q_in_stride != q_out_stride))
+    return FLAMIA_ERR_INVALID_ARG;
+  if (H_kv > 0 && (!valid_rows(k_in, k_in_stride) || !valid_rows(k_out, k_out_stride) ||
+                   (T > 1 && k_out_stride < static_cast<int64_t>(H_kv) * d) ||
+                   (k_in == k_out && k_in_stride != k_out_stride)))
+    return FLAMIA_ERR_INVALID_ARG;
+  g.q_in = static_cast<const __nv_bfloat16*>(q_in);
+  g.q_out = static_cast<__nv_bfloat16*>(q_out);
+  g.k_in = static_cast<const __nv_bfloat16*>(k_in);
+  g.k_out = static_cast<__nv_bfloat16*>(k_out);
+  g.q_in_stride = q_in_stride;
+  g.q_out_stride = q_out_stride;
+  g.k_in_stride = k_in_stride;
+  g.k_out_stride = k_out_stride;
+  g.turns = reinterpret_cast<const unsigned long long*>(turns);
+  g.cu = cu_seqlens;
+  g.status = dev_status;
+  g.T = T;
+  g.H = H;
+  g.H_kv = H_kv;
+  g.ndocs = ndocs;
+  g.rot = rot_dim;
+  g.mscale = mscale;
+  g.sign = (flags & FLAMIA_FLAG_ROPE_INVERSE) ? -1.f : 1.f;
+  const bool inter = (flags & FLAMIA_FLAG_ROPE_INTERLEAVED) != 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return (d == 128 ? launch<128, AXES>(g, inter, s) : launch<64, AXES>(g, inter, s))
+             ? FLAMIA_OK
+             : FLAMIA_ERR_CUDA;
 }
 
 }  // namespace
@@ -193,46 +260,27 @@ extern "C" flamia_status flamia_rope(const void* q_in, void* q_out, int64_t q_in
                                      float mscale, int flags, const int32_t* cu_seqlens,
                                      int ndocs, const int32_t* starts, int* dev_status,
                                      void* stream) {
-  if (!supported_dim(d)) return FLAMIA_ERR_UNSUPPORTED;
-  if (flags & ~(FLAMIA_FLAG_ROPE_INTERLEAVED | FLAMIA_FLAG_ROPE_INVERSE))
-    return FLAMIA_ERR_UNSUPPORTED;
-  if (rot_dim < 16 || rot_dim > d || rot_dim % 16 != 0) return FLAMIA_ERR_UNSUPPORTED;
-  if (!valid_batch(T, ndocs) || H <= 0 || H > 4096 || H_kv < 0 || H_kv > 4096 ||
-      !std::isfinite(mscale))
-    return FLAMIA_ERR_INVALID_ARG;
-  if (T == 0) return FLAMIA_OK;
-  if (turns == nullptr || cu_seqlens == nullptr || !aligned(turns, 8))
-    return FLAMIA_ERR_INVALID_ARG;
-  if (!valid_rows(q_in, q_in_stride) || !valid_rows(q_out, q_out_stride) ||
-      (T > 1 && q_out_stride < static_cast<int64_t>(H) * d) ||
-      (q_in == q_out && q_in_stride != q_out_stride))
-    return FLAMIA_ERR_INVALID_ARG;
-  if (H_kv > 0 && (!valid_rows(k_in, k_in_stride) || !valid_rows(k_out, k_out_stride) ||
-                   (T > 1 && k_out_stride < static_cast<int64_t>(H_kv) * d) ||
-                   (k_in == k_out && k_in_stride != k_out_stride)))
-    return FLAMIA_ERR_INVALID_ARG;
   RopeArgs g{};
-  g.q_in = static_cast<const __nv_bfloat16*>(q_in);
-  g.q_out = static_cast<__nv_bfloat16*>(q_out);
-  g.k_in = static_cast<const __nv_bfloat16*>(k_in);
-  g.k_out = static_cast<__nv_bfloat16*>(k_out);
-  g.q_in_stride = q_in_stride;
-  g.q_out_stride = q_out_stride;
-  g.k_in_stride = k_in_stride;
-  g.k_out_stride = k_out_stride;
-  g.turns = reinterpret_cast<const unsigned long long*>(turns);
-  g.cu = cu_seqlens;
   g.starts = starts;
-  g.status = dev_status;
-  g.T = T;
-  g.H = H;
-  g.H_kv = H_kv;
-  g.ndocs = ndocs;
-  g.rot = rot_dim;
-  g.mscale = mscale;
-  g.sign = (flags & FLAMIA_FLAG_ROPE_INVERSE) ? -1.f : 1.f;
-  const bool inter = (flags & FLAMIA_FLAG_ROPE_INTERLEAVED) != 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return (d == 128 ? launch<128>(g, inter, s) : launch<64>(g, inter, s)) ? FLAMIA_OK
-                                                                        : FLAMIA_ERR_CUDA;
+  return rope<false>(g, q_in, q_out, q_in_stride, q_out_stride, k_in, k_out, k_in_stride,
+                     k_out_stride, T, H, H_kv, d, turns, rot_dim, mscale, flags, cu_seqlens, ndocs,
+                     dev_status, stream);
+}
+
+extern "C" flamia_status flamia_rope_axes(const void* q_in, void* q_out, int64_t q_in_stride,
+                                          int64_t q_out_stride, const void* k_in, void* k_out,
+                                          int64_t k_in_stride, int64_t k_out_stride, int T, int H,
+                                          int H_kv, int d, const uint64_t* turns,
+                                          const uint8_t* axes, int rot_dim, float mscale, int flags,
+                                          const int32_t* positions, int64_t pos_stride, int naxes,
+                                          const int32_t* cu_seqlens, int ndocs, int* dev_status,
+                                          void* stream) {
+  RopeArgs g{};
+  g.axes = axes;
+  g.positions = positions;
+  g.pos_stride = pos_stride;
+  g.naxes = naxes;
+  return rope<true>(g, q_in, q_out, q_in_stride, q_out_stride, k_in, k_out, k_in_stride,
+                    k_out_stride, T, H, H_kv, d, turns, rot_dim, mscale, flags, cu_seqlens, ndocs,
+                    dev_status, stream);
 }

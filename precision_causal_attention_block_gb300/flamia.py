@@ -81,6 +81,15 @@ SIGNATURES = {
     "flamia_build_worklist_static": (_i, [_vp, _i, _i, _vp, _sz, _vp, _vp]),
     "flamia_rope": (_i, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i, _i, _i, _i, _vp, _i, _f,
                          _i, _vp, _i, _vp, _vp, _vp]),
+    "flamia_rope_axes": (_i, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i, _i, _i, _i, _vp, _vp,
+                              _i, _f, _i, _vp, _i64, _i, _vp, _i, _vp, _vp]),
+    "flamia_pages_copy": (_i, [_CP, _CP, _vp, _vp, _i, _vp, _vp]),
+    "flamia_pages_fork_workspace_bytes": (_sz, [_i, _i]),
+    "flamia_pages_fork": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp, _vp]),
+    "flamia_pages_reserve_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "flamia_pages_reserve": (_i, [_CP, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "flamia_pages_compact_workspace_bytes": (_sz, [_i]),
+    "flamia_pages_compact": (_i, [_CP, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp, _vp]),
     "flamia_cache_write": (_i, [_CP, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _i, _vp,
                                 _vp]),
     "flamia_cache_read": (_i, [_CP, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _vp, _vp]),
@@ -326,12 +335,28 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0,
     return w
 
 
+def rope_axes(sections, cyclic: bool = False):
+    """The axis of every pair, for Rotary: the first sections[0] pairs turn with axis 0,
+    the next sections[1] with axis 1, and so on; cyclic: axes by turns (0, 1, 2, 0, 1, 2,
+    ..), each until it has its pairs."""
+    left = [int(n) for n in sections]
+    if not left or min(left) < 0:
+        raise ValueError("sections must be counts of pairs")
+    if not cyclic:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    return [a for turn in range(max(left)) for a, n in enumerate(left) if turn < n]
+
+
 class Rotary:
     """Rotary positions with the angles p * frequencies[i] (see
-    rope_frequencies); holds the device table of turns per position."""
+    rope_frequencies); holds the device table of turns per position.
+
+    axes (see rope_axes): the axis of each pair.  Calls then take ``positions``, int32
+    [axes, T], instead of starts: those of every packed token (time, height and width
+    of a patch; the same number on all axes for text)."""
 
     def __init__(self, frequencies, interleaved: bool = False, mscale: float = 1.0,
-                 device="cuda"):
+                 device="cuda", axes=None):
         w = [float(f) for f in frequencies]
         self.rot_dim, self.interleaved, self.mscale = 2 * len(w), bool(interleaved), float(mscale)
         if not all(math.isfinite(f) for f in w):
@@ -340,21 +365,32 @@ class Rotary:
         self.turns = torch.tensor([s - (1 << 64) if s >> 63 else s for s in steps],
                                   dtype=torch.int64, device=device)
         self.flags = FLAG_ROPE_INTERLEAVED if interleaved else 0
+        self.axes, self.naxes = None, 0
+        if axes is not None:
+            a = [int(x) for x in axes]
+            if len(a) != len(w) or not a or min(a) < 0 or max(a) >= len(w):
+                raise ValueError("axes: expected an axis for each pair, fewer axes than pairs or as many")
+            self.naxes = max(a) + 1
+            self.axes = torch.tensor(a, dtype=torch.uint8, device=device)
 
     def __call__(self, q, k, cu_seqlens, starts=None, q_out=None, k_out=None,
-                 inverse: bool = False, dev_status=None):
+                 inverse: bool = False, dev_status=None, positions=None):
         """Rotated q and k (k may be None); inverse: gradients of the rotated
-        rows -> gradients of the rows.  q_out / k_out may be q / k."""
+        rows -> gradients of the rows.  q_out / k_out may be q / k.  positions: with
+        axes, and then instead of starts (it may have more rows than axes are used)."""
+        if (positions is None) != (self.axes is None) or not (positions is None or starts is None):
+            raise RuntimeError("positions: needed with axes, without starts, and only then")
         q_out = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
         if k is not None and k_out is None:
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
-        flamia_rope(q, q_out, k, k_out, self, cu_seqlens, starts, inverse, dev_status)
+        if positions is None:
+            flamia_rope(q, q_out, k, k_out, self, cu_seqlens, starts, inverse, dev_status)
+        else:
+            flamia_rope_axes(q, q_out, k, k_out, self, positions, cu_seqlens, inverse, dev_status)
         return q_out, k_out
 
 
-def flamia_rope(q_in, q_out, k_in, k_out, rotary: Rotary, cu_seqlens, starts=None,
-                inverse: bool = False, dev_status=None):
-    dev, stream = _current()
+def _rope_rows(q_in, q_out, k_in, k_out, rotary, dev):
     if q_in.dim() != 3:
         raise RuntimeError("q_in: flamia needs BF16 rows [T, heads, d]")
     T, H, d = q_in.shape
@@ -365,16 +401,42 @@ def flamia_rope(q_in, q_out, k_in, k_out, rotary: Rotary, cu_seqlens, starts=Non
         H_kv = k_in.shape[1]
         ki, kis = _rows(k_in, "k_in", T, H_kv, d, dev)
         ko, kos = _rows(k_out, "k_out", T, H_kv, d, dev, True)
-    n = cu_seqlens.numel() - 1
     if rotary.turns.get_device() != dev:
         _elsewhere("turns")
+    return qi, qo, qis, qos, ki, ko, kis, kos, T, H, H_kv, d, rotary.turns.data_ptr()
+
+
+def flamia_rope(q_in, q_out, k_in, k_out, rotary: Rotary, cu_seqlens, starts=None,
+                inverse: bool = False, dev_status=None):
+    dev, stream = _current()
+    rows = _rope_rows(q_in, q_out, k_in, k_out, rotary, dev)
+    n = cu_seqlens.numel() - 1
     st = (_LIB or load()).flamia_rope(
-        qi, qo, qis, qos, ki, ko, kis, kos, T, H, H_kv, d, rotary.turns.data_ptr(),
-        rotary.rot_dim, rotary.mscale, rotary.flags | (FLAG_ROPE_INVERSE if inverse else 0),
+        *rows, rotary.rot_dim, rotary.mscale,
+        rotary.flags | (FLAG_ROPE_INVERSE if inverse else 0),
         _ints(cu_seqlens, "cu_seqlens", 0, dev), n, _ints(starts, "starts", n, dev),
         _ints(dev_status, "dev_status", 0, dev), stream)
     if st:
         _check(st, "flamia_rope")
+
+
+def flamia_rope_axes(q_in, q_out, k_in, k_out, rotary: Rotary, positions, cu_seqlens,
+                     inverse: bool = False, dev_status=None):
+    dev, stream = _current()
+    rows = _rope_rows(q_in, q_out, k_in, k_out, rotary, dev)
+    T = q_in.shape[0]
+    if (positions.dtype is not _I32 or positions.dim() != 2 or positions.shape[0] < rotary.naxes
+            or positions.shape[1] != T or (T > 1 and positions.stride(1) != 1)):
+        raise RuntimeError(f"positions: expected int32 [{rotary.naxes}, {T}], tokens side by side")
+    if positions.get_device() != dev:
+        _elsewhere("positions")
+    st = (_LIB or load()).flamia_rope_axes(
+        *rows, rotary.axes.data_ptr(), rotary.rot_dim, rotary.mscale,
+        rotary.flags | (FLAG_ROPE_INVERSE if inverse else 0), positions.data_ptr(),
+        positions.stride(0), rotary.naxes, _ints(cu_seqlens, "cu_seqlens", 0, dev),
+        cu_seqlens.numel() - 1, _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_rope_axes")
 
 
 class KVCache:
@@ -438,6 +500,12 @@ class KVCache:
             v_out = torch.empty_like(k_out)
         flamia_cache_read(self, k_out, v_out, cu_seqlens, starts, page_table, dev_status)
         return k_out, v_out
+
+    def copy_pages(self, src, dst, source: "KVCache" = None, dev_status=None):
+        """Page dst[i] becomes page src[i] of `source` (None: of this cache); int32
+        tensors, pairs with a negative entry are left out.  No page may be a target
+        twice, or source and target."""
+        flamia_pages_copy(self if source is None else source, self, src, dst, dev_status)
 
     def attend(self, q, cu_seqlens, starts, page_table, softmax_scale: float, window: int = 0,
                sinks: int = 0, o=None, lse=None, ws=None, dev_status=None):
@@ -555,6 +623,143 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
         _ints(dev_status, "dev_status", 0, dev), stream)
     if st:
         _check(st, "flamia_attn_cache")
+
+
+def flamia_pages_copy(source: KVCache, target: KVCache, src, dst, dev_status=None):
+    dev, stream = _current()
+    n = src.numel()
+    sp, dp = _ints(src, "src", 0, dev), _ints(dst, "dst", n, dev)
+    if dst.numel() != n:
+        raise RuntimeError(f"dst: expected {n} entries")
+    if source.device_index != dev or target.device_index != dev:
+        _elsewhere("cache")
+    st = (_LIB or load()).flamia_pages_copy(source._ref, target._ref, sp, dp, n,
+                                            _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_pages_copy")
+
+
+def flamia_pages_fork_workspace_bytes(n: int, table_stride: int) -> int:
+    return int(load().flamia_pages_fork_workspace_bytes(n, table_stride))
+
+
+def flamia_pages_reserve_workspace_bytes(T: int, nseq: int, table_stride: int,
+                                         page_size: int) -> int:
+    return int(load().flamia_pages_reserve_workspace_bytes(T, nseq, table_stride, page_size))
+
+
+def flamia_pages_compact_workspace_bytes(num_pages: int) -> int:
+    return int(load().flamia_pages_compact_workspace_bytes(num_pages))
+
+
+class PagePool:
+    """Who uses which page of a cache: page_table int32 [nseq, width] (-1: no page) and
+    refs int32 [pages] (slots of the table that hold a page; 0: free), on the device and
+    the caller's to read.  Calls on one pool follow one another on one stream (or are
+    ordered by the caller); they can be captured.  Errors found on the device (no free
+    page, positions outside the table) show in check_status."""
+
+    def __init__(self, cache: KVCache, nseq: int, width: int):
+        dev = cache.k_codes.device
+        self._set(cache, torch.full((nseq, width), -1, dtype=torch.int32, device=dev),
+                  torch.zeros(cache.num_pages, dtype=torch.int32, device=dev))
+
+    @classmethod
+    def from_buffers(cls, cache: KVCache, page_table, refs):
+        """A pool over the caller's tensors, which have to agree."""
+        self = cls.__new__(cls)
+        self._set(cache, page_table, refs)
+        return self
+
+    def _set(self, cache, page_table, refs):
+        if page_table.dtype is not _I32 or page_table.dim() != 2 or not page_table.is_contiguous():
+            raise RuntimeError("page_table: expected contiguous int32 [sequences, pages]")
+        if refs.dtype is not _I32 or refs.shape != (cache.num_pages,) or not refs.is_contiguous():
+            raise RuntimeError(f"refs: expected contiguous int32 [{cache.num_pages}]")
+        if not page_table.device == refs.device == cache.k_codes.device:
+            raise RuntimeError("page_table, refs: expected on the cache's device")
+        self.cache, self.page_table, self.refs = cache, page_table, refs
+        self.nseq, self.width = page_table.shape
+        self.status = torch.zeros(1, dtype=torch.int32, device=refs.device)
+
+    def _begin(self):
+        dev, stream = _current()
+        if self.cache.device_index != dev:
+            _elsewhere("pool")
+        return dev, stream
+
+    def _workspace(self, size):
+        # (of the call: the allocator hands it on in the stream's order, or keeps it for
+        # the graph that is being captured)
+        return torch.empty(size, dtype=torch.uint8, device=self.refs.device)
+
+    def fork(self, parents, children, lens):
+        """Sequences children[i] go on from parents[i] (int32 tensors): they give their
+        pages back, share those of the parent's first lens[parent] tokens, and
+        lens[child] becomes lens[parent] (lens int32 [nseq]).  Negative parents, or None:
+        the pages are given back and the length is 0.  Children may be parents of
+        others; negative children are left out, and of a child's entries the last counts."""
+        dev, stream = self._begin()
+        n = children.numel()
+        cp = _ints(children, "children", 0, dev)
+        pp = _ints(parents, "parents", n, dev)
+        if parents is not None and parents.numel() != n:
+            raise RuntimeError(f"parents: expected {n} entries")
+        lp = _ints(lens, "lens", self.nseq, dev)
+        if n == 0:
+            return
+        lib = _LIB or load()
+        ws = self._workspace(lib.flamia_pages_fork_workspace_bytes(n, self.width))
+        st = lib.flamia_pages_fork(self.refs.data_ptr(), self.cache.num_pages,
+                                   self.page_table.data_ptr(), self.width, self.nseq,
+                                   self.cache.page_size, pp, cp, n, lp, ws.data_ptr(), ws.nbytes,
+                                   self.status.data_ptr(), stream)
+        if st:
+            _check(st, "flamia_pages_fork")
+
+    def release(self, sequences, lens):
+        """The sequences' pages are given back and their lengths become 0."""
+        self.fork(None, sequences, lens)
+
+    def reserve(self, cu_seqlens, starts, T: int = None):
+        """Pages for the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 at positions
+        starts[b] .. of every sequence: what is missing is taken from the free pages, and
+        a page with other users is replaced by a copy.  T: an upper bound of the number
+        of tokens (None: one that every table row could hold)."""
+        dev, stream = self._begin()
+        cp = _ints(cu_seqlens, "cu_seqlens", self.nseq + 1, dev)
+        sp = _ints(starts, "starts", self.nseq, dev)
+        if T is None:
+            T = min(1 << 20, self.nseq * self.width * self.cache.page_size)
+        lib = _LIB or load()
+        ws = self._workspace(lib.flamia_pages_reserve_workspace_bytes(T, self.nseq, self.width,
+                                                                      self.cache.page_size))
+        st = lib.flamia_pages_reserve(self.cache._ref, self.refs.data_ptr(),
+                                      self.page_table.data_ptr(), self.width, self.nseq, T, cp, sp,
+                                      ws.data_ptr(), ws.nbytes, self.status.data_ptr(), stream)
+        if st:
+            _check(st, "flamia_pages_reserve")
+
+    def compact(self, live=None):
+        """Moves the used pages to the front of the pool (page table and refs follow) and
+        returns their number, int32 [1] on the device."""
+        dev, stream = self._begin()
+        if live is None:
+            live = torch.empty(1, dtype=torch.int32, device=self.refs.device)
+        lib = _LIB or load()
+        ws = self._workspace(lib.flamia_pages_compact_workspace_bytes(self.cache.num_pages))
+        st = lib.flamia_pages_compact(self.cache._ref, self.refs.data_ptr(),
+                                      self.page_table.data_ptr(), self.width, self.nseq,
+                                      _ints(live, "live", 1, dev), ws.data_ptr(), ws.nbytes,
+                                      self.status.data_ptr(), stream)
+        if st:
+            _check(st, "flamia_pages_compact")
+        return live
+
+    def check_status(self):
+        st = int(self.status.item())
+        if st != 0:
+            raise RuntimeError(f"flamia device status 0x{st:x}")
 
 
 def flamia_debug_tmem_ldred(x, vals, mx):
