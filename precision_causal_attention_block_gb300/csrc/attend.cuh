@@ -31,6 +31,16 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
 constexpr int kLow = 60;        // keys whose eV lies further below E0 are summed apart
 
+// What a kernel's items are.  A call whose sequences share a prefix (attn_prefix.cu)
+// takes one kernel over the prefix's whole tiles, with the tokens of all sequences as the
+// query rows of each K / V head, and one over what comes behind them; both leave float32
+// results, and a last kernel joins those.
+enum Keys : int {
+  kAll = 0,     // items of every sequence: all its keys
+  kPrefix = 1,  // items of the whole call: the first `shared` tiles
+  kRest = 2     // items of every sequence: the tiles behind those (all, if it does not share)
+};
+
 struct AttendArgs {
   const uint8_t *k_scales, *v_scales;
   const __nv_bfloat16* q;
@@ -46,6 +56,12 @@ struct AttendArgs {
   int cap;           // positions that the page table has room for
   int whole;         // items stay whole
   float scale_log2;
+  // with a shared prefix
+  float* row_stats;  // [T][H]: stats of items that were not cut
+  float* rows;       // [T][H][d]: their o
+  long long* first;  // [ndocs + 1]: units before each sequence (kRest)
+  int shared;        // tiles of the prefix
+  int prefix;        // its tokens
 };
 
 // Two bounded waits of a converged warp whose latencies overlap: a wait for a
@@ -126,9 +142,26 @@ struct SeqWork {
   }
 };
 
-template <int R>
+// A sequence shares the prefix if all its new tokens see it.
+__device__ __forceinline__ bool shares(const AttendArgs& g, int start) {
+  return start >= g.prefix - 1;
+}
+
+template <int R, int KEYS>
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
   SeqWork w;
+  if constexpr (KEYS == kPrefix) {
+    // (positions behind the prefix: every row sees every key)
+    w.s = 0;
+    w.n = min(max(g.cu[g.ndocs], 0), g.T);
+    w.start = g.shared * 128;
+    w.row_tiles = b < g.ndocs
+                      ? static_cast<int>((static_cast<long long>(w.n) * g.G + R - 1) / R)
+                      : 0;  // (nobody shares it)
+    w.tiles = g.shared;
+    w.units = w.tiles + kItemCost<R>;
+    return w;
+  }
   const DocRange r = doc_range(g.cu, b, g.T);
   w.s = r.s;
   w.n = r.e - r.s;
@@ -139,7 +172,8 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
   // (no further than the page table: a wild first position costs no endless walk)
   const int end = min(max(w.start + w.n, 0), g.cap);
   int tiles = (end + 127) >> 7;
-  if (g.window > 0)
+  if (KEYS == kRest && shares(g, w.start)) tiles -= g.shared;
+  if (KEYS == kAll && g.window > 0)
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
                            ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);
   w.tiles = max(tiles, 1);
@@ -188,13 +222,37 @@ __device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long 
 // Total units, and this CTA's run of them: [u0, u1), starting at unit `off` of
 // sequence b.  Every thread sums a stretch of sequences; the one whose stretch
 // holds u0 walks it.
-template <int R, int kThreads, class Sm>
+template <int R, int KEYS, int kThreads, class Sm>
 __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int each = (g.ndocs + kThreads - 1) / kThreads;
   const int b0 = min(tid * each, g.ndocs), b1 = min(b0 + each, g.ndocs);
+  if constexpr (KEYS == kPrefix) {
+    // the first sequence that shares: its pages are read
+    if (tid == 0) sm.plan_b = g.ndocs;
+    __syncthreads();
+    for (int b = b0; b < b1; ++b) {
+      const DocRange r = doc_range(g.cu, b, g.T);
+      if (r.e > r.s && g.starts != nullptr && shares(g, g.starts[b])) {
+        atomicMin(&sm.plan_b, b);
+        break;
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      const SeqWork w = seq_work<R, KEYS>(g, sm.plan_b);
+      const long long total = w.total(g.H_kv), ctas = active_ctas<R>(g, total), c = blockIdx.x;
+      sm.plan_u0 = c < ctas ? mul_div(total, c, ctas) : total;
+      sm.plan_u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;
+      sm.plan_total = total;
+      sm.plan_seq = w;
+      sm.plan_off = sm.plan_u0;
+    }
+    __syncthreads();
+    return;
+  }
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_work<R>(g, b).total(g.H_kv);
+  for (int b = b0; b < b1; ++b) sum += seq_work<R, KEYS>(g, b).total(g.H_kv);
   long long inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -210,6 +268,14 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
   }
+  if (KEYS == kRest && blockIdx.x == 0) {  // for the kernel that joins
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      g.first[b] = at;
+      at += seq_work<R, KEYS>(g, b).total(g.H_kv);
+    }
+    if (tid == 0) g.first[g.ndocs] = total;
+  }
   const long long ctas = active_ctas<R>(g, total);
   const long long c = blockIdx.x;
   const long long u0 = c < ctas ? mul_div(total, c, ctas) : total;
@@ -222,10 +288,10 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   if (u0 < u1 && before <= u0 && u0 < before + sum) {
     long long off = u0 - before;
     int b = b0;
-    SeqWork w = seq_work<R>(g, b);
+    SeqWork w = seq_work<R, KEYS>(g, b);
     while (b < b1 - 1 && off >= w.total(g.H_kv)) {
       off -= w.total(g.H_kv);
-      w = seq_work<R>(g, ++b);
+      w = seq_work<R, KEYS>(g, ++b);
     }
     sm.plan_b = b;
     sm.plan_seq = w;
@@ -327,7 +393,24 @@ inline bool launch_large(void (*kern)(P...), std::atomic<unsigned long long>& ra
          (raise() && launch_after(kern, grid, threads, smem, s, args...));
 }
 
-// The kernel for many query rows (256 an item).
-flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
+// Checks of a call's arguments, and all of g but the workspace (T == 0: nothing).
+flamia_status attend_args(AttendArgs& g, const flamia_kvcache* cache, const void* q_bf16,
+                          int64_t q_stride, int T, int H, const int32_t* cu_seqlens, int ndocs,
+                          const int32_t* starts, const int32_t* page_table, int table_stride,
+                          float softmax_scale, int window, int sinks, void* o_bf16, float* lse,
+                          const void* ws, int* dev_status);
+// The kernel for many query rows (256 an item), and its CTAs.
+flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, Keys keys, cudaStream_t s);
+int rows_grid();
+// Those for 8, 16 or 32 rows an item.
+flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
+                         cudaStream_t s);
+int few_grid(int R);
+// Query rows side by side in one item: `rows` of a K / V head on average.
+constexpr int kManyRows = 256;
+int rows_per_item(long long rows);
+inline long long mean_rows(int T, int ndocs, int G) {
+  return ((static_cast<long long>(T) + ndocs - 1) / ndocs) * G;
+}
 
 }  // namespace flamia

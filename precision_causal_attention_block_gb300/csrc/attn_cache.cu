@@ -297,7 +297,7 @@ struct Queries {
   }
 };
 
-template <int DIM, int R>
+template <int DIM, int R, int KEYS>
 __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     attend_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttendArgs g) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
                 static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   tc_fence_before();
-  make_plan<R, C::kThreads>(g, sm);
+  make_plan<R, KEYS, C::kThreads>(g, sm);
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
@@ -389,10 +389,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
                                                       static_cast<long long>(sg.row0) + R - 1) /
                                                   g.G);
-        hi = max(pl + 1, 0);
+        hi = KEYS == kPrefix ? g.shared * 128 : max(pl + 1, 0);
         wlo = g.window > 0 ? max(pf - g.window + 1, 0) : 0;
-        sg.wt = wlo >> 7;
-        sg.ns = min((g.sinks + 127) >> 7, sg.wt);
+        sg.wt = KEYS == kRest && shares(g, w.start) ? g.shared : wlo >> 7;
+        sg.ns = KEYS == kAll ? min((g.sinks + 127) >> 7, sg.wt) : 0;
         const int list = sg.ns + max(((hi + 127) >> 7) - sg.wt, 0);
         sg.i0 = min(i0, list);
         sg.i1 = min(i1, list);
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           sg.slot = 2 * blockIdx.x;
         else if (i1 < w.tiles)
           sg.slot = 2 * blockIdx.x + 1;
-        if (first && i0 > 0) {
+        if (KEYS == kAll && first && i0 > 0) {
           // the second CTA of an item has it joined: parts are the CTA before
           // this one (slot 1) and slots 0 from here on
           const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             join1 = make_int4(sg.row0, 0, 0, 0);
           }
         }
-        if (lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
+        if (KEYS != kPrefix && lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
           const int raw = g.starts != nullptr ? g.starts[b] : 0;
           if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
         }
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (++hk == g.H_kv) {
           hk = 0;
           do {
-            w = seq_work<R>(g, ++b);  // there is one: u < u1
+            w = seq_work<R, KEYS>(g, ++b);  // there is one: u < u1
           } while (w.row_tiles == 0 && b + 1 < g.ndocs);
         }
       }
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       }
     }
     // what the second kernel has to join for this CTA's first item
-    if (lane == 0 && !g.whole) {
+    if (KEYS == kAll && lane == 0 && !g.whole) {
       g.joins[2 * blockIdx.x] = join0;
       g.joins[2 * blockIdx.x + 1] = join1;
     }
@@ -1005,6 +1005,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const int orow = sm.orow[tid];
         if (slot >= 0)
           g.stats[static_cast<size_t>(slot) * R + tid] = lg;
+        else if (KEYS != kAll)
+          g.row_stats[orow] = lg;
         else if (g.lse != nullptr)
           g.lse[static_cast<size_t>(orow % g.H) * g.T + orow / g.H] = lg * kLn2;
       }
@@ -1031,6 +1033,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
                        __uint_as_float(h[i])) * f * sm.ve[r];
             if (slot >= 0)
               g.partial[(static_cast<size_t>(slot) * R + r) * DIM + key_in] = v;
+            else if (KEYS != kAll)
+              g.rows[static_cast<size_t>(sm.orow[r]) * DIM + key_in] = v;
             else
               g.o[static_cast<size_t>(sm.orow[r]) * DIM + key_in] = __float2bfloat16(v);
           }
@@ -1055,23 +1059,6 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
 }
 
 // ------------------------------------------------------------------ host
-
-// Query rows side by side in one item: those of a K / V head's mean number of
-// new tokens, up to 32, or 256 (attn_cache_rows.cu).  More rows than there are cost
-// softmax time and resident CTAs (4 rows a head: 101, 109, 161 us with 8, 16, 32; one
-// row: 98, 127, 196), fewer read K and V again for each item (16 rows a head: 74,
-// 56, 80 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 55 and
-// 58 us, 96 rows 72 and 60, 128 rows 90 and 63; one sequence over 4,096, 64 rows 28
-// and 35, 128 rows 33 and 36; 64 sequences over 100, 400 rows 73 and 40; 505 rows over
-// 7,300 206 and 105.  The mean is of the whole call: prompts beside single tokens
-// give both the same rows (2,048 tokens over none and 63 single ones over 8,192, 32 /
-// 8 heads of 128: 613 us, apart 120 and 169).
-constexpr int kManyRows = 256;
-
-int rows_per_item(int T, int ndocs, int G) {
-  const long long rows = ((static_cast<long long>(T) + ndocs - 1) / ndocs) * G;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 96 ? 32 : kManyRows;
-}
 
 struct Workspace {
   size_t joins, stats, partial, total;
@@ -1103,22 +1090,63 @@ bool make_page_map(CUtensorMap* map, const uint8_t* codes, const flamia_kvcache*
 }
 
 template <int DIM, int R>
+constexpr int kResident = Cfg<DIM, R>::kCtas;
+static_assert(kResident<128, 8> == kResident<64, 8> && kResident<128, 16> == kResident<64, 16> &&
+              kResident<128, 32> == kResident<64, 32>, "few_grid");
+
+template <int DIM, int R, int KEYS>
 flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
   CUtensorMap mk, mv;
   if (!make_page_map(&mk, c->k_codes, c) || !make_page_map(&mv, c->v_codes, c))
     return FLAMIA_ERR_CUDA;
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM, R>)) + 1024;
   static_assert(Cfg<DIM, R>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
-  const int grid = min(kMaxCtas, num_sms() * Cfg<DIM, R>::kCtas);
+  const int grid = few_grid(R);
   static std::atomic<unsigned long long> raised{0};
-  return launch_large(attend_kernel<DIM, R>, raised, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk,
+  return launch_large(attend_kernel<DIM, R, KEYS>, raised, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk,
                       mv, g) &&
-                 (g.whole || launch_join<DIM, R>(grid, s, g))
+                 (KEYS != kAll || g.whole || launch_join<DIM, R>(grid, s, g))
              ? FLAMIA_OK
              : FLAMIA_ERR_CUDA;
 }
 
+template <int KEYS>
+flamia_status launch_few(const flamia_kvcache* c, const AttendArgs& g, int R, cudaStream_t s) {
+  if (c->d == 128)
+    return R == 8 ? launch<128, 8, KEYS>(c, g, s)
+                  : R == 16 ? launch<128, 16, KEYS>(c, g, s) : launch<128, 32, KEYS>(c, g, s);
+  return R == 8 ? launch<64, 8, KEYS>(c, g, s)
+                : R == 16 ? launch<64, 16, KEYS>(c, g, s) : launch<64, 32, KEYS>(c, g, s);
+}
+
 }  // namespace
+
+int few_grid(int R) {
+  const int ctas = R == 8 ? kResident<128, 8> : R == 16 ? kResident<128, 16> : kResident<128, 32>;
+  return min(kMaxCtas, num_sms() * ctas);
+}
+
+flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
+                         cudaStream_t s) {
+  return keys == kAll ? launch_few<kAll>(c, g, R, s)
+                      : keys == kPrefix ? launch_few<kPrefix>(c, g, R, s)
+                                        : launch_few<kRest>(c, g, R, s);
+}
+
+// Query rows side by side in one item: those of a K / V head's mean number of
+// new tokens, up to 32, or 256 (attn_cache_rows.cu).  More rows than there are cost
+// softmax time and resident CTAs (4 rows a head: 101, 109, 161 us with 8, 16, 32; one
+// row: 98, 127, 196), fewer read K and V again for each item (16 rows a head: 74,
+// 56, 80 us).  32 against 256 (heads of 128): 8 sequences over 2,048, 64 rows 55 and
+// 58 us, 96 rows 72 and 60, 128 rows 90 and 63; one sequence over 4,096, 64 rows 28
+// and 35, 128 rows 33 and 36; 64 sequences over 100, 400 rows 73 and 40; 505 rows over
+// 7,300 206 and 105.  The mean is of the whole call: prompts beside single tokens
+// give both the same rows (2,048 tokens over none and 63 single ones over 8,192, 32 /
+// 8 heads of 128: 613 us, apart 120 and 169).
+int rows_per_item(long long rows) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 96 ? 32 : kManyRows;
+}
+
 }  // namespace flamia
 
 using namespace flamia;
@@ -1127,16 +1155,16 @@ extern "C" size_t flamia_attn_cache_workspace_bytes(int T, int ndocs, int H, int
   if (!supported_dim(d) || !valid_batch(T, ndocs) || H <= 0 || H > 4096 || H_kv <= 0 ||
       H % H_kv != 0)
     return 0;
-  return layout(rows_per_item(T, ndocs, H / H_kv), d).total;
+  return layout(rows_per_item(mean_rows(T, ndocs, H / H_kv)), d).total;
 }
 
-extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const void* q_bf16,
-                                           int64_t q_stride, int T, int H,
-                                           const int32_t* cu_seqlens, int ndocs,
-                                           const int32_t* starts, const int32_t* page_table,
-                                           int table_stride, float softmax_scale, int window,
-                                           int sinks, void* o_bf16, float* lse, void* ws,
-                                           size_t ws_bytes, int* dev_status, void* stream) {
+namespace flamia {
+
+flamia_status attend_args(AttendArgs& g, const flamia_kvcache* cache, const void* q_bf16,
+                          int64_t q_stride, int T, int H, const int32_t* cu_seqlens, int ndocs,
+                          const int32_t* starts, const int32_t* page_table, int table_stride,
+                          float softmax_scale, int window, int sinks, void* o_bf16, float* lse,
+                          const void* ws, int* dev_status) {
   const flamia_status st = check_cache(cache);
   if (st != FLAMIA_OK) return st;
   if (!valid_batch(T, ndocs) || table_stride <= 0 || H <= 0 || H > 4096 || H % cache->H_kv != 0 ||
@@ -1148,11 +1176,6 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
       cu_seqlens == nullptr || page_table == nullptr || ws == nullptr || !aligned(ws, 256) ||
       !aligned(lse, 4))
     return FLAMIA_ERR_INVALID_ARG;
-  const int G = H / cache->H_kv, d = cache->d;
-  const int R = rows_per_item(T, ndocs, G);
-  const Workspace w = layout(R, d);
-  if (ws_bytes < w.total) return FLAMIA_ERR_WORKSPACE;
-  AttendArgs g{};
   g.k_scales = cache->k_scales;
   g.v_scales = cache->v_scales;
   g.q = static_cast<const __nv_bfloat16*>(q_bf16);
@@ -1161,15 +1184,12 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   g.cu = cu_seqlens;
   g.starts = starts;
   g.table = page_table;
-  g.joins = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + w.joins);
-  g.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.stats);
-  g.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.partial);
   g.status = dev_status;
   g.q_stride = q_stride;
   g.T = T;
   g.H = H;
   g.H_kv = cache->H_kv;
-  g.G = G;
+  g.G = H / cache->H_kv;
   g.ndocs = ndocs;
   g.table_stride = table_stride;
   g.num_pages = cache->num_pages;
@@ -1181,11 +1201,29 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   g.cap = static_cast<int>(cap < kMaxPos ? cap : kMaxPos);
   g.whole = cap <= 128 * kWholeTiles;
   g.scale_log2 = softmax_scale * 1.44269504088896340736f;
+  return FLAMIA_OK;
+}
+
+}  // namespace flamia
+
+extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const void* q_bf16,
+                                           int64_t q_stride, int T, int H,
+                                           const int32_t* cu_seqlens, int ndocs,
+                                           const int32_t* starts, const int32_t* page_table,
+                                           int table_stride, float softmax_scale, int window,
+                                           int sinks, void* o_bf16, float* lse, void* ws,
+                                           size_t ws_bytes, int* dev_status, void* stream) {
+  AttendArgs g{};
+  const flamia_status st =
+      attend_args(g, cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
+                  table_stride, softmax_scale, window, sinks, o_bf16, lse, ws, dev_status);
+  if (st != FLAMIA_OK || T == 0) return st;
+  const int R = rows_per_item(mean_rows(T, ndocs, g.G));
+  const Workspace w = layout(R, cache->d);
+  if (ws_bytes < w.total) return FLAMIA_ERR_WORKSPACE;
+  g.joins = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + w.joins);
+  g.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.stats);
+  g.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.partial);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (R == kManyRows) return attend_rows(cache, g, s);
-  if (d == 128)
-    return R == 8 ? launch<128, 8>(cache, g, s)
-                  : R == 16 ? launch<128, 16>(cache, g, s) : launch<128, 32>(cache, g, s);
-  return R == 8 ? launch<64, 8>(cache, g, s)
-                : R == 16 ? launch<64, 16>(cache, g, s) : launch<64, 32>(cache, g, s);
+  return R == kManyRows ? attend_rows(cache, g, kAll, s) : attend_few(cache, g, R, kAll, s);
 }

@@ -215,7 +215,7 @@ __device__ __forceinline__ uint32_t tile_at(int row, int j) {
 // ------------------------------------------------------------------ work
 
 // The segments of a CTA's run, in order.
-template <int R>
+template <int R, int KEYS>
 struct Walk {
   SeqWork w;
   long long u0, u, u1, total;
@@ -253,7 +253,7 @@ struct Walk {
       sg.pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
                                           static_cast<long long>(sg.row0) + R - 1) /
                                       g.G);
-      sg.hi = max(sg.pl + 1, 0);
+      sg.hi = KEYS == kPrefix ? g.shared * 128 : max(sg.pl + 1, 0);
       sg.wlo = g.window > 0 ? max(sg.pf - g.window + 1, 0) : 0;
       sg.wt = sg.wlo >> 7;
       sg.ns = min((g.sinks + 127) >> 7, sg.wt);
@@ -265,7 +265,7 @@ struct Walk {
         sg.slot = 2 * blockIdx.x;
       else if (i1 < w.tiles)
         sg.slot = 2 * blockIdx.x + 1;
-      if (first && i0 > 0) {
+      if (KEYS == kAll && first && i0 > 0) {
         // the second CTA of an item has it joined: parts are the CTA before this
         // one (slot 1) and slots 0 from here on
         const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
@@ -275,7 +275,7 @@ struct Walk {
           join1 = make_int4(sg.row0, 0, 0, 0);
         }
       }
-      if (reports && hk == 0 && rt == 0 && i0 == 0) {
+      if (KEYS == kAll && reports && hk == 0 && rt == 0 && i0 == 0) {
         const int raw = g.starts != nullptr ? g.starts[b] : 0;
         if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
       }
@@ -287,7 +287,7 @@ struct Walk {
         if (++hk == g.H_kv) {
           hk = 0;
           do {
-            w = seq_work<R>(g, ++b);  // there is one: u < u1
+            w = seq_work<R, KEYS>(g, ++b);  // there is one: u < u1
           } while (w.row_tiles == 0 && b + 1 < g.ndocs);
         }
       }
@@ -374,7 +374,7 @@ __device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev
   past.add(sum, top);
 }
 
-template <int DIM>
+template <int DIM, int KEYS>
 __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(const AttendArgs g,
                                                                            const uint8_t* k_codes,
                                                                            const uint8_t* v_codes) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
                 static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   tc_fence_before();
-  make_plan<R, C::kThreads>(g, sm);
+  make_plan<R, KEYS, C::kThreads>(g, sm);
   tc_fence_after();
   start_next();
   const uint32_t tmem = sm.tmem_base;
@@ -847,6 +847,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (live) {
           if (slot >= 0)
             g.stats[static_cast<size_t>(slot) * R + r] = lg;
+          else if (KEYS != kAll)
+            g.row_stats[out] = lg;
           else if (g.lse != nullptr)
             g.lse[static_cast<size_t>(hq) * g.T + sg.s + tok] = lg * kLn2;
         }
@@ -867,6 +869,11 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 p[j * R] = make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+            } else if (KEYS != kAll) {
+              uint4* p = reinterpret_cast<uint4*>(g.rows + out * DIM + c);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                p[j] = make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
             } else {
               uint4* p = reinterpret_cast<uint4*>(g.o + out * DIM + c);
 #pragma unroll
@@ -893,7 +900,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
     set_registers<false, 64>();  // (all four warps at once)
     if (warp == 13) {
       // ------------------------------------------------------------ walker
-      Walk<R> walk(sm);
+      Walk<R, KEYS> walk(sm);
       bool ok = true;
       for (int ns = 0; ok; ++ns) {
         const RowSegment sg = walk.next(g, lane == 0);
@@ -909,7 +916,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (sg.s < 0) break;
       }
       // what the second kernel has to join for this CTA's first item
-      if (lane == 0 && !g.whole) {
+      if (KEYS == kAll && lane == 0 && !g.whole) {
         g.joins[2 * blockIdx.x] = walk.join0;
         g.joins[2 * blockIdx.x + 1] = walk.join1;
       }
@@ -1003,22 +1010,27 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
   }
 }
 
-template <int DIM>
+template <int DIM, int KEYS>
 bool launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM>)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  const int grid = min(kRowsCtas, num_sms());
+  const int grid = rows_grid();
   static std::atomic<unsigned long long> raised{0};
-  return launch_large(attend_rows_kernel<DIM>, raised, dim3(grid), Cfg<DIM>::kThreads, smem, s, g,
-                      static_cast<const uint8_t*>(c->k_codes),
+  return launch_large(attend_rows_kernel<DIM, KEYS>, raised, dim3(grid), Cfg<DIM>::kThreads, smem,
+                      s, g, static_cast<const uint8_t*>(c->k_codes),
                       static_cast<const uint8_t*>(c->v_codes)) &&
-         (g.whole || launch_join<DIM, 256>(grid, s, g));
+         (KEYS != kAll || g.whole || launch_join<DIM, 256>(grid, s, g));
 }
 
 }  // namespace
 
-flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
-  return (c->d == 128 ? launch<128>(c, g, s) : launch<64>(c, g, s)) ? FLAMIA_OK : FLAMIA_ERR_CUDA;
+int rows_grid() { return min(kRowsCtas, num_sms()); }
+
+flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, Keys keys, cudaStream_t s) {
+  const bool ok = keys == kPrefix
+                      ? (c->d == 128 ? launch<128, kPrefix>(c, g, s) : launch<64, kPrefix>(c, g, s))
+                      : (c->d == 128 ? launch<128, kAll>(c, g, s) : launch<64, kAll>(c, g, s));
+  return ok ? FLAMIA_OK : FLAMIA_ERR_CUDA;
 }
 
 }  // namespace flamia

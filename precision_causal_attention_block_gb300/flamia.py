@@ -96,6 +96,9 @@ SIGNATURES = {
     "flamia_attn_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "flamia_attn_cache": (_i, [_CP, _vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i, _f, _i, _i, _vp,
                                _vp, _vp, _sz, _vp, _vp]),
+    "flamia_attn_cache_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "flamia_attn_cache_prefix": (_i, [_CP, _vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i, _i, _f, _vp,
+                                      _vp, _vp, _sz, _vp, _vp]),
     "flamia_status_str": (ctypes.c_char_p, [_i]),
     "flamia_debug_mma_tile": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "flamia_debug_bounded_waits": (_i, [_vp, _vp, _vp]),
@@ -508,9 +511,11 @@ class KVCache:
         flamia_pages_copy(self if source is None else source, self, src, dst, dev_status)
 
     def attend(self, q, cu_seqlens, starts, page_table, softmax_scale: float, window: int = 0,
-               sinks: int = 0, o=None, lse=None, ws=None, dev_status=None):
+               sinks: int = 0, o=None, lse=None, ws=None, dev_status=None, prefix: int = 0):
         """(o, lse) of queries q [T, H, d] at positions starts[b] .. over the
-        cache.  ws None: the workspace of the current stream and thread (42 MB, made
+        cache.  prefix: the sequences begin with the same so many tokens (those of which
+        all new tokens stand at prefix - 1 or behind), which are read once for all of
+        them; with a window each reads its own.  ws None: the workspace of the current stream and thread (42 MB, made
         by their first call, shared by all caches), or, while a graph is captured, one
         that belongs to the graph: calls that overlap never share one."""
         T, H = q.shape[0], q.shape[1]
@@ -518,8 +523,14 @@ class KVCache:
             o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-        flamia_attn_cache(self, q, cu_seqlens, starts, page_table, softmax_scale, window, sinks, o,
-                          lse, ws, dev_status)
+        if prefix and not window and not sinks:
+            flamia_attn_cache_prefix(self, q, cu_seqlens, starts, page_table, prefix, softmax_scale,
+                                     o, lse, ws, dev_status)
+        else:
+            if prefix < 0:
+                raise RuntimeError("prefix: expected 0 or more tokens")
+            flamia_attn_cache(self, q, cu_seqlens, starts, page_table, softmax_scale, window, sinks,
+                              o, lse, ws, dev_status)
         return o, lse
 
 
@@ -580,14 +591,12 @@ def flamia_attn_cache_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: 
     return int(load().flamia_attn_cache_workspace_bytes(T, ndocs, H, H_kv, d))
 
 
-def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax_scale, window,
-                      sinks, o, lse, ws=None, dev_status=None):
-    dev, stream = _current()
+def _attend_rows(cache, q, o, lse, dev):
+    """(pointer, stride, T, H) of the queries, pointer of lse."""
     if q.dim() != 3:
         raise RuntimeError("q: flamia needs BF16 rows [T, heads, d]")
     T, H, d = q.shape
     qp, qs = _rows(q, "q", T, H, cache.d, dev)
-    n = cu_seqlens.numel() - 1
     if o.dtype is not _BF16 or o.shape != q.shape or not o.is_contiguous():
         raise RuntimeError("o: expected contiguous BF16 of q's shape")
     lp = None
@@ -599,6 +608,22 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
             _elsewhere("lse")
     if cache.device_index != dev or o.get_device() != dev:
         _elsewhere("cache and o")
+    return qp, qs, T, H, lp
+
+
+def _given_workspace(ws, dev):
+    if not ws.is_contiguous():
+        raise RuntimeError("ws: expected a contiguous tensor")
+    if ws.get_device() != dev:
+        _elsewhere("ws")
+    return ws.data_ptr(), ws.nbytes
+
+
+def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax_scale, window,
+                      sinks, o, lse, ws=None, dev_status=None):
+    dev, stream = _current()
+    qp, qs, T, H, lp = _attend_rows(cache, q, o, lse, dev)
+    n = cu_seqlens.numel() - 1
     if ws is None:
         if torch._C._cuda_isCurrentStreamCapturing():
             # from the graph's pool: replays of two graphs may overlap
@@ -608,11 +633,7 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
         else:
             _, wp, wn = _eager_workspace(dev, stream)
     else:
-        wp, wn = ws.data_ptr(), ws.nbytes
-        if not ws.is_contiguous():
-            raise RuntimeError("ws: expected a contiguous tensor")
-        if ws.get_device() != dev:
-            _elsewhere("ws")
+        wp, wn = _given_workspace(ws, dev)
     if not (0 <= window <= _INT_MAX and 0 <= sinks <= _INT_MAX):
         # (ctypes would keep the low 32 bits; positions end before, negative ones are refused)
         window, sinks = (max(-1, min(x, _INT_MAX)) for x in (window, sinks))
@@ -623,6 +644,36 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
         _ints(dev_status, "dev_status", 0, dev), stream)
     if st:
         _check(st, "flamia_attn_cache")
+
+
+def flamia_attn_cache_prefix_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: int,
+                                             prefix: int) -> int:
+    return int(load().flamia_attn_cache_prefix_workspace_bytes(T, ndocs, H, H_kv, d,
+                                                               max(-1, min(prefix, _INT_MAX))))
+
+
+def flamia_attn_cache_prefix(cache: KVCache, q, cu_seqlens, starts, page_table, prefix,
+                             softmax_scale, o, lse, ws=None, dev_status=None):
+    dev, stream = _current()
+    qp, qs, T, H, lp = _attend_rows(cache, q, o, lse, dev)
+    n = cu_seqlens.numel() - 1
+    prefix = max(-1, min(prefix, _INT_MAX))  # (as windows: positions end before)
+    lib = _LIB or load()
+    if ws is None:
+        # (of the call: the allocator hands it on in the stream's order, or keeps it for
+        # the graph that is being captured; a byte for arguments that will be refused)
+        ws = torch.empty(max(1, lib.flamia_attn_cache_prefix_workspace_bytes(
+            T, n, H, cache.H_kv, cache.d, prefix)), dtype=torch.uint8, device=q.device)
+        wp, wn = ws.data_ptr(), ws.nbytes
+    else:
+        wp, wn = _given_workspace(ws, dev)
+    st = lib.flamia_attn_cache_prefix(
+        cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
+        _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
+        prefix, float(softmax_scale), o.data_ptr(), lp, wp, wn,
+        _ints(dev_status, "dev_status", 0, dev), stream)
+    if st:
+        _check(st, "flamia_attn_cache_prefix")
 
 
 def flamia_pages_copy(source: KVCache, target: KVCache, src, dst, dev_status=None):
@@ -845,15 +896,18 @@ class TrainingCall:
         # rotary positions (document-local): rotated Q and K before the
         # quantiser, dQ and dK turned back in place after the backward
         self.rope = rope
+        self.positions = None
         if rope is not None:
             self.xq = torch.empty((T, H, d), dtype=torch.bfloat16, device=device)
             self.xk = torch.empty((T, self.H_kv, d), dtype=torch.bfloat16, device=device)
 
-    def forward(self, xq, xk, xv):
+    def forward(self, xq, xk, xv, positions=None):
+        """positions: for a rope with axes (kept for the backward)."""
         main = torch.cuda.current_stream()
         if self.rope is not None:
+            self.positions = positions
             xq, xk = self.rope(xq, xk, self.cu, q_out=self.xq, k_out=self.xk,
-                               dev_status=self.status)
+                               dev_status=self.status, positions=positions)
         # cu_seqlens is ready and the previous call has finished with the list
         self.side.wait_stream(main)
         with torch.cuda.stream(self.side):
@@ -875,11 +929,11 @@ class TrainingCall:
                             self.dv, self.ws, self.bwd_flags, dev_status=self.status)
         if self.rope is not None:
             self.rope(self.dq, self.dk, self.cu, q_out=self.dq, k_out=self.dk, inverse=True,
-                      dev_status=self.status)
+                      dev_status=self.status, positions=self.positions)
         return self.dq, self.dk, self.dv
 
-    def __call__(self, xq, xk, xv, xdo):
-        self.forward(xq, xk, xv)
+    def __call__(self, xq, xk, xv, xdo, positions=None):
+        self.forward(xq, xk, xv, positions)
         return self.backward(xdo)
 
     def ds_zero_counts(self):
@@ -901,34 +955,52 @@ class DecodeCall:
     tokens of nseq sequences (cu_seqlens may end before T: the rows behind are
     padding, and sequences may be empty).  The calls read cu_seqlens, starts and page_table
     on the device, so a captured step can be replayed while the caller updates
-    them in place."""
+    them in place.
+
+    pool: the step begins with pages for its tokens (PagePool.reserve) and takes the
+    pool's page table.  prefix: the sequences begin with the same so many tokens, read
+    once for all of them (KVCache.attend)."""
 
     def __init__(self, cache: KVCache, T: int, nseq: int, H: int, softmax_scale: float,
-                 rope: Rotary = None, window: int = 0, sinks: int = 0):
+                 rope: Rotary = None, window: int = 0, sinks: int = 0, pool: PagePool = None,
+                 prefix: int = 0):
+        if pool is not None and (pool.cache is not cache or pool.nseq != nseq):
+            raise RuntimeError("pool: expected one over this cache with a row a sequence")
         dev = cache.k_codes.device
         self.cache, self.T, self.H, self.scale = cache, T, H, float(softmax_scale)
         self.rope, self.window, self.sinks = rope, int(window), int(sinks)
+        self.pool, self.prefix = pool, int(prefix)
         self.o = torch.empty((T, H, cache.d), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((H, T), dtype=torch.float32, device=dev)
-        self.ws = torch.empty(flamia_attn_cache_workspace_bytes(T, nseq, H, cache.H_kv, cache.d),
-                              dtype=torch.uint8, device=dev)
+        size = (flamia_attn_cache_workspace_bytes(T, nseq, H, cache.H_kv, cache.d)
+                if self.window or not self.prefix else
+                flamia_attn_cache_prefix_workspace_bytes(T, nseq, H, cache.H_kv, cache.d, self.prefix))
+        self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         if rope is not None:
             self.q = torch.empty((T, H, cache.d), dtype=torch.bfloat16, device=dev)
             self.k = torch.empty((T, cache.H_kv, cache.d), dtype=torch.bfloat16, device=dev)
 
-    def __call__(self, q, k, v, cu_seqlens, starts, page_table):
+    def __call__(self, q, k, v, cu_seqlens, starts, page_table=None, positions=None):
         """o [T, H, d] of the new tokens at positions starts[b] .. of each
-        sequence; rows behind the last sequence are left as they were."""
+        sequence; rows behind the last sequence are left as they were.  page_table:
+        without a pool; positions: for a rope with axes."""
+        if (page_table is None) != (self.pool is not None):
+            raise RuntimeError("page_table: needed without a pool, and only then")
+        if self.pool is not None:
+            self.pool.reserve(cu_seqlens, starts, self.T)
+            page_table = self.pool.page_table
         if self.rope is not None:
-            q, k = self.rope(q, k, cu_seqlens, starts, q_out=self.q, k_out=self.k,
-                             dev_status=self.status)
+            q, k = self.rope(q, k, cu_seqlens, starts if self.rope.axes is None else None,
+                             q_out=self.q, k_out=self.k, dev_status=self.status,
+                             positions=positions)
         self.cache.write(k, v, cu_seqlens, starts, page_table, dev_status=self.status)
         self.cache.attend(q, cu_seqlens, starts, page_table, self.scale, self.window, self.sinks,
-                          o=self.o, lse=self.lse, ws=self.ws, dev_status=self.status)
+                          o=self.o, lse=self.lse, ws=self.ws, dev_status=self.status,
+                          prefix=self.prefix)
         return self.o
 
     def check_status(self):
-        st = int(self.status.item())
+        st = int(self.status.item()) | (0 if self.pool is None else int(self.pool.status.item()))
         if st != 0:
             raise RuntimeError(f"flamia device status 0x{st:x}")
