@@ -31,15 +31,25 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
 constexpr int kLow = 60;        // keys whose eV lies further below E0 are summed apart
 
-// What a kernel's items are.  A call whose sequences share a prefix (attn_prefix.cu)
-// takes one kernel over the prefix's whole tiles, with the tokens of all sequences as the
-// query rows of each K / V head, and one over what comes behind them; both leave float32
-// results, and a last kernel joins those.
+// What a kernel's items are.  A call whose sequences share a prefix (attn_prefix.cu) has
+// items over the prefix's whole tiles, with the tokens of all sequences as the query rows
+// of each K / V head, and items of every sequence over what comes behind them.  They
+// leave float32 results, and a last kernel joins those.
 enum Keys : int {
   kAll = 0,     // items of every sequence: all its keys
   kPrefix = 1,  // items of the whole call: the first `shared` tiles
-  kRest = 2     // items of every sequence: the tiles behind those (all, if it does not share)
+  kRest = 2,    // items of every sequence: the tiles behind those (all, if it does not share)
+  kBoth = 3     // kPrefix's, then kRest's
 };
+
+// Where an item's result lies, kept for each of its rows (KEYS != kAll).  One part: in
+// `rows` and `row_stats`; more: part 0 in slot 1 of a CTA, the others in slots 0 from the
+// next one on.
+struct RowParts {
+  int at;  // cta | row in the item << 16
+  int n;   // | kShares: the row's sequence shares the prefix
+};
+constexpr int kShares = 1 << 30;
 
 struct AttendArgs {
   const uint8_t *k_scales, *v_scales;
@@ -56,10 +66,10 @@ struct AttendArgs {
   int cap;           // positions that the page table has room for
   int whole;         // items stay whole
   float scale_log2;
-  // with a shared prefix
-  float* row_stats;  // [T][H]: stats of items that were not cut
-  float* rows;       // [T][H][d]: their o
-  long long* first;  // [ndocs + 1]: units before each sequence (kRest)
+  // with a shared prefix; [0] of items over it, [1] of the others
+  RowParts* where[2];   // [T][H]
+  float* row_stats[2];  // [T][H]: stats of items that were not cut
+  float* rows[2];       // [T][H][d]: their o
   int shared;        // tiles of the prefix
   int prefix;        // its tokens
 };
@@ -147,21 +157,32 @@ __device__ __forceinline__ bool shares(const AttendArgs& g, int start) {
   return start >= g.prefix - 1;
 }
 
+// Entry v of the work list: the prefix, or a sequence.
+template <int KEYS>
+__device__ __forceinline__ bool of_prefix(int v) {
+  return KEYS == kPrefix || (KEYS == kBoth && v == 0);
+}
+template <int KEYS>
+__device__ __forceinline__ int seq_of(int v) {
+  return KEYS == kBoth ? v - 1 : v;
+}
+// `sharer`: the first sequence that shares the prefix, ndocs: none.
 template <int R, int KEYS>
-__device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
+__device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int v, int sharer) {
   SeqWork w;
-  if constexpr (KEYS == kPrefix) {
+  if (of_prefix<KEYS>(v)) {
     // (positions behind the prefix: every row sees every key)
     w.s = 0;
     w.n = min(max(g.cu[g.ndocs], 0), g.T);
     w.start = g.shared * 128;
-    w.row_tiles = b < g.ndocs
+    w.row_tiles = sharer < g.ndocs
                       ? static_cast<int>((static_cast<long long>(w.n) * g.G + R - 1) / R)
-                      : 0;  // (nobody shares it)
+                      : 0;
     w.tiles = g.shared;
     w.units = w.tiles + kItemCost<R>;
     return w;
   }
+  const int b = seq_of<KEYS>(v);
   const DocRange r = doc_range(g.cu, b, g.T);
   w.s = r.s;
   w.n = r.e - r.s;
@@ -172,7 +193,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int b) {
   // (no further than the page table: a wild first position costs no endless walk)
   const int end = min(max(w.start + w.n, 0), g.cap);
   int tiles = (end + 127) >> 7;
-  if (KEYS == kRest && shares(g, w.start)) tiles -= g.shared;
+  if (KEYS != kAll && shares(g, w.start)) tiles -= g.shared;
   if (KEYS == kAll && g.window > 0)
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
                            ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);
@@ -188,7 +209,10 @@ struct Segment {
   int i0, i1;       // its key tiles: list positions i0 .. i1 - 1
   int ns, wt;       // list position i is key tile i (i < ns) or i - ns + wt
   int slot;         // partial result slot, or -1: the whole item
+  int parts;        // KEYS != kAll: RowParts::n, if it holds the item's first tile; kOver:
+                    // of the prefix
 };
+constexpr int kOver = 1 << 29;
 
 __device__ __forceinline__ int tile_of(const Segment& g, int i) {
   return i < g.ns ? i : i - g.ns + g.wt;
@@ -225,34 +249,27 @@ __device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long 
 template <int R, int KEYS, int kThreads, class Sm>
 __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int each = (g.ndocs + kThreads - 1) / kThreads;
-  const int b0 = min(tid * each, g.ndocs), b1 = min(b0 + each, g.ndocs);
-  if constexpr (KEYS == kPrefix) {
-    // the first sequence that shares: its pages are read
-    if (tid == 0) sm.plan_b = g.ndocs;
+  int sharer = 0;
+  if constexpr (KEYS == kPrefix || KEYS == kBoth) {
+    const int each = (g.ndocs + kThreads - 1) / kThreads;
+    const int b0 = min(tid * each, g.ndocs), b1 = min(b0 + each, g.ndocs);
+    if (tid == 0) sm.sharer = g.ndocs;
     __syncthreads();
     for (int b = b0; b < b1; ++b) {
       const DocRange r = doc_range(g.cu, b, g.T);
       if (r.e > r.s && g.starts != nullptr && shares(g, g.starts[b])) {
-        atomicMin(&sm.plan_b, b);
+        atomicMin(&sm.sharer, b);
         break;
       }
     }
     __syncthreads();
-    if (tid == 0) {
-      const SeqWork w = seq_work<R, KEYS>(g, sm.plan_b);
-      const long long total = w.total(g.H_kv), ctas = active_ctas<R>(g, total), c = blockIdx.x;
-      sm.plan_u0 = c < ctas ? mul_div(total, c, ctas) : total;
-      sm.plan_u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;
-      sm.plan_total = total;
-      sm.plan_seq = w;
-      sm.plan_off = sm.plan_u0;
-    }
-    __syncthreads();
-    return;
+    sharer = sm.sharer;
   }
+  const int n = KEYS == kPrefix ? 1 : KEYS == kBoth ? g.ndocs + 1 : g.ndocs;
+  const int each = (n + kThreads - 1) / kThreads;
+  const int b0 = min(tid * each, n), b1 = min(b0 + each, n);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_work<R, KEYS>(g, b).total(g.H_kv);
+  for (int b = b0; b < b1; ++b) sum += seq_work<R, KEYS>(g, b, sharer).total(g.H_kv);
   long long inc = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -260,21 +277,13 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     if (lane >= off) inc += y;
   }
   if (lane == 31) sm.scan[warp] = inc;
-  if (tid == 0) sm.plan_b = g.ndocs;
+  if (tid == 0) sm.plan_b = n;
   __syncthreads();
   long long before = inc - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
-  }
-  if (KEYS == kRest && blockIdx.x == 0) {  // for the kernel that joins
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      g.first[b] = at;
-      at += seq_work<R, KEYS>(g, b).total(g.H_kv);
-    }
-    if (tid == 0) g.first[g.ndocs] = total;
   }
   const long long ctas = active_ctas<R>(g, total);
   const long long c = blockIdx.x;
@@ -288,16 +297,24 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   if (u0 < u1 && before <= u0 && u0 < before + sum) {
     long long off = u0 - before;
     int b = b0;
-    SeqWork w = seq_work<R, KEYS>(g, b);
+    SeqWork w = seq_work<R, KEYS>(g, b, sharer);
     while (b < b1 - 1 && off >= w.total(g.H_kv)) {
       off -= w.total(g.H_kv);
-      w = seq_work<R, KEYS>(g, ++b);
+      w = seq_work<R, KEYS>(g, ++b, sharer);
     }
     sm.plan_b = b;
     sm.plan_seq = w;
     sm.plan_off = off;
   }
   __syncthreads();
+}
+
+// RowParts::n of the item that begins at unit ui, for the CTA with its first tile.
+template <int R>
+__device__ __forceinline__ int parts_from_here(const AttendArgs& g, long long ui, int units,
+                                               long long total) {
+  const long long ctas = active_ctas<R>(g, total);
+  return static_cast<int>(div_up((ui + units) * ctas, total) - 1 - blockIdx.x) + 1;
 }
 
 // Joins the parts of an item that several CTAs shared (part 0 in slot 1 of the
@@ -399,13 +416,11 @@ flamia_status attend_args(AttendArgs& g, const flamia_kvcache* cache, const void
                           const int32_t* starts, const int32_t* page_table, int table_stride,
                           float softmax_scale, int window, int sinks, void* o_bf16, float* lse,
                           const void* ws, int* dev_status);
-// The kernel for many query rows (256 an item), and its CTAs.
+// The kernel for many query rows (256 an item): kAll or kPrefix.
 flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, Keys keys, cudaStream_t s);
-int rows_grid();
-// Those for 8, 16 or 32 rows an item.
+// Those for 8, 16 or 32 rows an item: kAll, kRest or kBoth.
 flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
                          cudaStream_t s);
-int few_grid(int R);
 // Query rows side by side in one item: `rows` of a K / V head on average.
 constexpr int kManyRows = 256;
 int rows_per_item(long long rows);

@@ -218,7 +218,7 @@ struct Smem {
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Segment seg[kSegSlots];
   int2 tile[C::kSS];            // first key; pieces that were loaded, kWhole
-  int plan_b;
+  int plan_b, sharer;
   SeqWork plan_seq;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
@@ -377,9 +377,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sg.s = -1;
       } else {
         const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
-        const int cost = g.whole ? 0 : kItemCost<R>;
+        const bool over = of_prefix<KEYS>(b), cut = !g.whole;
+        const int cost = cut ? kItemCost<R> : 0;
         const int i0 = max(o - cost, 0);
-        const int i1 = g.whole ? w.tiles : max(o + take - cost, 0);
+        const int i1 = cut ? max(o + take - cost, 0) : w.tiles;
         sg.s = w.s;
         sg.n = w.n;
         sg.start = w.start;
@@ -389,9 +390,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
                                                       static_cast<long long>(sg.row0) + R - 1) /
                                                   g.G);
-        hi = KEYS == kPrefix ? g.shared * 128 : max(pl + 1, 0);
+        hi = over ? g.shared * 128 : max(pl + 1, 0);
         wlo = g.window > 0 ? max(pf - g.window + 1, 0) : 0;
-        sg.wt = KEYS == kRest && shares(g, w.start) ? g.shared : wlo >> 7;
+        const bool sharing = KEYS != kAll && !over && shares(g, w.start);
+        sg.wt = sharing ? g.shared : wlo >> 7;
         sg.ns = KEYS == kAll ? min((g.sinks + 127) >> 7, sg.wt) : 0;
         const int list = sg.ns + max(((hi + 127) >> 7) - sg.wt, 0);
         sg.i0 = min(i0, list);
@@ -401,6 +403,9 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           sg.slot = 2 * blockIdx.x;
         else if (i1 < w.tiles)
           sg.slot = 2 * blockIdx.x + 1;
+        if (KEYS != kAll && i0 == 0 && i1 > 0)
+          sg.parts = (cut ? parts_from_here<R>(g, u - o, w.units, total) : 1) |
+                     (over ? kOver : 0) | (sharing ? kShares : 0);
         if (KEYS == kAll && first && i0 > 0) {
           // the second CTA of an item has it joined: parts are the CTA before
           // this one (slot 1) and slots 0 from here on
@@ -411,8 +416,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             join1 = make_int4(sg.row0, 0, 0, 0);
           }
         }
-        if (KEYS != kPrefix && lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
-          const int raw = g.starts != nullptr ? g.starts[b] : 0;
+        if (!over && lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
+          const int raw = g.starts != nullptr ? g.starts[seq_of<KEYS>(b)] : 0;
           if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
         }
         first = false;
@@ -432,7 +437,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       ++nseg;
       if (sg.s < 0) break;
       // its key tiles; the page-table entries of a tile are read one tile ahead
-      const int32_t* row = g.table + static_cast<long long>(b) * g.table_stride;
+      const int seq = of_prefix<KEYS>(b) ? sm.sharer : seq_of<KEYS>(b);
+      const int32_t* row = g.table + static_cast<long long>(seq) * g.table_stride;
       auto entry = [&](int i, bool& need, int& in_page) {
         const int kp = tile_of(sg, i) * 128 + lane * piece;
         need = lane < pieces && kp < hi &&
@@ -451,8 +457,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (++hk == g.H_kv) {
           hk = 0;
           do {
-            w = seq_work<R, KEYS>(g, ++b);  // there is one: u < u1
-          } while (w.row_tiles == 0 && b + 1 < g.ndocs);
+            w = seq_work<R, KEYS>(g, ++b, 0);  // there is one: u < u1
+          } while (w.row_tiles == 0 && seq_of<KEYS>(b) + 1 < g.ndocs);
         }
       }
       for (int i = sg.i0; i < sg.i1; ++i, ++tc) {
@@ -992,6 +998,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         tc_fence_after();
       }
       const int slot = sg.slot;
+      const int rest = sg.parts & kOver ? 0 : 1;  // (of an item that was not cut)
       sum_keys();
       sync();
       if (tid < rows) {
@@ -1006,9 +1013,12 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (slot >= 0)
           g.stats[static_cast<size_t>(slot) * R + tid] = lg;
         else if (KEYS != kAll)
-          g.row_stats[orow] = lg;
+          g.row_stats[rest][orow] = lg;
         else if (g.lse != nullptr)
           g.lse[static_cast<size_t>(orow % g.H) * g.T + orow / g.H] = lg * kLn2;
+        if (KEYS != kAll && sg.parts != 0)
+          g.where[rest][orow] =
+              RowParts{static_cast<int>(blockIdx.x) | (tid << 16), sg.parts & ~kOver};
       }
       sync();
       const bool active = DIM == 128 || key_in < DIM;
@@ -1034,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
             if (slot >= 0)
               g.partial[(static_cast<size_t>(slot) * R + r) * DIM + key_in] = v;
             else if (KEYS != kAll)
-              g.rows[static_cast<size_t>(sm.orow[r]) * DIM + key_in] = v;
+              g.rows[rest][static_cast<size_t>(sm.orow[r]) * DIM + key_in] = v;
             else
               g.o[static_cast<size_t>(sm.orow[r]) * DIM + key_in] = __float2bfloat16(v);
           }
@@ -1089,11 +1099,6 @@ bool make_page_map(CUtensorMap* map, const uint8_t* codes, const flamia_kvcache*
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DIM, int R>
-constexpr int kResident = Cfg<DIM, R>::kCtas;
-static_assert(kResident<128, 8> == kResident<64, 8> && kResident<128, 16> == kResident<64, 16> &&
-              kResident<128, 32> == kResident<64, 32>, "few_grid");
-
 template <int DIM, int R, int KEYS>
 flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
   CUtensorMap mk, mv;
@@ -1101,7 +1106,7 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
     return FLAMIA_ERR_CUDA;
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM, R>)) + 1024;
   static_assert(Cfg<DIM, R>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
-  const int grid = few_grid(R);
+  const int grid = min(kMaxCtas, num_sms() * Cfg<DIM, R>::kCtas);
   static std::atomic<unsigned long long> raised{0};
   return launch_large(attend_kernel<DIM, R, KEYS>, raised, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk,
                       mv, g) &&
@@ -1121,16 +1126,11 @@ flamia_status launch_few(const flamia_kvcache* c, const AttendArgs& g, int R, cu
 
 }  // namespace
 
-int few_grid(int R) {
-  const int ctas = R == 8 ? kResident<128, 8> : R == 16 ? kResident<128, 16> : kResident<128, 32>;
-  return min(kMaxCtas, num_sms() * ctas);
-}
-
 flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
                          cudaStream_t s) {
   return keys == kAll ? launch_few<kAll>(c, g, R, s)
-                      : keys == kPrefix ? launch_few<kPrefix>(c, g, R, s)
-                                        : launch_few<kRest>(c, g, R, s);
+                      : keys == kBoth ? launch_few<kBoth>(c, g, R, s)
+                                      : launch_few<kRest>(c, g, R, s);
 }
 
 // Query rows side by side in one item: those of a K / V head's mean number of

@@ -88,7 +88,7 @@ struct Smem {
   uint64_t q_full[2], drained;
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   RowSegment seg[kSegSlots];
-  int plan_b;
+  int plan_b, sharer;
   SeqWork plan_seq;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
@@ -225,7 +225,8 @@ struct Walk {
 
   template <class Sm>
   __device__ __forceinline__ explicit Walk(const Sm& sm)
-      : w{}, u0(sm.plan_u0), u(sm.plan_u0), u1(sm.plan_u1), total(sm.plan_total), b(sm.plan_b) {
+      : w{}, u0(sm.plan_u0), u(sm.plan_u0), u1(sm.plan_u1), total(sm.plan_total),
+        b(KEYS == kPrefix ? sm.sharer : sm.plan_b) {
     if (u < u1) {
       w = sm.plan_seq;
       const long long item = mul_div(sm.plan_off, 1, w.units);
@@ -265,6 +266,8 @@ struct Walk {
         sg.slot = 2 * blockIdx.x;
       else if (i1 < w.tiles)
         sg.slot = 2 * blockIdx.x + 1;
+      if (KEYS != kAll && i0 == 0 && i1 > 0)
+        sg.parts = parts_from_here<R>(g, u - o, w.units, total) | kOver;
       if (KEYS == kAll && first && i0 > 0) {
         // the second CTA of an item has it joined: parts are the CTA before this
         // one (slot 1) and slots 0 from here on
@@ -287,7 +290,7 @@ struct Walk {
         if (++hk == g.H_kv) {
           hk = 0;
           do {
-            w = seq_work<R, KEYS>(g, ++b);  // there is one: u < u1
+            w = seq_work<R, KEYS>(g, ++b, 0);  // there is one: u < u1
           } while (w.row_tiles == 0 && b + 1 < g.ndocs);
         }
       }
@@ -848,9 +851,12 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
           if (slot >= 0)
             g.stats[static_cast<size_t>(slot) * R + r] = lg;
           else if (KEYS != kAll)
-            g.row_stats[out] = lg;
+            g.row_stats[0][out] = lg;
           else if (g.lse != nullptr)
             g.lse[static_cast<size_t>(hq) * g.T + sg.s + tok] = lg * kLn2;
+          if (KEYS != kAll && sg.parts != 0)
+            g.where[0][out] =
+                RowParts{static_cast<int>(blockIdx.x) | (r << 16), sg.parts & ~kOver};
         }
 #pragma unroll
         for (int c = 0; c < DIM; c += 32) {
@@ -870,7 +876,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
               for (int j = 0; j < 8; ++j)
                 p[j * R] = make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
             } else if (KEYS != kAll) {
-              uint4* p = reinterpret_cast<uint4*>(g.rows + out * DIM + c);
+              uint4* p = reinterpret_cast<uint4*>(g.rows[0] + out * DIM + c);
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 p[j] = make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
@@ -1014,7 +1020,7 @@ template <int DIM, int KEYS>
 bool launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM>)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  const int grid = rows_grid();
+  const int grid = min(kRowsCtas, num_sms());
   static std::atomic<unsigned long long> raised{0};
   return launch_large(attend_rows_kernel<DIM, KEYS>, raised, dim3(grid), Cfg<DIM>::kThreads, smem,
                       s, g, static_cast<const uint8_t*>(c->k_codes),
@@ -1023,8 +1029,6 @@ bool launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
 }
 
 }  // namespace
-
-int rows_grid() { return min(kRowsCtas, num_sms()); }
 
 flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, Keys keys, cudaStream_t s) {
   const bool ok = keys == kPrefix

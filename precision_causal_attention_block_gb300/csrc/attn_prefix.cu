@@ -6,146 +6,189 @@
 // out by itself as a mean of values o_i with log2 of its sum of weights, lg_i:
 //   lg = log2 sum 2^lg_i,   o = sum 2^(lg_i - lg) o_i.
 //
-// Three kernels: the attention kernels of attn_cache.cu or attn_cache_rows.cu over the
-// prefix, with the tokens of all sequences as the query rows of each K / V head (no masks:
-// all of them see all of it), those of attn_cache.cu over what comes behind it, and one
-// that joins what they leave: float32 rows of items that were not cut, and the
-// parts of those that were (equal runs of key tiles for all CTAs, as there; nothing waits
-// for another CTA and no atomics, so results do not depend on timing).
+// Up to 96 query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
+// kernels over items of both kinds.  More: the kernel of attn_cache_rows.cu over the prefix
+// (no masks: all rows see all of it), then attn_cache.cu's over what comes behind it.
+// In both cases a last kernel joins what they leave: float32 rows of items that
+// were not cut and the parts of those that were (equal runs of key tiles for all CTAs, as
+// there; nothing waits for another CTA and there are no atomics on results, so these do not
+// depend on timing).  Each row's record of where its parts lie (RowParts) is written with
+// them, so that the join has no search and no plan before its first loads.
 #include "attend.cuh"
 
 namespace flamia {
 namespace {
 
-struct JoinArgs {
-  AttendArgs prefix, rest;
-  int prefix_rows, rest_rows;  // rows an item
-  int prefix_ctas, rest_ctas;  // of the launches
+// Results of one kind of items.
+struct Side {
+  const RowParts* where;
+  const float *row_stats, *rows, *stats, *partial;
+  int R;  // rows an item
 };
 
-// Where the parts of an item lie: part 0 in slot 1 of CTA c, the others in slots 0 from
-// there on; one part: the item was not cut.
+struct JoinArgs {
+  Side prefix, rest;
+  const int32_t* cu;
+  __nv_bfloat16* o;
+  float* lse;
+  int ndocs, T, H, G;
+};
+
+// A row's parts.  (Records out of range come from malformed offsets, for which none was
+// written.)
 struct Parts {
-  int n, c;
+  int n, cta, row;
+  __device__ __forceinline__ Parts(RowParts w, bool any, int R) {
+    n = any ? w.n & ~kShares : 0;
+    cta = w.at & 0xFFFF;
+    row = (w.at >> 16) & (R - 1);
+    if (cta >= kMaxCtas || n < 0 || n > kMaxCtas - cta) n = 0;
+  }
   __device__ __forceinline__ size_t slot(int p) const {
-    return static_cast<size_t>(p == 0 ? 2 * c + 1 : 2 * (c + p));
+    return static_cast<size_t>(p == 0 ? 2 * cta + 1 : 2 * (cta + p));
+  }
+  __device__ __forceinline__ float stat(const Side& s, int p, int own) const {
+    return n > 1 ? s.stats[slot(p) * s.R + row] : s.row_stats[own];
+  }
+  // Its values in [slot][row][d], or the whole row.
+  __device__ __forceinline__ const float* data(const Side& s, int p, int own, int d) const {
+    return n > 1 ? s.partial + (slot(p) * s.R + row) * d : s.rows + static_cast<size_t>(own) * d;
   }
 };
 
-// Of the item at units at .. at + units - 1, of which the first `cost` have no keys.
-__device__ __forceinline__ Parts parts_of(long long total, int grid, int least, long long at,
-                                          int units, int cost) {
-  const long long ctas = min(static_cast<long long>(grid), div_up(total, least));
-  const long long a = div_up((at + cost + 1) * ctas, total) - 1;
-  const long long b = div_up((at + units) * ctas, total) - 1;
-  return Parts{static_cast<int>(b - a) + 1, static_cast<int>(a)};
+__device__ __forceinline__ float max_or_nan(float m, float x) {
+  return x > m || x != x ? x : m;  // NaN stays
+}
+// Weights of parts are taken in two halves, as a small one may meet large values.
+__device__ __forceinline__ float half_weight(float stat, float ref) {
+  return exp2f(0.5f * (stat - ref));
+}
+__device__ __forceinline__ void add4(float (&acc)[4], float w, const float* x) {
+  const float4 v = *reinterpret_cast<const float4*>(x);
+  acc[0] = fmaf(w, w * v.x, acc[0]);
+  acc[1] = fmaf(w, w * v.y, acc[1]);
+  acc[2] = fmaf(w, w * v.z, acc[2]);
+  acc[3] = fmaf(w, w * v.w, acc[3]);
 }
 
-// A warp a row (token and query head); MANY: the prefix's items have 256 rows.
-template <int DIM, bool MANY>
-__global__ void __launch_bounds__(256) join_prefix_kernel(const JoinArgs a) {
-  constexpr int E = DIM / 32;  // elements a lane
-  const AttendArgs& g = a.rest;
+// One launch: a warp a row (token and query head), four elements a lane (d = 64: two rows
+// of parts side by side).
+template <int DIM>
+__global__ void __launch_bounds__(256) join_few_kernel(const JoinArgs g) {
+  constexpr int kLanes = DIM / 4, kSide = 32 / kLanes;
   const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int own = blockIdx.x * 8 + (threadIdx.x >> 5);
   wait_for_previous();
-  const int t = static_cast<int>(row / g.H), h = static_cast<int>(row - static_cast<long long>(t) * g.H);
-  if (t >= g.T) return;
-  const int b = warp_last_not_above(g.ndocs, t, lane, [&](int i) { return g.cu[i]; });
-  const DocRange r = doc_range(g.cu, b, g.T);
-  if (t < r.s || t >= r.e) return;
-  const int hk = h / g.G, hg = h - hk * g.G;
-  const int start = g.starts != nullptr ? g.starts[b] : 0;
-
-  // its parts: of the prefix, then of the rest
-  Parts pp{0, 0}, pr{1, 0};
-  int rp = 0, rr = 0;  // its row in the item
-  if (shares(g, start)) {
-    const int n = min(max(g.cu[g.ndocs], 0), g.T);
-    const int R = a.prefix_rows, cost = MANY ? kItemCost<256> : kItemCost<8>;
-    const int units = a.prefix.shared + cost;
-    const long long tiles = (static_cast<long long>(n) * g.G + R - 1) / R;
-    const long long at = static_cast<long long>(t) * g.G + hg, rt = at / R;
-    rp = static_cast<int>(at - rt * R);
-    pp = parts_of(tiles * g.H_kv * units, a.prefix_ctas, cost + 2, (hk * tiles + rt) * units, units,
-                  cost);
-  }
-  if (!g.whole) {
-    const int R = a.rest_rows;
-    const long long before = g.first[b], total = g.first[g.ndocs];
-    const long long tiles = (static_cast<long long>(r.e - r.s) * g.G + R - 1) / R;
-    const int units = static_cast<int>((g.first[b + 1] - before) / (tiles * g.H_kv));
-    const long long at = static_cast<long long>(t - r.s) * g.G + hg, rt = at / R;
-    rr = static_cast<int>(at - rt * R);
-    pr = parts_of(total, a.rest_ctas, kItemCost<8> + 2, before + (hk * tiles + rt) * units, units,
-                  kItemCost<8>);
-  }
-  const size_t own = static_cast<size_t>(t) * g.H + h;
+  if (own >= g.T * g.H) return;
+  const int t = own / g.H, h = own - t * g.H;
+  const int end = g.cu[g.ndocs];
+  const RowParts wr = g.rest.where[own], wp = g.prefix.where[own];
+  if (t >= end) return;
+  const Parts pr(wr, true, g.rest.R), pp(wp, (wr.n & kShares) != 0, g.prefix.R);
   const int parts = pp.n + pr.n;
   auto stat = [&](int p) {
-    if (p < pp.n)
-      return pp.n == 1 ? a.prefix.row_stats[own] : a.prefix.stats[pp.slot(p) * a.prefix_rows + rp];
-    return pr.n == 1 ? g.row_stats[own] : g.stats[pr.slot(p - pp.n) * a.rest_rows + rr];
+    return p < pp.n ? pp.stat(g.prefix, p, own) : pr.stat(g.rest, p - pp.n, own);
   };
-  auto data = [&](int p) -> const float* {
-    if (p < pp.n) {
-      if (pp.n == 1) return a.prefix.rows + own * DIM + lane * E;
-      const size_t s = pp.slot(p);
-      return MANY ? a.prefix.partial + (s * (DIM / 4) + lane * E / 4) * 256 * 4 + rp * 4 + lane * E % 4
-                  : a.prefix.partial + (s * a.prefix_rows + rp) * DIM + lane * E;
-    }
-    return pr.n == 1 ? g.rows + own * DIM + lane * E
-                     : g.partial + (pr.slot(p - pp.n) * a.rest_rows + rr) * DIM + lane * E;
-  };
-  float m = -INFINITY;
-  for (int p = lane; p < parts; p += 32) {
-    const float x = stat(p);
-    m = x > m || x != x ? x : m;
-  }
+  const float first = lane < parts ? stat(lane) : -INFINITY;
+  float m = first;
+  for (int p = 32 + lane; p < parts; p += 32) m = max_or_nan(m, stat(p));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float x = __shfl_xor_sync(0xffffffffu, m, o);
-    m = x > m || x != x ? x : m;  // NaN stays
-  }
-  // (weights in two halves, as a small one may meet large values)
+  for (int o = 16; o > 0; o >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[E] = {};
+  const int side = lane / kLanes, e = (lane % kLanes) * 4;
+  float l = 0.f, acc[4] = {};
   for (int p0 = 0; p0 < parts; p0 += 32) {
-    const float wt = p0 + lane < parts ? exp2f(0.5f * (stat(p0 + lane) - ref)) : 0.f;
+    const float wt =
+        p0 + lane < parts ? half_weight(p0 == 0 ? first : stat(p0 + lane), ref) : 0.f;
     l = fmaf(wt, wt, l);
     const int n = min(32, parts - p0);
 #pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const float w = __shfl_sync(0xffffffffu, wt, p);
-      const float* x = data(p0 + p);
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(x);
-        acc[0] = fmaf(w, w * v.x, acc[0]);
-        acc[1] = fmaf(w, w * v.y, acc[1]);
-        acc[2] = fmaf(w, w * v.z, acc[2]);
-        acc[3] = fmaf(w, w * v.w, acc[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(x);
-        acc[0] = fmaf(w, w * v.x, acc[0]);
-        acc[1] = fmaf(w, w * v.y, acc[1]);
-      }
+    for (int p = 0; p < n; p += kSide) {
+      const float w = __shfl_sync(0xffffffffu, wt, p + side);  // (behind the last part: 0)
+      const int q = min(p0 + p + side, parts - 1);
+      add4(acc, w,
+           (q < pp.n ? pp.data(g.prefix, q, own, DIM) : pr.data(g.rest, q - pp.n, own, DIM)) + e);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (kSide == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if (lane == 0 && g.lse != nullptr)
     g.lse[static_cast<size_t>(h) * g.T + t] = (ref + log2f(l)) * kLn2;
-  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(g.o + own * DIM + lane * E);
+  if (side == 0) {
+    __nv_bfloat162 b[2];
 #pragma unroll
-  for (int e = 0; e < E; e += 2)
-    out[e / 2] = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[e] * inv,
-                                       inv == 0.f ? 0.f : acc[e + 1] * inv);
+    for (int i = 0; i < 2; ++i)
+      b[i] = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[2 * i] * inv,
+                                   inv == 0.f ? 0.f : acc[2 * i + 1] * inv);
+    *reinterpret_cast<uint2*>(g.o + static_cast<size_t>(own) * DIM + e) =
+        make_uint2(*reinterpret_cast<uint32_t*>(&b[0]), *reinterpret_cast<uint32_t*>(&b[1]));
+  }
+}
+
+// Two launches: a thread a row and 16 elements, the rows those of an item over the prefix,
+// as its parts lie [slot][d / 4][256 rows][4].
+template <int DIM>
+__global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int row_tiles) {
+  const int hk = blockIdx.x / row_tiles;
+  const int row = (blockIdx.x - hk * row_tiles) * 256 + threadIdx.x;
+  const int t = row / g.G, h = hk * g.G + row - t * g.G;
+  const int c = blockIdx.y * 16;
+  wait_for_previous();
+  if (t >= g.T) return;
+  const int own = t * g.H + h;
+  const int end = g.cu[g.ndocs];
+  const RowParts wr = g.rest.where[own], wp = g.prefix.where[own];
+  if (t >= end) return;
+  const Parts pr(wr, true, g.rest.R), pp(wp, (wr.n & kShares) != 0, 256);
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int p = 0; p < pp.n; ++p) m = max_or_nan(m, pp.stat(g.prefix, p, own));
+  for (int p = 0; p < pr.n; ++p) m = max_or_nan(m, pr.stat(g.rest, p, own));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[4][4] = {};
+#pragma unroll 2
+  for (int p = 0; p < pp.n; ++p) {
+    const float w = half_weight(pp.stat(g.prefix, p, own), ref);
+    l = fmaf(w, w, l);
+    const bool cut = pp.n > 1;
+    const float* x = cut ? g.prefix.partial + (pp.slot(p) * (DIM / 4) + c / 4) * 1024 + pp.row * 4
+                         : g.prefix.rows + static_cast<size_t>(own) * DIM + c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add4(acc[j], w, x + j * (cut ? 1024 : 4));
+  }
+  for (int p = 0; p < pr.n; ++p) {
+    const float w = half_weight(pr.stat(g.rest, p, own), ref);
+    l = fmaf(w, w, l);
+    const float* x = pr.data(g.rest, p, own, DIM) + c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add4(acc[j], w, x + j * 4);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (c == 0 && g.lse != nullptr)
+    g.lse[static_cast<size_t>(h) * g.T + t] = (ref + log2f(l)) * kLn2;
+  uint4* out = reinterpret_cast<uint4*>(g.o + static_cast<size_t>(own) * DIM + c);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v =
+          __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[2 * j + i / 2][i % 2 * 2] * inv,
+                                inv == 0.f ? 0.f : acc[2 * j + i / 2][i % 2 * 2 + 1] * inv);
+      b[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    out[j] = make_uint4(b[0], b[1], b[2], b[3]);
+  }
 }
 
 // ------------------------------------------------------------------ host
 
-// Rows an item of the two attention kernels, or 0: the call is flamia_attn_cache's.
+// Rows an item over the prefix and over the rest, or 0: the call is flamia_attn_cache's.
 struct Forms {
   int prefix, rest;
 };
@@ -153,41 +196,50 @@ Forms forms(int T, int ndocs, int G, int prefix) {
   const int rest = rows_per_item(mean_rows(T, ndocs, G));
   // nothing to share; or every sequence fills a tensor-core operand by itself
   if (ndocs < 2 || prefix < 128 || prefix > kMaxPos || rest == kManyRows) return Forms{0, 0};
-  return Forms{rows_per_item(static_cast<long long>(T) * G), rest};
+  const int all = rows_per_item(static_cast<long long>(T) * G);
+  return Forms{all, all == kManyRows ? rest : all};
 }
 
-// Results of one attention kernel.
-size_t results(AttendArgs& g, uint8_t* ws, size_t at, int R, int d) {
-  const size_t slots = 2 * static_cast<size_t>(R == kManyRows ? kRowsCtas : kMaxCtas);
-  const size_t rows = static_cast<size_t>(g.T) * g.H;
+// The workspace, from ws on.
+struct Layout {
+  RowParts* where[2];
+  float *row_stats[2], *rows[2], *stats[2], *partial[2];
+  size_t total;
+};
+Layout layout(void* ws, const Forms& f, int T, int H, int d) {
+  Layout w{};
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const size_t rows = static_cast<size_t>(T) * H;
   auto take = [&](size_t n) {
-    float* p = reinterpret_cast<float*>(ws + at);
-    at += align_up(n * sizeof(float), 256);
+    uint8_t* p = base + w.total;
+    w.total += align_up(n, 256);
     return p;
   };
-  g.stats = take(slots * R);
-  g.row_stats = take(rows);
-  g.partial = take(slots * R * d);
-  g.rows = take(rows * d);
-  return at;
-}
-
-// All of the workspace, from ws on.
-size_t layout(AttendArgs& p, AttendArgs& r, void* ws, const Forms& f, int d) {
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  r.first = reinterpret_cast<long long*>(base);
-  size_t at = align_up(sizeof(long long) * (static_cast<size_t>(r.ndocs) + 1), 256);
-  at = results(p, base, at, f.prefix, d);
-  return results(r, base, at, f.rest, d);
+  const bool two = f.prefix == kManyRows;
+  for (int i = 0; i < 2; ++i) {
+    w.where[i] = reinterpret_cast<RowParts*>(take(sizeof(RowParts) * rows));
+    w.row_stats[i] = reinterpret_cast<float*>(take(sizeof(float) * rows));
+    w.rows[i] = reinterpret_cast<float*>(take(sizeof(float) * rows * d));
+    if (i == 0 && !two) continue;  // (one launch: in the same slots)
+    const int R = i == 0 ? f.prefix : f.rest;
+    const size_t slots = 2 * static_cast<size_t>(R == kManyRows ? kRowsCtas : kMaxCtas);
+    w.stats[i] = reinterpret_cast<float*>(take(sizeof(float) * slots * R));
+    w.partial[i] = reinterpret_cast<float*>(take(sizeof(float) * slots * R * d));
+  }
+  if (!two) {
+    w.stats[0] = w.stats[1];
+    w.partial[0] = w.partial[1];
+  }
+  return w;
 }
 
 template <int DIM>
-bool launch_join_prefix(const JoinArgs& a, cudaStream_t s) {
-  const long long rows = static_cast<long long>(a.rest.T) * a.rest.H;
-  const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
-  return a.prefix_rows == kManyRows
-             ? launch_after(join_prefix_kernel<DIM, true>, grid, 256, 0, s, a)
-             : launch_after(join_prefix_kernel<DIM, false>, grid, 256, 0, s, a);
+bool launch_join_prefix(const JoinArgs& a, int H_kv, cudaStream_t s) {
+  if (a.prefix.R != kManyRows)
+    return launch_after(join_few_kernel<DIM>, dim3((a.T * a.H + 7) / 8), 256, 0, s, a);
+  const int row_tiles = static_cast<int>((static_cast<long long>(a.T) * a.G + 255) / 256);
+  return launch_after(join_many_kernel<DIM>, dim3(row_tiles * H_kv, DIM / 16), 256, 0, s, a,
+                      row_tiles);
 }
 
 }  // namespace
@@ -200,12 +252,7 @@ extern "C" size_t flamia_attn_cache_prefix_workspace_bytes(int T, int ndocs, int
   const size_t plain = flamia_attn_cache_workspace_bytes(T, ndocs, H, H_kv, d);
   if (plain == 0 || prefix < 0) return 0;
   const Forms f = forms(T, ndocs, H / H_kv, prefix);
-  if (f.rest == 0) return plain;
-  AttendArgs p{}, r{};
-  p.T = r.T = T;
-  p.H = r.H = H;
-  p.ndocs = r.ndocs = ndocs;
-  return layout(p, r, nullptr, f, d);
+  return f.rest == 0 ? plain : layout(nullptr, f, T, H, d).total;
 }
 
 extern "C" flamia_status flamia_attn_cache_prefix(
@@ -213,35 +260,56 @@ extern "C" flamia_status flamia_attn_cache_prefix(
     const int32_t* cu_seqlens, int ndocs, const int32_t* starts, const int32_t* page_table,
     int table_stride, int prefix, float softmax_scale, void* o_bf16, float* lse, void* ws,
     size_t ws_bytes, int* dev_status, void* stream) {
-  JoinArgs a{};
+  AttendArgs g{};
   const flamia_status st =
-      attend_args(a.rest, cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
+      attend_args(g, cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
                   table_stride, softmax_scale, 0, 0, o_bf16, lse, ws, dev_status);
   if (st != FLAMIA_OK) return st;
   if (prefix < 0) return FLAMIA_ERR_INVALID_ARG;
   if (T == 0) return FLAMIA_OK;
-  const Forms f = forms(T, ndocs, a.rest.G, prefix);
+  const Forms f = forms(T, ndocs, g.G, prefix);
   if (f.rest == 0)
     return flamia_attn_cache(cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
                              table_stride, softmax_scale, 0, 0, o_bf16, lse, ws, ws_bytes,
                              dev_status, stream);
-  AttendArgs &r = a.rest, &p = a.prefix;
-  r.prefix = prefix;
-  r.shared = prefix / 128;
-  p = r;
-  if (layout(p, r, ws, f, cache->d) > ws_bytes) return FLAMIA_ERR_WORKSPACE;
-  p.whole = 0;
-  r.whole = r.cap - 128 * r.shared <= 128 * kWholeTiles;
-  a.prefix_rows = f.prefix;
-  a.rest_rows = f.rest;
-  a.prefix_ctas = f.prefix == kManyRows ? rows_grid() : few_grid(f.prefix);
-  a.rest_ctas = few_grid(f.rest);
+  const Layout w = layout(ws, f, T, H, cache->d);
+  if (w.total > ws_bytes) return FLAMIA_ERR_WORKSPACE;
+  JoinArgs a{};
+  for (int i = 0; i < 2; ++i) {
+    g.where[i] = w.where[i];
+    g.row_stats[i] = w.row_stats[i];
+    g.rows[i] = w.rows[i];
+    (i == 0 ? a.prefix : a.rest) = Side{w.where[i], w.row_stats[i], w.rows[i], w.stats[i],
+                                        w.partial[i], i == 0 ? f.prefix : f.rest};
+  }
+  a.cu = cu_seqlens;
+  a.o = g.o;
+  a.lse = lse;
+  a.ndocs = ndocs;
+  a.T = T;
+  a.H = H;
+  a.G = g.G;
+  g.prefix = prefix;
+  g.shared = prefix / 128;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  flamia_status done = f.prefix == kManyRows ? attend_rows(cache, p, kPrefix, s)
-                                             : attend_few(cache, p, f.prefix, kPrefix, s);
-  if (done == FLAMIA_OK) done = attend_few(cache, r, f.rest, kRest, s);
+  flamia_status done = FLAMIA_OK;
+  if (f.prefix == kManyRows) {
+    AttendArgs p = g;
+    p.whole = 0;
+    p.stats = w.stats[0];
+    p.partial = w.partial[0];
+    done = attend_rows(cache, p, kPrefix, s);
+  }
+  // items over the rest stay whole as flamia_attn_cache's do, but not beside items over the
+  // prefix, with which they have to be counted alike
+  g.whole = f.prefix == kManyRows && g.cap - 128 * g.shared <= 128 * kWholeTiles;
+  g.stats = w.stats[1];
+  g.partial = w.partial[1];
+  if (done == FLAMIA_OK)
+    done = attend_few(cache, g, f.rest, f.prefix == kManyRows ? kRest : kBoth, s);
   if (done != FLAMIA_OK) return done;
-  return (cache->d == 128 ? launch_join_prefix<128>(a, s) : launch_join_prefix<64>(a, s))
+  return (cache->d == 128 ? launch_join_prefix<128>(a, cache->H_kv, s)
+                          : launch_join_prefix<64>(a, cache->H_kv, s))
              ? FLAMIA_OK
              : FLAMIA_ERR_CUDA;
 }
