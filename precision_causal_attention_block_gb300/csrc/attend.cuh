@@ -416,8 +416,10 @@ flamia_status attend_args(AttendArgs& g, const flamia_kvcache* cache, const void
                           const int32_t* starts, const int32_t* page_table, int table_stride,
                           float softmax_scale, int window, int sinks, void* o_bf16, float* lse,
                           const void* ws, int* dev_status);
-// The kernel for many query rows (256 an item): kAll or kPrefix.
-flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, Keys keys, cudaStream_t s);
+// The kernel for many query rows (256 an item).
+flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
+// The same over a shared prefix (kPrefix).
+flamia_status attend_prefix_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
 // Those for 8, 16 or 32 rows an item: kAll, kRest or kBoth.
 flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
                          cudaStream_t s);

@@ -1225,5 +1225,5 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   g.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.stats);
   g.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.partial);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return R == kManyRows ? attend_rows(cache, g, kAll, s) : attend_few(cache, g, R, kAll, s);
+  return R == kManyRows ? attend_rows(cache, g, s) : attend_few(cache, g, R, kAll, s);
 }

@@ -37,34 +37,13 @@
 // and more code, too (181: spills, and misses in the instruction cache).
 #include <cmath>
 
-#include "attend.cuh"
+#include "attend_rows.cuh"
 
 namespace flamia {
 namespace {
 
-constexpr float kSlack = 8.f;
-// Columns 32 c .. 32 c + 31 of a tile: flags.
-constexpr int kUniform = 1;   // one K and one V exponent
-constexpr int kEvery = 2;     // every row sees every key
-constexpr int kHere = 4;      // there is a page
-constexpr int kLowShift = 8;  // from here on: the byte of the smallest eV that a row sees
-
-// A row of 32 keys' exponents.
-struct alignas(16) Keys32 {
-  float kf;     // 2^eK  (kUniform)
-  int ev;       // eV    (kUniform)
-  int top;      // the largest eV that a row sees; -127: none
-  int flags;
-};
-
 template <int DIM>
-struct Cfg {
-  static constexpr int kRows = 256;
-  static constexpr int kThreads = 512;  // (14 and 15 idle: registers move by four warps)
-  static constexpr int kBlock = 128 * 128;            // 64 columns of 128 rows, bytes
-  static constexpr int kTileBytes = DIM / 64 * kBlock;
-  static constexpr uint32_t kColO = 256;
-};
+using Cfg = RowsCfg<DIM>;
 
 // A segment with what the converters need: its keys' end hi, the first key wlo of
 // its window, positions pf and pl of its first and last row, its sequence.
@@ -88,7 +67,7 @@ struct Smem {
   uint64_t q_full[2], drained;
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   RowSegment seg[kSegSlots];
-  int plan_b, sharer;
+  int plan_b;
   SeqWork plan_seq;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
@@ -112,110 +91,10 @@ __device__ __forceinline__ bool group_vote(int id, bool p) {
   return r != 0;
 }
 
-// D (+)= A * B, FP16 x FP16 -> F32: A and B in shared memory, or A in tensor
-// memory (two elements a 32-bit column).  idesc_f8's fields serve: the operand
-// formats are 0 for FP16, too.  Descriptors come as their low words (the address)
-// and one high word.  Issued by one elected thread of a converged warp: under a
-// branch for one lane the eight products of a tile took 850 cycles to issue
-// (505 tokens over 7,866: 137 us against 122).
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t hi,
-                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 da, {%1, %3};\n\t"
-      "mov.b64 db, {%2, %3};\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
-                                           uint32_t hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b64 db, {%2, %3};\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// A warpgroup's registers a thread from here on.  The kernel starts with 128 each;
-// 2 x 168 + 112 + 64 is what four warpgroups then had.
-template <bool MORE, int N>
-__device__ __forceinline__ void set_registers() {
-  if (MORE)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, const uint4& w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w.x), "r"(w.y),
-               "r"(w.z), "r"(w.w)
-               : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 w;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-               : "r"(addr)
-               : "memory");
-  return w;
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t w;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
-  return w;
-}
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t w) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
-}
-
-// 16 bytes from global to shared memory, of which the first n are read (0 or 16;
-// the others become zeros), and the wait for all of the thread's.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-// Two E4M3 codes as FP16 (exact; NaN stays).
-__device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-      : "=r"(h)
-      : "r"(codes));
-  return h;
-}
-
-// Byte offset of 16-byte chunk j of a row in an FP16 operand tile: blocks of 64
-// columns, rows of 128 bytes, chunks swizzled as the 128-byte mode does.
-template <int DIM>
-__device__ __forceinline__ uint32_t tile_at(int row, int j) {
-  return (j >> 3) * Cfg<DIM>::kBlock + row * 128 + (((j & 7) ^ (row & 7)) << 4);
-}
-
 // ------------------------------------------------------------------ work
 
 // The segments of a CTA's run, in order.
-template <int R, int KEYS>
+template <int R>
 struct Walk {
   SeqWork w;
   long long u0, u, u1, total;
@@ -225,8 +104,7 @@ struct Walk {
 
   template <class Sm>
   __device__ __forceinline__ explicit Walk(const Sm& sm)
-      : w{}, u0(sm.plan_u0), u(sm.plan_u0), u1(sm.plan_u1), total(sm.plan_total),
-        b(KEYS == kPrefix ? sm.sharer : sm.plan_b) {
+      : w{}, u0(sm.plan_u0), u(sm.plan_u0), u1(sm.plan_u1), total(sm.plan_total), b(sm.plan_b) {
     if (u < u1) {
       w = sm.plan_seq;
       const long long item = mul_div(sm.plan_off, 1, w.units);
@@ -254,7 +132,7 @@ struct Walk {
       sg.pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
                                           static_cast<long long>(sg.row0) + R - 1) /
                                       g.G);
-      sg.hi = KEYS == kPrefix ? g.shared * 128 : max(sg.pl + 1, 0);
+      sg.hi = max(sg.pl + 1, 0);
       sg.wlo = g.window > 0 ? max(sg.pf - g.window + 1, 0) : 0;
       sg.wt = sg.wlo >> 7;
       sg.ns = min((g.sinks + 127) >> 7, sg.wt);
@@ -266,9 +144,7 @@ struct Walk {
         sg.slot = 2 * blockIdx.x;
       else if (i1 < w.tiles)
         sg.slot = 2 * blockIdx.x + 1;
-      if (KEYS != kAll && i0 == 0 && i1 > 0)
-        sg.parts = parts_from_here<R>(g, u - o, w.units, total) | kOver;
-      if (KEYS == kAll && first && i0 > 0) {
+      if (first && i0 > 0) {
         // the second CTA of an item has it joined: parts are the CTA before this
         // one (slot 1) and slots 0 from here on
         const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
@@ -278,7 +154,7 @@ struct Walk {
           join1 = make_int4(sg.row0, 0, 0, 0);
         }
       }
-      if (KEYS == kAll && reports && hk == 0 && rt == 0 && i0 == 0) {
+      if (reports && hk == 0 && rt == 0 && i0 == 0) {
         const int raw = g.starts != nullptr ? g.starts[b] : 0;
         if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
       }
@@ -290,7 +166,7 @@ struct Walk {
         if (++hk == g.H_kv) {
           hk = 0;
           do {
-            w = seq_work<R, KEYS>(g, ++b, 0);  // there is one: u < u1
+            w = seq_work<R, kAll>(g, ++b, 0);  // there is one: u < u1
           } while (w.row_tiles == 0 && b + 1 < g.ndocs);
         }
       }
@@ -298,49 +174,6 @@ struct Walk {
     }
     sg.s = -1;
     return sg;
-  }
-};
-
-// A converter warp's 32 keys of a tile, on their way from the cache.
-template <int DIM>
-struct Block32 {
-  static constexpr int kLanes = DIM / 16;       // lanes a row: 16 codes each
-  static constexpr int kPer = 32 / kLanes;      // rows side by side
-  static constexpr int kIters = 32 / kPer;
-  unsigned seen;   // its keys that some row of the item sees
-  uint4 w[kIters]; // K's codes, or V's
-
-  // Codes of the keys that some row of the item sees, zeros for the others (their
-  // weights are 0, and 0 x NaN would not be).
-  __device__ __forceinline__ void load(const uint8_t* src, int lane) {
-    src += lane * 16;
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      w[it] = make_uint4(0, 0, 0, 0);
-      if ((seen >> (it * kPer + lane / kLanes)) & 1)
-        w[it] = *reinterpret_cast<const uint4*>(src + it * kPer * DIM);
-    }
-  }
-  // As FP16 into rows row0 .. of an operand tile.
-  __device__ __forceinline__ void store(uint32_t tile, int row0, int lane) const {
-    const int c = lane % kLanes;
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      const int r = row0 + it * kPer + lane / kLanes;
-      const uint32_t x[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
-      uint32_t h[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[2 * j] = half2_of_codes(x[j] & 0xFFFFu);
-        h[2 * j + 1] = half2_of_codes(x[j] >> 16);
-      }
-      // (the lanes of a row's second half store the other chunk first: no bank
-      // conflicts)
-      const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-      const bool turn = c >= 4;
-      sts128(tile + tile_at<DIM>(r, 2 * c + turn), turn ? b : a);
-      sts128(tile + tile_at<DIM>(r, 2 * c + !turn), turn ? a : b);
-    }
   }
 };
 
@@ -377,7 +210,7 @@ __device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev
   past.add(sum, top);
 }
 
-template <int DIM, int KEYS>
+template <int DIM>
 __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(const AttendArgs g,
                                                                            const uint8_t* k_codes,
                                                                            const uint8_t* v_codes) {
@@ -420,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
                 static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   tc_fence_before();
-  make_plan<R, KEYS, C::kThreads>(g, sm);
+  make_plan<R, kAll, C::kThreads>(g, sm);
   tc_fence_after();
   start_next();
   const uint32_t tmem = sm.tmem_base;
@@ -850,13 +683,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (live) {
           if (slot >= 0)
             g.stats[static_cast<size_t>(slot) * R + r] = lg;
-          else if (KEYS != kAll)
-            g.row_stats[0][out] = lg;
           else if (g.lse != nullptr)
             g.lse[static_cast<size_t>(hq) * g.T + sg.s + tok] = lg * kLn2;
-          if (KEYS != kAll && sg.parts != 0)
-            g.where[0][out] =
-                RowParts{static_cast<int>(blockIdx.x) | (r << 16), sg.parts & ~kOver};
         }
 #pragma unroll
         for (int c = 0; c < DIM; c += 32) {
@@ -875,11 +703,6 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 p[j * R] = make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
-            } else if (KEYS != kAll) {
-              uint4* p = reinterpret_cast<uint4*>(g.rows[0] + out * DIM + c);
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                p[j] = make_uint4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
             } else {
               uint4* p = reinterpret_cast<uint4*>(g.o + out * DIM + c);
 #pragma unroll
@@ -906,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
     set_registers<false, 64>();  // (all four warps at once)
     if (warp == 13) {
       // ------------------------------------------------------------ walker
-      Walk<R, KEYS> walk(sm);
+      Walk<R> walk(sm);
       bool ok = true;
       for (int ns = 0; ok; ++ns) {
         const RowSegment sg = walk.next(g, lane == 0);
@@ -922,7 +745,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
         if (sg.s < 0) break;
       }
       // what the second kernel has to join for this CTA's first item
-      if (KEYS == kAll && lane == 0 && !g.whole) {
+      if (lane == 0 && !g.whole) {
         g.joins[2 * blockIdx.x] = walk.join0;
         g.joins[2 * blockIdx.x + 1] = walk.join1;
       }
@@ -1016,25 +839,22 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1) attend_rows_kernel(cons
   }
 }
 
-template <int DIM, int KEYS>
+template <int DIM>
 bool launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
   constexpr int smem = static_cast<int>(sizeof(Smem<DIM>)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
   const int grid = min(kRowsCtas, num_sms());
   static std::atomic<unsigned long long> raised{0};
-  return launch_large(attend_rows_kernel<DIM, KEYS>, raised, dim3(grid), Cfg<DIM>::kThreads, smem,
-                      s, g, static_cast<const uint8_t*>(c->k_codes),
+  return launch_large(attend_rows_kernel<DIM>, raised, dim3(grid), Cfg<DIM>::kThreads, smem, s, g,
+                      static_cast<const uint8_t*>(c->k_codes),
                       static_cast<const uint8_t*>(c->v_codes)) &&
-         (KEYS != kAll || g.whole || launch_join<DIM, 256>(grid, s, g));
+         (g.whole || launch_join<DIM, 256>(grid, s, g));
 }
 
 }  // namespace
 
-flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, Keys keys, cudaStream_t s) {
-  const bool ok = keys == kPrefix
-                      ? (c->d == 128 ? launch<128, kPrefix>(c, g, s) : launch<64, kPrefix>(c, g, s))
-                      : (c->d == 128 ? launch<128, kAll>(c, g, s) : launch<64, kAll>(c, g, s));
-  return ok ? FLAMIA_OK : FLAMIA_ERR_CUDA;
+flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
+  return (c->d == 128 ? launch<128>(c, g, s) : launch<64>(c, g, s)) ? FLAMIA_OK : FLAMIA_ERR_CUDA;
 }
 
 }  // namespace flamia

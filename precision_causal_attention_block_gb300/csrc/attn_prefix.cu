@@ -298,7 +298,7 @@ extern "C" flamia_status flamia_attn_cache_prefix(
     p.whole = 0;
     p.stats = w.stats[0];
     p.partial = w.partial[0];
-    done = attend_rows(cache, p, kPrefix, s);
+    done = attend_prefix_rows(cache, p, s);
   }
   // items over the rest stay whole as flamia_attn_cache's do, but not beside items over the
   // prefix, with which they have to be counted alike
