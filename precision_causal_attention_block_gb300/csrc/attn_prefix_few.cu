@@ -43,28 +43,11 @@ struct Few {
   static_assert(kRows * DIM * 4 <= kRing, "a warp's O takes the place of its ring");
 };
 
-// What the warps of a CTA work on: an item's keys k_lo .. k_hi - 1.
-struct Piece {
-  int s;                // its first packed row; -1: the run has ended
-  int rows;             // of the item
-  int start, row0, hk, seq;
-  int k_lo, k_hi;
-  int every;            // keys before this one are seen by all rows
-  int slot;             // partial result slot, or -1: the whole item
-  int side;             // 0: over the prefix, 1: not
-  int parts;            // RowParts::n if it holds the item's first tile, or 0
-};
-
 template <int DIM, int MT>
 struct Smem {
   using C = Few<DIM, MT>;
   alignas(128) uint8_t ring[kWarps][C::kRing];
-  uint4 q[MT][C::kKSteps][32];     // A fragments of the queries, by lane
-  float qf[C::kRows];              // 2^e x softmax scale x log2 e
-  int pos[C::kRows];               // -1: no such row
-  Sum past[kWarps][2 * MT][32];    // sum 2^(x + nref) of what is not in a lane's l
   float lg[kWarps][C::kRows];
-  Piece piece[2];
   int plan_b, sharer;
   SeqWork plan_seq;
   long long plan_off, plan_u0, plan_u1, plan_total;
@@ -80,17 +63,9 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four E4M3 codes as FP16 pairs (exact; NaN stays).
-__device__ __forceinline__ void halves_of_codes(uint32_t codes, uint32_t& a, uint32_t& b) {
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(codes));
-}
-
 // N bytes (8 or 16) from global to shared memory; zeros if there is nothing to read.
 template <int N>
-__device__ __forceinline__ void fetch(uint32_t dst, const void* src, bool there = true) {
+__device__ __forceinline__ void fetch(uint32_t dst, const void* src, bool there) {
   if (N == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(there ? 16 : 0)
@@ -110,68 +85,81 @@ __device__ __forceinline__ bool holds_nan(uint32_t codes) {
   return (((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
 }
 
-// The CTA's run, cut into pieces by one thread (its state stays in shared memory: sm.plan_*).
-template <int R, int KEYS, class Sm>
-__device__ __noinline__ void next_piece(const AttendArgs& g, Sm& sm, Piece& out) {
-  constexpr int kCost = kItemCost<R, KEYS>;
-  // plan_off: the unit inside sequence plan_b at which the run goes on
-  SeqWork w = sm.plan_seq;
-  long long u = sm.plan_u0;
-  const long long u1 = sm.plan_u1, total = sm.plan_total;
-  Piece p{};
-  p.s = -1;
-  while (u < u1) {
-    const long long item = mul_div(sm.plan_off, 1, w.units);
-    const int o = static_cast<int>(sm.plan_off - item * w.units);
-    const int hk = static_cast<int>(mul_div(item, 1, w.row_tiles));
-    const int rt = static_cast<int>(item - static_cast<long long>(hk) * w.row_tiles);
-    const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
-    const int i0 = g.whole ? 0 : max(o - kCost, 0);
-    const int i1 = g.whole ? w.tiles : max(o + take - kCost, 0);
-    const int v = sm.plan_b;
-    const bool over = of_prefix<KEYS>(v), sharing = !over && shares(g, w.start);
-    const int seq = over ? sm.sharer : seq_of<KEYS>(v);
-    if (!over && hk == 0 && rt == 0 && i0 == 0) {
-      const int raw = g.starts != nullptr ? g.starts[seq] : 0;
-      if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
+// What the warps of a CTA work on: an item's key tiles i0 .. i1 - 1 (list positions; key tile
+// i + wt), of keys below hi.
+struct Piece {
+  int s, n, start, hk, row0, i0, i1, wt, hi, seq;
+  bool over, sharing, cut;  // of the prefix; its sequence shares it; parts elsewhere
+  long long at;             // the item's first unit
+};
+
+// The CTA's run, walked by all warps alike.
+template <int R, int KEYS>
+struct Run {
+  SeqWork w;
+  long long u, u1, total;
+  int v, hk = 0, rt = 0, o = 0, sharer;
+
+  template <class Sm>
+  __device__ __forceinline__ explicit Run(const Sm& sm)
+      : w{}, u(sm.plan_u0), u1(sm.plan_u1), total(sm.plan_total), v(sm.plan_b), sharer(sm.sharer) {
+    if (u < u1) {
+      w = sm.plan_seq;
+      const long long item = mul_div(sm.plan_off, 1, w.units);
+      o = static_cast<int>(sm.plan_off - item * w.units);
+      hk = static_cast<int>(mul_div(item, 1, w.row_tiles));
+      rt = static_cast<int>(item - static_cast<long long>(hk) * w.row_tiles);
     }
-    if (i1 > i0) {  // (else the run ends before the item's first tile)
-      const int wt = sharing ? g.shared : 0;
-      const bool cut = i0 > 0 || i1 < w.tiles;
+  }
+  __device__ __forceinline__ bool next(const AttendArgs& g, Piece& p) {
+    while (u < u1) {
+      constexpr int kCost = kItemCost<R, KEYS>;
+      const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
+      const int i0 = g.whole ? 0 : max(o - kCost, 0);
+      const int i1 = g.whole ? w.tiles : max(o + take - kCost, 0);
       p.s = w.s;
-      p.row0 = rt * R;
-      p.rows = static_cast<int>(
-          min(static_cast<long long>(R), static_cast<long long>(w.n) * g.G - p.row0));
+      p.n = w.n;
       p.start = w.start;
       p.hk = hk;
-      p.seq = seq;
-      p.k_lo = (i0 + wt) * 128;
+      p.row0 = rt * R;
+      p.over = of_prefix<KEYS>(v);
+      p.sharing = !p.over && shares(g, w.start);
+      p.seq = p.over ? sharer : seq_of<KEYS>(v);
+      p.wt = p.sharing ? g.shared : 0;
       // behind the last key that its last row sees
-      const int hi = over ? g.shared * 128 : max(w.start + (p.row0 + p.rows - 1) / g.G + 1, 0);
-      p.k_hi = min((i1 + wt) * 128, hi);
-      p.every = over ? hi : w.start + p.row0 / g.G + 1;
-      p.slot = cut ? 2 * static_cast<int>(blockIdx.x) + (i0 == 0) : -1;
-      p.side = over ? 0 : 1;
-      p.parts = i0 > 0 ? 0
-                       : (cut ? parts_from_here<R, KEYS>(g, u - o, w.units, total) : 1) |
-                             (sharing ? kShares : 0);
+      const int rows = static_cast<int>(min(static_cast<long long>(w.n) * g.G - p.row0,
+                                            static_cast<long long>(R)));
+      p.hi = p.over ? g.shared * 128
+                    : max(w.start + static_cast<int>(static_cast<unsigned>(p.row0 + rows - 1) /
+                                                     static_cast<unsigned>(g.G)) + 1, 0);
+      p.i0 = i0;
+      p.i1 = i1;
+      p.cut = i0 > 0 || i1 < w.tiles;
+      p.at = u - o;
+      if (!p.over && hk == 0 && rt == 0 && i0 == 0 && threadIdx.x == 0) {
+        const int raw = g.starts != nullptr ? g.starts[p.seq] : 0;
+        if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
+      }
+      const int units = w.units;
+      u += take;
+      o = 0;
+      parts = 1;
+      if (p.cut && i0 == 0) parts = parts_from_here<R, KEYS>(g, p.at, units, total);
+      if (u < u1 && ++rt == w.row_tiles) {
+        rt = 0;
+        if (++hk == g.H_kv) {
+          hk = 0;
+          do {
+            w = seq_work<R, KEYS>(g, ++v, sharer);  // there is one: u < u1
+          } while (w.row_tiles == 0 && seq_of<KEYS>(v) + 1 < g.ndocs);
+        }
+      }
+      if (i1 > i0) return true;  // (else the run ends before the item's first tile)
     }
-    u += take;
-    sm.plan_off += take;
-    if (sm.plan_off == w.total(g.H_kv) && u < u1) {
-      int b = v;
-      do {
-        w = seq_work<R, KEYS>(g, ++b, sm.sharer);  // there is one: u < u1
-      } while (w.row_tiles == 0 && seq_of<KEYS>(b) + 1 < g.ndocs);
-      sm.plan_b = b;
-      sm.plan_seq = w;
-      sm.plan_off = 0;
-    }
-    if (p.s >= 0) break;
+    return false;
   }
-  sm.plan_u0 = u;
-  out = p;
-}
+  int parts = 1;  // of the last piece's item, if it holds the first
+};
 
 template <int DIM, int MT, int KEYS>
 __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
@@ -188,18 +176,16 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * kThreads + tid,
                 static_cast<long long>(gridDim.x) * kThreads, g.status);
   make_plan<R, KEYS, kThreads>(g, sm);
-  if (tid == 0) next_piece<R, KEYS>(g, sm, sm.piece[0]);
-  __syncthreads();
+  Run<R, KEYS> run(sm);
+  Piece pc;
   const uint32_t ring = smem_u32(sm.ring[warp]);
 
-#pragma unroll 1
-  for (int np = 0;; ++np) {
-    const Piece& pc = sm.piece[np & 1];
-    if (pc.s < 0) break;
+  while (run.next(g, pc)) {
     // ------------------------------------------------------------- keys
-    const int k_lo = pc.k_lo, k_hi = pc.k_hi;
-    // this warp's 32-key blocks (0 or less: none)
-    const int mine = ((max(k_hi - k_lo, 0) + 31) / 32 - warp + kWarps - 1) / kWarps;
+    const int k_lo = (pc.i0 + pc.wt) * 128, k_hi = min((pc.i1 + pc.wt) * 128, pc.hi);
+    const int blocks = (max(k_hi - k_lo, 0) + 31) / 32;
+    const int mine = (blocks - warp + kWarps - 1) / kWarps;  // this warp's (0 or less: none)
+    const int32_t* table = g.table + static_cast<long long>(pc.seq) * g.table_stride;
     int rows32 = -1;  // first rows of its next 32 blocks (a lane each) / 32; -1: no page
     auto key_of = [&](int m) { return k_lo + (warp + m * kWarps) * 32; };
     auto issue = [&](int m) {
@@ -207,9 +193,7 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
         if ((m & 31) == 0) {
           const int key0 = key_of(m + lane), slot = key0 / g.page_size;
           const bool need = m + lane < mine;
-          const int page = need && slot < g.table_stride
-                               ? g.table[static_cast<long long>(pc.seq) * g.table_stride + slot]
-                               : -1;
+          const int page = need && slot < g.table_stride ? table[slot] : -1;
           const bool there = page >= 0 && page < g.num_pages;
           if (need && !there) report(g.status, FLAMIA_DEV_BAD_PAGE);
           rows32 = there ? (page * g.H_kv + pc.hk) * (g.page_size / 32) +
@@ -219,107 +203,122 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
         const int row = __shfl_sync(0xffffffffu, rows32, m & 31);
         const long long base = static_cast<long long>(max(row, 0)) * 32;
         const int n = row < 0 ? 0 : k_hi - key_of(m);  // keys that are there (32 or more: all)
-        const uint32_t at = (m % C::kStages) * C::kStage;
-        const uint32_t kd = ring + at + lane * 16, vd = ring + at + C::kKBytes + lane * (DIM / 8);
-        const uint8_t* kc = k_codes + base * DIM + gr * DIM + t * (DIM / 4);
-        const uint8_t* vc = v_codes + base * DIM + 2 * t * DIM + gr * (DIM / 8);
-        auto all = [&](auto there) {
+        const uint32_t st = ring + (m % C::kStages) * C::kStage;
+        const uint8_t* kc = k_codes + base * DIM + t * (DIM / 4);
+        const uint8_t* vc = v_codes + base * DIM + gr * (DIM / 8);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int p = 0; p < DIM / 64; ++p)
-              fetch<16>(kd + (j * (DIM / 64) + p) * 512, kc + j * 8 * DIM + p * 16,
-                        there(j * 8 + gr));
+          for (int p = 0; p < DIM / 64; ++p)
+            fetch<16>(st + (j * (DIM / 64) + p) * 512 + lane * 16, kc + (j * 8 + gr) * DIM + p * 16,
+                      j * 8 + gr < n);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int key = (j >> 2) * 16 + ((j >> 1) & 1) * 8 + (j & 1);
-            fetch<DIM / 8>(vd + j * (4 * DIM), vc + key * DIM, there(key + 2 * t));
-          }
-        };
-        if (n >= 32)
-          all([](int) { return true; });
-        else
-          all([&](int key) { return key < n; });
+        for (int j = 0; j < 8; ++j) {
+          const int key = (j >> 2) * 16 + ((j >> 1) & 1) * 8 + 2 * t + (j & 1);
+          fetch<DIM / 8>(st + C::kKBytes + j * (4 * DIM) + lane * (DIM / 8), vc + key * DIM, key < n);
+        }
         if (lane == 0)
-          *reinterpret_cast<int*>(sm.ring[warp] + at + 2 * C::kKBytes + 64) = row >= 0;
+          *reinterpret_cast<int*>(sm.ring[warp] + (m % C::kStages) * C::kStage + 2 * C::kKBytes + 64) =
+              row >= 0;
         if (lane < 4)
-          fetch<16>(ring + at + 2 * C::kKBytes + lane * 16,
+          fetch<16>(st + 2 * C::kKBytes + lane * 16,
                     (lane < 2 ? g.k_scales : g.v_scales) + base + (lane & 1) * 16, n > 0);
       }
       fetch_commit();
     };
-#pragma unroll 1
+#pragma unroll
     for (int m = 0; m < C::kStages; ++m) issue(m);
 
     // ------------------------------------------------------------- queries
-    // DIM / 8 lanes a row; their numbers go to the lanes whose fragments hold them.
-    {
-      constexpr int kLanes = DIM / 8, kPer = kThreads / kLanes;
-      const int c = tid % kLanes;
-#pragma unroll 1
-      for (int r = tid / kLanes; r < R; r += kPer) {
+    const int rows =
+        static_cast<int>(min(static_cast<long long>(R), static_cast<long long>(pc.n) * g.G - pc.row0));
+    uint32_t q[MT][KS][4];
+    float qf[MT][2];
+    int pos[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = mt * 16 + half * 8 + gr;
         const int i = (pc.row0 + r) / g.G, h = pc.hk * g.G + pc.row0 + r - i * g.G;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < pc.rows)
-          w = *reinterpret_cast<const uint4*>(g.q + (pc.s + i) * g.q_stride +
-                                              static_cast<long long>(h) * DIM + c * 8);
-        uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        pos[mt][half] = r < rows ? max(pc.start + i, -1) : -1;
+        const __nv_bfloat16* src =
+            g.q + (pc.s + i) * g.q_stride + static_cast<long long>(h) * DIM + t * (DIM / 4);
+        uint4 x[DIM / 32];
+        uint32_t a = 0;
+#pragma unroll
+        for (int p = 0; p < DIM / 32; ++p) {
+          x[p] = make_uint4(0, 0, 0, 0);
+          if (r < rows) x[p] = reinterpret_cast<const uint4*>(src)[p];
+        }
         // magnitudes as integers; 0x7F80 and above: infinities and NaN, which become NaN
         // and stay out of the maximum
-        uint32_t a = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
-                              __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
+#pragma unroll
+        for (int p = 0; p < DIM / 32; ++p)
+          a = __vmaxu2(a, __vmaxu2(__vmaxu2(x[p].x & 0x7FFF7FFFu, x[p].y & 0x7FFF7FFFu),
+                                   __vmaxu2(x[p].z & 0x7FFF7FFFu, x[p].w & 0x7FFF7FFFu)));
         a = max(a & 0xFFFFu, a >> 16);
         if (a >= 0x7F80u) {
           a = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((x[e] & 0x7F80u) == 0x7F80u)
-              x[e] = (x[e] & 0xFFFF0000u) | 0x7FC0u;
-            else
-              a = max(a, x[e] & 0x7FFFu);
-            if ((x[e] & 0x7F800000u) == 0x7F800000u)
-              x[e] = (x[e] & 0xFFFFu) | 0x7FC00000u;
-            else
-              a = max(a, (x[e] >> 16) & 0x7FFFu);
+          for (int p = 0; p < DIM / 32; ++p) {
+            uint32_t* w = &x[p].x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y = e == 0 ? x[p].x : e == 1 ? x[p].y : e == 2 ? x[p].z : x[p].w;
+              if ((y & 0x7F80u) == 0x7F80u)
+                y = (y & 0xFFFF0000u) | 0x7FC0u;
+              else
+                a = max(a, y & 0x7FFFu);
+              if ((y & 0x7F800000u) == 0x7F800000u)
+                y = (y & 0xFFFFu) | 0x7FC00000u;
+              else
+                a = max(a, (y >> 16) & 0x7FFFu);
+              w[e] = y;
+            }
           }
         }
-#pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1)
-          a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
         const int ex = roundup_exponent(__uint_as_float(a << 16));
         const float2 inv = make_float2(exp2i(-ex), exp2i(-ex));
-        const int dd = c * 8 % (DIM / 4), to = (r & 7) * 4 + c * 8 / (DIM / 4), half = (r >> 3) & 1;
+        qf[mt][half] = g.scale_log2 * (ex < -126 ? 0x1p-127f : exp2i(ex));
+        auto half2 = [&](uint32_t w) {
+          return half2_of(__fmul2_rn(
+              make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)), inv));
+        };
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          (&sm.q[r >> 4][dd / 4 + e / 2][to].x)[(e & 1) * 2 + half] = half2_of(__fmul2_rn(
-              make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xFFFF0000u)), inv));
-        if (c == 0) {
-          sm.qf[r] = g.scale_log2 * (ex < -126 ? 0x1p-127f : exp2i(ex));
-          sm.pos[r] = r < pc.rows ? max(pc.start + i, -1) : -1;
+        for (int p = 0; p < DIM / 32; ++p) {
+          q[mt][2 * p][half] = half2(x[p].x);
+          q[mt][2 * p][2 + half] = half2(x[p].y);
+          q[mt][2 * p + 1][half] = half2(x[p].z);
+          q[mt][2 * p + 1][2 + half] = half2(x[p].w);
         }
       }
     }
-    __syncthreads();
-    if (warp == kWarps - 1 && lane == 0)  // (it has the fewest blocks)
-      next_piece<R, KEYS>(g, sm, sm.piece[(np + 1) & 1]);
-    __syncwarp();
+    // the first row's position: blocks up to it are seen by all rows
+    const int pf = pc.start + static_cast<int>(static_cast<unsigned>(pc.row0) /
+                                               static_cast<unsigned>(g.G));
 
     float o[MT][C::kOut][4];
-    float l[2 * MT], nref[2 * MT];  // by row: 16 (i / 2) + 8 (i % 2) + lane / 4
-    uint32_t has = 0;               // rows with a reference
+    float l[MT][2], nref[MT][2];
+    Sum past[MT][2];
+    bool has[MT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int i = 0; i < C::kOut; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-      l[i] = nref[i] = 0.f;
-      sm.past[warp][i][lane] = Sum{0.f, kNoExponent};
+      for (int half = 0; half < 2; ++half) {
+        l[mt][half] = nref[mt][half] = 0.f;
+        past[mt][half] = Sum{0.f, kNoExponent};
+        has[mt][half] = false;
+      }
     }
     int e0 = -127;
-    bool large = false;
+    bool large = false, begun = false;
 
     // ------------------------------------------------------------- blocks
 #pragma unroll 1
@@ -328,52 +327,38 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
       __syncwarp();
       const uint8_t* st = sm.ring[warp] + (m % C::kStages) * C::kStage;
       const int key0 = key_of(m);
+      const bool there = *reinterpret_cast<const int*>(st + 2 * C::kKBytes + 64) != 0;
       // scores
       float s[MT][4][4];
-      {
-        uint32_t kw[4][KS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; ++j) {
+        uint32_t kw[KS];
 #pragma unroll
-          for (int p = 0; p < DIM / 64; ++p) {
-            const uint4 x =
-                *reinterpret_cast<const uint4*>(st + (j * (DIM / 64) + p) * 512 + lane * 16);
-            kw[j][4 * p] = x.x, kw[j][4 * p + 1] = x.y, kw[j][4 * p + 2] = x.z,
-            kw[j][4 * p + 3] = x.w;
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
+        for (int p = 0; p < DIM / 64; ++p) {
+          const uint4 x =
+              *reinterpret_cast<const uint4*>(st + (j * (DIM / 64) + p) * 512 + lane * 16);
+          kw[4 * p] = x.x, kw[4 * p + 1] = x.y, kw[4 * p + 2] = x.z, kw[4 * p + 3] = x.w;
         }
 #pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
+#pragma unroll
         for (int k = 0; k < KS; ++k) {
-          uint32_t a[MT][4];
+          const uint32_t b0 = half2_of_codes(kw[k] & 0xFFFFu), b1 = half2_of_codes(kw[k] >> 16);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint4 x = sm.q[mt][k][lane];
-            a[mt][0] = x.x, a[mt][1] = x.y, a[mt][2] = x.z, a[mt][3] = x.w;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t b0, b1;
-            halves_of_codes(kw[j][k], b0, b1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][j], a[mt], b0, b1);
-          }
+          for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][j], q[mt][k], b0, b1);
         }
       }
       // exponents: one of K and one of V for all 32 keys, or each key's
       const uint8_t* ksc = st + 2 * C::kKBytes;
       const uint8_t* vsc = ksc + 32;
-      const bool there = *reinterpret_cast<const int*>(ksc + 64) != 0;
-      const bool all = there && key0 + 32 <= k_hi;          // every key is there
-      const bool every = all && key0 + 32 <= pc.every;      // and every row sees it
-      const int kb0 = ksc[0], vb0 = vsc[0];
-      const bool uniform =
-          __all_sync(0xffffffffu, ksc[lane] == kb0 && vsc[lane] == vb0) && all;
+      const bool all = there && key0 + 32 <= k_hi;         // every key is there
+      const bool every = all && (pc.over || key0 + 31 <= pf);  // and every row sees it
+      const int kb = ksc[lane], vb = vsc[lane];
+      const int kb0 = __shfl_sync(0xffffffffu, kb, 0), vb0 = __shfl_sync(0xffffffffu, vb, 0);
+      const bool uniform = __all_sync(0xffffffffu, kb == kb0 && vb == vb0) && all;
       uint32_t nan = 0;  // of this lane's keys: half seen, with a NaN in V
-      int top = vb0 - 127, low = top;  // the largest and the smallest eV of keys that are there
       if (!every) {
 #pragma unroll 1
         for (int j = 0; j < 8; ++j) {
@@ -388,155 +373,184 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
         nan |= __shfl_xor_sync(0xffffffffu, nan, 8);
         nan |= __shfl_xor_sync(0xffffffffu, nan, 16);
       }
+      // Of keys that some row sees: the largest and the smallest eV.
+      int top = vb0 - 127, low = vb0 - 127;
       if (!uniform) {
         const bool live = there && key0 + lane < k_hi;
-        const int v = vsc[lane] - 127;
-        top = __reduce_max_sync(0xffffffffu, live ? v : -127);
-        low = __reduce_min_sync(0xffffffffu, live ? v : 128);
+        top = __reduce_max_sync(0xffffffffu, live ? vb - 127 : -127);
+        low = __reduce_min_sync(0xffffffffu, live ? vb - 127 : 128);
       }
-      if (m == 0) {
+      if (!begun) {
         e0 = top;
+        begun = true;
       } else if (top > e0 + kHigh) {  // (as in attn_cache.cu)
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          sm.past[warp][i][lane].add(l[i], -static_cast<float>(e0));
-          l[i] = 0.f;
-        }
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            past[mt][half].add(l[mt][half], -static_cast<float>(e0));
+            l[mt][half] = 0.f;
+          }
         e0 = top;
       }
       const bool apart = low < e0 - kLow;  // some keys are not in l
       // y = x + eV - ref
+      int ev[4][2];
+      if (uniform) {
+        const float kf = pow2_byte(kb0), evf = static_cast<float>(vb0 - 127);
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
-        const float qf = sm.qf[(i >> 1) * 16 + (i & 1) * 8 + gr];
-        float* y0 = &s[i >> 1][0][0] + 2 * (i & 1);
-        if (uniform) {
-          const float f = pow2_byte(kb0) * qf, a = static_cast<float>(vb0 - 127) + nref[i];
+        for (int mt = 0; mt < MT; ++mt) {
+          const float f0 = kf * qf[mt][0], f1 = kf * qf[mt][1];
+          const float a0 = evf + nref[mt][0], a1 = evf + nref[mt][1];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            y0[4 * j] = fmaf(y0[4 * j], f, a);
-            y0[4 * j + 1] = fmaf(y0[4 * j + 1], f, a);
+            s[mt][j][0] = fmaf(s[mt][j][0], f0, a0);
+            s[mt][j][1] = fmaf(s[mt][j][1], f0, a0);
+            s[mt][j][2] = fmaf(s[mt][j][2], f1, a1);
+            s[mt][j][3] = fmaf(s[mt][j][3], f1, a1);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = j * 8 + 2 * t + e;
-              y0[4 * j + e] = fmaf(y0[4 * j + e], pow2_byte(ksc[key]) * qf,
-                                   static_cast<float>(vsc[key] - 127) + nref[i]);
-            }
         }
-        if (!every) {
-          // (key j * 8 + 2 t + e is V's number 2 j + e of this lane)
-          const int pos = pc.side == 0 ? k_hi : sm.pos[(i >> 1) * 16 + (i & 1) * 8 + gr];
+      } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = key0 + j * 8 + 2 * t + e;
-              float& y = y0[4 * j + e];
-              if ((nan >> (j * 2 + e)) & 1) y = __uint_as_float(0x7FC00000u);
-              if (!(there && key < k_hi && key <= pos)) y = -INFINITY;
-            }
-        }
+          for (int e = 0; e < 2; ++e) {
+            const int key = j * 8 + 2 * t + e;
+            const float kf = pow2_byte(ksc[key]);
+            ev[j][e] = vsc[key] - 127;
+            const float evf = static_cast<float>(ev[j][e]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                float& y = s[mt][j][2 * half + e];
+                y = fmaf(y, kf * qf[mt][half], evf + nref[mt][half]);
+              }
+          }
+      }
+      if (!every) {
+        // (key j * 8 + 2 t + e is V's number (j >> 1) * 4 + (j & 1) * 2 + e of this lane)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + j * 8 + 2 * t + e;
+            const bool bad = (nan >> (j * 2 + e)) & 1;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                float& y = s[mt][j][2 * half + e];
+                const bool seen = there && key < k_hi && (pc.over || key <= pos[mt][half]);
+                y = !seen ? -INFINITY : bad ? __uint_as_float(0x7FC00000u) : y;
+              }
+          }
       }
       // Do the references hold?
       bool need = false;
+      float mx[MT][2];
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
-        const float* y = &s[i >> 1][0][0] + 2 * (i & 1);
-        const float mx = fmaxf(fmax3(fmax3(y[0], y[1], y[4]), y[5], y[8]), fmax3(y[9], y[12], y[13]));
-        need |= (has >> i) & 1 ? mx > kSlack + room(nref[i]) : mx > -INFINITY;
-      }
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int c = 2 * half;
+          mx[mt][half] =
+              fmaxf(fmax3(fmax3(s[mt][0][c], s[mt][0][c + 1], s[mt][1][c]), s[mt][1][c + 1],
+                          s[mt][2][c]),
+                    fmax3(s[mt][2][c + 1], s[mt][3][c], s[mt][3][c + 1]));
+          need |= has[mt][half] ? mx[mt][half] > kSlack + room(nref[mt][half])
+                                : mx[mt][half] > -INFINITY;
+        }
       if (__any_sync(0xffffffffu, need)) {
         large = false;
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          float* y = &s[i >> 1][0][0] + 2 * (i & 1);
-          float x = fmaxf(fmax3(fmax3(y[0], y[1], y[4]), y[5], y[8]), fmax3(y[9], y[12], y[13]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));  // the row's, over its four lanes
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const bool had = (has >> i) & 1;
-          if (had ? x > kSlack + room(nref[i]) : x > -INFINITY) {
-            const float by = lowered(nref[i] - ceilf(x)) - nref[i];
-            const float f = had ? ex2_approx(by) : 1.f;
-            l[i] *= f;
-            nref[i] += by;
-            sm.past[warp][i][lane].e += by;
-            has |= 1u << i;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[4 * j] += by;
-              y[4 * j + 1] += by;
-            }
+          for (int half = 0; half < 2; ++half) {
+            float x = mx[mt][half];  // the row's, over its four lanes
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            float& ref = nref[mt][half];
+            const bool moves = has[mt][half] ? x > kSlack + room(ref) : x > -INFINITY;
+            if (moves) {
+              const float by = lowered(ref - ceilf(x)) - ref;
+              const float f = has[mt][half] ? ex2_approx(by) : 1.f;
+              l[mt][half] *= f;
+              ref += by;
+              past[mt][half].e += by;
+              has[mt][half] = true;
 #pragma unroll
-            for (int n = 0; n < C::kOut; ++n) {
-              o[i >> 1][n][2 * (i & 1)] *= f;
-              o[i >> 1][n][2 * (i & 1) + 1] *= f;
+              for (int j = 0; j < 4; ++j) {
+                s[mt][j][2 * half] += by;
+                s[mt][j][2 * half + 1] += by;
+              }
+#pragma unroll
+              for (int i = 0; i < C::kOut; ++i) {
+                o[mt][i][2 * half] *= f;
+                o[mt][i][2 * half + 1] *= f;
+              }
             }
+            large |= fabsf(ref) > kLarge;
           }
-          large |= fabsf(nref[i]) > kLarge;
-        }
         large = __any_sync(0xffffffffu, large);
       }
       if (apart) {  // keys that l does not hold: sum 2^(x + nref)
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) {
-          const float* y = &s[i >> 1][0][0] + 2 * (i & 1);
-          float x[8], most = kNoExponent, sum = 0.f;
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const int v = vsc[(n >> 1) * 8 + 2 * t + (n & 1)] - 127;
-            x[n] = v < e0 - kLow ? y[4 * (n >> 1) + (n & 1)] - static_cast<float>(v) : -INFINITY;
-            most = fmaxf(most, x[n]);
+          for (int half = 0; half < 2; ++half) {
+            float x[8], most = kNoExponent, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int v = uniform ? vb0 - 127 : ev[i / 2][i & 1];
+              x[i] = v < e0 - kLow ? s[mt][i / 2][2 * half + (i & 1)] - static_cast<float>(v)
+                                   : -INFINITY;
+              most = fmaxf(most, x[i]);
+            }
+            most = ceilf(most);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += ex2_approx(x[i] - most);
+            past[mt][half].add(sum, most);
           }
-          most = ceilf(most);
-#pragma unroll
-          for (int n = 0; n < 8; ++n) sum += ex2_approx(x[n] - most);
-          sm.past[warp][i][lane].add(sum, most);
-        }
       }
       // weights
       uint32_t p[MT][2][4];
-      if (large) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt) {
+        if (large) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[mt][j][e] = cut(s[mt][j][e], kSlack);
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][j][e] = ex2_approx(s[mt][j][e]);
 #pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
-        const float* y = &s[i >> 1][0][0] + 2 * (i & 1);
-        if (uniform) {
-          const float a = ((y[0] + y[1]) + (y[4] + y[5])) + ((y[8] + y[9]) + (y[12] + y[13]));
-          l[i] = fmaf(a, apart ? 0.f : exp2i(e0 - (vb0 - 127)), l[i]);
-        } else {
+        for (int half = 0; half < 2; ++half) {
+          const int c = 2 * half;
+          if (uniform) {
+            const float a = ((s[mt][0][c] + s[mt][0][c + 1]) + (s[mt][1][c] + s[mt][1][c + 1])) +
+                            ((s[mt][2][c] + s[mt][2][c + 1]) + (s[mt][3][c] + s[mt][3][c + 1]));
+            l[mt][half] = fmaf(a, apart ? 0.f : exp2i(e0 - (vb0 - 127)), l[mt][half]);
+          } else {
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const int v = vsc[(n >> 1) * 8 + 2 * t + (n & 1)] - 127;
-            if (v >= e0 - kLow && v <= e0 + kHigh)  // (else not there, or apart)
-              l[i] = fmaf(y[4 * (n >> 1) + (n & 1)], exp2i(e0 - v), l[i]);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (ev[j][e] >= e0 - kLow && ev[j][e] <= e0 + kHigh)  // (else unseen, or apart)
+                  l[mt][half] = fmaf(s[mt][j][c + e], exp2i(e0 - ev[j][e]), l[mt][half]);
           }
         }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          p[mt][kk][0] = half2_of(make_float2(s[mt][2 * kk][0], s[mt][2 * kk][1]));
+          p[mt][kk][1] = half2_of(make_float2(s[mt][2 * kk][2], s[mt][2 * kk][3]));
+          p[mt][kk][2] = half2_of(make_float2(s[mt][2 * kk + 1][0], s[mt][2 * kk + 1][1]));
+          p[mt][kk][3] = half2_of(make_float2(s[mt][2 * kk + 1][2], s[mt][2 * kk + 1][3]));
+        }
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float* y = &s[mt][2 * kk + (e >> 1)][2 * (e & 1)];
-            p[mt][kk][e] = half2_of(make_float2(y[0], y[1]));
-          }
       // O += P V
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
@@ -551,22 +565,22 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
             const uint2 x = *reinterpret_cast<const uint2*>(at);
             v[j][0] = x.x, v[j][1] = x.y;
           }
-        }
-        if (nan != 0) {
+          if ((nan >> (kk * 4 + j)) & 1) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if ((nan >> (kk * 4 + j)) & 1) {
-#pragma unroll
-              for (int w = 0; w < DIM / 32; ++w) v[j][w] = 0;
-            }
+            for (int w = 0; w < DIM / 32; ++w) v[j][w] = 0;
+          }
         }
 #pragma unroll
         for (int w = 0; w < DIM / 32; ++w) {
-          uint32_t b[4][2];
-          halves_of_codes(__byte_perm(v[0][w], v[1][w], 0x5140), b[0][0], b[1][0]);
-          halves_of_codes(__byte_perm(v[0][w], v[1][w], 0x7362), b[2][0], b[3][0]);
-          halves_of_codes(__byte_perm(v[2][w], v[3][w], 0x5140), b[0][1], b[1][1]);
-          halves_of_codes(__byte_perm(v[2][w], v[3][w], 0x7362), b[2][1], b[3][1]);
+          const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140);
+          const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+          const uint32_t c0 = __byte_perm(v[2][w], v[3][w], 0x5140);
+          const uint32_t c1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+          const uint32_t b[4][2] = {
+              {half2_of_codes(a0 & 0xFFFFu), half2_of_codes(c0 & 0xFFFFu)},
+              {half2_of_codes(a0 >> 16), half2_of_codes(c0 >> 16)},
+              {half2_of_codes(a1 & 0xFFFFu), half2_of_codes(c1 & 0xFFFFu)},
+              {half2_of_codes(a1 >> 16), half2_of_codes(c1 >> 16)}};
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -584,39 +598,43 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
     // swizzled by the row.
     float* out = reinterpret_cast<float*>(sm.ring[warp]);
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {
-      Sum all = sm.past[warp][i][lane];
-      all.add(l[i], -static_cast<float>(e0));
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int off = 1; off < 4; off <<= 1) {
-        const float a = __shfl_xor_sync(0xffffffffu, all.m, off);
-        const float b = __shfl_xor_sync(0xffffffffu, all.e, off);
-        all.add(a, b);
-      }
-      const int r = (i >> 1) * 16 + (i & 1) * 8 + gr;
-      const float lg = all.m == 0.f ? -INFINITY : log2f(all.m) + all.e - nref[i];
-      const int k = static_cast<int>(-all.e);
-      const float inv = all.m == 0.f ? 0.f : pow2_within(k / 2) / all.m;
-      const float ve = pow2_within(k - k / 2);
-      if (t == 0) sm.lg[warp][r] = lg;
-      // dims t (d / 4) + n, then + d / 8: column tile n's two columns of this lane
+      for (int half = 0; half < 2; ++half) {
+        Sum all = past[mt][half];
+        all.add(l[mt][half], -static_cast<float>(e0));
 #pragma unroll
-      for (int n = 0; n < C::kOut; n += 4)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = 2 * (i & 1) + e;
-          float4 x = make_float4(o[i >> 1][n][c] * inv * ve, o[i >> 1][n + 1][c] * inv * ve,
-                                 o[i >> 1][n + 2][c] * inv * ve, o[i >> 1][n + 3][c] * inv * ve);
-          if (inv == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
-          const int chunk = (t * (DIM / 4) + e * (DIM / 8) + n) / 4;
-          *reinterpret_cast<float4*>(out + r * DIM + (chunk ^ (r & 7)) * 4) = x;
+        for (int off = 1; off < 4; off <<= 1) {
+          const float a = __shfl_xor_sync(0xffffffffu, all.m, off);
+          const float b = __shfl_xor_sync(0xffffffffu, all.e, off);
+          all.add(a, b);
         }
-    }
+        const int r = mt * 16 + half * 8 + gr;
+        const float lg = all.m == 0.f ? -INFINITY : log2f(all.m) + all.e - nref[mt][half];
+        const int k = static_cast<int>(-all.e);
+        const float inv = all.m == 0.f ? 0.f : pow2_within(k / 2) / all.m;
+        const float ve = pow2_within(k - k / 2);
+        if (t == 0) sm.lg[warp][r] = lg;
+        // dims t (d / 4) + i, then + d / 8: column tile i's two columns of this lane
+#pragma unroll
+        for (int i = 0; i < C::kOut; i += 4)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float4 x;
+            x.x = o[mt][i][2 * half + e] * inv * ve;
+            x.y = o[mt][i + 1][2 * half + e] * inv * ve;
+            x.z = o[mt][i + 2][2 * half + e] * inv * ve;
+            x.w = o[mt][i + 3][2 * half + e] * inv * ve;
+            if (inv == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int chunk = (t * (DIM / 4) + e * (DIM / 8) + i) / 4;
+            *reinterpret_cast<float4*>(out + r * DIM + (chunk ^ (r & 7)) * 4) = x;
+          }
+      }
     __syncthreads();
     // the four warps' joined: kThreads / R threads a row
     constexpr int kPer = kThreads / R, kMine = DIM / kPer;  // threads a row, dims a thread
     const int r = tid / kPer, d0 = tid % kPer * kMine;
-    if (r < pc.rows) {
+    if (r < rows) {
       float lg[kWarps], ref = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
@@ -642,8 +660,9 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int i = (pc.row0 + r) / g.G, hq = pc.hk * g.G + pc.row0 + r - i * g.G;
       const size_t own = static_cast<size_t>(pc.s + i) * g.H + hq;
-      float* dst = (pc.slot >= 0 ? g.partial + (static_cast<size_t>(pc.slot) * R + r) * DIM
-                                 : g.rows[pc.side] + own * DIM) + d0;
+      const int side = pc.over ? 0 : 1, slot = 2 * blockIdx.x + (pc.i0 == 0);
+      float* dst = (pc.cut ? g.partial + (static_cast<size_t>(slot) * R + r) * DIM
+                           : g.rows[side] + own * DIM) + d0;
 #pragma unroll
       for (int e = 0; e < kMine; e += 4) {
         float4 v = make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
@@ -652,12 +671,13 @@ __global__ void __launch_bounds__(kThreads, Few<DIM, MT>::kCtas)
       }
       if (d0 == 0) {
         const float st = base + log2f(sum);
-        if (pc.slot >= 0)
-          g.stats[static_cast<size_t>(pc.slot) * R + r] = st;
+        if (pc.cut)
+          g.stats[static_cast<size_t>(slot) * R + r] = st;
         else
-          g.row_stats[pc.side][own] = st;
-        if (pc.parts != 0)
-          g.where[pc.side][own] = RowParts{static_cast<int>(blockIdx.x) | (r << 16), pc.parts};
+          g.row_stats[side][own] = st;
+        if (pc.i0 == 0)
+          g.where[side][own] = RowParts{static_cast<int>(blockIdx.x) | (r << 16),
+                                        run.parts | (pc.sharing ? kShares : 0)};
       }
     }
     __syncthreads();
