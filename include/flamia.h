@@ -664,9 +664,8 @@ flamia_status flamia_attn_cache(const flamia_kvcache* cache, const void* q_bf16,
  * with new tokens are read for all of them.  The others (and calls that gain nothing:
  * one sequence, a prefix below 128, more than 96 query rows a sequence and K / V head on
  * average) are flamia_attn_cache's.  The results are what that call gives, in other
- * roundings: a softmax weight is rounded to FP16 (2^-11 of itself, or 2^-24 of the row's
- * largest weight times value scale), and queries below 2^-14 of their row's largest element to
- * 2^-24 of that.
+ * roundings: with more than 8 query rows in the batch and K / V head (T * H / H_kv) a weight
+ * of a prefix key is rounded to 2^-11 of itself.
  *
  *  ws         flamia_attn_cache_prefix_workspace_bytes bytes, 256-byte aligned, as for
  *             flamia_attn_cache (a call is three kernels).

@@ -20,7 +20,6 @@ SOURCES = ["abi.cu", "quantize.cu", "worklist.cu", "attn_fwd.cu", "attn_bwd.cu",
            "attn_short.cu",
            "attn_bwd_pair.cu", "rope.cu", "cache.cu", "pages.cu", "attn_cache.cu",
            "attn_cache_rows.cu", "attn_prefix.cu", "attn_prefix_rows.cu",
-           "attn_prefix_few.cu",
            "probe_mma.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]

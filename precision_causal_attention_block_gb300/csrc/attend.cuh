@@ -17,6 +17,20 @@ constexpr int kSlots = 2 * kMaxCtas;  // partial results
 constexpr int kRowsCtas = 160;        // the same with 256 rows an item
 constexpr int kSegSlots = 4;
 constexpr int kMaxPos = 1 << 30;
+// An item's own steps (queries, first references, output) in tiles.  2 .. 6 are
+// within 3% of one another on the ragged and the windowed batch; with 256 rows an
+// item, 505 tokens over 7,866: 116, 113, 112, 113, 113 us with 1, 3, 5, 7, 9; 4,096
+// tokens over none: 198, 198, 201, 203, 208.
+template <int R>
+constexpr int kItemCost = R == 256 ? 5 : 3;
+// Items of at most so many tiles (as the page table's width bounds them) stay whole: 64
+// sequences over 512 tokens 19.9 us whole, 23.7 cut and joined; over 1,024 tokens 38.9
+// against 37.9.
+constexpr int kWholeTiles = 4;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
+constexpr int kLow = 60;        // keys whose eV lies further below E0 are summed apart
+
 // What a kernel's items are.  A call whose sequences share a prefix (attn_prefix.cu) has
 // items over the prefix's whole tiles, with the tokens of all sequences as the query rows
 // of each K / V head, and items of every sequence over what comes behind them.  They
@@ -27,21 +41,6 @@ enum Keys : int {
   kRest = 2,    // items of every sequence: the tiles behind those (all, if it does not share)
   kBoth = 3     // kPrefix's, then kRest's
 };
-
-// An item's own steps (queries, first references, output) in tiles.  2 .. 6 are
-// within 3% of one another on the ragged and the windowed batch; with 256 rows an
-// item, 505 tokens over 7,866: 116, 113, 112, 113, 113 us with 1, 3, 5, 7, 9; 4,096
-// tokens over none: 198, 198, 201, 203, 208.
-// (KEYS: see Keys; those of attn_prefix.cu's kernels stand there.)
-template <int R, int KEYS>
-constexpr int kItemCost = KEYS == kAll ? (R == 256 ? 5 : 3) : R == 256 ? 5 : 3;
-// Items of at most so many tiles (as the page table's width bounds them) stay whole: 64
-// sequences over 512 tokens 19.9 us whole, 23.7 cut and joined; over 1,024 tokens 38.9
-// against 37.9.
-constexpr int kWholeTiles = 4;
-constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
-constexpr int kLow = 60;        // keys whose eV lies further below E0 are summed apart
 
 // Where an item's result lies, kept for each of its rows (KEYS != kAll).  One part: in
 // `rows` and `row_stats`; more: part 0 in slot 1 of a CTA, the others in slots 0 from the
@@ -180,7 +179,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int v, int shar
                       ? static_cast<int>((static_cast<long long>(w.n) * g.G + R - 1) / R)
                       : 0;
     w.tiles = g.shared;
-    w.units = w.tiles + kItemCost<R, KEYS>;
+    w.units = w.tiles + kItemCost<R>;
     return w;
   }
   const int b = seq_of<KEYS>(v);
@@ -199,7 +198,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int v, int shar
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
                            ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);
   w.tiles = max(tiles, 1);
-  w.units = g.whole ? 1 : w.tiles + kItemCost<R, KEYS>;
+  w.units = g.whole ? 1 : w.tiles + kItemCost<R>;
   return w;
 }
 
@@ -210,7 +209,10 @@ struct Segment {
   int i0, i1;       // its key tiles: list positions i0 .. i1 - 1
   int ns, wt;       // list position i is key tile i (i < ns) or i - ns + wt
   int slot;         // partial result slot, or -1: the whole item
+  int parts;        // KEYS != kAll: RowParts::n, if it holds the item's first tile; kOver:
+                    // of the prefix
 };
+constexpr int kOver = 1 << 29;
 
 __device__ __forceinline__ int tile_of(const Segment& g, int i) {
   return i < g.ns ? i : i - g.ns + g.wt;
@@ -235,9 +237,9 @@ __device__ __forceinline__ long long div_up(long long a, long long c) {
 }
 
 // CTAs that get a run: at least two tiles each, as far as there are any.
-template <int R, int KEYS>
+template <int R>
 __device__ __forceinline__ long long active_ctas(const AttendArgs& g, long long total) {
-  const int least = g.whole ? 1 : kItemCost<R, KEYS> + 2;
+  const int least = g.whole ? 1 : kItemCost<R> + 2;
   return min(static_cast<long long>(gridDim.x), div_up(total, least));
 }
 
@@ -283,7 +285,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     if (w < warp) before += sm.scan[w];
     total += sm.scan[w];
   }
-  const long long ctas = active_ctas<R, KEYS>(g, total);
+  const long long ctas = active_ctas<R>(g, total);
   const long long c = blockIdx.x;
   const long long u0 = c < ctas ? mul_div(total, c, ctas) : total;
   const long long u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;
@@ -308,10 +310,10 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
 }
 
 // RowParts::n of the item that begins at unit ui, for the CTA with its first tile.
-template <int R, int KEYS>
+template <int R>
 __device__ __forceinline__ int parts_from_here(const AttendArgs& g, long long ui, int units,
                                                long long total) {
-  const long long ctas = active_ctas<R, KEYS>(g, total);
+  const long long ctas = active_ctas<R>(g, total);
   return static_cast<int>(div_up((ui + units) * ctas, total) - 1 - blockIdx.x) + 1;
 }
 
@@ -416,11 +418,11 @@ flamia_status attend_args(AttendArgs& g, const flamia_kvcache* cache, const void
                           const void* ws, int* dev_status);
 // The kernel for many query rows (256 an item).
 flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
-// The same over a shared prefix (kPrefix), and few rows an item (kBoth, or kRest): 32 of heads
-// of 64 where there are more than 16, else 16.
+// The same over a shared prefix (kPrefix).
 flamia_status attend_prefix_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
-flamia_status attend_prefix_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
-                                cudaStream_t s);
+// Those for 8, 16 or 32 rows an item: kAll, kRest or kBoth.
+flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
+                         cudaStream_t s);
 // Query rows side by side in one item: `rows` of a K / V head on average.
 constexpr int kManyRows = 256;
 int rows_per_item(long long rows);

@@ -218,7 +218,7 @@ struct Smem {
   uint64_t seg_full[kSegSlots], seg_empty[kSegSlots];
   Segment seg[kSegSlots];
   int2 tile[C::kSS];            // first key; pieces that were loaded, kWhole
-  int plan_b;
+  int plan_b, sharer;
   SeqWork plan_seq;
   long long plan_off, plan_u0, plan_u1, plan_total;
   long long scan[C::kThreads / 32];
@@ -297,7 +297,7 @@ struct Queries {
   }
 };
 
-template <int DIM, int R>
+template <int DIM, int R, int KEYS>
 __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     attend_kernel(const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttendArgs g) {
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
                 static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   tc_fence_before();
-  make_plan<R, kAll, C::kThreads>(g, sm);
+  make_plan<R, KEYS, C::kThreads>(g, sm);
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
@@ -377,9 +377,10 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sg.s = -1;
       } else {
         const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
-        const int cost = g.whole ? 0 : kItemCost<R, kAll>;
+        const bool over = of_prefix<KEYS>(b), cut = !g.whole;
+        const int cost = cut ? kItemCost<R> : 0;
         const int i0 = max(o - cost, 0);
-        const int i1 = g.whole ? w.tiles : max(o + take - cost, 0);
+        const int i1 = cut ? max(o + take - cost, 0) : w.tiles;
         sg.s = w.s;
         sg.n = w.n;
         sg.start = w.start;
@@ -389,10 +390,11 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
                                                       static_cast<long long>(sg.row0) + R - 1) /
                                                   g.G);
-        hi = max(pl + 1, 0);
+        hi = over ? g.shared * 128 : max(pl + 1, 0);
         wlo = g.window > 0 ? max(pf - g.window + 1, 0) : 0;
-        sg.wt = wlo >> 7;
-        sg.ns = min((g.sinks + 127) >> 7, sg.wt);
+        const bool sharing = KEYS != kAll && !over && shares(g, w.start);
+        sg.wt = sharing ? g.shared : wlo >> 7;
+        sg.ns = KEYS == kAll ? min((g.sinks + 127) >> 7, sg.wt) : 0;
         const int list = sg.ns + max(((hi + 127) >> 7) - sg.wt, 0);
         sg.i0 = min(i0, list);
         sg.i1 = min(i1, list);
@@ -401,18 +403,21 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           sg.slot = 2 * blockIdx.x;
         else if (i1 < w.tiles)
           sg.slot = 2 * blockIdx.x + 1;
-        if (first && i0 > 0) {
+        if (KEYS != kAll && i0 == 0 && i1 > 0)
+          sg.parts = (cut ? parts_from_here<R>(g, u - o, w.units, total) : 1) |
+                     (over ? kOver : 0) | (sharing ? kShares : 0);
+        if (KEYS == kAll && first && i0 > 0) {
           // the second CTA of an item has it joined: parts are the CTA before
           // this one (slot 1) and slots 0 from here on
-          const long long ctas = active_ctas<R, kAll>(g, total), c = blockIdx.x, ui = u0 - o;
-          if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost<R, kAll>) {
+          const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
+          if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost<R>) {
             const long long last = div_up((ui + w.units) * ctas, total) - 1;
             join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, hk);
             join1 = make_int4(sg.row0, 0, 0, 0);
           }
         }
-        if (lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
-          const int raw = g.starts != nullptr ? g.starts[b] : 0;
+        if (!over && lane == 0 && hk == 0 && rt == 0 && i0 == 0) {
+          const int raw = g.starts != nullptr ? g.starts[seq_of<KEYS>(b)] : 0;
           if (raw > g.cap - w.n) report(g.status, FLAMIA_DEV_BAD_PAGE);
         }
         first = false;
@@ -432,7 +437,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       ++nseg;
       if (sg.s < 0) break;
       // its key tiles; the page-table entries of a tile are read one tile ahead
-      const int32_t* row = g.table + static_cast<long long>(b) * g.table_stride;
+      const int seq = of_prefix<KEYS>(b) ? sm.sharer : seq_of<KEYS>(b);
+      const int32_t* row = g.table + static_cast<long long>(seq) * g.table_stride;
       auto entry = [&](int i, bool& need, int& in_page) {
         const int kp = tile_of(sg, i) * 128 + lane * piece;
         need = lane < pieces && kp < hi &&
@@ -451,8 +457,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (++hk == g.H_kv) {
           hk = 0;
           do {
-            w = seq_work<R, kAll>(g, ++b, 0);  // there is one: u < u1
-          } while (w.row_tiles == 0 && b + 1 < g.ndocs);
+            w = seq_work<R, KEYS>(g, ++b, 0);  // there is one: u < u1
+          } while (w.row_tiles == 0 && seq_of<KEYS>(b) + 1 < g.ndocs);
         }
       }
       for (int i = sg.i0; i < sg.i1; ++i, ++tc) {
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       }
     }
     // what the second kernel has to join for this CTA's first item
-    if (lane == 0 && !g.whole) {
+    if (KEYS == kAll && lane == 0 && !g.whole) {
       g.joins[2 * blockIdx.x] = join0;
       g.joins[2 * blockIdx.x + 1] = join1;
     }
@@ -992,6 +998,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         tc_fence_after();
       }
       const int slot = sg.slot;
+      const int rest = sg.parts & kOver ? 0 : 1;  // (of an item that was not cut)
       sum_keys();
       sync();
       if (tid < rows) {
@@ -1005,8 +1012,13 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const int orow = sm.orow[tid];
         if (slot >= 0)
           g.stats[static_cast<size_t>(slot) * R + tid] = lg;
+        else if (KEYS != kAll)
+          g.row_stats[rest][orow] = lg;
         else if (g.lse != nullptr)
           g.lse[static_cast<size_t>(orow % g.H) * g.T + orow / g.H] = lg * kLn2;
+        if (KEYS != kAll && sg.parts != 0)
+          g.where[rest][orow] =
+              RowParts{static_cast<int>(blockIdx.x) | (tid << 16), sg.parts & ~kOver};
       }
       sync();
       const bool active = DIM == 128 || key_in < DIM;
@@ -1031,6 +1043,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
                        __uint_as_float(h[i])) * f * sm.ve[r];
             if (slot >= 0)
               g.partial[(static_cast<size_t>(slot) * R + r) * DIM + key_in] = v;
+            else if (KEYS != kAll)
+              g.rows[rest][static_cast<size_t>(sm.orow[r]) * DIM + key_in] = v;
             else
               g.o[static_cast<size_t>(sm.orow[r]) * DIM + key_in] = __float2bfloat16(v);
           }
@@ -1085,7 +1099,7 @@ bool make_page_map(CUtensorMap* map, const uint8_t* codes, const flamia_kvcache*
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DIM, int R>
+template <int DIM, int R, int KEYS>
 flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s) {
   CUtensorMap mk, mv;
   if (!make_page_map(&mk, c->k_codes, c) || !make_page_map(&mv, c->v_codes, c))
@@ -1094,22 +1108,30 @@ flamia_status launch(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t 
   static_assert(Cfg<DIM, R>::kCtas * (smem + 1024) <= 228 * 1024, "shared memory");
   const int grid = min(kMaxCtas, num_sms() * Cfg<DIM, R>::kCtas);
   static std::atomic<unsigned long long> raised{0};
-  return launch_large(attend_kernel<DIM, R>, raised, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk,
+  return launch_large(attend_kernel<DIM, R, KEYS>, raised, dim3(grid), Cfg<DIM, R>::kThreads, smem, s, mk,
                       mv, g) &&
-                 (g.whole || launch_join<DIM, R>(grid, s, g))
+                 (KEYS != kAll || g.whole || launch_join<DIM, R>(grid, s, g))
              ? FLAMIA_OK
              : FLAMIA_ERR_CUDA;
 }
 
-flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, cudaStream_t s) {
+template <int KEYS>
+flamia_status launch_few(const flamia_kvcache* c, const AttendArgs& g, int R, cudaStream_t s) {
   if (c->d == 128)
-    return R == 8 ? launch<128, 8>(c, g, s)
-                  : R == 16 ? launch<128, 16>(c, g, s) : launch<128, 32>(c, g, s);
-  return R == 8 ? launch<64, 8>(c, g, s)
-                : R == 16 ? launch<64, 16>(c, g, s) : launch<64, 32>(c, g, s);
+    return R == 8 ? launch<128, 8, KEYS>(c, g, s)
+                  : R == 16 ? launch<128, 16, KEYS>(c, g, s) : launch<128, 32, KEYS>(c, g, s);
+  return R == 8 ? launch<64, 8, KEYS>(c, g, s)
+                : R == 16 ? launch<64, 16, KEYS>(c, g, s) : launch<64, 32, KEYS>(c, g, s);
 }
 
 }  // namespace
+
+flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
+                         cudaStream_t s) {
+  return keys == kAll ? launch_few<kAll>(c, g, R, s)
+                      : keys == kBoth ? launch_few<kBoth>(c, g, R, s)
+                                      : launch_few<kRest>(c, g, R, s);
+}
 
 // Query rows side by side in one item: those of a K / V head's mean number of
 // new tokens, up to 32, or 256 (attn_cache_rows.cu).  More rows than there are cost
@@ -1203,5 +1225,5 @@ extern "C" flamia_status flamia_attn_cache(const flamia_kvcache* cache, const vo
   g.stats = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.stats);
   g.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.partial);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return R == kManyRows ? attend_rows(cache, g, s) : attend_few(cache, g, R, s);
+  return R == kManyRows ? attend_rows(cache, g, s) : attend_few(cache, g, R, kAll, s);
 }

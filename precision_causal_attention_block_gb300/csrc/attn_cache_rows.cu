@@ -119,7 +119,7 @@ struct Walk {
     RowSegment sg{};
     while (u < u1) {
       const int take = static_cast<int>(min(u1 - u, static_cast<long long>(w.units - o)));
-      const int cost = g.whole ? 0 : kItemCost<R, kAll>;
+      const int cost = g.whole ? 0 : kItemCost<R>;
       const int i0 = max(o - cost, 0);
       const int i1 = g.whole ? w.tiles : max(o + take - cost, 0);
       sg.seq = b;
@@ -147,8 +147,8 @@ struct Walk {
       if (first && i0 > 0) {
         // the second CTA of an item has it joined: parts are the CTA before this
         // one (slot 1) and slots 0 from here on
-        const long long ctas = active_ctas<R, kAll>(g, total), c = blockIdx.x, ui = u0 - o;
-        if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost<R, kAll>) {
+        const long long ctas = active_ctas<R>(g, total), c = blockIdx.x, ui = u0 - o;
+        if (c > 0 && mul_div(total, c - 1, ctas) <= ui + kItemCost<R>) {
           const long long last = div_up((ui + w.units) * ctas, total) - 1;
           join0 = make_int4(static_cast<int>(last - c + 2), w.s, w.n, hk);
           join1 = make_int4(sg.row0, 0, 0, 0);

@@ -192,14 +192,12 @@ __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int ro
 struct Forms {
   int prefix, rest;
 };
-Forms forms(int T, int ndocs, int G, int d, int prefix) {
-  const long long mean = mean_rows(T, ndocs, G), all = static_cast<long long>(T) * G;
+Forms forms(int T, int ndocs, int G, int prefix) {
+  const int rest = rows_per_item(mean_rows(T, ndocs, G));
   // nothing to share; or every sequence fills a tensor-core operand by itself
-  if (ndocs < 2 || prefix < 128 || prefix > kMaxPos || rows_per_item(mean) == kManyRows)
-    return Forms{0, 0};
-  const bool many = rows_per_item(all) == kManyRows;
-  const int few = d == 64 && (many ? mean : all) > 16 ? 32 : 16;
-  return Forms{many ? kManyRows : few, few};
+  if (ndocs < 2 || prefix < 128 || prefix > kMaxPos || rest == kManyRows) return Forms{0, 0};
+  const int all = rows_per_item(static_cast<long long>(T) * G);
+  return Forms{all, all == kManyRows ? rest : all};
 }
 
 // The workspace, from ws on.
@@ -253,7 +251,7 @@ extern "C" size_t flamia_attn_cache_prefix_workspace_bytes(int T, int ndocs, int
                                                            int prefix) {
   const size_t plain = flamia_attn_cache_workspace_bytes(T, ndocs, H, H_kv, d);
   if (plain == 0 || prefix < 0) return 0;
-  const Forms f = forms(T, ndocs, H / H_kv, d, prefix);
+  const Forms f = forms(T, ndocs, H / H_kv, prefix);
   return f.rest == 0 ? plain : layout(nullptr, f, T, H, d).total;
 }
 
@@ -269,7 +267,7 @@ extern "C" flamia_status flamia_attn_cache_prefix(
   if (st != FLAMIA_OK) return st;
   if (prefix < 0) return FLAMIA_ERR_INVALID_ARG;
   if (T == 0) return FLAMIA_OK;
-  const Forms f = forms(T, ndocs, g.G, cache->d, prefix);
+  const Forms f = forms(T, ndocs, g.G, prefix);
   if (f.rest == 0)
     return flamia_attn_cache(cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
                              table_stride, softmax_scale, 0, 0, o_bf16, lse, ws, ws_bytes,
@@ -308,7 +306,7 @@ extern "C" flamia_status flamia_attn_cache_prefix(
   g.stats = w.stats[1];
   g.partial = w.partial[1];
   if (done == FLAMIA_OK)
-    done = attend_prefix_few(cache, g, f.rest, f.prefix == kManyRows ? kRest : kBoth, s);
+    done = attend_few(cache, g, f.rest, f.prefix == kManyRows ? kRest : kBoth, s);
   if (done != FLAMIA_OK) return done;
   return (cache->d == 128 ? launch_join_prefix<128>(a, cache->H_kv, s)
                           : launch_join_prefix<64>(a, cache->H_kv, s))

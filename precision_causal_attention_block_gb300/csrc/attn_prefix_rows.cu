@@ -22,7 +22,7 @@ namespace {
 template <int DIM>
 using Cfg = RowsCfg<DIM>;
 constexpr int kR = 256;
-constexpr int kCost = kItemCost<kR, kPrefix>;
+constexpr int kCost = kItemCost<kR>;
 
 template <int DIM>
 struct Smem {
@@ -65,7 +65,7 @@ struct Run {
     tiles = g.shared;
     units = tiles + kCost;
     total = static_cast<long long>(row_tiles) * g.H_kv * units;
-    const long long ctas = active_ctas<kR, kPrefix>(g, total), c = blockIdx.x;
+    const long long ctas = active_ctas<kR>(g, total), c = blockIdx.x;
     u = c < ctas ? mul_div(total, c, ctas) : total;
     u1 = c < ctas ? mul_div(total, c + 1, ctas) : total;
     hk = rt = o = 0;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1)
             g.row_stats[0][out] = lg;
           if (pc.i0 == 0)
             g.where[0][out] = RowParts{static_cast<int>(blockIdx.x) | (r << 16),
-                                       parts_from_here<kR, kPrefix>(g, pc.at, run.units, run.total)};
+                                       parts_from_here<kR>(g, pc.at, run.units, run.total)};
         }
 #pragma unroll
         for (int c = 0; c < DIM; c += 32) {
