@@ -130,14 +130,14 @@ __global__ void __launch_bounds__(256) join_few_kernel(const JoinArgs g) {
   }
 }
 
-// Two launches: a thread a row and 16 elements, the rows those of an item over the prefix,
-// as its parts lie [slot][d / 4][256 rows][4].
+// Two launches: a thread a row and 8 elements, the rows those of an item over the prefix,
+// as its parts lie [slot][d / 4][256 rows][4].  Loads of four parts at a time.
 template <int DIM>
 __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int row_tiles) {
   const int hk = blockIdx.x / row_tiles;
   const int row = (blockIdx.x - hk * row_tiles) * 256 + threadIdx.x;
   const int t = row / g.G, h = hk * g.G + row - t * g.G;
-  const int c = blockIdx.y * 16;
+  const int c = blockIdx.y * 8;
   wait_for_previous();
   if (t >= g.T) return;
   const int own = t * g.H + h;
@@ -145,45 +145,67 @@ __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int ro
   const RowParts wr = g.rest.where[own], wp = g.prefix.where[own];
   if (t >= end) return;
   const Parts pr(wr, true, g.rest.R), pp(wp, (wr.n & kShares) != 0, 256);
+  const int parts = pp.n + pr.n;
+  auto stat = [&](int p) {
+    return p >= parts ? -INFINITY
+                      : p < pp.n ? pp.stat(g.prefix, p, own) : pr.stat(g.rest, p - pp.n, own);
+  };
   float m = -INFINITY;
-#pragma unroll 4
-  for (int p = 0; p < pp.n; ++p) m = max_or_nan(m, pp.stat(g.prefix, p, own));
-  for (int p = 0; p < pr.n; ++p) m = max_or_nan(m, pr.stat(g.rest, p, own));
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[4][4] = {};
-#pragma unroll 2
-  for (int p = 0; p < pp.n; ++p) {
-    const float w = half_weight(pp.stat(g.prefix, p, own), ref);
-    l = fmaf(w, w, l);
-    const bool cut = pp.n > 1;
-    const float* x = cut ? g.prefix.partial + (pp.slot(p) * (DIM / 4) + c / 4) * 1024 + pp.row * 4
-                         : g.prefix.rows + static_cast<size_t>(own) * DIM + c;
+#pragma unroll 1
+  for (int p = 0; p < parts; p += 8) {
+    float x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add4(acc[j], w, x + j * (cut ? 1024 : 4));
+    for (int i = 0; i < 8; ++i) x[i] = stat(p + i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_or_nan(m, x[i]);
   }
-  for (int p = 0; p < pr.n; ++p) {
-    const float w = half_weight(pr.stat(g.rest, p, own), ref);
-    l = fmaf(w, w, l);
-    const float* x = pr.data(g.rest, p, own, DIM) + c;
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[2][4] = {};
+#pragma unroll 1
+  for (int p = 0; p < parts; p += 4) {
+    float x[4], v[4][8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) add4(acc[j], w, x + j * 4);
+    for (int i = 0; i < 4; ++i) {
+      const int q = p + i;
+      x[i] = stat(q);
+      const float* at = nullptr;
+      int step = 4;
+      if (q < pp.n) {
+        at = pp.n > 1 ? g.prefix.partial + (pp.slot(q) * (DIM / 4) + c / 4) * 1024 + pp.row * 4
+                      : g.prefix.rows + static_cast<size_t>(own) * DIM + c;
+        step = pp.n > 1 ? 1024 : 4;
+      } else if (q < parts) {
+        at = pr.data(g.rest, q - pp.n, own, DIM) + c;
+      }
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      if (at != nullptr) {
+        a = *reinterpret_cast<const float4*>(at);
+        b = *reinterpret_cast<const float4*>(at + step);
+      }
+      v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+      v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = half_weight(x[i], ref);  // (behind the last part: 0)
+      l = fmaf(w, w, l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e / 4][e % 4] = fmaf(w, w * v[i][e], acc[e / 4][e % 4]);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if (c == 0 && g.lse != nullptr)
     g.lse[static_cast<size_t>(h) * g.T + t] = (ref + log2f(l)) * kLn2;
-  uint4* out = reinterpret_cast<uint4*>(g.o + static_cast<size_t>(own) * DIM + c);
+  uint32_t b[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v =
-          __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[2 * j + i / 2][i % 2 * 2] * inv,
-                                inv == 0.f ? 0.f : acc[2 * j + i / 2][i % 2 * 2 + 1] * inv);
-      b[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    out[j] = make_uint4(b[0], b[1], b[2], b[3]);
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v =
+        __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[i / 2][i % 2 * 2] * inv,
+                              inv == 0.f ? 0.f : acc[i / 2][i % 2 * 2 + 1] * inv);
+    b[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
+  *reinterpret_cast<uint4*>(g.o + static_cast<size_t>(own) * DIM + c) =
+      make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // ------------------------------------------------------------------ host
@@ -238,7 +260,7 @@ bool launch_join_prefix(const JoinArgs& a, int H_kv, cudaStream_t s) {
   if (a.prefix.R != kManyRows)
     return launch_after(join_few_kernel<DIM>, dim3((a.T * a.H + 7) / 8), 256, 0, s, a);
   const int row_tiles = static_cast<int>((static_cast<long long>(a.T) * a.G + 255) / 256);
-  return launch_after(join_many_kernel<DIM>, dim3(row_tiles * H_kv, DIM / 16), 256, 0, s, a,
+  return launch_after(join_many_kernel<DIM>, dim3(row_tiles * H_kv, DIM / 8), 256, 0, s, a,
                       row_tiles);
 }
 
