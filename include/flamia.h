@@ -151,6 +151,11 @@ typedef enum {
 #define FLAMIA_FLAG_ROPE_INVERSE 0x4000 /* the transposed rotation: gradients of the
                                        rotated rows -> gradients of the rows      */
 
+/* Shared-prefix flag. */
+#define FLAMIA_FLAG_PREFIX_ALWAYS 0x8000 /* flamia_attn_cache_prefix: the prefix is read once
+                                       for all sequences whatever the sizes (default: where
+                                       that was measured faster)                  */
+
 /*
  * One quantised operand, all device pointers owned by the caller.
  *  codes        u8  [T, H, d]     E4M3 codes.
@@ -661,23 +666,25 @@ flamia_status flamia_attn_cache(const flamia_kvcache* cache, const void* q_bf16,
  * about.  A sequence whose new tokens all stand at prefix - 1 or behind (starts[b] >=
  * prefix - 1) shares it: its first `prefix` positions hold what those of the other sharing
  * sequences hold, as a rule in the same pages, and those of the first such sequence
- * with new tokens are read for all of them.  The others (and calls that gain nothing:
- * one sequence, a prefix below 128, more than 96 query rows a sequence and K / V head on
- * average) are flamia_attn_cache's.  The results are what that call gives, in other
- * roundings: with more than 8 query rows in the batch and K / V head (T * H / H_kv) a weight
- * of a prefix key is rounded to 2^-11 of itself.
+ * with new tokens are read for all of them.  The others, and calls that gain nothing by it
+ * (one sequence, a prefix below 128, more than 96 query rows a sequence and K / V head on
+ * average; without FLAMIA_FLAG_PREFIX_ALWAYS those that save too few bytes) are
+ * flamia_attn_cache's.  The results are what that call gives, in other roundings: with more
+ * than 8 query rows of a K / V head in the batch (T * H / H_kv) a weight is rounded
+ * to 2^-11 of itself.
  *
+ *  flags      0 or FLAMIA_FLAG_PREFIX_ALWAYS.
  *  ws         flamia_attn_cache_prefix_workspace_bytes bytes, 256-byte aligned, as for
- *             flamia_attn_cache (a call is three kernels).
+ *             flamia_attn_cache (a call is two or three kernels).
  */
 size_t flamia_attn_cache_prefix_workspace_bytes(int T, int ndocs, int H, int H_kv, int d,
-                                                int prefix);
+                                                int prefix, int flags);
 flamia_status flamia_attn_cache_prefix(const flamia_kvcache* cache, const void* q_bf16,
                                        int64_t q_stride, int T, int H, const int32_t* cu_seqlens,
                                        int ndocs, const int32_t* starts, const int32_t* page_table,
                                        int table_stride, int prefix, float softmax_scale,
-                                       void* o_bf16, float* lse, void* ws, size_t ws_bytes,
-                                       int* dev_status, void* stream);
+                                       int flags, void* o_bf16, float* lse, void* ws,
+                                       size_t ws_bytes, int* dev_status, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* flamia_status_str(flamia_status s);

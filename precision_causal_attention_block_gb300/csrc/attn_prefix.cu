@@ -6,7 +6,7 @@
 // out by itself as a mean of values o_i with log2 of its sum of weights, lg_i:
 //   lg = log2 sum 2^lg_i,   o = sum 2^(lg_i - lg) o_i.
 //
-// Up to 96 query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
+// Up to 64 query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
 // kernels over items of both kinds.  More: the kernel of attn_cache_rows.cu over the prefix
 // (no masks: all rows see all of it), then attn_cache.cu's over what comes behind it.
 // In both cases a last kernel joins what they leave: float32 rows of items that
@@ -214,11 +214,24 @@ __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int ro
 struct Forms {
   int prefix, rest;
 };
-Forms forms(int T, int ndocs, int G, int prefix) {
+// 256 rows an item beyond 64 in the batch (heads of 128, 32,768 shared, 64 rows 64 us with 32
+// an item and 68 with 256, 96 rows 78 and 68; heads of 64, 32 rows 118 and 146, 64 rows
+// 232 and 168).
+// What sharing saves is the reading of the prefix by every sequence but one, at some 10 TB/s,
+// as the L2 cache serves most of that; what it costs is the join and, with 256 rows, a
+// launch and the larger items.  So it is done from so many bytes on.  Shared against plain,
+// us, below and above: 8 rows 18.3 (plain) and 20.5 at 15 MB, 21.9 and 20.5 at 59; 16 rows 27.9
+// and 28.8 at 101 MB, 39.9 and 36.5 at 203; 32 rows 34.8 and 35.8 at 194 MB, 38.6 and 36.5 at
+// 237; 256 rows 41.2 and 44.7 at 262 MB, 66.1 and 60.0 at 532.
+Forms forms(int T, int ndocs, int G, int H_kv, int d, int prefix, int flags) {
   const int rest = rows_per_item(mean_rows(T, ndocs, G));
   // nothing to share; or every sequence fills a tensor-core operand by itself
   if (ndocs < 2 || prefix < 128 || prefix > kMaxPos || rest == kManyRows) return Forms{0, 0};
-  const int all = rows_per_item(static_cast<long long>(T) * G);
+  const long long rows = static_cast<long long>(T) * G;
+  const int all = rows > 64 ? kManyRows : rows_per_item(rows);
+  const double saved = (ndocs - 1.) * (prefix / 128 * 128) * H_kv * 2. * (d + 1);
+  const double least = all == 8 ? 45e6 : all == 16 ? 120e6 : all == 32 ? 200e6 : 350e6;
+  if (saved < least && !(flags & FLAMIA_FLAG_PREFIX_ALWAYS)) return Forms{0, 0};
   return Forms{all, all == kManyRows ? rest : all};
 }
 
@@ -270,26 +283,27 @@ bool launch_join_prefix(const JoinArgs& a, int H_kv, cudaStream_t s) {
 using namespace flamia;
 
 extern "C" size_t flamia_attn_cache_prefix_workspace_bytes(int T, int ndocs, int H, int H_kv, int d,
-                                                           int prefix) {
+                                                           int prefix, int flags) {
   const size_t plain = flamia_attn_cache_workspace_bytes(T, ndocs, H, H_kv, d);
-  if (plain == 0 || prefix < 0) return 0;
-  const Forms f = forms(T, ndocs, H / H_kv, prefix);
+  if (plain == 0 || prefix < 0 || (flags & ~FLAMIA_FLAG_PREFIX_ALWAYS)) return 0;
+  const Forms f = forms(T, ndocs, H / H_kv, H_kv, d, prefix, flags);
   return f.rest == 0 ? plain : layout(nullptr, f, T, H, d).total;
 }
 
 extern "C" flamia_status flamia_attn_cache_prefix(
     const flamia_kvcache* cache, const void* q_bf16, int64_t q_stride, int T, int H,
     const int32_t* cu_seqlens, int ndocs, const int32_t* starts, const int32_t* page_table,
-    int table_stride, int prefix, float softmax_scale, void* o_bf16, float* lse, void* ws,
+    int table_stride, int prefix, float softmax_scale, int flags, void* o_bf16, float* lse, void* ws,
     size_t ws_bytes, int* dev_status, void* stream) {
   AttendArgs g{};
   const flamia_status st =
       attend_args(g, cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
                   table_stride, softmax_scale, 0, 0, o_bf16, lse, ws, dev_status);
   if (st != FLAMIA_OK) return st;
+  if (flags & ~FLAMIA_FLAG_PREFIX_ALWAYS) return FLAMIA_ERR_UNSUPPORTED;
   if (prefix < 0) return FLAMIA_ERR_INVALID_ARG;
   if (T == 0) return FLAMIA_OK;
-  const Forms f = forms(T, ndocs, g.G, prefix);
+  const Forms f = forms(T, ndocs, g.G, g.H_kv, cache->d, prefix, flags);
   if (f.rest == 0)
     return flamia_attn_cache(cache, q_bf16, q_stride, T, H, cu_seqlens, ndocs, starts, page_table,
                              table_stride, softmax_scale, 0, 0, o_bf16, lse, ws, ws_bytes,

@@ -37,6 +37,7 @@ FLAG_BWD_CTA_PAIR = 0x800
 FLAG_BWD_ONE_CTA = 0x1000
 FLAG_ROPE_INTERLEAVED = 0x2000
 FLAG_ROPE_INVERSE = 0x4000
+FLAG_PREFIX_ALWAYS = 0x8000
 DEV_BAD_SEQLENS = 0x1
 DEV_CAPACITY = 0x2
 DEV_TIMEOUT = 0x4
@@ -96,9 +97,9 @@ SIGNATURES = {
     "flamia_attn_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "flamia_attn_cache": (_i, [_CP, _vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i, _f, _i, _i, _vp,
                                _vp, _vp, _sz, _vp, _vp]),
-    "flamia_attn_cache_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
-    "flamia_attn_cache_prefix": (_i, [_CP, _vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i, _i, _f, _vp,
-                                      _vp, _vp, _sz, _vp, _vp]),
+    "flamia_attn_cache_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "flamia_attn_cache_prefix": (_i, [_CP, _vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i, _i, _f, _i,
+                                      _vp, _vp, _vp, _sz, _vp, _vp]),
     "flamia_status_str": (ctypes.c_char_p, [_i]),
     "flamia_debug_mma_tile": (_i, [_i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "flamia_debug_bounded_waits": (_i, [_vp, _vp, _vp]),
@@ -511,11 +512,13 @@ class KVCache:
         flamia_pages_copy(self if source is None else source, self, src, dst, dev_status)
 
     def attend(self, q, cu_seqlens, starts, page_table, softmax_scale: float, window: int = 0,
-               sinks: int = 0, o=None, lse=None, ws=None, dev_status=None, prefix: int = 0):
+               sinks: int = 0, o=None, lse=None, ws=None, dev_status=None, prefix: int = 0,
+               always_share: bool = False):
         """(o, lse) of queries q [T, H, d] at positions starts[b] .. over the
         cache.  prefix: the sequences begin with the same so many tokens (those of which
         all new tokens stand at prefix - 1 or behind), which are read once for all of
-        them; with a window each reads its own.  ws None: the workspace of the current stream and thread (42 MB, made
+        them where that is faster (always_share: in any case); with a window each reads
+        its own.  ws None: the workspace of the current stream and thread (42 MB, made
         by their first call, shared by all caches), or, while a graph is captured, one
         that belongs to the graph: calls that overlap never share one."""
         T, H = q.shape[0], q.shape[1]
@@ -525,7 +528,8 @@ class KVCache:
             lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         if prefix and not window and not sinks:
             flamia_attn_cache_prefix(self, q, cu_seqlens, starts, page_table, prefix, softmax_scale,
-                                     o, lse, ws, dev_status)
+                                     o, lse, ws, dev_status,
+                                     FLAG_PREFIX_ALWAYS if always_share else 0)
         else:
             if prefix < 0:
                 raise RuntimeError("prefix: expected 0 or more tokens")
@@ -647,13 +651,13 @@ def flamia_attn_cache(cache: KVCache, q, cu_seqlens, starts, page_table, softmax
 
 
 def flamia_attn_cache_prefix_workspace_bytes(T: int, ndocs: int, H: int, H_kv: int, d: int,
-                                             prefix: int) -> int:
-    return int(load().flamia_attn_cache_prefix_workspace_bytes(T, ndocs, H, H_kv, d,
-                                                               max(-1, min(prefix, _INT_MAX))))
+                                             prefix: int, flags: int = 0) -> int:
+    return int(load().flamia_attn_cache_prefix_workspace_bytes(
+        T, ndocs, H, H_kv, d, max(-1, min(prefix, _INT_MAX)), flags))
 
 
 def flamia_attn_cache_prefix(cache: KVCache, q, cu_seqlens, starts, page_table, prefix,
-                             softmax_scale, o, lse, ws=None, dev_status=None):
+                             softmax_scale, o, lse, ws=None, dev_status=None, flags: int = 0):
     dev, stream = _current()
     qp, qs, T, H, lp = _attend_rows(cache, q, o, lse, dev)
     n = cu_seqlens.numel() - 1
@@ -663,14 +667,14 @@ def flamia_attn_cache_prefix(cache: KVCache, q, cu_seqlens, starts, page_table, 
         # (of the call: the allocator hands it on in the stream's order, or keeps it for
         # the graph that is being captured; a byte for arguments that will be refused)
         ws = torch.empty(max(1, lib.flamia_attn_cache_prefix_workspace_bytes(
-            T, n, H, cache.H_kv, cache.d, prefix)), dtype=torch.uint8, device=q.device)
+            T, n, H, cache.H_kv, cache.d, prefix, flags)), dtype=torch.uint8, device=q.device)
         wp, wn = ws.data_ptr(), ws.nbytes
     else:
         wp, wn = _given_workspace(ws, dev)
     st = lib.flamia_attn_cache_prefix(
         cache._ref, qp, qs, T, H, _ints(cu_seqlens, "cu_seqlens", 0, dev), n,
         _ints(starts, "starts", n, dev), _page_table(page_table, n, dev), page_table.shape[1],
-        prefix, float(softmax_scale), o.data_ptr(), lp, wp, wn,
+        prefix, float(softmax_scale), flags, o.data_ptr(), lp, wp, wn,
         _ints(dev_status, "dev_status", 0, dev), stream)
     if st:
         _check(st, "flamia_attn_cache_prefix")

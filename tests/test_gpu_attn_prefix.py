@@ -72,7 +72,7 @@ def _run(fl, pair, rng, H, n, starts, prefix, T=None, scale=None, q=None):
     o = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full((H, T), 7.0, device=DEV)
     pair.gpu.attend(q, offsets(n), i32(starts), pair.table, scale, prefix=prefix, o=o, lse=lse,
-                    dev_status=pair.status)
+                    dev_status=pair.status, always_share=True)
     return q, o, lse, scale
 
 
@@ -160,10 +160,12 @@ def test_nobody_shares(lib):
     for starts in ([7, 298, 100], None):
         q = bf16(rng, (6, 8, 64)).to(DEV)
         s = None if starts is None else i32(starts)
-        o, lse = pair.gpu.attend(q, offsets(n), s, pair.table, 0.1, prefix=300, dev_status=pair.status)
+        o, lse = pair.gpu.attend(q, offsets(n), s, pair.table, 0.1, prefix=300, dev_status=pair.status,
+                                 always_share=True)
         _check(o, lse, pair, q, n, starts or [0, 0, 0], 0.1)
     o = torch.full((6, 8, 64), 3.0, dtype=torch.bfloat16, device=DEV)
-    pair.gpu.attend(q, offsets([0, 0, 0]), i32([400] * 3), pair.table, 0.1, prefix=300, o=o, dev_status=pair.status)
+    pair.gpu.attend(q, offsets([0, 0, 0]), i32([400] * 3), pair.table, 0.1, prefix=300, o=o, dev_status=pair.status,
+                     always_share=True)
     assert (o == 3).all() and pair.status.item() == 0
 
 
@@ -177,7 +179,7 @@ def test_calls_that_gain_nothing_are_the_plain_one(lib):
         starts = [a - b for a, b in zip(pair.lens, n)]
         q = bf16(rng, (sum(n), 4, 64)).to(DEV)
         args = q, offsets(n), i32(starts), pair.table, 0.125
-        a = pair.gpu.attend(*args, window=window, sinks=4 if window else 0, prefix=prefix)
+        a = pair.gpu.attend(*args, window=window, sinks=4 if window else 0, prefix=prefix, always_share=True)
         b = pair.gpu.attend(*args, window=window, sinks=4 if window else 0)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
@@ -247,7 +249,7 @@ def test_runs_repeat_and_streams_and_graphs_agree(lib):
     q = [bf16(rng, (nseq, H, d)).to(DEV) for _ in range(2)]
     cu, st = offsets(n), i32(starts)
     args = cu, st, pair.table, d ** -0.5
-    want = [pair.gpu.attend(x, *args, prefix=prefix) for x in q]
+    want = [pair.gpu.attend(x, *args, prefix=prefix, always_share=True) for x in q]
     streams = [torch.cuda.Stream() for _ in range(2)]
     for s in streams:
         s.wait_stream(torch.cuda.current_stream())
@@ -255,14 +257,14 @@ def test_runs_repeat_and_streams_and_graphs_agree(lib):
     for _ in range(5):
         for i, s in enumerate(streams):
             with torch.cuda.stream(s):
-                got[i].append(pair.gpu.attend(q[i], *args, prefix=prefix))
+                got[i].append(pair.gpu.attend(q[i], *args, prefix=prefix, always_share=True))
     graphs, outs = [], []
     torch.cuda.synchronize()
     for i, s in enumerate(streams):
         with torch.cuda.stream(s):
             g = torch.cuda.CUDAGraph()
             with torch.cuda.graph(g, stream=s):
-                outs.append(pair.gpu.attend(q[i], *args, prefix=prefix))
+                outs.append(pair.gpu.attend(q[i], *args, prefix=prefix, always_share=True))
             graphs.append(g)
     torch.cuda.synchronize()
     for _ in range(5):
@@ -276,11 +278,11 @@ def test_runs_repeat_and_streams_and_graphs_agree(lib):
     # strided queries, no lse, a workspace of the caller's
     big = torch.zeros(nseq, H + 2, d, dtype=torch.bfloat16, device=DEV)
     big[:, 1:H + 1] = q[0]
-    ws = torch.empty(fl.flamia_attn_cache_prefix_workspace_bytes(nseq, nseq, H, H_kv, d, prefix), dtype=torch.uint8,
-                     device=DEV)
+    ws = torch.empty(fl.flamia_attn_cache_prefix_workspace_bytes(nseq, nseq, H, H_kv, d, prefix, fl.FLAG_PREFIX_ALWAYS),
+                     dtype=torch.uint8, device=DEV)
     o = torch.empty_like(q[0])
     fl.flamia_attn_cache_prefix(pair.gpu, big[:, 1:H + 1], cu, st, pair.table, prefix, d ** -0.5, o, None, ws,
-                                pair.status)
+                                pair.status, fl.FLAG_PREFIX_ALWAYS)
     assert torch.equal(o, want[0][0]) and pair.status.item() == 0
 
 
