@@ -736,6 +736,10 @@ class PagePool:
         self.cache, self.page_table, self.refs = cache, page_table, refs
         self.nseq, self.width = page_table.shape
         self.status = torch.zeros(1, dtype=torch.int32, device=refs.device)
+        self._at = refs.data_ptr(), page_table.data_ptr(), self.status.data_ptr()
+        self._sizes = {}    # workspace bytes by call
+        self._held = []     # workspaces of eager calls, the last one in use
+        self._ws = 0, 0     # its pointer and size
 
     def _begin(self):
         dev, stream = _current()
@@ -743,10 +747,21 @@ class PagePool:
             _elsewhere("pool")
         return dev, stream
 
-    def _workspace(self, size):
-        # (of the call: the allocator hands it on in the stream's order, or keeps it for
-        # the graph that is being captured)
-        return torch.empty(size, dtype=torch.uint8, device=self.refs.device)
+    def _workspace(self, name, *sizes):
+        """(tensor to keep until the call is made, pointer, bytes).  Eager calls follow one
+        another and share one, which is never given back while the pool lives (another
+        stream may be in it); a captured call has one from its graph's pool."""
+        size = self._sizes.get((name, sizes))
+        if size is None:
+            size = self._sizes[name, sizes] = int(getattr(load(), name)(*sizes))
+        if torch._C._cuda_isCurrentStreamCapturing():
+            t = torch.empty(max(1, size), dtype=torch.uint8, device=self.refs.device)
+            return t, t.data_ptr(), size
+        if size > self._ws[1]:
+            t = torch.empty(2 * size, dtype=torch.uint8, device=self.refs.device)
+            self._held.append(t)
+            self._ws = t.data_ptr(), t.nbytes
+        return (None,) + self._ws
 
     def fork(self, parents, children, lens):
         """Sequences children[i] go on from parents[i] (int32 tensors): they give their
@@ -763,12 +778,11 @@ class PagePool:
         lp = _ints(lens, "lens", self.nseq, dev)
         if n == 0:
             return
-        lib = _LIB or load()
-        ws = self._workspace(lib.flamia_pages_fork_workspace_bytes(n, self.width))
-        st = lib.flamia_pages_fork(self.refs.data_ptr(), self.cache.num_pages,
-                                   self.page_table.data_ptr(), self.width, self.nseq,
-                                   self.cache.page_size, pp, cp, n, lp, ws.data_ptr(), ws.nbytes,
-                                   self.status.data_ptr(), stream)
+        refs, table, status = self._at
+        keep, wp, wn = self._workspace("flamia_pages_fork_workspace_bytes", n, self.width)
+        st = (_LIB or load()).flamia_pages_fork(refs, self.cache.num_pages, table, self.width,
+                                                self.nseq, self.cache.page_size, pp, cp, n, lp, wp,
+                                                wn, status, stream)
         if st:
             _check(st, "flamia_pages_fork")
 
@@ -786,12 +800,11 @@ class PagePool:
         sp = _ints(starts, "starts", self.nseq, dev)
         if T is None:
             T = min(1 << 20, self.nseq * self.width * self.cache.page_size)
-        lib = _LIB or load()
-        ws = self._workspace(lib.flamia_pages_reserve_workspace_bytes(T, self.nseq, self.width,
-                                                                      self.cache.page_size))
-        st = lib.flamia_pages_reserve(self.cache._ref, self.refs.data_ptr(),
-                                      self.page_table.data_ptr(), self.width, self.nseq, T, cp, sp,
-                                      ws.data_ptr(), ws.nbytes, self.status.data_ptr(), stream)
+        refs, table, status = self._at
+        keep, wp, wn = self._workspace("flamia_pages_reserve_workspace_bytes", T, self.nseq,
+                                       self.width, self.cache.page_size)
+        st = (_LIB or load()).flamia_pages_reserve(self.cache._ref, refs, table, self.width,
+                                                   self.nseq, T, cp, sp, wp, wn, status, stream)
         if st:
             _check(st, "flamia_pages_reserve")
 
@@ -801,12 +814,11 @@ class PagePool:
         dev, stream = self._begin()
         if live is None:
             live = torch.empty(1, dtype=torch.int32, device=self.refs.device)
-        lib = _LIB or load()
-        ws = self._workspace(lib.flamia_pages_compact_workspace_bytes(self.cache.num_pages))
-        st = lib.flamia_pages_compact(self.cache._ref, self.refs.data_ptr(),
-                                      self.page_table.data_ptr(), self.width, self.nseq,
-                                      _ints(live, "live", 1, dev), ws.data_ptr(), ws.nbytes,
-                                      self.status.data_ptr(), stream)
+        refs, table, status = self._at
+        keep, wp, wn = self._workspace("flamia_pages_compact_workspace_bytes", self.cache.num_pages)
+        st = (_LIB or load()).flamia_pages_compact(self.cache._ref, refs, table, self.width,
+                                                   self.nseq, _ints(live, "live", 1, dev), wp, wn,
+                                                   status, stream)
         if st:
             _check(st, "flamia_pages_compact")
         return live

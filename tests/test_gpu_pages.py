@@ -151,6 +151,25 @@ def test_the_last_user_keeps_a_page(lib):
     both.pool.check_status()
 
 
+@pytest.mark.parametrize("nseq,width", [(129, 4), (40, 130), (128, 32), (127, 33)])
+def test_forks_of_many_slots(lib, nseq, width):
+    """One CTA keeps the rows, or a launch reads and a launch writes them: an order of all
+    sequences, some of them ended and some twice parents."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(nseq)
+    both = Both(fl, rng, nseq * 3 + width, 32, 1, 64, nseq, width)
+    n = rng.integers(0, 65, nseq)
+    n[3] = 32 * width
+    both.append(np.random.default_rng(1), [int(min(x, 40)) if i != 3 else 32 for i, x in enumerate(n)])
+    for _ in range(3):
+        both.fork([int(x) for x in rng.integers(-1, nseq, nseq)], [int(x) for x in rng.permutation(nseq)])
+        both.check()
+        k = nseq // 2
+        both.fork([int(x) for x in rng.integers(0, nseq, k)], [int(x) for x in rng.integers(-1, nseq, k)])
+        both.check()
+    both.pool.check_status()
+
+
 def test_no_free_page_changes_nothing(lib):
     from precision_causal_attention_block_gb300 import flamia as fl
     rng = np.random.default_rng(6)
