@@ -8,6 +8,7 @@ returns an error status, a RuntimeError is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -545,9 +546,24 @@ class _Held(threading.local):
 
     def __init__(self):
         self.ws = {}
+        self.prefix = {}  # of calls with a shared prefix: as large as they were
 
 
 _HELD = _Held()
+
+
+@functools.lru_cache(maxsize=1024)
+def _prefix_bytes(*sizes):
+    return int(load().flamia_attn_cache_prefix_workspace_bytes(*sizes))
+
+
+def _prefix_workspace(dev, stream, size):
+    held = _HELD.prefix.get((dev, stream))
+    if held is None or held[2] < size:
+        # (the one before is the stream's again, behind the calls that use it)
+        t = torch.empty(max(1, size), dtype=torch.uint8, device=torch.device("cuda", dev))
+        held = _HELD.prefix[dev, stream] = t, t.data_ptr(), t.nbytes
+    return held
 
 
 def _eager_workspace(dev, stream):
@@ -664,11 +680,12 @@ def flamia_attn_cache_prefix(cache: KVCache, q, cu_seqlens, starts, page_table, 
     prefix = max(-1, min(prefix, _INT_MAX))  # (as windows: positions end before)
     lib = _LIB or load()
     if ws is None:
-        # (of the call: the allocator hands it on in the stream's order, or keeps it for
-        # the graph that is being captured; a byte for arguments that will be refused)
-        ws = torch.empty(max(1, lib.flamia_attn_cache_prefix_workspace_bytes(
-            T, n, H, cache.H_kv, cache.d, prefix, flags)), dtype=torch.uint8, device=q.device)
-        wp, wn = ws.data_ptr(), ws.nbytes
+        size = _prefix_bytes(T, n, H, cache.H_kv, cache.d, prefix, flags)  # (0: to be refused)
+        if torch._C._cuda_isCurrentStreamCapturing():  # (as in flamia_attn_cache)
+            ws = torch.empty(max(1, size), dtype=torch.uint8, device=q.device)
+            wp, wn = ws.data_ptr(), ws.nbytes
+        else:
+            _, wp, wn = _prefix_workspace(dev, stream, size)
     else:
         wp, wn = _given_workspace(ws, dev)
     st = lib.flamia_attn_cache_prefix(
@@ -736,6 +753,7 @@ class PagePool:
         self.cache, self.page_table, self.refs = cache, page_table, refs
         self.nseq, self.width = page_table.shape
         self.status = torch.zeros(1, dtype=torch.int32, device=refs.device)
+        self.live = torch.zeros(1, dtype=torch.int32, device=refs.device)
         self._at = refs.data_ptr(), page_table.data_ptr(), self.status.data_ptr()
         self._sizes = {}    # workspace bytes by call
         self._held = []     # workspaces of eager calls, the last one in use
@@ -810,10 +828,11 @@ class PagePool:
 
     def compact(self, live=None):
         """Moves the used pages to the front of the pool (page table and refs follow) and
-        returns their number, int32 [1] on the device."""
+        returns their number, int32 [1] on the device (live None: the pool's own tensor,
+        the same in every call)."""
         dev, stream = self._begin()
         if live is None:
-            live = torch.empty(1, dtype=torch.int32, device=self.refs.device)
+            live = self.live
         refs, table, status = self._at
         keep, wp, wn = self._workspace("flamia_pages_compact_workspace_bytes", self.cache.num_pages)
         st = (_LIB or load()).flamia_pages_compact(self.cache._ref, refs, table, self.width,
