@@ -116,13 +116,12 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Two E4M3 codes as FP16 (exact; NaN stays).
-__device__ __forceinline__ uint32_t half2_of_codes(uint32_t codes) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}"
-      : "=r"(h)
+// Four E4M3 codes as FP16 pairs (exact; NaN stays).
+__device__ __forceinline__ void halves_of_codes(uint32_t codes, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(a), "=r"(b)
       : "r"(codes));
-  return h;
 }
 
 // Byte offset of 16-byte chunk j of a row in an FP16 operand tile: blocks of 64
@@ -161,10 +160,7 @@ struct Block32 {
       const uint32_t x[4] = {w[it].x, w[it].y, w[it].z, w[it].w};
       uint32_t h[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[2 * j] = half2_of_codes(x[j] & 0xFFFFu);
-        h[2 * j + 1] = half2_of_codes(x[j] >> 16);
-      }
+      for (int j = 0; j < 4; ++j) halves_of_codes(x[j], h[2 * j], h[2 * j + 1]);
       // (the lanes of a row's second half store the other chunk first: no bank
       // conflicts)
       const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);

@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         sg.hk = hk;
         sg.row0 = rt * R;
         pf = w.start + sg.row0 / g.G;
-        pl = w.start + static_cast<int>(min(static_cast<long long>(w.n) * g.G - 1,
-                                                      static_cast<long long>(sg.row0) + R - 1) /
-                                                  g.G);
+        // (rows of a call are below 2^31)
+        const unsigned last = min(static_cast<unsigned>(w.n) * g.G, static_cast<unsigned>(sg.row0 + R)) - 1;
+        pl = w.start + static_cast<int>(last / g.G);
         hi = over ? g.shared * 128 : max(pl + 1, 0);
         wlo = g.window > 0 ? max(pf - g.window + 1, 0) : 0;
         const bool sharing = KEYS != kAll && !over && shares(g, w.start);

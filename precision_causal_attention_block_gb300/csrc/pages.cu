@@ -464,6 +464,7 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(const CompactArgs g) {
     }
   };
   int mine = 0, live;
+#pragma unroll 4
   for (long long p = 8 * tid; p < g.num_pages; p += 8 * kPlan) {
     int r[8];
     counts(p, r);
