@@ -119,6 +119,54 @@ __device__ __noinline__ void sum_apart(Sum& past, const float* kf, const int* ev
   past.add(sum, top);
 }
 
+// The products of one half: N of them, operands kStep apart, issued by one elected thread that
+// is elected once.  (mma_f16's descriptors, as their low words and one high word.)
+template <int DIM>
+__device__ __forceinline__ void mma_scores(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t hi,
+                                           uint32_t idesc) {
+  static_assert(RowsCfg<DIM>::kBlock / 16 == 1024, "blocks of 64 columns");
+  if constexpr (DIM == 128) {
+    asm volatile(
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+#define FLAMIA_MMA(off, p)                                                  \
+  "add.u32 x, %1, " off ";\n\tadd.u32 y, %2, " off ";\n\t"                 \
+  "mov.b64 da, {x, %3};\n\tmov.b64 db, {y, %3};\n\t"                       \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, " p ";\n\t"
+        FLAMIA_MMA("0", "f") FLAMIA_MMA("2", "t") FLAMIA_MMA("4", "t") FLAMIA_MMA("6", "t")
+        FLAMIA_MMA("1024", "t") FLAMIA_MMA("1026", "t") FLAMIA_MMA("1028", "t")
+        FLAMIA_MMA("1030", "t") "}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, t, f;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\tsetp.ne.b32 f, 0, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t" FLAMIA_MMA("0", "f") FLAMIA_MMA("2", "t")
+            FLAMIA_MMA("4", "t") FLAMIA_MMA("6", "t") "}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc)
+        : "memory");
+#undef FLAMIA_MMA
+  }
+}
+__device__ __forceinline__ void mma_values(uint32_t d_tmem, uint32_t a_tmem, uint32_t b,
+                                           uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, t, p;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+#define FLAMIA_MMA(aoff, boff, p)                                           \
+  "add.u32 x, %1, " aoff ";\n\tadd.u32 y, %2, " boff ";\n\t"               \
+  "mov.b64 db, {y, %3};\n\t"                                               \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %4, " p ";\n\t"
+      FLAMIA_MMA("0", "0", "p") FLAMIA_MMA("8", "128", "t") FLAMIA_MMA("16", "256", "t")
+      FLAMIA_MMA("24", "384", "t") "}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+#undef FLAMIA_MMA
+}
+
 // This warp's 32 query rows as FP16 numbers x 2^-e into rows row0 .. of an operand tile, and
 // their factors; d / 8 lanes a row, four loads ahead.  (Rolled: code that runs once comes from
 // L2, and with all 16 steps side by side an item's queries took 12,000 cycles.)
@@ -576,11 +624,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1)
       auto issue_s = [&](int y, int h) {
         const uint32_t b = k0 + (y & 1) * kStep + h * (8192 / 16);
         __syncwarp();
-#pragma unroll
-        for (int ks = 0; ks < DIM / 16; ++ks) {
-          const uint32_t at = (ks >> 2) * (C::kBlock / 16) + (ks & 3) * 2;
-          mma_f16(t_s + h * 64, q0 + at, b + at, hi, id_s, ks > 0);
-        }
+        mma_scores<DIM>(t_s + h * 64, q0, b, hi, id_s);
         tc_commit_w(smem_u32(&sm.s_full[w][h]));
         if (h == 1) tc_commit_w(smem_u32(&sm.k_empty[y & 1]));
         __syncwarp();
@@ -613,10 +657,7 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1)
           tc_fence_after();
           __syncwarp();
           const uint32_t b = v0 + (y & 1) * kStep + h * (8192 / 16);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16_ts(t_o, t_s + h * 64 + ks * 8, b + ks * (2048 / 16), hi, id_o,
-                       j > 0 || ks > 0);
+          mma_values(t_o, t_s + h * 64, b, hi, id_o, j > 0);
           tc_commit_w(smem_u32(&sm.pv_done[w][h]));
           if (h == 1) tc_commit_w(smem_u32(&sm.v_empty[y & 1]));
           __syncwarp();
