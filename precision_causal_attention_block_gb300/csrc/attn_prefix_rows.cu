@@ -33,7 +33,6 @@ struct Smem {
   alignas(16) float kf[4][128];   // 2^eK, eV of each key: a ring of four tiles, as
   alignas(16) int ev[4][128];     // the softmax is done two score products later
   Keys32 col[4][4];
-  float qf[kR];                   // a row's 2^e x softmax scale x log2 e
   Sum past[kR];                   // sum 2^(x + nref) of what is not in a row's l
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], sc_full[4];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by row tile and half
@@ -167,69 +166,76 @@ __device__ __forceinline__ void mma_values(uint32_t d_tmem, uint32_t a_tmem, uin
 #undef FLAMIA_MMA
 }
 
-// This warp's 32 query rows as FP16 numbers x 2^-e into rows row0 .. of an operand tile, and
-// their factors; d / 8 lanes a row, four loads ahead.  (Rolled: code that runs once comes from
-// L2, and with all 16 steps side by side an item's queries took 12,000 cycles.)
+// This warp's 32 query rows as FP16 numbers x 2^-e into rows row0 .. of an operand tile: copied
+// to their place by 16-byte chunks, d / 8 lanes a row, then each lane converts its own row
+// there.  Returns the lane's row's factor.  (Instructions set the pace: with rows worked
+// out anew in every step and maxima across lanes an item's queries took 11,000 cycles.)
 template <int DIM>
-__device__ __forceinline__ void load_queries(const AttendArgs& g, int hk, int first, int rows,
-                                             int row0, uint32_t tile, float* qf, int lane) {
-  constexpr int kLanes = DIM / 8, kPer = 32 / kLanes, kIters = 32 / kPer, kAhead = 4;
-  const int sub = lane / kLanes, c = lane % kLanes;
-  int i = (first + row0 + sub) / g.G, h = first + row0 + sub - i * g.G;
-#pragma unroll 1
-  for (int it0 = 0; it0 < kIters; it0 += kAhead) {
-    uint4 w[kAhead];
-#pragma unroll
-    for (int m = 0; m < kAhead; ++m) {
-      w[m] = make_uint4(0, 0, 0, 0);
-      if (row0 + (it0 + m) * kPer + sub < rows)
-        w[m] = *reinterpret_cast<const uint4*>(
-            g.q + i * g.q_stride + static_cast<long long>(hk * g.G + h) * DIM + c * 8);
-      h += kPer;
-      while (h >= g.G) {
-        h -= g.G;
-        ++i;
-      }
-    }
-#pragma unroll 1
-    for (int m = 0; m < kAhead; ++m) {
-      uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-      for (int n = 0; n + 1 < kAhead; ++n) w[n] = w[n + 1];
-      // magnitudes as integers; 0x7F80 and above: infinities and NaN, which become NaN and
-      // stay out of the maximum
-      uint32_t a = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
-                            __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
-      a = max(a & 0xFFFFu, a >> 16);
-      if (a >= 0x7F80u) {
-        a = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if ((x[j] & 0x7F80u) == 0x7F80u)
-            x[j] = (x[j] & 0xFFFF0000u) | 0x7FC0u;
-          else
-            a = max(a, x[j] & 0x7FFFu);
-          if ((x[j] & 0x7F800000u) == 0x7F800000u)
-            x[j] = (x[j] & 0xFFFFu) | 0x7FC00000u;
-          else
-            a = max(a, (x[j] >> 16) & 0x7FFFu);
-        }
-      }
-#pragma unroll
-      for (int off = kLanes / 2; off > 0; off >>= 1)
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
-      const int ex = roundup_exponent(__uint_as_float(a << 16));
-      const float2 inv = make_float2(exp2i(-ex), exp2i(-ex));
-      uint32_t y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        y[j] = half2_of(__fmul2_rn(
-            make_float2(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u)), inv));
-      const int r = (it0 + m) * kPer + sub;
-      sts128(tile + tile_at<DIM>((row0 & 127) + r, c), make_uint4(y[0], y[1], y[2], y[3]));
-      if (c == 0) qf[row0 + r] = g.scale_log2 * (ex < -126 ? 0x1p-127f : exp2i(ex));
+__device__ __forceinline__ float load_queries(const AttendArgs& g, int hk, int first, int rows,
+                                              int row0, uint32_t tile, int lane) {
+  constexpr int kLanes = DIM / 8, kPer = 32 / kLanes;
+  const int sub = lane / kLanes, c = lane % kLanes, in = row0 & 127;
+  const int i = (first + row0 + sub) / g.G;
+  int h = first + row0 + sub - i * g.G;
+  const __nv_bfloat16* src =
+      g.q + i * g.q_stride + static_cast<long long>(hk * g.G + h) * DIM + c * 8;
+  const long long step = g.q_stride - static_cast<long long>(g.G) * DIM;  // to the next token
+#pragma unroll 2
+  for (int r = sub; r < 32; r += kPer) {
+    const bool there = row0 + r < rows;
+    copy16(tile + tile_at<DIM>(in + r, c), there ? src : g.q, there ? 16 : 0);
+    src += kPer * DIM;
+    h += kPer;
+    while (h >= g.G) {
+      h -= g.G;
+      src += step;
     }
   }
+  copies_wait();
+  __syncwarp();
+  // magnitudes as integers; 0x7F80 and above: infinities and NaN, which become NaN and stay
+  // out of the maximum
+  const int r = in + lane;
+  uint32_t a = 0;
+#pragma unroll 4
+  for (int c = 0; c < DIM / 8; ++c) {
+    const uint4 w = lds128(tile + tile_at<DIM>(r, c));
+    a = __vmaxu2(a, __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                             __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu)));
+  }
+  a = max(a & 0xFFFFu, a >> 16);
+  if (a >= 0x7F80u) {
+    a = 0;
+#pragma unroll 1
+    for (int e = 0; e < DIM / 2; ++e) {
+      const uint32_t at = tile + tile_at<DIM>(r, e >> 2) + (e & 3) * 4;
+      uint32_t w = lds32(at);
+      if ((w & 0x7F80u) == 0x7F80u)
+        w = (w & 0xFFFF0000u) | 0x7FC0u;
+      else
+        a = max(a, w & 0x7FFFu);
+      if ((w & 0x7F800000u) == 0x7F800000u)
+        w = (w & 0xFFFFu) | 0x7FC00000u;
+      else
+        a = max(a, (w >> 16) & 0x7FFFu);
+      sts32(at, w);
+    }
+  }
+  const int ex = roundup_exponent(__uint_as_float(a << 16));
+  const float2 inv = make_float2(exp2i(-ex), exp2i(-ex));
+#pragma unroll 4
+  for (int c = 0; c < DIM / 8; ++c) {
+    const uint32_t at = tile + tile_at<DIM>(r, c);
+    const uint4 w = lds128(at);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      y[j] = half2_of(__fmul2_rn(
+          make_float2(__uint_as_float(ww[j] << 16), __uint_as_float(ww[j] & 0xFFFF0000u)), inv));
+    sts128(at, make_uint4(y[0], y[1], y[2], y[3]));
+  }
+  return g.scale_log2 * (ex < -126 ? 0x1p-127f : exp2i(ex));
 }
 
 template <int DIM>
@@ -388,13 +394,13 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1)
       const int nt = pc.i1 - pc.i0, first = pc.rt * kR;
       const int rows = min(kR, n_rows - first);
       const bool active = wg == 0 || rows > 128;
+      float qf = 0.f;  // the row's 2^e x softmax scale x log2 e
       if (active) {
-        load_queries<DIM>(g, pc.hk, first, rows, warp * 32, smem_u32(sm.q[wg]), sm.qf, lane);
+        qf = load_queries<DIM>(g, pc.hk, first, rows, warp * 32, smem_u32(sm.q[wg]), lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[wg]));
       }
-      const float qf = active ? sm.qf[r] : 0.f;
       float l = 0.f, nref = 0.f;  // nref: -reference
       bool has = false;           // the row has a reference
       bool large = false;         // some row's of the warp is beyond kLarge
