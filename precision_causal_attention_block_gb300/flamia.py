@@ -833,11 +833,11 @@ class PagePool:
         dev, stream = self._begin()
         if live is None:
             live = self.live
+        lp = _ints(live, "live", 1, dev)
         refs, table, status = self._at
         keep, wp, wn = self._workspace("flamia_pages_compact_workspace_bytes", self.cache.num_pages)
         st = (_LIB or load()).flamia_pages_compact(self.cache._ref, refs, table, self.width,
-                                                   self.nseq, _ints(live, "live", 1, dev), wp, wn,
-                                                   status, stream)
+                                                   self.nseq, lp, wp, wn, status, stream)
         if st:
             _check(st, "flamia_pages_compact")
         return live
@@ -993,23 +993,24 @@ class DecodeCall:
     them in place.
 
     pool: the step begins with pages for its tokens (PagePool.reserve) and takes the
-    pool's page table.  prefix: the sequences begin with the same so many tokens, read
-    once for all of them (KVCache.attend)."""
+    pool's page table.  prefix, always_share: the sequences begin with the same so many
+    tokens, read once for all of them (KVCache.attend)."""
 
     def __init__(self, cache: KVCache, T: int, nseq: int, H: int, softmax_scale: float,
                  rope: Rotary = None, window: int = 0, sinks: int = 0, pool: PagePool = None,
-                 prefix: int = 0):
+                 prefix: int = 0, always_share: bool = False):
         if pool is not None and (pool.cache is not cache or pool.nseq != nseq):
             raise RuntimeError("pool: expected one over this cache with a row a sequence")
         dev = cache.k_codes.device
         self.cache, self.T, self.H, self.scale = cache, T, H, float(softmax_scale)
         self.rope, self.window, self.sinks = rope, int(window), int(sinks)
-        self.pool, self.prefix = pool, int(prefix)
+        self.pool, self.prefix, self.always_share = pool, int(prefix), bool(always_share)
         self.o = torch.empty((T, H, cache.d), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((H, T), dtype=torch.float32, device=dev)
         size = (flamia_attn_cache_workspace_bytes(T, nseq, H, cache.H_kv, cache.d)
                 if self.window or not self.prefix else
-                flamia_attn_cache_prefix_workspace_bytes(T, nseq, H, cache.H_kv, cache.d, self.prefix))
+                flamia_attn_cache_prefix_workspace_bytes(T, nseq, H, cache.H_kv, cache.d, self.prefix,
+                                                         FLAG_PREFIX_ALWAYS if always_share else 0))
         self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         if rope is not None:
@@ -1032,7 +1033,7 @@ class DecodeCall:
         self.cache.write(k, v, cu_seqlens, starts, page_table, dev_status=self.status)
         self.cache.attend(q, cu_seqlens, starts, page_table, self.scale, self.window, self.sinks,
                           o=self.o, lse=self.lse, ws=self.ws, dev_status=self.status,
-                          prefix=self.prefix)
+                          prefix=self.prefix, always_share=self.always_share)
         return self.o
 
     def check_status(self):
