@@ -157,6 +157,13 @@ __device__ __forceinline__ bool shares(const AttendArgs& g, int start) {
   return start >= g.prefix - 1;
 }
 
+// Its pages may be read for all: it has new tokens, and positions inside its table row.
+__device__ __forceinline__ bool reads_for_all(const AttendArgs& g, int b) {
+  const DocRange r = doc_range(g.cu, b, g.T);
+  const int start = g.starts != nullptr ? g.starts[b] : 0;
+  return r.e > r.s && shares(g, start) && start <= g.cap - (r.e - r.s);
+}
+
 // Entry v of the work list: the prefix, or a sequence.
 template <int KEYS>
 __device__ __forceinline__ bool of_prefix(int v) {
@@ -256,8 +263,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     if (tid == 0) sm.sharer = g.ndocs;
     __syncthreads();
     for (int b = b0; b < b1; ++b) {
-      const DocRange r = doc_range(g.cu, b, g.T);
-      if (r.e > r.s && g.starts != nullptr && shares(g, g.starts[b])) {
+      if (reads_for_all(g, b)) {
         atomicMin(&sm.sharer, b);
         break;
       }

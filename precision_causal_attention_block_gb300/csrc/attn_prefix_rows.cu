@@ -279,9 +279,8 @@ __global__ void __launch_bounds__(Cfg<DIM>::kThreads, 1)
   check_offsets(g.cu, g.ndocs, g.T, static_cast<long long>(blockIdx.x) * C::kThreads + tid,
                 static_cast<long long>(gridDim.x) * C::kThreads, g.status);
   // the first sequence that shares the prefix: its pages are read
-  for (int b = tid; b < g.ndocs && g.starts != nullptr; b += C::kThreads) {
-    const DocRange r = doc_range(g.cu, b, g.T);
-    if (shares(g, g.starts[b]) && r.e > r.s) {
+  for (int b = tid; b < g.ndocs; b += C::kThreads) {
+    if (reads_for_all(g, b)) {
       atomicMin(&sm.sharer, b);
       break;
     }

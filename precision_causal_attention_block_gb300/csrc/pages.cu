@@ -116,8 +116,8 @@ flamia_status launch_copy(CopyArgs& g, const flamia_kvcache* from, const flamia_
   g.to_pages = to->num_pages;
   g.blocks = (from->page_size + kCopyRows - 1) / kCopyRows;
   // (2 x 4096 x 2^14 blocks at most: an int)
-  const long long per = 2ll * g.H_kv * g.blocks;
-  long long ctas = (most * per * 32 + kCopyThreads - 1) / kCopyThreads;
+  const long long units = most * (2ll * g.H_kv * g.blocks);
+  long long ctas = units / (kCopyThreads / 32) + 1;
   const long long remap = (g.entries + kCopyThreads - 1) / kCopyThreads;
   if (ctas < remap) ctas = remap;
   const long long cap = 16ll * num_sms();

@@ -317,3 +317,23 @@ def test_more_sequences_than_threads(lib):
     q, o, lse, scale = _run(fl, pair, rng, 2, n, starts, prefix)
     assert pair.status.item() == 0
     _check(o, lse, pair, q, n, starts, scale)
+
+
+@pytest.mark.parametrize("nseq,H", [(5, 2), (30, 8)])
+def test_a_sequence_outside_its_row_spoils_no_other(lib, nseq, H):
+    """The first sequence stands behind its table row: it is reported, and the pages of the
+    next one are read for the others."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(8)
+    prefix = 300
+    pair = Forked(fl, rng, prefix, [5 + b for b in range(nseq)], 64, 1, 64)
+    n, starts = [1] * nseq, [x - 1 for x in pair.lens]
+    pair.share([0] + n[1:], starts)
+    pair.table[0] = -1
+    starts[0] = 64 * pair.t.shape[1]
+    q, o, lse, scale = _run(fl, pair, rng, H, n, starts, prefix)
+    assert pair.status.item() == fl.DEV_BAD_PAGE
+    for b in range(1, nseq):
+        k, v = pair.k.values(b), pair.v.values(b)
+        ref, _ = S.attend(q[b:b + 1].double().cpu().numpy(), k, v, starts[b], scale)
+        assert np.abs(o[b:b + 1].double().cpu().numpy() - ref).max() <= 2.0 ** -7 * np.abs(v).max()
