@@ -6,7 +6,7 @@
 // out by itself as a mean of values o_i with log2 of its sum of weights, lg_i:
 //   lg = log2 sum 2^lg_i,   o = sum 2^(lg_i - lg) o_i.
 //
-// Up to 64 query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
+// Up to 32 query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
 // kernels over items of both kinds.  More: the kernel of attn_cache_rows.cu over the prefix
 // (no masks: all rows see all of it), then attn_cache.cu's over what comes behind it.
 // In both cases a last kernel joins what they leave: float32 rows of items that
@@ -214,23 +214,23 @@ __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int ro
 struct Forms {
   int prefix, rest;
 };
-// 256 rows an item beyond 64 in the batch (heads of 128, 32,768 shared, 64 rows 64 us with 32
-// an item and 68 with 256, 96 rows 78 and 68; heads of 64, 32 rows 118 and 146, 64 rows
-// 232 and 168).
+// 256 rows an item beyond 32 in the batch (16,384 shared: heads of 128, 16 of them, 40 rows
+// 75.5 us with 32 an item and 69.8 with 256, 64 rows 95 and 82, 8 heads 64 rows 45.4 and
+// 46.5; heads of 64, 24 rows 77 and 82, 40 rows 129 and 91, 64 rows 164 and 112).
 // What sharing saves is the reading of the prefix by every sequence but one, at some 10 TB/s,
 // as the L2 cache serves most of that; what it costs is the join and, with 256 rows, a
 // launch and the larger items.  So it is done from so many bytes on.  Shared against plain,
-// us, below and above: 8 rows 18.3 (plain) and 20.5 at 15 MB, 21.9 and 20.5 at 59; 16 rows 27.9
-// and 28.8 at 101 MB, 39.9 and 36.5 at 203; 32 rows 34.8 and 35.8 at 194 MB, 38.6 and 36.5 at
-// 237; 256 rows 41.2 and 44.7 at 262 MB, 66.1 and 60.0 at 532.
+// us, below and above: 8 rows 18.4 and 18.0 at 25 MB, 19.7 and 21.1 at 51; 16 rows 23.4 and
+// 21.1 at 51 MB, 20.7 and 30.0 at 127; 32 rows 30.6 and 27.4 at 118 MB, 36.0 and 38.5 at
+// 237; 256 rows 41.8 and 40.9 at 262 MB, 43.5 and 50.7 at 389.
 Forms forms(int T, int ndocs, int G, int H_kv, int d, int prefix, int flags) {
   const int rest = rows_per_item(mean_rows(T, ndocs, G));
   // nothing to share; or every sequence fills a tensor-core operand by itself
   if (ndocs < 2 || prefix < 128 || prefix > kMaxPos || rest == kManyRows) return Forms{0, 0};
   const long long rows = static_cast<long long>(T) * G;
-  const int all = rows > 64 ? kManyRows : rows_per_item(rows);
+  const int all = rows > 32 ? kManyRows : rows_per_item(rows);
   const double saved = (ndocs - 1.) * (prefix / 128 * 128) * H_kv * 2. * (d + 1);
-  const double least = all == 8 ? 45e6 : all == 16 ? 120e6 : all == 32 ? 200e6 : 350e6;
+  const double least = all == 8 ? 40e6 : all == 16 ? 80e6 : all == 32 ? 150e6 : 300e6;
   if (saved < least && !(flags & FLAMIA_FLAG_PREFIX_ALWAYS)) return Forms{0, 0};
   return Forms{all, all == kManyRows ? rest : all};
 }

@@ -84,11 +84,15 @@ def _run(fl, pair, rng, H, n, starts, prefix, T=None, scale=None, q=None):
     # 9 .. 16; 4 and 8 rows a sequence
     (8, 2, 128, 32, 517, [9, 1, 260], [1, 1, 1]),
     (8, 1, 64, 128, 640, [300, 2], [1, 1]),
-    # 32 rows: 20 and 96, sequences of 4, 9 and 32
+    # 32 rows: 20, 17 and 32, sequences of 4, 1, 8 and 16
     (16, 4, 128, 256, 1291, [17, 400, 3, 90, 1], [1] * 5),
+    (2, 2, 64, 64, 700, [1 + 30 * (i % 5) for i in range(17)], [1] * 17),
+    (8, 1, 64, 128, 515, [1, 300, 44, 7], [1] * 4),
+    (8, 2, 128, 32, 4000, [4, 200], [4, 4]),
+    # 256 rows: 33, 69, 96, 97, 128, 200, 256, 260 and 520 of them, one to 32 a sequence
+    (1, 1, 128, 32, 400, [1 + i for i in range(33)], [1] * 33),
     (3, 1, 64, 32, 257, [6, 3, 37, 90, 4, 3, 11, 21], [3, 3, 3, 2, 4, 3, 3, 3]),
     (8, 1, 128, 64, 384, [4, 130, 20], [4, 4, 4]),
-    # 256 rows: 97, 128, 200, 256, 260 and 520 of them, one to 32 a sequence
     (1, 1, 128, 64, 260, [1 + i % 7 for i in range(97)], [1] * 97),
     (16, 2, 64, 32, 700, [1 + 9 * i for i in range(16)], [1] * 16),
     (40, 5, 128, 128, 555, [1 + 3 * i for i in range(25)], [1] * 25),
