@@ -99,6 +99,10 @@ def _run(fl, pair, rng, H, n, starts, prefix, T=None, scale=None, q=None):
     (8, 1, 128, 256, 512, [1 + 40 * (i % 5) for i in range(32)], [1] * 32),
     (4, 1, 64, 64, 1023, [5 + i for i in range(13)], [5] * 13),
     (8, 2, 128, 32, 129, [8 + 17 * i for i in range(17)], [8, 7, 8, 8, 8, 6, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8]),
+    # runs of the work split that hold whole items, two to three of them
+    (16, 16, 128, 32, 140, [1 + i for i in range(34)], [1] * 34),
+    (8, 8, 64, 64, 300, [1 + i % 9 for i in range(40)], [1] * 40),
+    (64, 8, 128, 64, 270, [1 + 5 * (i % 6) for i in range(38)], [1] * 38),
 ])
 @pytest.mark.parametrize("token", [False, True])
 def test_against_the_oracle(lib, H, H_kv, d, page, prefix, own, n, token):
