@@ -42,7 +42,8 @@ struct Parts {
     n = any ? w.n & ~kShares : 0;
     cta = w.at & 0xFFFF;
     row = (w.at >> 16) & (R - 1);
-    if (cta >= kMaxCtas || n < 0 || n > kMaxCtas - cta) n = 0;
+    const int ctas = R == kManyRows ? kRowsCtas : kMaxCtas;
+    if (cta >= ctas || n < 0 || n > ctas - cta) n = 0;
   }
   __device__ __forceinline__ size_t slot(int p) const {
     return static_cast<size_t>(p == 0 ? 2 * cta + 1 : 2 * (cta + p));

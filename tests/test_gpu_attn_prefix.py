@@ -345,3 +345,30 @@ def test_a_sequence_outside_its_row_spoils_no_other(lib, nseq, H):
         k, v = pair.k.values(b), pair.v.values(b)
         ref, _ = S.attend(q[b:b + 1].double().cpu().numpy(), k, v, starts[b], scale)
         assert np.abs(o[b:b + 1].double().cpu().numpy() - ref).max() <= 2.0 ** -7 * np.abs(v).max()
+
+
+@pytest.mark.parametrize("nseq,H", [(5, 2), (5, 8), (7, 16)])
+def test_rows_of_no_sequence(lib, nseq, H):
+    """Offsets that begin behind the first rows are reported; whatever the workspace held for
+    those rows, the others' results are right."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(nseq + H)
+    prefix, own, H_kv, d = 300, [3 + 40 * b for b in range(nseq)], 1, 64
+    pair = Forked(fl, rng, prefix, own, 64, H_kv, d)
+    n, gap = [1] * nseq, 3
+    starts = [x - 1 for x in pair.lens]
+    pair.share(n, starts)
+    T = nseq + gap
+    q = bf16(rng, (T, H, d)).to(DEV)
+    o, lse = (torch.full(s, 7.0, dtype=t, device=DEV)
+              for s, t in (((T, H, d), torch.bfloat16), ((H, T), torch.float32)))
+    size = fl.flamia_attn_cache_prefix_workspace_bytes(T, nseq, H, H_kv, d, prefix,
+                                                       fl.FLAG_PREFIX_ALWAYS)
+    # records of parts beyond the last CTA of 256 rows an item; then of no CTA at all
+    for at, parts in ((320, 100 | 1 << 30), (511, 1 << 30 | 1), (-1, -1)):
+        ws = i32([at, parts]).repeat((size + 7) // 8).view(torch.uint8)[:size]
+        pair.status.zero_()
+        pair.gpu.attend(q, offsets(n) + gap, i32(starts), pair.table, d ** -0.5, prefix=prefix, o=o,
+                        lse=lse, ws=ws, dev_status=pair.status, always_share=True)
+        assert pair.status.item() == 1
+        _check(o[gap:], lse[:, gap:], pair, q[gap:], n, starts, d ** -0.5)
