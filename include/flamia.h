@@ -603,14 +603,19 @@ flamia_status flamia_pages_fork(int32_t* refs, int num_pages, int32_t* page_tabl
  * whose positions lie outside its row gets none.
  * cu_seqlens and starts as for flamia_cache_write (cu_seqlens may end before T).
  * T == 0 enqueues nothing.
+ *  granted    device int32[nseq + 1], not cu_seqlens, or NULL: the offsets for the step's
+ *             other calls.  cu_seqlens, or zeros if there were not as many pages or a
+ *             sequence's positions lie outside its row: with those the calls do nothing, where with
+ *             cu_seqlens they would write into pages that other sequences hold as well.
  *  ws         flamia_pages_reserve_workspace_bytes(T, nseq, table_stride, page_size)
  *             bytes, 256-byte aligned.
  */
 size_t flamia_pages_reserve_workspace_bytes(int T, int nseq, int table_stride, int page_size);
 flamia_status flamia_pages_reserve(const flamia_kvcache* cache, int32_t* refs,
                                    int32_t* page_table, int table_stride, int nseq, int T,
-                                   const int32_t* cu_seqlens, const int32_t* starts, void* ws,
-                                   size_t ws_bytes, int* dev_status, void* stream);
+                                   const int32_t* cu_seqlens, const int32_t* starts,
+                                   int32_t* granted, void* ws, size_t ws_bytes, int* dev_status,
+                                   void* stream);
 
 /*
  * Moves the pages in use to the front of the pool: with `live` of them, the k-th used

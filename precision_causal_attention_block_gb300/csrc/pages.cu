@@ -297,6 +297,7 @@ struct Slot {
 struct ReserveArgs {
   int32_t *refs, *table;
   const int32_t *cu, *starts;
+  int32_t* granted;  // [nseq + 1]
   Slot* slots;     // [cap]
   int32_t* rank;   // [cap]: which of the new pages a slot takes, -1: none
   int32_t* fresh;  // [cap]: the new pages
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g) {
   // the slots, in order of sequence and position (a sequence's first two by its own
   // thread; those of longer ones by the whole warp)
   int n = 0;
+  bool outside = false;  // some sequence's positions are, of its row
   auto put = [&](int b, int slot, int at) {
     if (at >= g.cap) return;  // (cannot be: see reserve_slots)
     const int page = g.table[static_cast<long long>(b) * g.stride + slot];
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g) {
         const long long last = (static_cast<long long>(start) + (r.e - r.s) - 1) / g.page_size;
         if (start < 0 || last >= g.stride) {
           report(g.status, FLAMIA_DEV_BAD_PAGE);  // (none of the sequence's)
+          outside = true;
         } else {
           first = start / g.page_size;
           cnt = static_cast<int>(last) - first + 1;
@@ -437,8 +440,10 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g) {
       g.refs[s.page] = 1;  // kept
     }
   }
-  __syncthreads();
+  outside = __syncthreads_or(outside);
   if (tid == 0) *g.count = s_copies;
+  if (g.granted != nullptr)
+    for (int i = tid; i <= g.nseq; i += kPlan) g.granted[i] = enough && !outside ? g.cu[i] : 0;
 }
 
 struct CompactArgs {
@@ -657,14 +662,15 @@ extern "C" size_t flamia_pages_reserve_workspace_bytes(int T, int nseq, int tabl
 extern "C" flamia_status flamia_pages_reserve(const flamia_kvcache* cache, int32_t* refs,
                                               int32_t* page_table, int table_stride, int nseq,
                                               int T, const int32_t* cu_seqlens,
-                                              const int32_t* starts, void* ws, size_t ws_bytes,
-                                              int* dev_status, void* stream) {
+                                              const int32_t* starts, int32_t* granted, void* ws,
+                                              size_t ws_bytes, int* dev_status, void* stream) {
   const flamia_status st = check_cache(cache);
   if (st != FLAMIA_OK) return st;
   if (!valid_pool(cache->num_pages, cache->page_size, nseq, table_stride) || !valid_batch(T, nseq))
     return FLAMIA_ERR_INVALID_ARG;
   if (T == 0) return FLAMIA_OK;
-  if (!valid_books(refs, page_table) || cu_seqlens == nullptr || ws == nullptr || !aligned(ws, 256))
+  if (!valid_books(refs, page_table) || cu_seqlens == nullptr || ws == nullptr ||
+      !aligned(ws, 256) || !aligned(granted, 4) || granted == cu_seqlens)
     return FLAMIA_ERR_INVALID_ARG;
   ReserveArgs g{};
   g.nseq = nseq;
@@ -674,6 +680,7 @@ extern "C" flamia_status flamia_pages_reserve(const flamia_kvcache* cache, int32
   g.table = page_table;
   g.cu = cu_seqlens;
   g.starts = starts;
+  g.granted = granted;
   g.status = dev_status;
   g.T = T;
   g.stride = table_stride;

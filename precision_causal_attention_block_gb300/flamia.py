@@ -89,7 +89,7 @@ SIGNATURES = {
     "flamia_pages_fork_workspace_bytes": (_sz, [_i, _i]),
     "flamia_pages_fork": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp, _vp]),
     "flamia_pages_reserve_workspace_bytes": (_sz, [_i, _i, _i, _i]),
-    "flamia_pages_reserve": (_i, [_CP, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "flamia_pages_reserve": (_i, [_CP, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     "flamia_pages_compact_workspace_bytes": (_sz, [_i]),
     "flamia_pages_compact": (_i, [_CP, _vp, _vp, _i, _i, _vp, _vp, _sz, _vp, _vp]),
     "flamia_cache_write": (_i, [_CP, _vp, _i64, _vp, _i64, _i, _vp, _i, _vp, _vp, _i, _i, _vp,
@@ -808,21 +808,25 @@ class PagePool:
         """The sequences' pages are given back and their lengths become 0."""
         self.fork(None, sequences, lens)
 
-    def reserve(self, cu_seqlens, starts, T: int = None):
+    def reserve(self, cu_seqlens, starts, T: int = None, granted=None):
         """Pages for the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 at positions
         starts[b] .. of every sequence: what is missing is taken from the free pages, and
         a page with other users is replaced by a copy.  T: an upper bound of the number
-        of tokens (None: one that every table row could hold)."""
+        of tokens (None: one that every table row could hold).  granted: int32 [nseq + 1]
+        that becomes cu_seqlens, or zeros if pages ran out or positions lie outside the
+        table, for the calls that write to the pages."""
         dev, stream = self._begin()
         cp = _ints(cu_seqlens, "cu_seqlens", self.nseq + 1, dev)
         sp = _ints(starts, "starts", self.nseq, dev)
+        gp = _ints(granted, "granted", self.nseq + 1, dev)
         if T is None:
             T = min(1 << 20, self.nseq * self.width * self.cache.page_size)
         refs, table, status = self._at
         keep, wp, wn = self._workspace("flamia_pages_reserve_workspace_bytes", T, self.nseq,
                                        self.width, self.cache.page_size)
         st = (_LIB or load()).flamia_pages_reserve(self.cache._ref, refs, table, self.width,
-                                                   self.nseq, T, cp, sp, wp, wn, status, stream)
+                                                   self.nseq, T, cp, sp, gp, wp, wn, status,
+                                                   stream)
         if st:
             _check(st, "flamia_pages_reserve")
 
@@ -993,7 +997,8 @@ class DecodeCall:
     them in place.
 
     pool: the step begins with pages for its tokens (PagePool.reserve) and takes the
-    pool's page table.  prefix, always_share: the sequences begin with the same so many
+    pool's page table; where it cannot have them it does nothing more (check_status), as
+    other sequences may hold the pages that it would write to.  prefix, always_share: the sequences begin with the same so many
     tokens, read once for all of them (KVCache.attend)."""
 
     def __init__(self, cache: KVCache, T: int, nseq: int, H: int, softmax_scale: float,
@@ -1013,6 +1018,7 @@ class DecodeCall:
                                                          FLAG_PREFIX_ALWAYS if always_share else 0))
         self.ws = torch.empty(size, dtype=torch.uint8, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.granted = None if pool is None else torch.zeros(nseq + 1, dtype=torch.int32, device=dev)
         if rope is not None:
             self.q = torch.empty((T, H, cache.d), dtype=torch.bfloat16, device=dev)
             self.k = torch.empty((T, cache.H_kv, cache.d), dtype=torch.bfloat16, device=dev)
@@ -1024,7 +1030,8 @@ class DecodeCall:
         if (page_table is None) != (self.pool is not None):
             raise RuntimeError("page_table: needed without a pool, and only then")
         if self.pool is not None:
-            self.pool.reserve(cu_seqlens, starts, self.T)
+            self.pool.reserve(cu_seqlens, starts, self.T, self.granted)
+            cu_seqlens = self.granted
             page_table = self.pool.page_table
         if self.rope is not None:
             q, k = self.rope(q, k, cu_seqlens, starts if self.rope.axes is None else None,

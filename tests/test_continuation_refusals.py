@@ -84,12 +84,12 @@ def test_pages_reserve(env):
     need = lib.flamia_pages_reserve_workspace_bytes(10, 4, 8, 64)
     assert need > 0
     c = lambda **kw: ctypes.byref(_cache(fl, at, **kw))
-    a = dict(c=c(), refs=at, table=at, stride=8, nseq=4, T=10, cu=at, starts=None, ws=at, size=need, st=None, s=None)
+    a = dict(c=c(), refs=at, table=at, stride=8, nseq=4, T=10, cu=at, starts=None, granted=None, ws=at, size=need, st=None, s=None)
     run = lambda **kw: _call(lib.flamia_pages_reserve, a, kw)
     assert run(T=0) == OK and run(T=0, cu=None, ws=None) == OK
     for kw in (dict(c=None), dict(refs=None), dict(refs=at + 1), dict(table=None), dict(stride=0), dict(nseq=0),
                dict(nseq=65537), dict(T=-1), dict(T=(1 << 20) + 1), dict(cu=None), dict(ws=None), dict(ws=at + 4),
-               dict(c=c(num_pages=0))):
+               dict(c=c(num_pages=0)), dict(granted=at), dict(granted=at + 2)):
         assert run(**kw) == INVALID, kw
     assert run(size=need - 1) == WORKSPACE and run(c=c(d=32)) == UNSUPPORTED
     for args in ((-1, 4, 8, 64), (10, 0, 8, 64), (10, 4, 0, 64), (10, 4, 8, 0), (1 << 21, 4, 8, 64)):
@@ -201,6 +201,7 @@ def test_the_binding_s_page_calls(monkeypatch):
     pool.fork(i(0), i(0), i(2))  # nothing to do
     for bad in (lambda: pool.fork(i(3), i(2), i(2)), lambda: pool.fork(i(0), i(2), i(2)), lambda: pool.fork(i(2), i(2), i(3)),
                 lambda: pool.fork(i(2).long(), i(2), i(2)), lambda: pool.reserve(i(2), i(2)), lambda: pool.reserve(i(3), i(3)),
+                lambda: pool.reserve(i(3), i(2), 5, i(2)),
                 lambda: pool.compact(i(2)), lambda: fl.flamia_pages_copy(cache, cache, i(2), i(3)),
                 lambda: fl.flamia_pages_copy(cache, cache, i(0), i(3))):
         with pytest.raises(RuntimeError):

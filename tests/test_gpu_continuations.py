@@ -163,3 +163,52 @@ def test_training_call_with_axes(lib):
     assert torch.equal(call.o, o2) and torch.equal(call.lse, lse2) and torch.equal(dv, dv2)
     dq2, dk2 = rot(dq2, dk2, cu, positions=pos, inverse=True)
     assert torch.equal(dq, dq2) and torch.equal(dk, dk2)
+
+
+@pytest.mark.parametrize("far", [False, True])
+def test_a_step_without_its_pages_does_nothing(lib, far):
+    """Two continuations share a half-filled page.  A step for which there is no page left (or
+    with a sequence behind its row) leaves pages, books and outputs as they are and says so;
+    with pages it goes on from there."""
+    from precision_causal_attention_block_gb300 import flamia as fl
+    rng = np.random.default_rng(7)
+    H, H_kv, d, page, prompt, nseq = 4, 2, 64, 64, 160, 3
+    cache = fl.KVCache(3 if not far else 9, page, H_kv, d)
+    pool = fl.PagePool(cache, nseq, 4)
+    lens = torch.zeros(nseq, dtype=torch.int32, device=DEV)
+    cu = offsets([prompt, 0, 0])
+    pool.reserve(cu, lens)
+    x = bf16(rng, (prompt, H_kv, d)).to(DEV)
+    cache.write(x, x, cu, lens, pool.page_table)
+    lens[0] = prompt
+    pool.fork(i32([0]), i32([1]), lens)
+    call = fl.DecodeCall(cache, 3, nseq, H, d ** -0.5, rope=fl.Rotary(fl.rope_frequencies(d)), pool=pool)
+    cu = offsets([1, 1, 1])
+    starts = lens.clone()
+    if far:
+        starts[2] = 4 * page
+    else:
+        cu[3] = 2
+    q, k, v = (bf16(rng, (3, h, d), 50.0).to(DEV) for h in (H, H_kv, H_kv))
+    call.o.fill_(7)
+    call.lse.fill_(7)
+    held = [t.clone() for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)]
+    table = pool.page_table.clone()
+    call(q, k, v, cu, starts)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="0x10" if far else "0x2$"):
+        call.check_status()
+    assert (call.o == 7).all() and (call.lse == 7).all() and (call.granted == 0).all()
+    if far:  # (the books keep what the others took)
+        assert torch.equal(pool.page_table[2], table[2])
+        assert set(pool.page_table[:2].flatten().tolist()) == set(table[0].tolist()) | {3}
+    else:
+        assert torch.equal(pool.page_table, table)
+        assert all(map(torch.equal, held, (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)))
+    # one of the two alone has pages enough, after the other has gone
+    pool.release(i32([1]), lens)
+    pool.status.zero_()
+    call(q, k, v, offsets([1, 0, 0]), lens)
+    call.check_status()
+    assert torch.equal(call.granted, offsets([1, 0, 0]))
+    assert (call.o[0] != 7).any() and (call.o[1:] == 7).all()
