@@ -645,7 +645,13 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
   } else {
     // ------------------------------------------------------------ softmax
     constexpr int RW = C::kRows;
-    const int half = C::kHalves == 1 ? 0 : warp >> 2, r0 = half * RW;     // this thread's rows r0 ..
+    // This thread's rows: eight from r0 on, and with 32 an item eight from r0 + 16 on if it
+    // has any there.  (A row is a column of the products, and nothing else depends on what stays
+    // in one without a row.  131,072 keys shared by 24 rows of 32 heads of 64: 265 -> 221
+    // us; 16,384 by 32 rows of 16 heads of 128: 61.7 -> 62.6.  The same for the first eight
+    // costs 16 rows an item 55 -> 58 us.)
+    constexpr int kNext = 8 * C::kHalves;
+    const int half = C::kHalves == 1 ? 0 : warp >> 2, r0 = half * 8;
     const int key_in = tid & 127;                   // its key inside a tile
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     auto vote = [&](bool p) { return softmax_vote<C::kSoftmax>(p); };
@@ -697,6 +703,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full));
       }
       sync();  // row tables
+      auto has_rows = [&](int c) { return c == 0 || r0 + c < rows; };
       float2 l[RW / 2];
 #pragma unroll
       for (int r = 0; r < RW / 2; ++r) l[r] = make_float2(0.f, 0.f);
@@ -707,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           float s = r & 1 ? l[r / 2].y : l[r / 2].x;
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          if (lane == 0) sm.red[warp & 3][r0 + r] = s;
+          if (lane == 0) sm.red[warp & 3][r0 + r / 8 * kNext + r % 8] = s;
         }
       };
       auto sum_of = [&](int r) {
@@ -812,7 +819,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         if (t > 0) {
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < RW; c += 8) {
+          for (int c = 0; c < R; c += kNext) {
+            if (!has_rows(c)) break;
             float2 y[4];
             scores(c, y);
 #pragma unroll
@@ -848,7 +856,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           }
           const bool apart = low < e0 - kLow;
 #pragma unroll 1
-          for (int c = 0; c < RW; c += 8) {
+          for (int c = 0; c < R; c += kNext) {
+            if (!has_rows(c)) break;
             float2 y[4];
             scores(c, y);
 #pragma unroll
@@ -902,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           large = sm.large;
 #pragma unroll
           for (int r = 0; r < RW; r += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(sm.fac + r0 + r);
+            const float4 f = *reinterpret_cast<const float4*>(sm.fac + r0 + r / 8 * kNext + r % 8);
             l[r / 2] = __fmul2_rn(l[r / 2], make_float2(f.x, f.y));
             l[r / 2 + 1] = __fmul2_rn(l[r / 2 + 1], make_float2(f.z, f.w));
           }
@@ -911,14 +920,15 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
               fail();
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 3 * RW; c += 8) {
-              const int col = c / RW * R + r0 + c % RW;
+            for (int c = 0; c < 3 * R; c += kNext) {
+              const int in = r0 + c % R, col = c + r0;
+              if (R == 32 && in >= rows) continue;
               uint32_t a[8];
               tmem_ld8(tmem + lanes + C::kColO + col, a);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                a[i] = __float_as_uint(__uint_as_float(a[i]) * sm.fac[r0 + c % RW + i]);
+                a[i] = __float_as_uint(__uint_as_float(a[i]) * sm.fac[in + i]);
               tmem_st8(tmem + lanes + C::kColO + col, a);
             }
             tmem_st_wait();
@@ -932,7 +942,9 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         const float gl = ev < e0 - kLow ? 0.f : exp2i(e0 - ev);
         const float2 g2 = make_float2(gl, gl);
 #pragma unroll
-        for (int c = 0; c < RW; c += 8) {
+        for (int c = 0; c < R; c += kNext) {
+          if (!has_rows(c)) break;
+          const int at8 = c / kNext * 4;  // in l
           float2 y[4];
           scores(c, y);
           if (!whole && sm.nan[buf][key_in]) {
@@ -954,8 +966,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
           for (int r = 0; r < 8; r += 4) {
             float2 a = make_float2(ex2_approx(y[r / 2].x), ex2_approx(y[r / 2].y));
             float2 b = make_float2(ex2_approx(y[r / 2 + 1].x), ex2_approx(y[r / 2 + 1].y));
-            l[(c + r) / 2] = __ffma2_rn(a, g2, l[(c + r) / 2]);
-            l[(c + r) / 2 + 1] = __ffma2_rn(b, g2, l[(c + r) / 2 + 1]);
+            l[at8 + r / 2] = __ffma2_rn(a, g2, l[at8 + r / 2]);
+            l[at8 + r / 2 + 1] = __ffma2_rn(b, g2, l[at8 + r / 2 + 1]);
             if constexpr (C::kHalfWeights) {
               uint32_t ha = half2_of(a), hb = half2_of(b);
               tw[0][r / 4] = take_term(ha, hb);
@@ -1023,7 +1035,8 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
       sync();
       const bool active = DIM == 128 || key_in < DIM;
 #pragma unroll
-      for (int c = 0; c < RW; c += 8) {
+      for (int c = 0; c < R; c += kNext) {
+        if (!has_rows(c)) break;
         uint32_t h[8], m[8], lo[8];
         if (nt > 0) {
           const uint32_t at = tmem + lanes + C::kColO + r0 + c;
