@@ -64,81 +64,93 @@ __device__ __forceinline__ float max_or_nan(float m, float x) {
 __device__ __forceinline__ float half_weight(float stat, float ref) {
   return exp2f(0.5f * (stat - ref));
 }
-__device__ __forceinline__ void add4(float (&acc)[4], float w, const float* x) {
-  const float4 v = *reinterpret_cast<const float4*>(x);
+// What is summed so far, when the reference goes from m to m1 (of nothing: nothing).
+__device__ __forceinline__ float rescale(float m, float m1) {
+  return m == -INFINITY ? 0.f : half_weight(m, m1);
+}
+__device__ __forceinline__ void add4(float (&acc)[4], float w, const float4& v) {
   acc[0] = fmaf(w, w * v.x, acc[0]);
   acc[1] = fmaf(w, w * v.y, acc[1]);
   acc[2] = fmaf(w, w * v.z, acc[2]);
   acc[3] = fmaf(w, w * v.w, acc[3]);
 }
+__device__ __forceinline__ uint2 mean4(const float (&acc)[4], float inv) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[0] * inv,
+                                                 inv == 0.f ? 0.f : acc[1] * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[2] * inv,
+                                                 inv == 0.f ? 0.f : acc[3] * inv);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
 
-// One launch: a warp a row (token and query head), four elements a lane (d = 64: two rows
-// of parts side by side).
+// Both joins wait for memory: the values of 32 (8) parts are loaded beside their statistics,
+// before the weights are known, and the reference moves from batch to batch.
+//
+// One launch: four warps a row (token and query head), four elements a lane, parts by turns
+// (d = 64: two of a warp's side by side).
+constexpr int kJoinWarps = 4;
 template <int DIM>
-__global__ void __launch_bounds__(256) join_few_kernel(const JoinArgs g) {
-  constexpr int kLanes = DIM / 4, kSide = 32 / kLanes;
-  const int lane = threadIdx.x & 31;
-  const int own = blockIdx.x * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(32 * kJoinWarps) join_few_kernel(const JoinArgs g) {
+  constexpr int kLanes = DIM / 4, kTurns = 32 / kLanes * kJoinWarps;
+  __shared__ float4 s_acc[kTurns][kLanes];
+  const int lane = threadIdx.x & 31, own = blockIdx.x;
+  const int turn = threadIdx.x / kLanes, e = lane % kLanes;
   wait_for_previous();
-  if (own >= g.T * g.H) return;
   const int t = own / g.H, h = own - t * g.H;
   const int end = g.cu[g.ndocs];
   const RowParts wr = g.rest.where[own], wp = g.prefix.where[own];
   if (t >= end) return;
   const Parts pr(wr, true, g.rest.R), pp(wp, (wr.n & kShares) != 0, g.prefix.R);
   const int parts = pp.n + pr.n;
-  auto stat = [&](int p) {
-    return p < pp.n ? pp.stat(g.prefix, p, own) : pr.stat(g.rest, p - pp.n, own);
-  };
-  const float first = lane < parts ? stat(lane) : -INFINITY;
-  float m = first;
-  for (int p = 32 + lane; p < parts; p += 32) m = max_or_nan(m, stat(p));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float ref = m == -INFINITY ? 0.f : m;
-  const int side = lane / kLanes, e = (lane % kLanes) * 4;
-  float l = 0.f, acc[4] = {};
+  float m = -INFINITY, l = 0.f, acc[4] = {};
   for (int p0 = 0; p0 < parts; p0 += 32) {
-    const float wt =
-        p0 + lane < parts ? half_weight(p0 == 0 ? first : stat(p0 + lane), ref) : 0.f;
-    l = fmaf(wt, wt, l);
-    const int n = min(32, parts - p0);
-#pragma unroll 4
-    for (int p = 0; p < n; p += kSide) {
-      const float w = __shfl_sync(0xffffffffu, wt, p + side);  // (behind the last part: 0)
-      const int q = min(p0 + p + side, parts - 1);
-      add4(acc, w,
-           (q < pp.n ? pp.data(g.prefix, q, own, DIM) : pr.data(g.rest, q - pp.n, own, DIM)) + e);
+    float4 v[32 / kTurns];
+#pragma unroll
+    for (int j = 0; j < 32 / kTurns; ++j) {
+      const int q = p0 + j * kTurns + turn;
+      v[j] = q >= parts ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : reinterpret_cast<const float4*>(
+                              q < pp.n ? pp.data(g.prefix, q, own, DIM)
+                                       : pr.data(g.rest, q - pp.n, own, DIM))[e];
     }
+    const int p = p0 + lane;
+    const float x = p >= parts ? -INFINITY
+                               : p < pp.n ? pp.stat(g.prefix, p, own) : pr.stat(g.rest, p - pp.n, own);
+    float m1 = max_or_nan(m, x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m1 = max_or_nan(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+    const float ref = m1 == -INFINITY ? 0.f : m1, f = rescale(m, ref);
+    const float wt = half_weight(x, ref);  // (behind the last part: 0)
+    l = fmaf(wt, wt, f * f * l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = f * (f * acc[i]);
+#pragma unroll
+    for (int j = 0; j < 32 / kTurns; ++j)
+      add4(acc, __shfl_sync(0xffffffffu, wt, j * kTurns + turn), v[j]);
+    m = m1;
   }
+  s_acc[turn][e] = make_float4(acc[0], acc[1], acc[2], acc[3]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (kSide == 2) {
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  float sum[4] = {};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 16);
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (lane == 0 && g.lse != nullptr)
-    g.lse[static_cast<size_t>(h) * g.T + t] = (ref + log2f(l)) * kLn2;
-  if (side == 0) {
-    __nv_bfloat162 b[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      b[i] = __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[2 * i] * inv,
-                                   inv == 0.f ? 0.f : acc[2 * i + 1] * inv);
-    *reinterpret_cast<uint2*>(g.o + static_cast<size_t>(own) * DIM + e) =
-        make_uint2(*reinterpret_cast<uint32_t*>(&b[0]), *reinterpret_cast<uint32_t*>(&b[1]));
-  }
+  for (int j = 0; j < kTurns; ++j) add4(sum, 1.f, s_acc[j][e]);
+  if (threadIdx.x == 0 && g.lse != nullptr)
+    g.lse[static_cast<size_t>(h) * g.T + t] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+  *reinterpret_cast<uint2*>(g.o + static_cast<size_t>(own) * DIM + e * 4) =
+      mean4(sum, l == 0.f ? 0.f : 1.f / l);
 }
 
-// Two launches: a thread a row and 8 elements, the rows those of an item over the prefix,
-// as its parts lie [slot][d / 4][256 rows][4].  Loads of four parts at a time.
+// Two launches: a thread a row and 4 elements, the rows those of an item over the prefix,
+// as its parts lie [slot][d / 4][256 rows][4].
 template <int DIM>
 __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int row_tiles) {
+  constexpr int kBatch = 8;
   const int hk = blockIdx.x / row_tiles;
   const int row = (blockIdx.x - hk * row_tiles) * 256 + threadIdx.x;
   const int t = row / g.G, h = hk * g.G + row - t * g.G;
-  const int c = blockIdx.y * 8;
+  const int c = blockIdx.y;
   wait_for_previous();
   if (t >= g.T) return;
   const int own = t * g.H + h;
@@ -147,66 +159,44 @@ __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int ro
   if (t >= end) return;
   const Parts pr(wr, true, g.rest.R), pp(wp, (wr.n & kShares) != 0, 256);
   const int parts = pp.n + pr.n;
-  auto stat = [&](int p) {
-    return p >= parts ? -INFINITY
-                      : p < pp.n ? pp.stat(g.prefix, p, own) : pr.stat(g.rest, p - pp.n, own);
-  };
-  float m = -INFINITY;
+  float m = -INFINITY, l = 0.f, acc[4] = {};
 #pragma unroll 1
-  for (int p = 0; p < parts; p += 8) {
-    float x[8];
+  for (int p = 0; p < parts; p += kBatch) {
+    float x[kBatch], m1 = m;
+    float4 v[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = stat(p + i);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_or_nan(m, x[i]);
-  }
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[2][4] = {};
-#pragma unroll 1
-  for (int p = 0; p < parts; p += 4) {
-    float x[4], v[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       const int q = p + i;
-      x[i] = stat(q);
-      const float* at = nullptr;
-      int step = 4;
+      x[i] = -INFINITY;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (q < pp.n) {
-        at = pp.n > 1 ? g.prefix.partial + (pp.slot(q) * (DIM / 4) + c / 4) * 1024 + pp.row * 4
-                      : g.prefix.rows + static_cast<size_t>(own) * DIM + c;
-        step = pp.n > 1 ? 1024 : 4;
+        x[i] = pp.stat(g.prefix, q, own);
+        v[i] = reinterpret_cast<const float4*>(
+            pp.n > 1 ? g.prefix.partial + (pp.slot(q) * (DIM / 4) + c) * 1024 + pp.row * 4
+                     : g.prefix.rows + static_cast<size_t>(own) * DIM + c * 4)[0];
       } else if (q < parts) {
-        at = pr.data(g.rest, q - pp.n, own, DIM) + c;
+        x[i] = pr.stat(g.rest, q - pp.n, own);
+        v[i] = reinterpret_cast<const float4*>(pr.data(g.rest, q - pp.n, own, DIM))[c];
       }
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-      if (at != nullptr) {
-        a = *reinterpret_cast<const float4*>(at);
-        b = *reinterpret_cast<const float4*>(at + step);
-      }
-      v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
-      v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kBatch; ++i) m1 = max_or_nan(m1, x[i]);
+    const float ref = m1 == -INFINITY ? 0.f : m1, f = rescale(m, ref);
+    l *= f * f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = f * (f * acc[e]);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
       const float w = half_weight(x[i], ref);  // (behind the last part: 0)
       l = fmaf(w, w, l);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e / 4][e % 4] = fmaf(w, w * v[i][e], acc[e / 4][e % 4]);
+      add4(acc, w, v[i]);
     }
+    m = m1;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   if (c == 0 && g.lse != nullptr)
-    g.lse[static_cast<size_t>(h) * g.T + t] = (ref + log2f(l)) * kLn2;
-  uint32_t b[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v =
-        __floats2bfloat162_rn(inv == 0.f ? 0.f : acc[i / 2][i % 2 * 2] * inv,
-                              inv == 0.f ? 0.f : acc[i / 2][i % 2 * 2 + 1] * inv);
-    b[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  *reinterpret_cast<uint4*>(g.o + static_cast<size_t>(own) * DIM + c) =
-      make_uint4(b[0], b[1], b[2], b[3]);
+    g.lse[static_cast<size_t>(h) * g.T + t] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+  *reinterpret_cast<uint2*>(g.o + static_cast<size_t>(own) * DIM + c * 4) =
+      mean4(acc, l == 0.f ? 0.f : 1.f / l);
 }
 
 // ------------------------------------------------------------------ host
@@ -272,9 +262,9 @@ Layout layout(void* ws, const Forms& f, int T, int H, int d) {
 template <int DIM>
 bool launch_join_prefix(const JoinArgs& a, int H_kv, cudaStream_t s) {
   if (a.prefix.R != kManyRows)
-    return launch_after(join_few_kernel<DIM>, dim3((a.T * a.H + 7) / 8), 256, 0, s, a);
+    return launch_after(join_few_kernel<DIM>, dim3(a.T * a.H), 32 * kJoinWarps, 0, s, a);
   const int row_tiles = static_cast<int>((static_cast<long long>(a.T) * a.G + 255) / 256);
-  return launch_after(join_many_kernel<DIM>, dim3(row_tiles * H_kv, DIM / 8), 256, 0, s, a,
+  return launch_after(join_many_kernel<DIM>, dim3(row_tiles * H_kv, DIM / 4), 256, 0, s, a,
                       row_tiles);
 }
 
