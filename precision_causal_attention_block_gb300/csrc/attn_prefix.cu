@@ -6,8 +6,8 @@
 // out by itself as a mean of values o_i with log2 of its sum of weights, lg_i:
 //   lg = log2 sum 2^lg_i,   o = sum 2^(lg_i - lg) o_i.
 //
-// Up to 32 query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
-// kernels over items of both kinds.  More: the kernel of attn_cache_rows.cu over the prefix
+// Few query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
+// kernels over items of both kinds.  Many: the kernel of attn_cache_rows.cu over the prefix
 // (no masks: all rows see all of it), then attn_cache.cu's over what comes behind it.
 // In both cases a last kernel joins what they leave: float32 rows of items that
 // were not cut and the parts of those that were (equal runs of key tiles for all CTAs, as
@@ -205,23 +205,26 @@ __global__ void __launch_bounds__(256) join_many_kernel(const JoinArgs g, int ro
 struct Forms {
   int prefix, rest;
 };
-// 256 rows an item beyond 32 in the batch (16,384 shared: heads of 128, 16 of them, 40 rows
-// 75.5 us with 32 an item and 69.8 with 256, 64 rows 95 and 82, 8 heads 64 rows 45.4 and
-// 46.5; heads of 64, 24 rows 77 and 82, 40 rows 129 and 91, 64 rows 164 and 112).
+// Beyond 32 rows in the batch 256 an item, with 8 an item over the rest, or 32 in both where
+// there is little to do: up to 64 rows, counted in key tiles (two for what is a sequence's own).
+// 32 against 256 an item, us, heads of 128, 16,384 shared: 4 of them, 40 rows 26.5 and 39.4;
+// 8, 36 rows 35.8 and 41.6, 64 rows 40.5 and 40.8; 16, 40 rows 71 and 70, 64 rows 93 and 83.
+// 2,048 shared: 16 heads, 64 rows 52.8 and 54.6; 32 heads of 64, 40 rows 63 and 55.
 // What sharing saves is the reading of the prefix by every sequence but one, at some 10 TB/s,
 // as the L2 cache serves most of that; what it costs is the join and, with 256 rows, a
 // launch and the larger items.  So it is done from so many bytes on.  Shared against plain,
-// us, below and above: 8 rows 18.4 and 18.0 at 25 MB, 19.7 and 21.1 at 51; 16 rows 23.4 and
-// 21.1 at 51 MB, 20.7 and 30.0 at 127; 32 rows 30.6 and 27.4 at 118 MB, 36.0 and 38.5 at
-// 237; 256 rows 41.8 and 40.9 at 262 MB, 43.5 and 50.7 at 389.
+// us, below and above: 8 rows 16.6 and 16.6 at 7.5 MB, 17.0 and 18.1 at 14.8; 16 rows 19.3 and
+// 19.0 at 16 MB, 17.9 and 19.0 at 23; 32 rows 30.8 and 29.9 at 65 MB, 33.5 and 35.5 at
+// 131; 256 rows 50.9 and 45.5 at 266 MB, 55.4 and 61.4 at 401.
 Forms forms(int T, int ndocs, int G, int H_kv, int d, int prefix, int flags) {
   const int rest = rows_per_item(mean_rows(T, ndocs, G));
   // nothing to share; or every sequence fills a tensor-core operand by itself
   if (ndocs < 2 || prefix < 128 || prefix > kMaxPos || rest == kManyRows) return Forms{0, 0};
   const long long rows = static_cast<long long>(T) * G;
-  const int all = rows > 32 ? kManyRows : rows_per_item(rows);
+  const bool little = rows <= 64 && H_kv * (2ll * (prefix / 128) + 2ll * ndocs) <= 2560;
+  const int all = rows <= 32 ? rows_per_item(rows) : little ? 32 : kManyRows;
   const double saved = (ndocs - 1.) * (prefix / 128 * 128) * H_kv * 2. * (d + 1);
-  const double least = all == 8 ? 40e6 : all == 16 ? 80e6 : all == 32 ? 150e6 : 300e6;
+  const double least = all == 8 ? 10e6 : all == 16 ? 20e6 : all == 32 ? 100e6 : 300e6;
   if (saved < least && !(flags & FLAMIA_FLAG_PREFIX_ALWAYS)) return Forms{0, 0};
   return Forms{all, all == kManyRows ? rest : all};
 }

@@ -89,7 +89,8 @@ def _run(fl, pair, rng, H, n, starts, prefix, T=None, scale=None, q=None):
     (2, 2, 64, 64, 700, [1 + 30 * (i % 5) for i in range(17)], [1] * 17),
     (8, 1, 64, 128, 515, [1, 300, 44, 7], [1] * 4),
     (8, 2, 128, 32, 4000, [4, 200], [4, 4]),
-    # 256 rows: 33, 69, 96, 97, 128, 200, 256, 260 and 520 of them, one to 32 a sequence
+    # 33 rows (two items of 32), and with 256 an item 69, 96, 97, 128, 200, 256, 260 and 520,
+    # one to 32 a sequence
     (1, 1, 128, 32, 400, [1 + i for i in range(33)], [1] * 33),
     (3, 1, 64, 32, 257, [6, 3, 37, 90, 4, 3, 11, 21], [3, 3, 3, 2, 4, 3, 3, 3]),
     (8, 1, 128, 64, 384, [4, 130, 20], [4, 4, 4]),
@@ -103,6 +104,10 @@ def _run(fl, pair, rng, H, n, starts, prefix, T=None, scale=None, q=None):
     (16, 16, 128, 32, 140, [1 + i for i in range(34)], [1] * 34),
     (8, 8, 64, 64, 300, [1 + i % 9 for i in range(40)], [1] * 40),
     (64, 8, 128, 64, 270, [1 + 5 * (i % 6) for i in range(38)], [1] * 38),
+    (32, 16, 64, 32, 140, [1 + i for i in range(36)], [1] * 36),
+    (16, 8, 128, 64, 300, [1 + i % 9 for i in range(35)], [1] * 35),
+    # 33 .. 64 rows with 256 an item: many heads
+    (40, 40, 64, 32, 300, [1 + i % 40 for i in range(33)], [1] * 33),
 ])
 @pytest.mark.parametrize("token", [False, True])
 def test_against_the_oracle(lib, H, H_kv, d, page, prefix, own, n, token):
