@@ -13,10 +13,11 @@
 // Measured: 89 tokens of 32 query and 8 K / V heads of 128 (356 rows a head) over 16,384 keys,
 // 41 to 45 us with the launch and the set-up; the bytes alone (34 MB) take 5, the products 13 at
 // the burst rate.  The tensor pipe is busy 30% of the time and the schedulers issue in 46% of
-// the cycles: a row tile's softmax (two of 256 rows, or one of the 100 that are left) is the
-// chain, behind it the conversion of the codes, which an item with one row tile pays in full.
-// Sharing that one tile's keys between both softmax warpgroups was slower (batch of 96 81.7
-// -> 86.7 us: twice the parts to join, and the converters set the pace).
+// the cycles.  Clock stamps: a half of a row tile takes its softmax warps 2,150 cycles (scores
+// 350, weights 500, their stores 390, waits 250), a block of K or V its converters 2,050 (1,090
+// of them to convert and store it, 700 until it is there), whatever the rows: the two chains
+// are equally long.  One row tile's keys shared between both softmax warpgroups was slower
+// (batch of 96 81.7 -> 86.7 us: the converters, and twice the parts to join).
 //
 // Warps 0-3 and 4-7: softmax of the two row tiles (thread = row = TMEM lane); 8-11:
 // converters, a 32-key block each; 12 and 13: MMA issuers of the row tiles.
