@@ -8,17 +8,17 @@
 // in ascending order by (sequence, slot), counts are sums, and of the users of a page
 // that all want to write it the last in order keeps it.  Books are small (4 bytes a page
 // and a table entry), so one CTA works them out between barriers of its own; what it
-// decides is left as a list of copies for a second kernel on the whole GPU.
+// decides is left as a list of copies for a second kernel on the whole GPU, or, if these are
+// few, copied by itself.
 //
-// That one is HBM-bound: a warp takes up to 64 rows of one head of K or V (8 or 4 KB),
+// Copies are HBM-bound: a warp takes up to 64 rows of one head of K or V (8 or 4 KB),
 // all its loads before its stores.  4,099 pages of 64 tokens, 8 heads of 128 (1.08 GB both
 // ways): 160 us, 6.8 TB/s; 7 small pages: 2.1 us on the device, 10 with the host's call.
 //
 // The books are chains of dependent loads between a CTA's barriers: fork of 8 rows of 9 slots
-// with the pages of their next tokens 10.5 us on the device (three kernels), of 192 rows of
-// 128 slots 5 + 4 us and 10 for the pages; compact of 5,451 pages, half of them in use, 8
-// us beside 52 for its copies.  The host's calls of small ones take longer than the device; a
-// captured step has neither.
+// with the pages of their next tokens 13 us on the device (two kernels) and 20 with the host's
+// calls, of 192 rows of 128 slots 5 + 4 us and 10 for the pages; compact of 5,451 pages, half
+// of them in use, 8 us beside 52 for its copies.
 #include "paged.cuh"
 
 namespace flamia {
@@ -43,27 +43,27 @@ struct CopyArgs {
   const int* live;
   int32_t* table;
   long long entries;
-  int n, H_kv, page_size, from_pages, to_pages, blocks;  // blocks of kCopyRows a page
+  int n, H_kv, page_size, from_pages, to_pages;
 };
 
-template <int DIM>
-__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs g) {
-  constexpr int kPer = kCopyRows * DIM / 16 / 32;  // 16-byte pieces a lane
+// Table entries of moved pages, by the warp's lanes.
+__device__ __forceinline__ void renumber(const CopyArgs& g, int live, long long warp0,
+                                         long long warps) {
   const int lane = threadIdx.x & 31;
-  const long long warps = static_cast<long long>(gridDim.x) * (kCopyThreads / 32);
-  const long long warp0 =
-      static_cast<long long>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5);
-  start_next();
-  wait_for_previous();
-  if (g.moved != nullptr) {
-    const int live = *g.live;
-    for (long long i = warp0 * 32 + lane; i < g.entries; i += warps * 32) {
-      const int p = g.table[i];
-      if (p >= live && p < g.from_pages) g.table[i] = g.moved[p];
-    }
+  for (long long i = warp0 * 32 + lane; i < g.entries; i += warps * 32) {
+    const int p = g.table[i];
+    if (p >= live && p < g.from_pages) g.table[i] = g.moved[p];
   }
-  const int n = g.count != nullptr ? *g.count : g.n;
-  const int per = 2 * g.H_kv * g.blocks;  // units of a page: K / V, head, block of rows
+}
+
+// n entries, units of ROWS rows of a page's head (K or V) by warps in turn.
+template <int DIM, int ROWS>
+__device__ __forceinline__ void copy_units(const CopyArgs& g, int n, long long warp0,
+                                           long long warps) {
+  constexpr int kPer = ROWS * DIM / 16 / 32;  // 16-byte pieces a lane
+  const int lane = threadIdx.x & 31;
+  const int blocks = (g.page_size + ROWS - 1) / ROWS;
+  const int per = 2 * g.H_kv * blocks;  // units of a page: K / V, head, block of rows
   const long long units = static_cast<long long>(n) * per;
   for (long long u = warp0; u < units; u += warps) {
     const int i = static_cast<int>(u / per);
@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs g) {
       if (lane == 0) report(g.status, FLAMIA_DEV_BAD_PAGE);
       continue;
     }
-    const int kv = at >= g.H_kv * g.blocks;
-    at -= kv * g.H_kv * g.blocks;
-    const int h = at / g.blocks, r0 = (at - h * g.blocks) * kCopyRows;
-    const int rows = min(min(e.z, g.page_size) - r0, kCopyRows);
+    const int kv = at >= g.H_kv * blocks;
+    at -= kv * g.H_kv * blocks;
+    const int h = at / blocks, r0 = (at - h * blocks) * ROWS;
+    const int rows = min(min(e.z, g.page_size) - r0, ROWS);
     if (rows <= 0) continue;
     const long long from = (static_cast<long long>(e.x) * g.H_kv + h) * g.page_size + r0;
     const long long to = (static_cast<long long>(e.y) * g.H_kv + h) * g.page_size + r0;
@@ -106,9 +106,19 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs g) {
   }
 }
 
-// `most`: as many entries as there can be.
-flamia_status launch_copy(CopyArgs& g, const flamia_kvcache* from, const flamia_kvcache* to,
-                          long long most, cudaStream_t s) {
+template <int DIM>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CopyArgs g) {
+  const long long warps = static_cast<long long>(gridDim.x) * (kCopyThreads / 32);
+  const long long warp0 =
+      static_cast<long long>(blockIdx.x) * (kCopyThreads / 32) + (threadIdx.x >> 5);
+  start_next();
+  wait_for_previous();
+  if (g.moved != nullptr) renumber(g, *g.live, warp0, warps);
+  copy_units<DIM, kCopyRows>(g, g.count != nullptr ? *g.count : g.n, warp0, warps);
+}
+
+// All of the arguments but the entries.
+void copy_args(CopyArgs& g, const flamia_kvcache* from, const flamia_kvcache* to) {
   g.from[0] = from->k_codes;
   g.from[1] = from->v_codes;
   g.from[2] = from->k_scales;
@@ -121,15 +131,18 @@ flamia_status launch_copy(CopyArgs& g, const flamia_kvcache* from, const flamia_
   g.page_size = from->page_size;
   g.from_pages = from->num_pages;
   g.to_pages = to->num_pages;
-  g.blocks = (from->page_size + kCopyRows - 1) / kCopyRows;
+}
+
+// `most`: as many entries as there can be.
+flamia_status launch_copy(const CopyArgs& g, int d, long long most, cudaStream_t s) {
   // (2 x 4096 x 2^14 blocks at most: an int)
-  const long long units = most * (2ll * g.H_kv * g.blocks);
+  const long long units = most * (2ll * g.H_kv * ((g.page_size + kCopyRows - 1) / kCopyRows));
   long long ctas = units / (kCopyThreads / 32) + 1;
   const long long remap = (g.entries + kCopyThreads - 1) / kCopyThreads;
   if (ctas < remap) ctas = remap;
   const long long cap = 16ll * num_sms();
   if (ctas > cap) ctas = cap;
-  return launch_after(from->d == 128 ? copy_kernel<128> : copy_kernel<64>,
+  return launch_after(d == 128 ? copy_kernel<128> : copy_kernel<64>,
                       dim3(static_cast<unsigned>(ctas < 1 ? 1 : ctas)), kCopyThreads, 0, s, g)
              ? FLAMIA_OK
              : FLAMIA_ERR_CUDA;
@@ -259,6 +272,19 @@ __global__ void __launch_bounds__(kSmallThreads) fork_small_kernel(const ForkArg
 
 // ------------------------------------------------------------------ books
 
+// The CTA that keeps the books makes their copies itself if these can be no more than so many
+// bytes.  That saves a launch: reserve of a step that copies nothing, as most do, 5.7 us and not
+// 7.5, captured 3.7 and not 4.9.  But copies by one CTA take longer: with fork, 4 of at most
+// 162 KB 19.1 us and not 21.8, captured 11.9 and not 11.0; 8 of 292 KB 19.1 and 21.8, 13.8
+// and 11.1; 16 of 552 KB 19.9 and 21.9, 17.2 and 10.9; 32 of 1,072 KB 26.2 and 21.4, 24.7
+// and 11.5; compact of at most 471 KB 18.7 and 20.7, 12.5 and 8.8.
+constexpr long long kOwnBytes = 512 << 10;
+constexpr long long kOwnEntries = 1 << 15;  // of the page table, that compact numbers anew
+constexpr int kOwnRows = 32;  // rows a warp copies then (1,024 threads: 64 registers)
+bool makes_copies(const flamia_kvcache* c, long long most) {
+  return most * 2 * c->H_kv * c->page_size * (c->d + 1) <= kOwnBytes;
+}
+
 // Exclusive prefix of x over the CTA's threads, and their sum.  (Two barriers; scratch
 // may be used again at once.)
 __device__ __forceinline__ int cta_prefix(int x, int* scratch, int& total) {
@@ -314,7 +340,8 @@ struct ReserveArgs {
   int T, nseq, stride, num_pages, page_size, cap;
 };
 
-__global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g) {
+template <int DIM>  // 0: the copies are left to a second kernel
+__global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g, const CopyArgs c) {
   __shared__ int scratch[32];
   __shared__ int s_copies;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -451,6 +478,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g) {
   if (tid == 0) *g.count = s_copies;
   if (g.granted != nullptr)
     for (int i = tid; i <= g.nseq; i += kPlan) g.granted[i] = enough && !outside ? g.cu[i] : 0;
+  if constexpr (DIM > 0) copy_units<DIM, kOwnRows>(c, s_copies, tid >> 5, kPlan / 32);
 }
 
 struct CompactArgs {
@@ -462,7 +490,8 @@ struct CompactArgs {
   int num_pages, page_size;
 };
 
-__global__ void __launch_bounds__(kPlan) compact_kernel(const CompactArgs g) {
+template <int DIM>  // (as above)
+__global__ void __launch_bounds__(kPlan) compact_kernel(const CompactArgs g, const CopyArgs c) {
   __shared__ int scratch[32];
   const int tid = threadIdx.x;
   start_next();
@@ -526,6 +555,11 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(const CompactArgs g) {
     *g.count = movers;
     *g.live = live;
     if (g.live_out != nullptr) *g.live_out = live;
+  }
+  if constexpr (DIM > 0) {
+    __syncthreads();
+    renumber(c, live, tid >> 5, kPlan / 32);
+    copy_units<DIM, kOwnRows>(c, movers, tid >> 5, kPlan / 32);
   }
 }
 
@@ -609,7 +643,8 @@ extern "C" flamia_status flamia_pages_copy(const flamia_kvcache* from, const fla
   g.dst = dst;
   g.n = n;
   g.status = dev_status;
-  return launch_copy(g, from, to, n, static_cast<cudaStream_t>(stream));
+  copy_args(g, from, to);
+  return launch_copy(g, from->d, n, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t flamia_pages_fork_workspace_bytes(int n, int table_stride) {
@@ -647,7 +682,7 @@ extern "C" flamia_status flamia_pages_fork(int32_t* refs, int num_pages, int32_t
   g.page_size = page_size;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // (8 rows of 9 slots with the pages of their next tokens 22 us on the host against 37 with two
-  // launches and a workspace of the call; 10.5 against 15.7 on the device)
+  // launches and a workspace of the call; 10.5 against 15.7 on the device, reserve as two kernels)
   if (n <= kSmallForks && static_cast<long long>(n) * table_stride <= kSmallSlots)
     return launch_after(fork_small_kernel, dim3(1), kSmallThreads, 0, s, g) ? FLAMIA_OK
                                                                             : FLAMIA_ERR_CUDA;
@@ -694,12 +729,15 @@ extern "C" flamia_status flamia_pages_reserve(const flamia_kvcache* cache, int32
   g.num_pages = cache->num_pages;
   g.page_size = cache->page_size;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!launch_after(reserve_kernel, dim3(1), kPlan, 0, s, g)) return FLAMIA_ERR_CUDA;
   CopyArgs c{};
   c.list = g.list;
   c.count = g.count;
   c.status = dev_status;
-  return launch_copy(c, cache, cache, nseq, s);
+  copy_args(c, cache, cache);
+  const bool own = makes_copies(cache, nseq);
+  const auto kern = !own ? reserve_kernel<0> : cache->d == 128 ? reserve_kernel<128> : reserve_kernel<64>;
+  if (!launch_after(kern, dim3(1), kPlan, 0, s, g, c)) return FLAMIA_ERR_CUDA;
+  return own ? FLAMIA_OK : launch_copy(c, cache->d, nseq, s);
 }
 
 extern "C" size_t flamia_pages_compact_workspace_bytes(int num_pages) {
@@ -725,7 +763,6 @@ extern "C" flamia_status flamia_pages_compact(const flamia_kvcache* cache, int32
   g.page_size = cache->page_size;
   g.live_out = live;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (!launch_after(compact_kernel, dim3(1), kPlan, 0, s, g)) return FLAMIA_ERR_CUDA;
   CopyArgs c{};
   c.list = g.list;
   c.count = g.count;
@@ -734,5 +771,10 @@ extern "C" flamia_status flamia_pages_compact(const flamia_kvcache* cache, int32
   c.live = g.live;
   c.table = page_table;
   c.entries = static_cast<long long>(nseq) * table_stride;
-  return launch_copy(c, cache, cache, cache->num_pages / 2, s);
+  copy_args(c, cache, cache);
+  const long long most = cache->num_pages / 2;
+  const bool own = makes_copies(cache, most) && c.entries <= kOwnEntries;
+  const auto kern = !own ? compact_kernel<0> : cache->d == 128 ? compact_kernel<128> : compact_kernel<64>;
+  if (!launch_after(kern, dim3(1), kPlan, 0, s, g, c)) return FLAMIA_ERR_CUDA;
+  return own ? FLAMIA_OK : launch_copy(c, cache->d, most, s);
 }
