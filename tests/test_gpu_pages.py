@@ -99,7 +99,8 @@ def test_copy(lib, pages, page, H_kv, d, n):
     assert all(torch.equal(x, y) for x, y in zip(before, _arrays(a)))
 
 
-@pytest.mark.parametrize("page,H_kv,d,seed", [(32, 2, 64, 0), (64, 1, 128, 1), (256, 3, 64, 2)])
+@pytest.mark.parametrize("page,H_kv,d,seed", [(32, 2, 64, 0), (64, 1, 128, 1), (256, 3, 64, 2),
+                                                 (128, 2, 128, 3), (256, 2, 128, 4)])
 def test_long_stories(lib, page, H_kv, d, seed):
     """Forks, new orders, truncations, ends and compactions in random turns."""
     from precision_causal_attention_block_gb300 import flamia as fl
