@@ -599,14 +599,16 @@ flamia_status flamia_pages_fork(int32_t* refs, int num_pages, int32_t* page_tabl
  * the lowest free one; one whose page has other users takes the lowest free one, to which
  * the rows of positions below starts[b] are copied, and leaves the old one; if all the
  * users of a page are among the call's slots, the last of them keeps it.  If there are not
- * as many free pages, nothing is changed and FLAMIA_DEV_CAPACITY is set.  A sequence
- * whose positions lie outside its row gets none.
+ * as many free pages, nothing is changed and FLAMIA_DEV_CAPACITY is set; nor is it where
+ * cu_seqlens is malformed (it falls, does not begin with 0 or ends behind T:
+ * FLAMIA_DEV_BAD_SEQLENS).  A sequence whose positions lie outside its row gets none.
  * cu_seqlens and starts as for flamia_cache_write (cu_seqlens may end before T).
- * T == 0 enqueues nothing.
+ * T == 0 enqueues nothing (granted stays as it was).
  *  granted    device int32[nseq + 1], not cu_seqlens, or NULL: the offsets for the step's
- *             other calls.  cu_seqlens, or zeros if there were not as many pages or a
- *             sequence's positions lie outside its row: with those the calls do nothing, where with
- *             cu_seqlens they would write into pages that other sequences hold as well.
+ *             other calls.  cu_seqlens, or zeros if there were not as many pages, cu_seqlens
+ *             is malformed or a sequence's positions lie outside its row: with those the calls
+ *             do nothing, where with cu_seqlens they would write into pages that other
+ *             sequences hold as well.
  *  ws         flamia_pages_reserve_workspace_bytes(T, nseq, table_stride, page_size)
  *             bytes, 256-byte aligned.
  */

@@ -348,13 +348,17 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g, con
   if (tid == 0) s_copies = 0;
   start_next();
   wait_for_previous();
-  check_offsets(g.cu, g.nseq, g.T, tid, kPlan, g.status);
+  // Malformed offsets: ranges that overlap touch more slots than there is room for, and a page
+  // that a slot did not get may be another sequence's as well.  So nobody gets any.
+  bool malformed = tid == 0 && (g.cu[0] != 0 || g.cu[g.nseq] > g.T);
+  for (int i = tid; i < g.nseq; i += kPlan) malformed |= g.cu[i] > g.cu[i + 1];
+  if (malformed) report(g.status, FLAMIA_DEV_BAD_SEQLENS);
   // the slots, in order of sequence and position (a sequence's first two by its own
   // thread; those of longer ones by the whole warp)
   int n = 0;
   bool outside = false;  // some sequence's positions are, of its row
   auto put = [&](int b, int slot, int at) {
-    if (at >= g.cap) return;  // (cannot be: see reserve_slots)
+    if (at >= g.cap) return;  // (malformed offsets only: see reserve_slots)
     const int page = g.table[static_cast<long long>(b) * g.stride + slot];
     Slot s{b, slot, page, 0};
     if (page >= g.num_pages) {
@@ -396,8 +400,8 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g, con
     }
     n += total;
   }
-  n = min(n, g.cap);
-  __syncthreads();
+  malformed = __syncthreads_or(malformed);
+  if (malformed) n = 0;
   // A page with other users: every slot here that holds it gives it up; if nobody is
   // left, the last of them keeps it.
   bool shared = false;
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const ReserveArgs g, con
   outside = __syncthreads_or(outside);
   if (tid == 0) *g.count = s_copies;
   if (g.granted != nullptr)
-    for (int i = tid; i <= g.nseq; i += kPlan) g.granted[i] = enough && !outside ? g.cu[i] : 0;
+    for (int i = tid; i <= g.nseq; i += kPlan) g.granted[i] = enough && !outside && !malformed ? g.cu[i] : 0;
   if constexpr (DIM > 0) copy_units<DIM, kOwnRows>(c, s_copies, tid >> 5, kPlan / 32);
 }
 
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(kPlan) compact_kernel(const CompactArgs g, con
 // ------------------------------------------------------------------ host
 
 // Slots that the new tokens of a call can touch: T tokens fill T / page_size pages and
-// begin and end inside two more a sequence.
+// begin and end inside two more a sequence (if no two sequences have the same tokens).
 long long reserve_slots(int T, int nseq, int stride, int page_size) {
   const long long by_tokens = T / page_size + 2ll * nseq, all = static_cast<long long>(nseq) * stride;
   return by_tokens < all ? by_tokens : all;

@@ -813,8 +813,8 @@ class PagePool:
         starts[b] .. of every sequence: what is missing is taken from the free pages, and
         a page with other users is replaced by a copy.  T: an upper bound of the number
         of tokens (None: one that every table row could hold).  granted: int32 [nseq + 1]
-        that becomes cu_seqlens, or zeros if pages ran out or positions lie outside the
-        table, for the calls that write to the pages."""
+        that becomes cu_seqlens, or zeros if pages ran out, positions lie outside the
+        table or cu_seqlens is malformed, for the calls that write to the pages."""
         dev, stream = self._begin()
         cp = _ints(cu_seqlens, "cu_seqlens", self.nseq + 1, dev)
         sp = _ints(starts, "starts", self.nseq, dev)
