@@ -152,16 +152,14 @@ struct SeqWork {
   }
 };
 
-// A sequence shares the prefix if all its new tokens see it.
-__device__ __forceinline__ bool shares(const AttendArgs& g, int start) {
-  return start >= g.prefix - 1;
+// A sequence of n new tokens shares the prefix if all of them see it and have positions inside
+// its table row: so the first one that shares has pages to read for all.
+__device__ __forceinline__ bool shares(const AttendArgs& g, int start, int n) {
+  return start >= g.prefix - 1 && start <= g.cap - n;
 }
-
-// Its pages may be read for all: it has new tokens, and positions inside its table row.
 __device__ __forceinline__ bool reads_for_all(const AttendArgs& g, int b) {
   const DocRange r = doc_range(g.cu, b, g.T);
-  const int start = g.starts != nullptr ? g.starts[b] : 0;
-  return r.e > r.s && shares(g, start) && start <= g.cap - (r.e - r.s);
+  return r.e > r.s && shares(g, g.starts != nullptr ? g.starts[b] : 0, r.e - r.s);
 }
 
 // Entry v of the work list: the prefix, or a sequence.
@@ -200,7 +198,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& g, int v, int shar
   // (no further than the page table: a wild first position costs no endless walk)
   const int end = min(max(w.start + w.n, 0), g.cap);
   int tiles = (end + 127) >> 7;
-  if (KEYS != kAll && shares(g, w.start)) tiles -= g.shared;
+  if (KEYS != kAll && shares(g, w.start, w.n)) tiles -= g.shared;
   if (KEYS == kAll && g.window > 0)
     tiles = min(tiles, ((min(g.sinks, end) + 127) >> 7) +
                            ((min(g.window, end) + R / g.G + 1 + 127) >> 7) + 1);

@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
         pl = w.start + static_cast<int>(last / g.G);
         hi = over ? g.shared * 128 : max(pl + 1, 0);
         wlo = g.window > 0 ? max(pf - g.window + 1, 0) : 0;
-        const bool sharing = KEYS != kAll && !over && shares(g, w.start);
+        const bool sharing = KEYS != kAll && !over && shares(g, w.start, w.n);
         sg.wt = sharing ? g.shared : wlo >> 7;
         sg.ns = KEYS == kAll ? min((g.sinks + 127) >> 7, sg.wt) : 0;
         const int list = sg.ns + max(((hi + 127) >> 7) - sg.wt, 0);
