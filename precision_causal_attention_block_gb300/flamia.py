@@ -395,6 +395,12 @@ class Rotary:
         return q_out, k_out
 
 
+def _positions_fit(rope, positions):
+    """Positions belong to a rope with axes (Rotary checks its own calls)."""
+    if (positions is None) != (rope is None or rope.axes is None):
+        raise RuntimeError("positions: needed for a rope with axes, and only then")
+
+
 def _rope_rows(q_in, q_out, k_in, k_out, rotary, dev):
     if q_in.dim() != 3:
         raise RuntimeError("q_in: flamia needs BF16 rows [T, heads, d]")
@@ -942,6 +948,7 @@ class TrainingCall:
 
     def forward(self, xq, xk, xv, positions=None):
         """positions: for a rope with axes (kept for the backward)."""
+        _positions_fit(self.rope, positions)
         main = torch.cuda.current_stream()
         if self.rope is not None:
             self.positions = positions
@@ -1029,6 +1036,7 @@ class DecodeCall:
         without a pool; positions: for a rope with axes."""
         if (page_table is None) != (self.pool is not None):
             raise RuntimeError("page_table: needed without a pool, and only then")
+        _positions_fit(self.rope, positions)
         if self.pool is not None:
             self.pool.reserve(cu_seqlens, starts, self.T, self.granted)
             cu_seqlens = self.granted
