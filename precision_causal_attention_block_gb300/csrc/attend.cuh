@@ -32,14 +32,15 @@ constexpr int kHigh = 30;       // eV may exceed E0 by this before E0 moves
 constexpr int kLow = 60;        // keys whose eV lies further below E0 are summed apart
 
 // What a kernel's items are.  A call whose sequences share a prefix (attn_prefix.cu) has
-// items over the prefix's whole tiles, with the tokens of all sequences as the query rows
-// of each K / V head, and items of every sequence over what comes behind them.  They
-// leave float32 results, and a last kernel joins those.
+// items over the prefix's whole tiles (bit 0), with the tokens of all sequences as the query
+// rows of each K / V head, and items of every sequence over what comes behind them (bit 1).
+// They leave float32 results, and a last kernel joins those.  (attn_prefix_rows.cu has items
+// over the prefix alone, and walks them by itself.)
 enum Keys : int {
-  kAll = 0,     // items of every sequence: all its keys
-  kPrefix = 1,  // items of the whole call: the first `shared` tiles
-  kRest = 2,    // items of every sequence: the tiles behind those (all, if it does not share)
-  kBoth = 3     // kPrefix's, then kRest's
+  kAll = 0,   // items of every sequence: all its keys
+  kRest = 2,  // items of every sequence: the tiles behind the first `shared` (all, if it does
+              // not share)
+  kBoth = 3   // items of the whole call: the first `shared` tiles; then kRest's
 };
 
 // Where an item's result lies, kept for each of its rows (KEYS != kAll).  One part: in
@@ -165,7 +166,7 @@ __device__ __forceinline__ bool reads_for_all(const AttendArgs& g, int b) {
 // Entry v of the work list: the prefix, or a sequence.
 template <int KEYS>
 __device__ __forceinline__ bool of_prefix(int v) {
-  return KEYS == kPrefix || (KEYS == kBoth && v == 0);
+  return KEYS == kBoth && v == 0;
 }
 template <int KEYS>
 __device__ __forceinline__ int seq_of(int v) {
@@ -255,7 +256,7 @@ template <int R, int KEYS, int kThreads, class Sm>
 __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int sharer = 0;
-  if constexpr (KEYS == kPrefix || KEYS == kBoth) {
+  if constexpr (KEYS == kBoth) {
     const int each = (g.ndocs + kThreads - 1) / kThreads;
     const int b0 = min(tid * each, g.ndocs), b1 = min(b0 + each, g.ndocs);
     if (tid == 0) sm.sharer = g.ndocs;
@@ -269,7 +270,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& g, Sm& sm) {
     __syncthreads();
     sharer = sm.sharer;
   }
-  const int n = KEYS == kPrefix ? 1 : KEYS == kBoth ? g.ndocs + 1 : g.ndocs;
+  const int n = KEYS == kBoth ? g.ndocs + 1 : g.ndocs;
   const int each = (n + kThreads - 1) / kThreads;
   const int b0 = min(tid * each, n), b1 = min(b0 + each, n);
   long long sum = 0;
@@ -422,7 +423,7 @@ flamia_status attend_args(AttendArgs& g, const flamia_kvcache* cache, const void
                           const void* ws, int* dev_status);
 // The kernel for many query rows (256 an item).
 flamia_status attend_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
-// The same over a shared prefix (kPrefix).
+// The same over a shared prefix's whole tiles.
 flamia_status attend_prefix_rows(const flamia_kvcache* c, const AttendArgs& g, cudaStream_t s);
 // Those for 8, 16 or 32 rows an item: kAll, kRest or kBoth.
 flamia_status attend_few(const flamia_kvcache* c, const AttendArgs& g, int R, Keys keys,
