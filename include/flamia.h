@@ -671,14 +671,15 @@ flamia_status flamia_attn_cache(const flamia_kvcache* cache, const void* q_bf16,
  * flamia_attn_cache (without a window) for a batch whose sequences begin with the same
  * `prefix` tokens: a prompt that was forked, a system prompt, a document that all ask
  * about.  A sequence whose new tokens all stand at prefix - 1 or behind (starts[b] >=
- * prefix - 1), and inside its table row, shares it: its first `prefix` positions hold what those of the other sharing
- * sequences hold, as a rule in the same pages, and those of the first such sequence
- * with new tokens are read for all of them.  The others, and calls that gain nothing by it
- * (one sequence, a prefix below 128, more than 96 query rows a sequence and K / V head on
- * average; without FLAMIA_FLAG_PREFIX_ALWAYS those that save too few bytes) are
- * flamia_attn_cache's.  The results are what that call gives, in other roundings: with more
- * than 8 query rows of a K / V head in the batch (T * H / H_kv) a weight is rounded
- * to 2^-11 of itself.
+ * prefix - 1), and inside its table row, shares it: its first `prefix` positions hold what
+ * those of the other sharing sequences hold, as a rule in the same pages, and those of the
+ * first such sequence with new tokens are read for all of them.  Nothing checks this: a
+ * sequence as long as that which begins with something else goes into another call.  The
+ * others, and calls that gain nothing by it (one sequence, a prefix below 128, more than 96
+ * query rows a sequence and K / V head on average; without FLAMIA_FLAG_PREFIX_ALWAYS those
+ * that save too few bytes) are flamia_attn_cache's.  The results are what that call gives, in
+ * other roundings: with more than 8 query rows of a K / V head in the batch (T * H / H_kv) a
+ * weight is rounded to 2^-11 of itself.
  *
  *  flags      0 or FLAMIA_FLAG_PREFIX_ALWAYS.
  *  ws         flamia_attn_cache_prefix_workspace_bytes bytes, 256-byte aligned, as for

@@ -648,8 +648,11 @@ __global__ void __launch_bounds__(Cfg<DIM, R>::kThreads, Cfg<DIM, R>::kCtas)
     // This thread's rows: eight from r0 on, and with 32 an item eight from r0 + 16 on if it
     // has any there.  (A row is a column of the products, and nothing else depends on what stays
     // in one without a row.  131,072 keys shared by 24 rows of 32 heads of 64: 265 -> 221
-    // us; 16,384 by 32 rows of 16 heads of 128: 61.7 -> 62.6.  The same for the first eight
-    // costs 16 rows an item 55 -> 58 us.)
+    // us; 16,384 by 32 rows of 16 heads of 128: 61.7 -> 62.6.  Plain calls, 16 sequences over
+    // 4,096: 24 rows of 16 heads of 64 77.8 -> 71.6, 25 77.8 -> 75.8, 17 of 8 heads of 128 58.3
+    // -> 56.3; 32 rows, 8 over 8,192, 32 heads of 64 124.9 -> 122.9, 8 of 128 59.4 and 60.4 ->
+    // 58.4 and 59.4; one over 16,384 41.0 in both.  The same for the first eight costs 16 rows
+    // an item 55 -> 58 us.)
     constexpr int kNext = 8 * C::kHalves;
     const int half = C::kHalves == 1 ? 0 : warp >> 2, r0 = half * 8;
     const int key_in = tid & 127;                   // its key inside a tile

@@ -7,7 +7,7 @@
 //   lg = log2 sum 2^lg_i,   o = sum 2^(lg_i - lg) o_i.
 //
 // Few query rows of a K / V head in the whole batch: one launch of attn_cache.cu's
-// kernels over items of both kinds.  Many: the kernel of attn_cache_rows.cu over the prefix
+// kernels over items of both kinds.  Many: the kernel of attn_prefix_rows.cu over the prefix
 // (no masks: all rows see all of it), then attn_cache.cu's over what comes behind it.
 // In both cases a last kernel joins what they leave: float32 rows of items that
 // were not cut and the parts of those that were (equal runs of key tiles for all CTAs, as
@@ -17,10 +17,10 @@
 //
 // Floor: K and V of the prefix once (2 H_kv (d + 1) bytes a token) and of each own tail.
 // Measured, the whole call (us; plain: flamia_attn_cache on the same batch): 8 tokens over
-// 2,048, 16 heads of 128, 17.2 (floor 1.4, plain 22.0: latency); 89 of 96 sequences over
-// 16,421, 32 / 8 heads of 128, 81 (12.7, 255: 44 over the prefix, 28 the tails, 9 the join);
-// 24 over 131,072, 32 heads of 64, 221 (84, 1,735: the softmax of 24 rows a tile); 128 x 4
-// drafted tokens over 8,191, 16 / 4 heads of 128, 81 (17.9, 161: as the batch).
+// 2,048, 16 heads of 128, 16.7 (floor 1.4, plain 22.0: latency); 89 of 96 sequences over
+// 16,421, 32 / 8 heads of 128, 83 (12.7, 255: 43 over the prefix, 29 the tails, 11 the join);
+// 24 over 131,072, 32 heads of 64, 216 (84, 1,735: the softmax of 24 rows a tile); 128 x 4
+// drafted tokens over 8,191, 16 / 4 heads of 128, 85 (17.9, 161: as the batch).
 #include "attend.cuh"
 
 namespace flamia {

@@ -525,9 +525,14 @@ class KVCache:
         cache.  prefix: the sequences begin with the same so many tokens (those of which
         all new tokens stand at prefix - 1 or behind), which are read once for all of
         them where that is faster (always_share: in any case); with a window each reads
-        its own.  ws None: the workspace of the current stream and thread (42 MB, made
-        by their first call, shared by all caches), or, while a graph is captured, one
-        that belongs to the graph: calls that overlap never share one."""
+        its own.  Nothing checks that they are the same: every sequence as long as that is
+        given the first one's keys and values there, so one that begins with something else
+        has to go into another call.  With a prefix read once and more than 8 query rows of
+        a K / V head in the batch, softmax weights are rounded to 2^-11 of themselves (plain
+        calls: with more than 8 rows a sequence).  ws None: the workspace of the current
+        stream and thread (42 MB, made by their first call, shared by all caches; beside it
+        one for calls with a prefix, as large as their largest needed), or, while a graph is
+        captured, one that belongs to the graph: calls that overlap never share one."""
         T, H = q.shape[0], q.shape[1]
         if o is None:
             o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -735,7 +740,8 @@ class PagePool:
     refs int32 [pages] (slots of the table that hold a page; 0: free), on the device and
     the caller's to read.  Calls on one pool follow one another on one stream (or are
     ordered by the caller); they can be captured.  Errors found on the device (no free
-    page, positions outside the table) show in check_status."""
+    page, positions outside the table) show in check_status until the caller sets `status`
+    to zero."""
 
     def __init__(self, cache: KVCache, nseq: int, width: int):
         dev = cache.k_codes.device
@@ -1005,8 +1011,10 @@ class DecodeCall:
 
     pool: the step begins with pages for its tokens (PagePool.reserve) and takes the
     pool's page table; where it cannot have them it does nothing more (check_status), as
-    other sequences may hold the pages that it would write to.  prefix, always_share: the sequences begin with the same so many
-    tokens, read once for all of them (KVCache.attend)."""
+    other sequences may hold the pages that it would write to.  `granted` holds the step's
+    offsets then: cu_seqlens, or zeros, so lengths are to grow by granted.diff().  prefix,
+    always_share: the sequences begin with the same so many tokens, read once for all of
+    them (KVCache.attend, which says what is not checked)."""
 
     def __init__(self, cache: KVCache, T: int, nseq: int, H: int, softmax_scale: float,
                  rope: Rotary = None, window: int = 0, sinks: int = 0, pool: PagePool = None,
